@@ -37,7 +37,8 @@
  *     a launch failure from the HIP runtime.  Nothing is printed and no
  *     C++ exception crosses the ABI.
  *   - Inputs must be finite (no NaN or infinity); other inputs give
- *     unspecified bytes.
+ *     unspecified bytes (the operators between the GEMMs say what they do
+ *     with them).
  *   - Empty shapes (a zero dimension) are valid and enqueue nothing except
  *     the hash of an empty output where one is requested.
  *   - The library allocates no device memory at run time.  Calls that
@@ -310,6 +311,194 @@ size_t output_hash_workspace_bytes(void);
 int output_hash(const float* C, int64_t M, int64_t N, int64_t ldc,
                 uint64_t* hash, void* workspace, size_t workspace_bytes,
                 void* stream);
+
+/* ------------------------------------------------------------------------
+ * The operators between the GEMMs of a training step: layer norm, activation
+ * checkpoints in 8 bits, log probabilities of given tokens.
+ *
+ * Value matrices are f32, bf16 or f16 (`dtype`), row-major, with any leading
+ * dimension >= cols and the alignment of their element type; every matrix of
+ * values in one call has the same dtype.  Statistics, scales, weights and
+ * their gradients are f32.  Sizes are at most 2^31 - 1.  Infinities and NaN
+ * are allowed here: they make their own row (for a checkpoint their own
+ * group, for a column sum or column scale their own column) NaN and nothing
+ * else.  Results depend on sizes and values only, never on timing: no sum is
+ * taken with atomics, and two calls give the same bytes.
+ * ------------------------------------------------------------------------ */
+#define I8G_F32  0u
+#define I8G_BF16 1u
+#define I8G_F16  2u
+
+/*
+ * layer_norm -- y = (x - mean) / sqrt(var + eps) * gamma + beta on the rows
+ * of X, var being the mean of (x - mean)^2:
+ *   mean = RN(sum x / cols), rstd = RN(1 / sqrt(var + eps)), the sums and the
+ *   root in binary64, rounded to binary32 once;
+ *   Y = RN(RN(RN(RN(x - mean) * rstd) * gamma) + beta), rounded once more to
+ *   `dtype`.
+ *   X, Y   rows x cols of `dtype`; Y may be X itself (with ldy = ldx).
+ *   gamma, beta  cols f32 each, or NULL for ones / zeros.
+ *   mean, rstd   rows f32 each (inputs of the backward pass), or NULL.
+ * A row of one value or of equal values has var = 0 and gives beta.
+ * Errors: I8G_EINVAL (null pointer, unknown dtype, negative size, cols == 0
+ * with rows > 0, leading dimension < cols, misaligned element pointer, eps
+ * negative or not finite), I8G_EHIP.
+ */
+int layer_norm(const void* X, uint32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+               const float* gamma, const float* beta, double eps,
+               void* Y, int64_t ldy, float* mean, float* rstd, void* stream);
+
+/*
+ * layer_norm_quantize_rows -- quantize_rows of the binary32 output of
+ * layer_norm, which is never stored: the A operand of the next GEMM.  Q and
+ * scale equal quantize_rows(layer_norm(X)) byte for byte; a row that holds an
+ * infinity or a NaN gets a NaN scale and codes 0.
+ *   Q      rows x cols int8, leading dimension ldq >= cols.
+ *   scale  rows f32.
+ * Otherwise as layer_norm.
+ */
+int layer_norm_quantize_rows(const void* X, uint32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+                             const float* gamma, const float* beta, double eps,
+                             int8_t* Q, int64_t ldq, float* scale, float* mean, float* rstd,
+                             void* stream);
+
+/*
+ * layer_norm_bwd -- the gradients of layer_norm for the gradient dY of Y:
+ *   xh = RN(RN(x - mean) * rstd)    w  = RN(dy * gamma)
+ *   c1 = RN(sum_j w / cols)         c2 = RN(sum_j w * xh / cols)
+ *   dX = RN(rstd * RN(RN(w - c1) - RN(xh * c2))), rounded once more to dtype
+ *   dgamma = RN(sum_i dy * xh)      dbeta = RN(sum_i dy)
+ * all sums in binary64.
+ *   mean, rstd   rows f32 each, as layer_norm wrote them.
+ *   gamma  cols f32, or NULL for ones.
+ *   dX     rows x cols of dtype, or NULL; dX may be dY itself.
+ *   dgamma, dbeta  cols f32, either may be NULL.  With rows == 0 they are 0.
+ *   workspace  device scratch of layer_norm_bwd_workspace_bytes(rows, cols),
+ *          256-byte aligned, any contents; not needed (may be NULL) when
+ *          dgamma and dbeta are both NULL.
+ * Errors: as layer_norm, and I8G_EWORKSPACE.
+ */
+size_t layer_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+int layer_norm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ldx, uint32_t dtype,
+                   int64_t rows, int64_t cols, const float* gamma, const float* mean,
+                   const float* rstd, void* dX, int64_t lddx, float* dgamma, float* dbeta,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * checkpoint_i8 -- stores an activation for the backward pass in 8 bits: the
+ * rule of quantize_rows applied to each group of `group` columns of a row
+ * (the last group of a row may be shorter).
+ *   group  32, 64, 128 or 256.
+ *   Q      rows x cols int8, leading dimension ldq >= cols.
+ *   scale  rows x ceil(cols/group) f32, leading dimension lds.
+ * A value is off by at most half its group's scale, a(group)/254, and the
+ * roundings of s and RN(q*s): RN(127*s) may be above a by 2^-23 of it, which
+ * overflows for |a| within 2^-22 of the largest binary32 value.  A group with an infinity or a NaN gets a NaN scale
+ * and codes 0, so that it restores as NaN.
+ * The calls that read a checkpoint also take group = 0, one scale per row,
+ * scale[i * lds]: with lds = 1 that is the output of quantize_rows or of
+ * layer_norm_quantize_rows, so the codes a GEMM has read serve as the saved
+ * activation too.  The value a code stands for is RN(q * s).
+ * Errors: I8G_EINVAL (null pointer, unknown dtype or group, negative size,
+ * leading dimension too small, misaligned element pointer), I8G_EHIP.
+ */
+int checkpoint_i8(const void* X, uint32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+                  int32_t group, int8_t* Q, int64_t ldq, float* scale, int64_t lds, void* stream);
+
+/* checkpoint_restore -- Y = RN(q * s), rounded once more to dtype. */
+int checkpoint_restore(const int8_t* Q, int64_t ldq, const float* scale, int64_t lds, int32_t group,
+                       int64_t rows, int64_t cols, void* Y, uint32_t dtype, int64_t ldy,
+                       void* stream);
+
+/*
+ * checkpoint_act_bwd -- the gradient of an activation function at the
+ * checkpoint's values x = RN(q * s): dX = dY * act'(x).
+ *   act    I8G_ACT_RELU: act' = 1 for x > 0, else 0 (dX is dY or +0);
+ *          I8G_ACT_GELU: the tanh form, gelu(x) = x (1 + tanh u) / 2 with
+ *          u = sqrt(2/pi) (x + 0.044715 x^3).
+ *   dY, dX rows x cols of dtype; dX may be dY itself.
+ * Errors: as checkpoint_i8; I8G_EINVAL for an unknown act.
+ */
+#define I8G_ACT_RELU 1u
+#define I8G_ACT_GELU 2u
+int checkpoint_act_bwd(const int8_t* Q, int64_t ldq, const float* scale, int64_t lds, int32_t group,
+                       int64_t rows, int64_t cols, uint32_t act, const void* dY, int64_t lddy,
+                       void* dX, int64_t lddx, uint32_t dtype, void* stream);
+
+/*
+ * checkpoint_quantize_cols -- quantize_cols of the checkpoint's values, which
+ * are not stored: the transposed operand of the weight gradient's GEMM
+ * (dW = X^T dY) straight from the codes.  Qt and scale_out equal
+ * quantize_cols(checkpoint_restore(...)) byte for byte; a column that holds a
+ * NaN gets a NaN scale and codes 0.
+ *   Qt     cols x rows int8, leading dimension ldqt >= rows.
+ *   scale_out  cols f32 (also scratch while the call runs).
+ * Errors: as checkpoint_i8.
+ */
+int checkpoint_quantize_cols(const int8_t* Q, int64_t ldq, const float* scale, int64_t lds,
+                             int32_t group, int64_t rows, int64_t cols, int8_t* Qt, int64_t ldqt,
+                             float* scale_out, void* stream);
+
+/*
+ * layer_norm_bwd_checkpoint -- layer_norm_bwd with the input's values taken
+ * from its checkpoint, x = RN(q * s); mean and rstd are those of the input
+ * that the forward pass saw.  Arguments otherwise as layer_norm_bwd.
+ */
+int layer_norm_bwd_checkpoint(const void* dY, int64_t lddy, uint32_t dtype, const int8_t* Q,
+                              int64_t ldq, const float* scale, int64_t lds, int32_t group,
+                              int64_t rows, int64_t cols, const float* gamma, const float* mean,
+                              const float* rstd, void* dX, int64_t lddx, float* dgamma, float* dbeta,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * token_logprobs -- for each row x of logits: lse = log sum_j exp(x_j), the
+ * log probability x_t - lse of the row's given token t, the entropy
+ * -sum_j p_j log p_j, and the `topk` best tokens with their log
+ * probabilities, best first, equal logits in the order of their index.
+ *   logits   rows x vocab of dtype; vocab is at most I8G_VOCAB_MAX.
+ *   targets  rows int64 token numbers; one outside [0, vocab) is no token
+ *            (padding): its logprob is 0.  May be NULL with logprob NULL.
+ *   topk     0 .. I8G_TOPK_MAX, at most vocab.
+ *   logprob, entropy, lse   rows f32 each, any may be NULL.
+ *   top_index, top_logprob  rows x topk int32 / f32 (not used for topk 0).
+ *   workspace  device scratch of token_logprobs_workspace_bytes(rows, vocab,
+ *            topk), 256-byte aligned, any contents.
+ * Sums are held against the row's maximum, in binary32 over at most 128
+ * values and binary64 beyond.  A logit of -inf has probability 0 and adds
+ * nothing to the entropy.  A row of -inf only has lse and every log
+ * probability -inf, entropy 0, and its first topk tokens as the best.  A row
+ * with a NaN or +inf has NaN outputs; for the order of its best tokens a NaN
+ * counts as -inf.
+ * Errors: I8G_EINVAL (null pointer, unknown dtype, negative or too large
+ * size, vocab == 0 with rows > 0, ld < vocab, topk out of range, misaligned
+ * pointer), I8G_EWORKSPACE, I8G_EHIP.
+ */
+#define I8G_TOPK_MAX  32
+#define I8G_VOCAB_MAX 4194304
+size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int32_t topk);
+int token_logprobs(const void* logits, uint32_t dtype, int64_t rows, int64_t vocab, int64_t ld,
+                   const int64_t* targets, int32_t topk, float* logprob, float* entropy, float* lse,
+                   int32_t* top_index, float* top_logprob, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/*
+ * token_logprobs_bwd -- the gradient of the logits for the gradients
+ * g_logprob of the given tokens' log probabilities and g_entropy of the
+ * entropies (rows f32 each; either may be NULL for 0, not both):
+ *   dlogits_j = g ([j = t] - p_j) - g_entropy p_j (log p_j + H),
+ * p_j = exp(x_j - lse), g = 0 for a row without a token.  lse and entropy (H)
+ * are those of token_logprobs; entropy is needed with g_entropy only, targets
+ * with g_logprob only.  Where p_j is 0 so is the gradient.  p_j is as exact
+ * as lse, which is off by |lse| 2^-24; a row with |lse| >= 2^24, where that is
+ * more than a factor e (a row of -inf only, one masked by the type's lowest
+ * value throughout), gets 0.
+ *   dlogits  rows x vocab of dtype; it may be logits itself (lddl = ld).
+ * Errors: as token_logprobs.
+ */
+int token_logprobs_bwd(const void* logits, uint32_t dtype, int64_t rows, int64_t vocab, int64_t ld,
+                       const int64_t* targets, const float* lse, const float* entropy,
+                       const float* g_logprob, const float* g_entropy, void* dlogits, int64_t lddl,
+                       void* stream);
 
 /* ------------------------------------------------------------------------
  * Self-checks, after the defence layers of the page "Verification -- why

@@ -14,6 +14,19 @@ entry points have the names of the C ABI in ``include/int8_gemm.h``:
                                      storage formats (int4: 16*ceil(len/32) bytes per line)
     gemm_i8_blockscaled(..., K=K, a_int4=True / b_int4=True)  int4 operands
 
+and, between the GEMMs of a training step (f32, bf16 or f16 values):
+
+    layer_norm(X, weight, bias, eps)                -> (Y, mean, rstd)
+    layer_norm_quantize_rows(X, weight, bias, eps)  -> (Q, scale, mean, rstd)
+    layer_norm_bwd(dY, X, mean, rstd, weight)       -> (dX, dweight, dbias)
+    layer_norm_bwd_checkpoint(dY, Q, scale, group, mean, rstd, weight)
+    checkpoint_i8(X, group)                         -> (Q, scale)
+    checkpoint_restore(Q, scale, group, dtype)      -> Y
+    checkpoint_act_bwd(dY, Q, scale, group, act)    -> dX
+    checkpoint_quantize_cols(Q, scale, group)       -> (Qt, scale)
+    token_logprobs(logits, targets, topk)           -> (logprob, entropy, lse, top_index, top_logprob)
+    token_logprobs_bwd(logits, targets, lse, entropy, g_logprob, g_entropy)  -> dlogits
+
 Hash tensors hold the 64-bit hash in an int64 element; ``hash_value``
 returns it as a Python int in [0, 2^64).  If the library is not built, or
 cannot be loaded, every entry point raises: there is no fallback.
@@ -27,7 +40,10 @@ import torch
 __all__ = ["quantize_rows", "quantize_cols", "gemm_i8_blockscaled", "output_hash",
            "blockscaled_gemm", "hash_value", "workspace_bytes", "library_path", "load",
            "I8G_RELU", "I8G_HASH", "K_MAX", "I8GError", "quantize_rows_fmt", "quantize_cols_fmt",
-           "FMT_POW2", "FMT_INT4", "int4_line_bytes", "gemm_i8_requant", "quantize_batch"]
+           "FMT_POW2", "FMT_INT4", "int4_line_bytes", "gemm_i8_requant", "quantize_batch",
+           "layer_norm", "layer_norm_quantize_rows", "layer_norm_bwd", "layer_norm_bwd_checkpoint",
+           "checkpoint_i8", "checkpoint_restore", "checkpoint_act_bwd", "checkpoint_quantize_cols",
+           "token_logprobs", "token_logprobs_bwd"]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libint8_gemm.so")
@@ -44,7 +60,10 @@ EXPORTED = ("quantize_rows", "quantize_cols", "gemm_i8_blockscaled", "gemm_i8_wo
             "i8g_probe_hash", "i8g_probe_workspace_bytes", "quantize_rows_fmt", "quantize_cols_fmt",
             "gemm_i8_requant", "gemm_i8_requant_workspace_bytes", "quantize_batch",
             "gemm_i8_workspace_bytes_flags", "i8g_audit_quantize_fmt", "i8g_set_test_overrides",
-            "i8g_plan_query", "gemm_i8_blockscaled_noalloc")
+            "i8g_plan_query", "gemm_i8_blockscaled_noalloc", "layer_norm", "layer_norm_quantize_rows",
+            "layer_norm_bwd", "layer_norm_bwd_workspace_bytes", "layer_norm_bwd_checkpoint", "checkpoint_i8",
+            "checkpoint_restore", "checkpoint_act_bwd", "checkpoint_quantize_cols", "token_logprobs",
+            "token_logprobs_workspace_bytes", "token_logprobs_bwd")
 
 _lib = None
 _ws = {}
@@ -126,6 +145,29 @@ def load():
     lib.i8g_plan_query.argtypes = [c_i64, c_i64, c_i64, c_i64, c_u32, ctypes.POINTER(c_i32),
                                    ctypes.POINTER(c_i32)]
     lib.i8g_plan_query.restype = ctypes.c_int
+    c_f64 = ctypes.c_double
+    ckpt = [c_vp, c_i64, c_vp, c_i64, c_i32, c_i64, c_i64]     # Q, ldq, scale, lds, group, rows, cols
+    ln_grad = [c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_vp, c_sz, c_vp]
+    for name, args in (
+            ("layer_norm", [c_vp, c_u32, c_i64, c_i64, c_i64, c_vp, c_vp, c_f64, c_vp, c_i64, c_vp, c_vp, c_vp]),
+            ("layer_norm_quantize_rows", [c_vp, c_u32, c_i64, c_i64, c_i64, c_vp, c_vp, c_f64, c_vp, c_i64, c_vp,
+                                          c_vp, c_vp, c_vp]),
+            ("layer_norm_bwd", [c_vp, c_i64, c_vp, c_i64, c_u32, c_i64, c_i64, *ln_grad]),
+            ("layer_norm_bwd_checkpoint", [c_vp, c_i64, c_u32, *ckpt, *ln_grad]),
+            ("checkpoint_i8", [c_vp, c_u32, c_i64, c_i64, c_i64, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp]),
+            ("checkpoint_restore", [*ckpt, c_vp, c_u32, c_i64, c_vp]),
+            ("checkpoint_act_bwd", [*ckpt, c_u32, c_vp, c_i64, c_vp, c_i64, c_u32, c_vp]),
+            ("checkpoint_quantize_cols", [*ckpt, c_vp, c_i64, c_vp, c_vp]),
+            ("token_logprobs", [c_vp, c_u32, c_i64, c_i64, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                c_sz, c_vp]),
+            ("token_logprobs_bwd", [c_vp, c_u32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64,
+                                    c_vp])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_int
+    lib.layer_norm_bwd_workspace_bytes.argtypes = [c_i64, c_i64]
+    lib.layer_norm_bwd_workspace_bytes.restype = c_sz
+    lib.token_logprobs_workspace_bytes.argtypes = [c_i64, c_i64, c_i32]
+    lib.token_logprobs_workspace_bytes.restype = c_sz
     _lib = lib
     return lib
 
@@ -489,3 +531,257 @@ def blockscaled_gemm(A, B, relu=False, want_hash=False):
     QA, s_row = quantize_rows(A)
     QBt, s_col = quantize_cols(B)
     return gemm_i8_blockscaled(QA, s_row, QBt, s_col, relu=relu, want_hash=want_hash)
+
+
+# ---- the operators between the GEMMs --------------------------------------
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_ACTS = {"relu": 1, "gelu": 2}
+
+
+def _values(x, name, like=None):
+    """(rows, cols, ld) of a 2-D matrix of f32, bf16 or f16 values (of the
+    dtype and device of `like`, if given)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {x.dtype}")
+    if like is not None and (x.dtype != like.dtype or x.shape != like.shape):
+        raise ValueError(f"{name} must have the dtype and shape of the other values: "
+                         f"{like.dtype} {tuple(like.shape)}, got {x.dtype} {tuple(x.shape)}")
+    return _layout(x, name, like)
+
+
+def _layout(x, name, like=None):
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be on a GPU")
+    if like is not None and x.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {x.device}")
+    rows, cols = x.shape
+    if cols > 1 and rows > 0 and x.stride(1) != 1:
+        raise ValueError(f"{name} must be row-major (unit column stride)")
+    if rows > 1 and x.stride(0) < cols:
+        raise ValueError(f"{name} has overlapping rows (expanded?): call .contiguous() first")
+    return rows, cols, x.stride(0) if rows > 1 else max(cols, 1)
+
+
+def _vector(x, n, name, like, optional=False):
+    """The address of a contiguous f32 vector of n values."""
+    if x is None and optional:
+        return None
+    if not isinstance(x, torch.Tensor) or x.dtype != torch.float32 or x.dim() != 1 or x.numel() != n:
+        raise ValueError(f"{name} must be a 1-D float32 tensor of {n} values")
+    if x.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {x.device}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return x.data_ptr()
+
+
+def _enqueue(fn, like, *args):
+    """fn(*args, stream) on torch's current stream of like's device.  The
+    stream's handle is read without making a Stream object (1.9 us of a call
+    that takes 10)."""
+    dev = like.get_device()
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc:
+        _check(rc)
+
+
+def _like(x):
+    """An uninitialized contiguous matrix of x's shape and dtype."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+def layer_norm(X, weight=None, bias=None, eps=1e-5):
+    """Layer norm of the rows of X: (Y, mean, rstd), Y of X's dtype; weight
+    and bias are f32 (None: ones, zeros)."""
+    rows, cols, ldx = _values(X, "X")
+    w, b = _vector(weight, cols, "weight", X, True), _vector(bias, cols, "bias", X, True)
+    Y = _like(X)
+    stats = torch.empty((2, rows), dtype=torch.float32, device=X.device)
+    mean, rstd = stats.unbind(0)
+    _enqueue(load().layer_norm, X, X.data_ptr(), _DTYPES[X.dtype], rows, cols, ldx, w, b, eps, Y.data_ptr(),
+             max(cols, 1), mean.data_ptr(), rstd.data_ptr())
+    return Y, mean, rstd
+
+
+def layer_norm_quantize_rows(X, weight=None, bias=None, eps=1e-5):
+    """quantize_rows of layer_norm's binary32 output: (Q, scale, mean, rstd)."""
+    rows, cols, ldx = _values(X, "X")
+    w, b = _vector(weight, cols, "weight", X, True), _vector(bias, cols, "bias", X, True)
+    Q = _int8_padded(rows, cols, X.device)
+    stats = torch.empty((3, rows), dtype=torch.float32, device=X.device)
+    scale, mean, rstd = stats.unbind(0)
+    _enqueue(load().layer_norm_quantize_rows, X, X.data_ptr(), _DTYPES[X.dtype], rows, cols, ldx, w, b, eps,
+             Q.data_ptr(), Q.stride(0), scale.data_ptr(), mean.data_ptr(), rstd.data_ptr())
+    return Q, scale, mean, rstd
+
+
+def _ln_grads(dY, cols, weight_grad):
+    """dX, dweight, dbias and their scratch (which lives as long as torch's
+    current stream needs it)."""
+    dX = _like(dY)
+    if not weight_grad:
+        return dX, None, None, None, 0
+    nbytes = load().layer_norm_bwd_workspace_bytes(dY.shape[0], cols)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dY.device)
+    dw, db = torch.empty((2, cols), dtype=torch.float32, device=dY.device).unbind(0)
+    return dX, dw, db, ws, nbytes
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def layer_norm_bwd(dY, X, mean, rstd, weight=None, weight_grad=True):
+    """(dX, dweight, dbias) for the gradient dY of layer_norm's output; the
+    last two are None without weight_grad."""
+    rows, cols, lddy = _values(dY, "dY")
+    _, _, ldx = _values(X, "X", dY)
+    m, r, w = (_vector(mean, rows, "mean", dY), _vector(rstd, rows, "rstd", dY),
+               _vector(weight, cols, "weight", dY, True))
+    dX, dw, db, ws, nbytes = _ln_grads(dY, cols, weight_grad)
+    _enqueue(load().layer_norm_bwd, dY, dY.data_ptr(), lddy, X.data_ptr(), ldx, _DTYPES[dY.dtype], rows, cols, w,
+             m, r, dX.data_ptr(), max(cols, 1), _addr(dw), _addr(db), _addr(ws), nbytes)
+    return dX, dw, db
+
+
+def _checkpoint(Q, scale, group, shape=None, like=None):
+    """The leading arguments of the calls that read a checkpoint."""
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 2 or Q.dtype != torch.int8:
+        raise ValueError("Q must be a 2-D int8 tensor")
+    if shape is not None and tuple(Q.shape) != tuple(shape):
+        raise ValueError(f"Q must have the shape {tuple(shape)}, got {tuple(Q.shape)}")
+    rows, cols, ldq = _layout(Q, "Q", like)
+    if group not in (0, 32, 64, 128, 256):
+        raise ValueError("group must be 32, 64, 128 or 256, or 0 for one scale per row")
+    groups = -(-cols // group) if group else min(cols, 1)
+    if not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32 or \
+            not (tuple(scale.shape) == (rows, groups) or (group == 0 and tuple(scale.shape) == (rows,))):
+        raise ValueError(f"scale must be a float32 tensor of shape ({rows}, {groups})"
+                         + (f" or ({rows},)" if group == 0 else ""))
+    if scale.device != Q.device:
+        raise ValueError(f"scale must be on {Q.device}, got {scale.device}")
+    if scale.dim() == 2 and groups > 1 and scale.stride(1) != 1:
+        raise ValueError("scale must be row-major (unit column stride)")
+    lds = scale.stride(0) if rows > 1 else max(groups, 1)
+    if lds < groups:
+        raise ValueError("scale has overlapping rows (expanded?): call .contiguous() first")
+    return Q.data_ptr(), ldq, scale.data_ptr(), lds, group, rows, cols
+
+
+def layer_norm_bwd_checkpoint(dY, Q, scale, group, mean, rstd, weight=None, weight_grad=True):
+    """layer_norm_bwd with the input taken from its 8-bit checkpoint."""
+    rows, cols, lddy = _values(dY, "dY")
+    ck = _checkpoint(Q, scale, group, dY.shape, dY)
+    m, r, w = (_vector(mean, rows, "mean", dY), _vector(rstd, rows, "rstd", dY),
+               _vector(weight, cols, "weight", dY, True))
+    dX, dw, db, ws, nbytes = _ln_grads(dY, cols, weight_grad)
+    _enqueue(load().layer_norm_bwd_checkpoint, dY, dY.data_ptr(), lddy, _DTYPES[dY.dtype], *ck, w, m, r,
+             dX.data_ptr(), max(cols, 1), _addr(dw), _addr(db), _addr(ws), nbytes)
+    return dX, dw, db
+
+
+def checkpoint_i8(X, group=128):
+    """An activation in 8 bits: (Q, scale) with one scale for each row and
+    group of 32, 64, 128 or 256 columns."""
+    rows, cols, ldx = _values(X, "X")
+    if group not in (32, 64, 128, 256):
+        raise ValueError("group must be 32, 64, 128 or 256")
+    Q = _int8_padded(rows, cols, X.device)
+    groups = -(-cols // group)
+    scale = torch.empty((rows, groups), dtype=torch.float32, device=X.device)
+    _enqueue(load().checkpoint_i8, X, X.data_ptr(), _DTYPES[X.dtype], rows, cols, ldx, group, Q.data_ptr(),
+             Q.stride(0), scale.data_ptr(), max(groups, 1))
+    return Q, scale
+
+
+def checkpoint_restore(Q, scale, group, dtype=torch.float32):
+    """The values of a checkpoint.  group 0: one scale per row, as
+    quantize_rows and layer_norm_quantize_rows give them."""
+    ck = _checkpoint(Q, scale, group)
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    Y = torch.empty(Q.shape, dtype=dtype, device=Q.device)
+    _enqueue(load().checkpoint_restore, Q, *ck, Y.data_ptr(), _DTYPES[dtype], max(Q.shape[1], 1))
+    return Y
+
+
+def checkpoint_act_bwd(dY, Q, scale, group, act="gelu"):
+    """dX = dY * act'(x) at the checkpoint's values x; act is "relu" or
+    "gelu" (the tanh form)."""
+    _, cols, lddy = _values(dY, "dY")
+    ck = _checkpoint(Q, scale, group, dY.shape, dY)
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    dX = _like(dY)
+    _enqueue(load().checkpoint_act_bwd, dY, *ck, _ACTS[act], dY.data_ptr(), lddy, dX.data_ptr(), max(cols, 1),
+             _DTYPES[dY.dtype])
+    return dX
+
+
+def checkpoint_quantize_cols(Q, scale, group):
+    """quantize_cols of the checkpoint's values: (Qt, scale), the transposed
+    operand of a weight gradient's GEMM."""
+    ck = _checkpoint(Q, scale, group)
+    rows, cols = Q.shape
+    Qt = _int8_padded(cols, rows, Q.device)
+    s = torch.empty(cols, dtype=torch.float32, device=Q.device)
+    _enqueue(load().checkpoint_quantize_cols, Q, *ck, Qt.data_ptr(), Qt.stride(0), s.data_ptr())
+    return Qt, s
+
+
+def _targets(t, rows, like):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int64 or t.dim() != 1 or t.numel() != rows:
+        raise ValueError(f"targets must be a 1-D int64 tensor of {rows} token numbers")
+    if t.device != like.device:
+        raise ValueError(f"targets must be on {like.device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("targets must be contiguous")
+    return t.data_ptr()
+
+
+def token_logprobs(logits, targets, topk=0):
+    """(logprob, entropy, lse, top_index, top_logprob) of each row of logits:
+    the log probability of its target (0 for a target outside the
+    vocabulary), and its topk best tokens (None, None for topk 0)."""
+    rows, vocab, ld = _values(logits, "logits")
+    t = _targets(targets, rows, logits)
+    if topk < 0 or topk > 32 or (rows > 0 and topk > vocab):
+        raise ValueError(f"topk must be between 0 and min(32, {vocab}), got {topk}")
+    dev = logits.device
+    out = torch.empty((3, rows), dtype=torch.float32, device=dev)
+    logprob, entropy, lse = out.unbind(0)
+    index = torch.empty((rows, topk), dtype=torch.int32, device=dev) if topk else None
+    top = torch.empty((rows, topk), dtype=torch.float32, device=dev) if topk else None
+    nbytes = load().token_logprobs_workspace_bytes(rows, vocab, topk)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _enqueue(load().token_logprobs, logits, logits.data_ptr(), _DTYPES[logits.dtype], rows, vocab, ld, t, topk,
+             logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), _addr(index), _addr(top), ws.data_ptr(), nbytes)
+    return logprob, entropy, lse, index, top
+
+
+def token_logprobs_bwd(logits, targets, lse, entropy=None, g_logprob=None, g_entropy=None, out=None):
+    """The gradient of the logits for those of the log probabilities and the
+    entropies of token_logprobs (either may be None); out may be logits."""
+    rows, vocab, ld = _values(logits, "logits")
+    t = _targets(targets, rows, logits) if targets is not None else None
+    if g_logprob is None and g_entropy is None:
+        raise ValueError("g_logprob or g_entropy is needed")
+    if g_logprob is not None and t is None:
+        raise ValueError("targets are needed with g_logprob")
+    if g_entropy is not None and entropy is None:
+        raise ValueError("entropy is needed with g_entropy")
+    vecs = [_vector(lse, rows, "lse", logits), _vector(entropy, rows, "entropy", logits, True),
+            _vector(g_logprob, rows, "g_logprob", logits, True), _vector(g_entropy, rows, "g_entropy", logits, True)]
+    if out is None:
+        out = _like(logits)
+    _, _, ldo = _values(out, "out", logits)
+    _enqueue(load().token_logprobs_bwd, logits, logits.data_ptr(), _DTYPES[logits.dtype], rows, vocab, ld, t, *vecs,
+             out.data_ptr(), ldo)
+    return out

@@ -20,7 +20,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_NAME = "libint8_gemm.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
-SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "hash.hip", "verify.hip"]
+SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "hash.hip", "verify.hip", "norm.hip", "checkpoint.hip",
+           "logprob.hip"]
 ARCH = "gfx950"
 
 

@@ -256,6 +256,208 @@ int quantize_cols(const float* X, int64_t rows, int64_t cols, int64_t ldx, int8_
   return quantize_cols_fmt(X, rows, cols, ldx, Qt, ldqt, scale, 0u, stream);
 }
 
+// ---------------------------------------------------------------------------
+// The operators between the GEMMs
+// ---------------------------------------------------------------------------
+static int64_t dtype_bytes(uint32_t dtype) { return dtype == I8G_F32 ? 4 : dtype <= I8G_F16 ? 2 : 0; }
+
+// A rows x cols matrix of elements of `bytes` bytes; only one with elements
+// needs memory.
+static bool bad_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t bytes) {
+  if (ld < cols) return true;
+  return rows > 0 && cols > 0 && (!p || (uintptr_t)p % (uintptr_t)bytes != 0);
+}
+static bool bad_f32(const void* p) { return (uintptr_t)p % 4 != 0; }   // (null is aligned)
+
+static bool bad_sizes(int64_t rows, int64_t cols) {
+  return rows < 0 || cols < 0 || rows > INT32_MAX || cols > INT32_MAX;
+}
+
+static int layer_norm_fwd(const void* X, uint32_t dtype, int64_t rows, int64_t cols, int64_t ldx, const float* gamma,
+                          const float* beta, double eps, void* Y, int64_t ldy, int64_t y_bytes, float* scale,
+                          float* mean, float* rstd, void* stream) {
+  const int64_t bytes = dtype_bytes(dtype);
+  if (bytes == 0 || bad_sizes(rows, cols) || (cols == 0 && rows > 0)) return I8G_EINVAL;
+  if (bad_matrix(X, rows, cols, ldx, bytes) || bad_matrix(Y, rows, cols, ldy, y_bytes ? y_bytes : bytes)) return I8G_EINVAL;
+  if (bad_f32(gamma) || bad_f32(beta) || bad_f32(scale) || bad_f32(mean) || bad_f32(rstd)) return I8G_EINVAL;
+  if (!(eps >= 0.0 && eps <= 1.7976931348623157e308)) return I8G_EINVAL;
+  if (y_bytes && rows > 0 && !scale) return I8G_EINVAL;
+  if (rows == 0) return I8G_OK;
+  LnFwdArgs a{X, rows, cols, ldx, gamma, beta, eps, 1.0 / (double)cols, Y, ldy, scale, mean, rstd};
+  return hip_status(launch_ln_fwd(a, (int)dtype, y_bytes != 0, as_stream(stream)));
+}
+
+int layer_norm(const void* X, uint32_t dtype, int64_t rows, int64_t cols, int64_t ldx, const float* gamma,
+               const float* beta, double eps, void* Y, int64_t ldy, float* mean, float* rstd, void* stream) {
+  return layer_norm_fwd(X, dtype, rows, cols, ldx, gamma, beta, eps, Y, ldy, 0, nullptr, mean, rstd, stream);
+}
+
+int layer_norm_quantize_rows(const void* X, uint32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+                             const float* gamma, const float* beta, double eps, int8_t* Q, int64_t ldq, float* scale,
+                             float* mean, float* rstd, void* stream) {
+  return layer_norm_fwd(X, dtype, rows, cols, ldx, gamma, beta, eps, Q, ldq, 1, scale, mean, rstd, stream);
+}
+
+size_t layer_norm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols <= 0 || bad_sizes(rows, cols)) return 256;
+  return ((size_t)ln_bwd_groups(rows, cols) * 2 * (size_t)cols * sizeof(double) + 255) / 256 * 256;
+}
+
+// group -> shift of a checkpoint's column index; -1 for a size that is none.
+static int group_shift(int32_t group, bool store) {
+  switch (group) {
+    case 0: return store ? -1 : 31;
+    case 32: return 5;
+    case 64: return 6;
+    case 128: return 7;
+    case 256: return 8;
+    default: return -1;
+  }
+}
+
+// Validates a checkpoint and fills c.
+static bool bad_checkpoint(const int8_t* Q, int64_t ldq, const float* scale, int64_t lds, int32_t group, int64_t rows,
+                           int64_t cols, bool store, Checkpoint* c) {
+  const int shift = group_shift(group, store);
+  if (shift < 0 || bad_sizes(rows, cols) || bad_matrix(Q, rows, cols, ldq, 1)) return true;
+  const int64_t groups = cols == 0 ? 0 : ((cols - 1) >> shift) + 1;
+  if (bad_matrix(scale, rows, groups, lds, 4)) return true;
+  *c = Checkpoint{const_cast<int8_t*>(Q), ldq, const_cast<float*>(scale), lds, rows, cols, shift};
+  return false;
+}
+
+static int layer_norm_backward(const void* dY, int64_t lddy, uint32_t dtype, const void* X, int64_t ldx,
+                               const Checkpoint* c, int64_t rows, int64_t cols, const float* gamma, const float* mean,
+                               const float* rstd, void* dX, int64_t lddx, float* dgamma, float* dbeta,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  const int64_t bytes = dtype_bytes(dtype);
+  if (bytes == 0 || bad_sizes(rows, cols) || (cols == 0 && rows > 0)) return I8G_EINVAL;
+  if (bad_matrix(dY, rows, cols, lddy, bytes) || (!c && bad_matrix(X, rows, cols, ldx, bytes))) return I8G_EINVAL;
+  if (dX && bad_matrix(dX, rows, cols, lddx, bytes)) return I8G_EINVAL;
+  if (rows > 0 && (!mean || !rstd)) return I8G_EINVAL;
+  if (bad_f32(gamma) || bad_f32(mean) || bad_f32(rstd) || bad_f32(dgamma) || bad_f32(dbeta)) return I8G_EINVAL;
+  const bool sums = cols > 0 && (dgamma || dbeta);
+  if (sums && (!workspace || (uintptr_t)workspace % 256 != 0 ||
+               workspace_bytes < layer_norm_bwd_workspace_bytes(rows, cols)))
+    return I8G_EWORKSPACE;
+  if (!sums && (rows == 0 || !dX)) return I8G_OK;
+  LnBwdArgs a{dY, X, rows, cols, lddy, ldx, nullptr, 0, 31, gamma, mean, rstd, 1.0 / (double)cols, dX, lddx,
+              sums ? static_cast<double*>(workspace) : nullptr};
+  if (c) {
+    a.X = c->Q;
+    a.ldx = c->ldq;
+    a.scale = c->scale;
+    a.lds = c->lds;
+    a.gshift = c->gshift;
+  }
+  return hip_status(launch_ln_bwd(a, (int)dtype, c != nullptr, dgamma, dbeta, as_stream(stream)));
+}
+
+int layer_norm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ldx, uint32_t dtype, int64_t rows, int64_t cols,
+                   const float* gamma, const float* mean, const float* rstd, void* dX, int64_t lddx, float* dgamma,
+                   float* dbeta, void* workspace, size_t workspace_bytes, void* stream) {
+  return layer_norm_backward(dY, lddy, dtype, X, ldx, nullptr, rows, cols, gamma, mean, rstd, dX, lddx, dgamma, dbeta,
+                             workspace, workspace_bytes, stream);
+}
+
+int layer_norm_bwd_checkpoint(const void* dY, int64_t lddy, uint32_t dtype, const int8_t* Q, int64_t ldq,
+                              const float* scale, int64_t lds, int32_t group, int64_t rows, int64_t cols,
+                              const float* gamma, const float* mean, const float* rstd, void* dX, int64_t lddx,
+                              float* dgamma, float* dbeta, void* workspace, size_t workspace_bytes, void* stream) {
+  Checkpoint c;
+  if (bad_checkpoint(Q, ldq, scale, lds, group, rows, cols, false, &c)) return I8G_EINVAL;
+  return layer_norm_backward(dY, lddy, dtype, nullptr, 0, &c, rows, cols, gamma, mean, rstd, dX, lddx, dgamma, dbeta,
+                             workspace, workspace_bytes, stream);
+}
+
+int checkpoint_i8(const void* X, uint32_t dtype, int64_t rows, int64_t cols, int64_t ldx, int32_t group, int8_t* Q,
+                  int64_t ldq, float* scale, int64_t lds, void* stream) {
+  Checkpoint c;
+  const int64_t bytes = dtype_bytes(dtype);
+  if (bytes == 0 || bad_checkpoint(Q, ldq, scale, lds, group, rows, cols, true, &c)) return I8G_EINVAL;
+  if (bad_matrix(X, rows, cols, ldx, bytes)) return I8G_EINVAL;
+  if (rows == 0 || cols == 0) return I8G_OK;
+  return hip_status(launch_checkpoint_store(X, ldx, (int)dtype, c, as_stream(stream)));
+}
+
+int checkpoint_restore(const int8_t* Q, int64_t ldq, const float* scale, int64_t lds, int32_t group, int64_t rows,
+                       int64_t cols, void* Y, uint32_t dtype, int64_t ldy, void* stream) {
+  Checkpoint c;
+  const int64_t bytes = dtype_bytes(dtype);
+  if (bytes == 0 || bad_checkpoint(Q, ldq, scale, lds, group, rows, cols, false, &c)) return I8G_EINVAL;
+  if (bad_matrix(Y, rows, cols, ldy, bytes)) return I8G_EINVAL;
+  if (rows == 0 || cols == 0) return I8G_OK;
+  return hip_status(launch_checkpoint_read(c, ACT_NONE, nullptr, 0, Y, ldy, (int)dtype, as_stream(stream)));
+}
+
+int checkpoint_act_bwd(const int8_t* Q, int64_t ldq, const float* scale, int64_t lds, int32_t group, int64_t rows,
+                       int64_t cols, uint32_t act, const void* dY, int64_t lddy, void* dX, int64_t lddx,
+                       uint32_t dtype, void* stream) {
+  Checkpoint c;
+  const int64_t bytes = dtype_bytes(dtype);
+  if (bytes == 0 || bad_checkpoint(Q, ldq, scale, lds, group, rows, cols, false, &c)) return I8G_EINVAL;
+  if (act != I8G_ACT_RELU && act != I8G_ACT_GELU) return I8G_EINVAL;
+  if (bad_matrix(dY, rows, cols, lddy, bytes) || bad_matrix(dX, rows, cols, lddx, bytes)) return I8G_EINVAL;
+  if (rows == 0 || cols == 0) return I8G_OK;
+  return hip_status(launch_checkpoint_read(c, (int)act, dY, lddy, dX, lddx, (int)dtype, as_stream(stream)));
+}
+
+int checkpoint_quantize_cols(const int8_t* Q, int64_t ldq, const float* scale, int64_t lds, int32_t group, int64_t rows,
+                             int64_t cols, int8_t* Qt, int64_t ldqt, float* scale_out, void* stream) {
+  Checkpoint c;
+  if (bad_checkpoint(Q, ldq, scale, lds, group, rows, cols, false, &c)) return I8G_EINVAL;
+  if (bad_matrix(Qt, cols, rows, ldqt, 1)) return I8G_EINVAL;
+  if (cols == 0) return I8G_OK;
+  if (!scale_out || bad_f32(scale_out)) return I8G_EINVAL;
+  return hip_status(launch_checkpoint_cols(c, Qt, ldqt, scale_out, as_stream(stream)));
+}
+
+static bool bad_i64(const void* p) { return (uintptr_t)p % 8 != 0; }
+
+// Bytes of the parts' sums, rounded so that the candidates behind them are aligned.
+static size_t lp_sums_bytes(int64_t rows, int parts) {
+  return ((size_t)rows * (size_t)parts * sizeof(LpPart) + 255) / 256 * 256;
+}
+
+size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int32_t topk) {
+  if (rows <= 0 || rows > INT32_MAX || vocab <= 0 || vocab > I8G_VOCAB_MAX || topk < 0 || topk > I8G_TOPK_MAX) return 256;
+  const LpSplit sp = lp_split(rows, vocab);
+  if (sp.parts == 1) return 256;
+  return lp_sums_bytes(rows, sp.parts) + ((size_t)rows * sp.parts * topk * 8 + 255) / 256 * 256;
+}
+
+int token_logprobs(const void* logits, uint32_t dtype, int64_t rows, int64_t vocab, int64_t ld, const int64_t* targets,
+                   int32_t topk, float* logprob, float* entropy, float* lse, int32_t* top_index, float* top_logprob,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  const int64_t bytes = dtype_bytes(dtype);
+  if (bytes == 0 || bad_sizes(rows, vocab) || vocab > I8G_VOCAB_MAX || (vocab == 0 && rows > 0)) return I8G_EINVAL;
+  if (topk < 0 || topk > I8G_TOPK_MAX || (rows > 0 && topk > vocab)) return I8G_EINVAL;
+  if (bad_matrix(logits, rows, vocab, ld, bytes) || bad_i64(targets)) return I8G_EINVAL;
+  if (bad_f32(logprob) || bad_f32(entropy) || bad_f32(lse) || bad_f32(top_index) || bad_f32(top_logprob)) return I8G_EINVAL;
+  if (rows > 0 && ((logprob && !targets) || (topk > 0 && (!top_index || !top_logprob)))) return I8G_EINVAL;
+  if (rows == 0) return I8G_OK;
+  const LpSplit sp = lp_split(rows, vocab);
+  if (!workspace || (uintptr_t)workspace % 256 != 0 || workspace_bytes < token_logprobs_workspace_bytes(rows, vocab, topk))
+    return I8G_EWORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  LpArgs a{logits, rows, vocab, ld, targets, sp.parts, sp.seg, topk, logprob, entropy, lse, top_index, top_logprob,
+           reinterpret_cast<LpPart*>(ws), reinterpret_cast<unsigned long long*>(ws + lp_sums_bytes(rows, sp.parts))};
+  return hip_status(launch_token_logprobs(a, (int)dtype, as_stream(stream)));
+}
+
+int token_logprobs_bwd(const void* logits, uint32_t dtype, int64_t rows, int64_t vocab, int64_t ld,
+                       const int64_t* targets, const float* lse, const float* entropy, const float* g_logprob,
+                       const float* g_entropy, void* dlogits, int64_t lddl, void* stream) {
+  const int64_t bytes = dtype_bytes(dtype);
+  if (bytes == 0 || bad_sizes(rows, vocab) || vocab > I8G_VOCAB_MAX || (vocab == 0 && rows > 0)) return I8G_EINVAL;
+  if (bad_matrix(logits, rows, vocab, ld, bytes) || bad_matrix(dlogits, rows, vocab, lddl, bytes)) return I8G_EINVAL;
+  if (bad_i64(targets) || bad_f32(lse) || bad_f32(entropy) || bad_f32(g_logprob) || bad_f32(g_entropy)) return I8G_EINVAL;
+  if (rows == 0) return I8G_OK;
+  if (!lse || (!g_logprob && !g_entropy) || (g_logprob && !targets) || (g_entropy && !entropy)) return I8G_EINVAL;
+  LpBwdArgs a{logits, rows, vocab, ld, targets, lse, entropy, g_logprob, g_entropy, dlogits, lddl};
+  return hip_status(launch_token_logprobs_bwd(a, (int)dtype, as_stream(stream)));
+}
+
 size_t gemm_i8_workspace_bytes_flags(int64_t M, int64_t N, int64_t K, uint32_t flags) {
   if (M <= 0 || N <= 0) return 256;
   // the plan may depend on ldc (very wide rows exclude the persistent

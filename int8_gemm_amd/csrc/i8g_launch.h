@@ -152,6 +152,87 @@ hipError_t launch_output_hash(const float* C, int64_t M, int64_t N, int64_t ldc,
 hipError_t launch_hash_parts_finalize(const unsigned long long* parts, int n, int64_t M, int64_t N,
                                       uint64_t* hash_out, hipStream_t stream);
 
+// ---------------------------------------------------------------------------
+// The operators between the GEMMs (norm.hip, checkpoint.hip, logprob.hip)
+// ---------------------------------------------------------------------------
+enum DType : int { DT_F32 = 0, DT_BF16 = 1, DT_F16 = 2 };   // I8G_F32, I8G_BF16, I8G_F16
+
+struct LnFwdArgs {
+  const void* X;
+  int64_t rows, cols, ldx;
+  const float *gamma, *beta;   // null: ones, zeros
+  double eps, inv_n;           // inv_n = 1 / cols
+  void* Y;                     // values of X's type, or int8 codes
+  int64_t ldy;
+  float* scale;                // row scales of the codes
+  float *mean, *rstd;          // may be null
+};
+hipError_t launch_ln_fwd(const LnFwdArgs& a, int dtype, bool quant, hipStream_t stream);
+
+struct LnBwdArgs {
+  const void* dY;
+  const void* X;               // values of dY's type, or int8 codes with `scale`
+  int64_t rows, cols, lddy, ldx;
+  const float* scale;          // rows x groups of 2^gshift columns
+  int64_t lds;
+  int gshift;
+  const float *gamma, *mean, *rstd;
+  double inv_n;
+  void* dX;                    // may be null
+  int64_t lddx;
+  double* parts;               // [ln_bwd_groups][2][cols], null without dgamma and dbeta
+};
+// Partial sums (= workgroups) of the backward pass.
+int ln_bwd_groups(int64_t rows, int64_t cols);
+hipError_t launch_ln_bwd(const LnBwdArgs& a, int dtype, bool from_codes, float* dgamma, float* dbeta,
+                         hipStream_t stream);
+
+// An 8-bit checkpoint: rows x cols codes and a scale for each row and group
+// of 2^gshift columns (gshift 31: one for the row).
+struct Checkpoint {
+  int8_t* Q;
+  int64_t ldq;
+  float* scale;
+  int64_t lds, rows, cols;
+  int gshift;
+};
+enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2 };   // ACT_NONE: restore
+hipError_t launch_checkpoint_store(const void* X, int64_t ldx, int dtype, const Checkpoint& c, hipStream_t stream);
+// Y = RN(q*s) (ACT_NONE), or Y = dY * act'(RN(q*s)).
+hipError_t launch_checkpoint_read(const Checkpoint& c, int act, const void* dY, int64_t lddy, void* Y, int64_t ldy,
+                                  int dtype, hipStream_t stream);
+hipError_t launch_checkpoint_cols(const Checkpoint& c, int8_t* Qt, int64_t ldqt, float* scale, hipStream_t stream);
+
+struct LpPart {                // sums of one part of a row (see logprob.hip)
+  double s, t;
+  float m, unused;
+};
+struct LpSplit {
+  int parts, seg;              // parts of a row and columns of a part
+};
+LpSplit lp_split(int64_t rows, int64_t cols);
+struct LpArgs {
+  const void* X;
+  int64_t rows, cols, ldx;
+  const int64_t* targets;
+  int parts, seg, topk;
+  float *logprob, *entropy, *lse;   // may be null
+  int32_t* top_index;
+  float* top_logprob;
+  LpPart* sums;                // [rows][parts], with more than one part
+  unsigned long long* cands;   // [rows][parts][topk], with more than one part
+};
+hipError_t launch_token_logprobs(const LpArgs& a, int dtype, hipStream_t stream);
+struct LpBwdArgs {
+  const void* X;
+  int64_t rows, cols, ldx;
+  const int64_t* targets;
+  const float *lse, *entropy, *g_logprob, *g_entropy;   // either gradient may be null
+  void* dX;
+  int64_t lddx;
+};
+hipError_t launch_token_logprobs_bwd(const LpBwdArgs& a, int dtype, hipStream_t stream);
+
 // Workspace layout shared by every call: a 256-byte header (word 0 is the
 // share ticket, zero between calls), then 8-byte hash shares, then (GEMM
 // split-K only) int32 partial sums.

@@ -1,0 +1,603 @@
+// norm.hip -- layer norm: forward (to values or to the int8 codes of the
+// next GEMM's A operand) and backward with the reduction of the weight's and
+// the bias's gradient.
+//
+// Forward, for a row x of n values (the sums in binary64, everything else in
+// separately rounded binary32 steps):
+//   mean = RN(sum x / n)      rstd = RN(1 / sqrt(sum (x-m)^2 / n + eps))
+//   y_j  = RN(RN(RN(RN(x_j - mean) * rstd) * gamma_j) + beta_j)
+// Backward, for the gradient dy of y:
+//   xh = RN(RN(x - mean) * rstd)      w  = RN(dy * gamma)
+//   c1 = RN(sum w / n)                c2 = RN(sum w*xh / n)
+//   dx = RN(rstd * RN(RN(w - c1) - RN(xh * c2)))
+//   dgamma_j = RN(sum over rows of dy*xh)     dbeta_j = RN(sum over rows of dy)
+// A product of two binary32 values is exact in binary64, and a binary64 sum
+// of them is off by less than 2^-40 of its terms' magnitude, so the rounded
+// sums do not depend on the order of addition except next to a rounding
+// border; the order is fixed by the sizes all the same (no atomics), so two
+// runs give the same bytes.
+//
+// Both directions are bound by memory: every value is read once and written
+// once, a row staying in registers in between.  A row of up to 1024 values is
+// held by one wave, 16 values a lane; a longer one by 2 to 16 waves of one
+// workgroup; rows beyond 16384 values are read again instead of held.
+#include "i8g_launch.h"
+#include "i8g_row.h"
+
+namespace i8g {
+namespace {
+
+constexpr int kHeldMax = 16384;      // longest row held in registers: 16 waves of 64 lanes x 16 values
+
+// 1 / sqrt(a) in binary64: the hardware's estimate (relative error below
+// 2^-20) and one third-order step.
+__device__ __forceinline__ double rsqrt_f64(double a) {
+  if (a == 0.0) return __builtin_huge_val();
+  const double y = __builtin_amdgcn_rsq(a);
+  const double e = 1.0 - a * y * y;
+  return y + y * e * (0.5 + 0.375 * e);
+}
+
+// Row sums of two binary64 values over the W waves that share a row; the
+// result is in every lane.  `red` has two halves used in turn, so one
+// barrier per call is enough: a wave can reach the call after the next one
+// only when every wave has read this one's half.
+template <int W>
+__device__ __forceinline__ void row_sum2(double& a, double& b, double (*red)[2 * W], int& turn) {
+  a = wave_sum_f64(a);
+  b = wave_sum_f64(b);
+  if constexpr (W > 1) {
+    double* half = red[turn];
+    turn ^= 1;
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+      half[wave] = a;
+      half[W + wave] = b;
+    }
+    __syncthreads();
+    a = 0.0;
+    b = 0.0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      a += half[w];
+      b += half[W + w];
+    }
+  }
+}
+
+template <int W>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (*red)[W], int& turn) {
+  v = lanes_max_u32<64>(v);
+  if constexpr (W > 1) {
+    uint32_t* half = red[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) half[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) v = max(v, half[w]);
+  }
+  return v;
+}
+
+struct RowStats {
+  float mean, rstd;
+};
+
+// s1 = sum (x - x0), s2 = sum (x - x0)^2 with the row's first value x0 as the
+// pivot: it lies within sqrt(n) standard deviations of the mean, so
+// s2 - s1^2/n loses at most a factor n of binary64's 2^-53.
+__device__ __forceinline__ RowStats stats_of(double x0, double s1, double s2, double inv_n, double eps) {
+  const double d = s1 * inv_n;
+  double var = s2 * inv_n - d * d;
+  var = var < 0.0 ? 0.0 : var;            // (a NaN stays)
+  return RowStats{(float)(x0 + d), (float)rsqrt_f64(var + eps)};
+}
+
+template <class T, int NV, int W, bool QUANT>
+__global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) ln_fwd_kernel(LnFwdArgs a) {
+  constexpr int N = kVec<T>;
+  __shared__ double red[2][2 * W];
+  __shared__ uint32_t redm[2][W];
+  int turn = 0, turnm = 0;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t step = W == 1 ? (int64_t)gridDim.x * 4 : gridDim.x;
+  const int64_t c0 = (W == 1 ? 0 : (int64_t)wave * 64 * N * NV) + lane * N;
+  const T* X = static_cast<const T*>(a.X);
+  for (int64_t r = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x; r < a.rows; r += step) {
+    const T* xr = X + r * a.ldx;
+    const float x0f = to_f32(xr[0]);
+    float v[NV][N];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) load_row<T, N>(xr, c0 + i * 64 * N, a.cols, x0f, v[i]);
+    const double x0 = x0f;
+    double s1 = 0.0, s2 = 0.0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const double d = (double)v[i][e] - x0;      // 0 behind the row's end
+        s1 += d;
+        s2 += d * d;
+      }
+    row_sum2<W>(s1, s2, red, turn);
+    const RowStats st = stats_of(x0, s1, s2, a.inv_n, a.eps);
+    if ((W == 1 || wave == 0) && lane == 0) {
+      if (a.mean) a.mean[r] = st.mean;
+      if (a.rstd) a.rstd[r] = st.rstd;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = c0 + i * 64 * N;
+      float g[N], b[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        g[e] = 1.0f;
+        b[e] = 0.0f;
+      }
+      if (a.gamma) load_row<float, N>(a.gamma, c, a.cols, 0.0f, g);
+      if (a.beta) load_row<float, N>(a.beta, c, a.cols, 0.0f, b);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float xh = mul_rn(add_rn(v[i][e], -st.mean), st.rstd);
+        v[i][e] = add_rn(mul_rn(xh, g[e]), b[e]);
+        if (QUANT && c + e < a.cols) m = max(m, abs_bits(v[i][e]));
+      }
+      if (!QUANT) store_row<T, N>(static_cast<T*>(a.Y) + r * a.ldy, c, a.cols, v[i]);
+    }
+    if constexpr (QUANT) {
+      m = row_max<W>(m, redm, turnm);
+      const float s = scale_of_bits(m);
+      const bool fine = m < kInfBits;
+      const float inv = recip_rn(s);
+      if ((W == 1 || wave == 0) && lane == 0) a.scale[r] = s;
+      int8_t* qr = static_cast<int8_t*>(a.Y) + r * a.ldy;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        int q[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) q[e] = fine ? quantize1(v[i][e], inv) : 0;
+        store_codes<N>(qr, c0 + i * 64 * N, a.cols, q);
+      }
+    }
+  }
+}
+
+// Rows that no workgroup holds: a workgroup of 16 waves per row, which reads
+// the row again (from cache) for each step.
+template <class T, bool QUANT>
+__global__ void __launch_bounds__(1024) ln_fwd_long_kernel(LnFwdArgs a) {
+  constexpr int N = kVec<T>;
+  constexpr int64_t STEP = 1024 * N;
+  __shared__ double red[2][32];
+  __shared__ uint32_t redm[2][16];
+  int turn = 0, turnm = 0;
+  const int64_t c0 = (int64_t)threadIdx.x * N;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const T* xr = static_cast<const T*>(a.X) + r * a.ldx;
+    const float x0f = to_f32(xr[0]);
+    const double x0 = x0f;
+    double s1 = 0.0, s2 = 0.0;
+    for (int64_t c = c0; c < a.cols; c += STEP) {
+      float v[N];
+      load_row<T, N>(xr, c, a.cols, x0f, v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const double d = (double)v[e] - x0;
+        s1 += d;
+        s2 += d * d;
+      }
+    }
+    row_sum2<16>(s1, s2, red, turn);
+    const RowStats st = stats_of(x0, s1, s2, a.inv_n, a.eps);
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[r] = st.mean;
+      if (a.rstd) a.rstd[r] = st.rstd;
+    }
+    auto values = [&](int64_t c, float (&v)[N]) __attribute__((always_inline)) {
+      float g[N], b[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        g[e] = 1.0f;
+        b[e] = 0.0f;
+      }
+      load_row<T, N>(xr, c, a.cols, x0f, v);
+      if (a.gamma) load_row<float, N>(a.gamma, c, a.cols, 0.0f, g);
+      if (a.beta) load_row<float, N>(a.beta, c, a.cols, 0.0f, b);
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        v[e] = add_rn(mul_rn(mul_rn(add_rn(v[e], -st.mean), st.rstd), g[e]), b[e]);
+    };
+    uint32_t m = 0;
+    if constexpr (QUANT) {
+      for (int64_t c = c0; c < a.cols; c += STEP) {
+        float v[N];
+        values(c, v);
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (c + e < a.cols) m = max(m, abs_bits(v[e]));
+      }
+      m = row_max<16>(m, redm, turnm);
+      if (threadIdx.x == 0) a.scale[r] = scale_of_bits(m);
+    }
+    const bool fine = m < kInfBits;
+    const float inv = QUANT ? recip_rn(scale_of_bits(m)) : 0.0f;
+    for (int64_t c = c0; c < a.cols; c += STEP) {
+      float v[N];
+      values(c, v);
+      if constexpr (QUANT) {
+        int q[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) q[e] = fine ? quantize1(v[e], inv) : 0;
+        store_codes<N>(static_cast<int8_t*>(a.Y) + r * a.ldy, c, a.cols, q);
+      } else {
+        store_row<T, N>(static_cast<T*>(a.Y) + r * a.ldy, c, a.cols, v);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward.  The input's values come from X, or are RN(q*s) of its 8-bit
+// checkpoint (CK).
+// ---------------------------------------------------------------------------
+template <class T, bool CK>
+struct Input {
+  const T* row;
+  const int8_t* codes;
+  const float* scale;
+  int gshift;
+  __device__ __forceinline__ Input(const LnBwdArgs& a, int64_t r) {
+    if constexpr (CK) {
+      codes = static_cast<const int8_t*>(a.X) + r * a.ldx;
+      scale = a.scale + r * a.lds;
+      gshift = a.gshift;
+    } else {
+      row = static_cast<const T*>(a.X) + r * a.ldx;
+    }
+  }
+  template <int N>
+  __device__ __forceinline__ void load(int64_t c, int64_t cols, float (&v)[N]) const {
+    if constexpr (CK) {
+      int q[N];
+      load_codes<N>(codes, c, cols, q);
+      const float s = c < cols ? scale[c >> gshift] : 0.0f;
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = mul_rn((float)q[e], s);
+    } else {
+      load_row<T, N>(row, c, cols, 0.0f, v);
+    }
+  }
+};
+
+// One row's terms: xh and w in place of x and dy.
+template <int N>
+__device__ __forceinline__ void bwd_terms(float (&x)[N], float (&dy)[N], const float (&g)[N], float mean,
+                                          float rstd) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    x[e] = mul_rn(add_rn(x[e], -mean), rstd);
+    dy[e] = mul_rn(dy[e], g[e]);
+  }
+}
+
+__device__ __forceinline__ float bwd_dx(float w, float xh, float rstd, float c1, float c2) {
+  return mul_rn(rstd, add_rn(add_rn(w, -c1), -mul_rn(xh, c2)));
+}
+
+// Rows held in registers.  The workgroups walk the rows with a fixed stride;
+// with PARTS each lane adds its columns' terms of dgamma and dbeta in
+// binary64, and the workgroup leaves one partial sum per column in
+// parts[block][2][cols] for ln_bwd_cols_kernel.
+template <class T, bool CK, int NV, int W, bool PARTS>
+__global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) ln_bwd_kernel(LnBwdArgs a) {
+  constexpr int N = kVec<T>;
+  constexpr int S = W == 1 ? 4 : 1;                 // rows of a workgroup at a time
+  __shared__ double red[2][2 * W];
+  __shared__ double part[W == 1 && PARTS ? 2 : 1][W == 1 && PARTS ? NV * N : 1][64];
+  int turn = 0;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c0 = (W == 1 ? 0 : (int64_t)wave * 64 * N * NV) + lane * N;
+  float g[NV][N];
+  double ag[PARTS ? NV : 1][N], ab[PARTS ? NV : 1][N];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      g[i][e] = 1.0f;
+      if constexpr (PARTS) ag[i][e] = ab[i][e] = 0.0;
+    }
+    if (a.gamma) load_row<float, N>(a.gamma, c0 + i * 64 * N, a.cols, 0.0f, g[i]);
+  }
+  for (int64_t r = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x; r < a.rows;
+       r += (int64_t)gridDim.x * S) {
+    const Input<T, CK> in(a, r);
+    const T* dyr = static_cast<const T*>(a.dY) + r * a.lddy;
+    float x[NV][N], w[NV][N];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      in.template load<N>(c0 + i * 64 * N, a.cols, x[i]);
+      load_row<T, N>(dyr, c0 + i * 64 * N, a.cols, 0.0f, w[i]);
+    }
+    const float mean = a.mean[r], rstd = a.rstd[r];
+    double s1 = 0.0, s2 = 0.0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float xh = mul_rn(add_rn(x[i][e], -mean), rstd);
+        if constexpr (PARTS) {
+          ag[i][e] += (double)w[i][e] * (double)xh;
+          ab[i][e] += (double)w[i][e];
+        }
+        x[i][e] = xh;
+        w[i][e] = mul_rn(w[i][e], g[i][e]);
+        s1 += (double)w[i][e];                        // (dy and so w are 0 behind the row's end)
+        s2 += (double)w[i][e] * (double)xh;
+      }
+    }
+    if (a.dX) {                                       // (the same for the whole grid)
+      row_sum2<W>(s1, s2, red, turn);
+      const float c1 = (float)(s1 * a.inv_n), c2 = (float)(s2 * a.inv_n);
+      T* dxr = static_cast<T*>(a.dX) + r * a.lddx;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) w[i][e] = bwd_dx(w[i][e], x[i][e], rstd, c1, c2);
+        store_row<T, N>(dxr, c0 + i * 64 * N, a.cols, w[i]);
+      }
+    }
+  }
+  if constexpr (PARTS) {
+    // the four waves of a workgroup add up in wave order
+    if constexpr (W == 1) {
+      for (int k = 0; k < 4; ++k) {
+        if (wave == k) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              if (k > 0) {
+                ag[i][e] += part[0][i * N + e][lane];
+                ab[i][e] += part[1][i * N + e][lane];
+              }
+              part[0][i * N + e][lane] = ag[i][e];
+              part[1][i * N + e][lane] = ab[i][e];
+            }
+        }
+        __syncthreads();
+      }
+      if (wave != 3) return;
+    }
+    double* out = a.parts + (int64_t)blockIdx.x * 2 * a.cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int64_t c = c0 + i * 64 * N + e;
+        if (c < a.cols) {
+          out[c] = ag[i][e];
+          out[a.cols + c] = ab[i][e];
+        }
+      }
+  }
+}
+
+// dx of rows that no workgroup holds.
+template <class T, bool CK>
+__global__ void __launch_bounds__(1024) ln_bwd_long_kernel(LnBwdArgs a) {
+  constexpr int N = kVec<T>;
+  constexpr int64_t STEP = 1024 * N;
+  __shared__ double red[2][32];
+  int turn = 0;
+  const int64_t c0 = (int64_t)threadIdx.x * N;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const Input<T, CK> in(a, r);
+    const T* dyr = static_cast<const T*>(a.dY) + r * a.lddy;
+    const float mean = a.mean[r], rstd = a.rstd[r];
+    auto terms = [&](int64_t c, float (&x)[N], float (&w)[N]) __attribute__((always_inline)) {
+      float g[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) g[e] = 1.0f;
+      in.template load<N>(c, a.cols, x);
+      load_row<T, N>(dyr, c, a.cols, 0.0f, w);
+      if (a.gamma) load_row<float, N>(a.gamma, c, a.cols, 0.0f, g);
+      bwd_terms<N>(x, w, g, mean, rstd);
+    };
+    double s1 = 0.0, s2 = 0.0;
+    for (int64_t c = c0; c < a.cols; c += STEP) {
+      float x[N], w[N];
+      terms(c, x, w);
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (c + e < a.cols) {
+          s1 += (double)w[e];
+          s2 += (double)w[e] * (double)x[e];
+        }
+    }
+    row_sum2<16>(s1, s2, red, turn);
+    const float c1 = (float)(s1 * a.inv_n), c2 = (float)(s2 * a.inv_n);
+    for (int64_t c = c0; c < a.cols; c += STEP) {
+      float x[N], w[N];
+      terms(c, x, w);
+#pragma unroll
+      for (int e = 0; e < N; ++e) w[e] = bwd_dx(w[e], x[e], rstd, c1, c2);
+      store_row<T, N>(static_cast<T*>(a.dX) + r * a.lddx, c, a.cols, w);
+    }
+  }
+}
+
+// Partial sums of dgamma and dbeta for the same rows: a thread per vector of
+// columns, blockIdx.y over the row ranges.
+template <class T, bool CK>
+__global__ void __launch_bounds__(64) ln_bwd_long_parts_kernel(LnBwdArgs a) {
+  constexpr int N = kVec<T>;
+  const int64_t c = ((int64_t)blockIdx.x * 64 + threadIdx.x) * N;
+  if (c >= a.cols) return;
+  double ag[N], ab[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) ag[e] = ab[e] = 0.0;
+  for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
+    const Input<T, CK> in(a, r);
+    float x[N], dy[N];
+    in.template load<N>(c, a.cols, x);
+    load_row<T, N>(static_cast<const T*>(a.dY) + r * a.lddy, c, a.cols, 0.0f, dy);
+    const float mean = a.mean[r], rstd = a.rstd[r];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      ag[e] += (double)dy[e] * (double)mul_rn(add_rn(x[e], -mean), rstd);
+      ab[e] += (double)dy[e];
+    }
+  }
+  double* out = a.parts + (int64_t)blockIdx.y * 2 * a.cols;
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    if (c + e < a.cols) {
+      out[c + e] = ag[e];
+      out[a.cols + c + e] = ab[e];
+    }
+}
+
+// The partial sums of 64 columns (of dgamma, then of dbeta) added up by a
+// workgroup of 16 waves, each over every 16th partial.
+__global__ void __launch_bounds__(1024) ln_bwd_cols_kernel(const double* __restrict__ parts, int n_parts,
+                                                           int64_t cols, float* __restrict__ dgamma,
+                                                           float* __restrict__ dbeta) {
+  __shared__ double red[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  float* const out = blockIdx.y ? dbeta : dgamma;
+  if (!out) return;
+  double s = 0.0;
+  if (c < cols)
+    for (int p = wave; p < n_parts; p += 16) s += parts[((int64_t)p * 2 + blockIdx.y) * cols + c];
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < cols) {
+#pragma unroll
+    for (int w = 1; w < 16; ++w) s += red[w][lane];
+    out[c] = (float)s;
+  }
+}
+
+// Waves of a row and vectors of a lane (of N values each, 16 at most): the
+// shortest that hold the row.
+struct RowShape {
+  int waves, nv;   // waves == 0: too long to hold
+};
+RowShape row_shape(int64_t cols, int n) {
+  const int per = 64 * n, most = 16 / n;
+  if (cols > kHeldMax) return RowShape{0, 0};
+  int w = 1;
+  while ((int64_t)w * per * most < cols) w *= 2;
+  const int nv = (int)((cols + (int64_t)w * per - 1) / ((int64_t)w * per));
+  return RowShape{w, nv};
+}
+
+// Workgroups of a kernel whose workgroups walk the rows.
+unsigned int row_grid(int64_t rows, int per_group, int64_t most) {
+  const int64_t g = (rows + per_group - 1) / per_group;
+  return (unsigned int)(g < most ? g : most);
+}
+
+template <class T, bool QUANT, int NV, int W>
+void ln_fwd_held(const LnFwdArgs& a, hipStream_t stream) {
+  const unsigned int grid = row_grid(a.rows, W == 1 ? 4 : 1, int64_t(1) << 20);
+  hipLaunchKernelGGL((ln_fwd_kernel<T, NV, W, QUANT>), dim3(grid), dim3(W == 1 ? 256 : 64 * W), 0, stream, a);
+}
+
+template <class T, bool QUANT>
+hipError_t ln_fwd(const LnFwdArgs& a, hipStream_t stream) {
+  constexpr int M = 16 / kVec<T>;                    // vectors of a full lane
+  const RowShape s = row_shape(a.cols, kVec<T>);
+  switch (s.waves) {
+    case 0: {
+      const unsigned int grid = row_grid(a.rows, 1, int64_t(1) << 20);
+      hipLaunchKernelGGL((ln_fwd_long_kernel<T, QUANT>), dim3(grid), dim3(1024), 0, stream, a);
+      break;
+    }
+    case 1:
+      if (s.nv == 1) ln_fwd_held<T, QUANT, 1, 1>(a, stream);
+      else if (s.nv == 2) ln_fwd_held<T, QUANT, 2, 1>(a, stream);
+      else if (s.nv == 3) ln_fwd_held<T, QUANT, M < 3 ? M : 3, 1>(a, stream);
+      else ln_fwd_held<T, QUANT, M, 1>(a, stream);
+      break;
+    case 2: ln_fwd_held<T, QUANT, M, 2>(a, stream); break;
+    case 4: ln_fwd_held<T, QUANT, M, 4>(a, stream); break;
+    case 8: ln_fwd_held<T, QUANT, M, 8>(a, stream); break;
+    default: ln_fwd_held<T, QUANT, M, 16>(a, stream); break;
+  }
+  return hipGetLastError();
+}
+
+template <class T, bool CK, int NV, int W>
+void ln_bwd_held(const LnBwdArgs& a, int groups, hipStream_t stream) {
+  const dim3 block(W == 1 ? 256 : 64 * W);
+  if (a.parts)
+    hipLaunchKernelGGL((ln_bwd_kernel<T, CK, NV, W, true>), dim3(groups), block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((ln_bwd_kernel<T, CK, NV, W, false>), dim3(groups), block, 0, stream, a);
+}
+
+template <class T, bool CK>
+hipError_t ln_bwd(const LnBwdArgs& a, float* dgamma, float* dbeta, hipStream_t stream) {
+  constexpr int N = kVec<T>, M = 16 / N;
+  const int groups = ln_bwd_groups(a.rows, a.cols);
+  const RowShape s = row_shape(a.cols, N);
+  switch (s.waves) {
+    case 0:
+      if (a.parts)   // before dX, which may be dY's memory
+        hipLaunchKernelGGL((ln_bwd_long_parts_kernel<T, CK>), dim3((unsigned int)((a.cols + 64 * N - 1) / (64 * N)), groups),
+                           dim3(64), 0, stream, a);
+      if (a.dX && a.rows > 0)
+        hipLaunchKernelGGL((ln_bwd_long_kernel<T, CK>), dim3(row_grid(a.rows, 1, int64_t(1) << 20)), dim3(1024), 0,
+                           stream, a);
+      break;
+    case 1:
+      if (s.nv == 1) ln_bwd_held<T, CK, 1, 1>(a, groups, stream);
+      else if (s.nv == 2) ln_bwd_held<T, CK, 2, 1>(a, groups, stream);
+      else if (s.nv == 3) ln_bwd_held<T, CK, M < 3 ? M : 3, 1>(a, groups, stream);
+      else ln_bwd_held<T, CK, M, 1>(a, groups, stream);
+      break;
+    case 2: ln_bwd_held<T, CK, M, 2>(a, groups, stream); break;
+    case 4: ln_bwd_held<T, CK, M, 4>(a, groups, stream); break;
+    case 8: ln_bwd_held<T, CK, M, 8>(a, groups, stream); break;
+    default: ln_bwd_held<T, CK, M, 16>(a, groups, stream); break;
+  }
+  if (a.parts)
+    hipLaunchKernelGGL(ln_bwd_cols_kernel, dim3((unsigned int)((a.cols + 63) / 64), 2), dim3(1024), 0, stream, a.parts,
+                       groups, a.cols, dgamma, dbeta);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int ln_bwd_groups(int64_t rows, int64_t cols) {
+  const int per_group = cols <= 1024 ? 4 : 1;
+  const int64_t g = (rows + per_group - 1) / per_group;
+  const int most = 512;
+  return (int)(g < 1 ? 1 : g < most ? g : most);
+}
+
+hipError_t launch_ln_fwd(const LnFwdArgs& a, int dtype, bool quant, hipStream_t stream) {
+  switch (dtype) {
+    case DT_F32: return quant ? ln_fwd<float, true>(a, stream) : ln_fwd<float, false>(a, stream);
+    case DT_BF16: return quant ? ln_fwd<bf16_t, true>(a, stream) : ln_fwd<bf16_t, false>(a, stream);
+    default: return quant ? ln_fwd<f16_t, true>(a, stream) : ln_fwd<f16_t, false>(a, stream);
+  }
+}
+
+hipError_t launch_ln_bwd(const LnBwdArgs& a, int dtype, bool from_codes, float* dgamma, float* dbeta,
+                         hipStream_t stream) {
+  switch (dtype) {
+    case DT_F32:
+      return from_codes ? ln_bwd<float, true>(a, dgamma, dbeta, stream) : ln_bwd<float, false>(a, dgamma, dbeta, stream);
+    case DT_BF16:
+      return from_codes ? ln_bwd<bf16_t, true>(a, dgamma, dbeta, stream) : ln_bwd<bf16_t, false>(a, dgamma, dbeta, stream);
+    default:
+      return from_codes ? ln_bwd<f16_t, true>(a, dgamma, dbeta, stream) : ln_bwd<f16_t, false>(a, dgamma, dbeta, stream);
+  }
+}
+
+}  // namespace i8g

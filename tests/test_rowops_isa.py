@@ -1,0 +1,58 @@
+"""Structural guard on the built gfx950 code of the operators between the
+GEMMs, beside tests/test_isa_guard.py: no packed binary32 instruction, no
+approximate transcendental or reciprocal outside the expansion of the
+correctly rounded division, and no fused multiply-add in the kernels whose
+bytes are defined step by step (layer norm's elements, the codes)."""
+import os
+import re
+
+import pytest
+
+from int8_gemm_amd import build as B
+from test_isa_guard import FORBIDDEN, compile_asm, have_hipcc, scan
+
+SOURCES = ["norm.hip", "checkpoint.hip", "logprob.hip"]
+KERNELS = ["ln_fwd_kernel", "ln_fwd_long_kernel", "ln_bwd_kernel", "ln_bwd_long_kernel", "ln_bwd_cols_kernel",
+           "checkpoint_store_kernel", "checkpoint_read_kernel", "lp_part_kernel", "lp_join_kernel", "lp_bwd_kernel"]
+# the exponential is written with fused steps on purpose (GELU's gradient, the
+# log probabilities)
+FUSED = re.compile(r"checkpoint_read_kernel\w*Li2E|lp_\w+_kernel")
+
+pytestmark = pytest.mark.skipif(not have_hipcc(), reason="hipcc (ROCm) is needed to build the code")
+
+
+@pytest.fixture(scope="module")
+def functions(tmp_path_factory):
+    d = tmp_path_factory.mktemp("rowops_asm")
+    procs = [(s, str(d / (s + ".s"))) for s in SOURCES]
+    procs = [(s, out, compile_asm(os.path.join(B.CSRC, s), out)) for s, out in procs]
+    found = {}
+    for s, out, p in procs:
+        _, err = p.communicate()
+        assert p.returncode == 0, f"hipcc -S {s} failed:\n{err[-2000:]}"
+        found.update(scan(out))
+    return found
+
+
+@pytest.mark.timeout(600)
+def test_every_kernel_is_there(functions):
+    names = " ".join(functions)
+    assert not [k for k in KERNELS if k not in names]
+
+
+@pytest.mark.timeout(600)
+def test_float_instructions(functions):
+    bad = []
+    for fn, c in functions.items():
+        # binary64 estimates are refined to binary64 precision; binary32 ones are not allowed
+        fused = FUSED.search(fn) is not None
+        bad += [(fn, op, n) for op, n in c.items()
+                if FORBIDDEN.match(op) and not op.endswith("_f64") and not (fused and op == "v_fmaak_f32")]
+        n_div = c["v_div_fixup_f32"]
+        if c["v_div_fmas_f32"] != n_div or c["v_div_scale_f32"] != 2 * n_div:
+            bad.append((fn, "division", dict(c)))
+        if not fused:
+            for op, n in (("v_fma_f32", 3 * n_div), ("v_fmac_f32", 2 * n_div)):
+                if c[op] != n:
+                    bad.append((fn, op, c[op], n))
+    assert not bad, bad[:10]
