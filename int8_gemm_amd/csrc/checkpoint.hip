@@ -62,20 +62,20 @@ __global__ void __launch_bounds__(kBlock) checkpoint_store_kernel(const T* __res
   if (unit % LANES == 0) c.scale[row * c.lds + unit / LANES] = s;
 }
 
-// The derivative of GELU in its tanh form: with u = sqrt(2/pi) (x + 0.044715
-// x^3) and p = (1 + tanh u)/2 = 1/(1 + exp(-2u)),
-//   gelu(x) = x p,   gelu'(x) = p + x p (1-p) 2 u'.
-// exp of the negative side is taken for both signs: with z = exp(-2|u|),
-// p = 1/(1+z) or z/(1+z), and p (1-p) = z/(1+z)^2.
+// The derivative of GELU in its tanh form: with v = 2 sqrt(2/pi) (x + 0.044715
+// x^3) and p = 1/(1 + exp(-v)),
+//   gelu(x) = x p,   gelu'(x) = p + x v' p (1-p).
+// With z = exp(-|v|) and d = 1/(1+z), the two of p and 1-p are d and z d.
+// Beyond |x| = 10 the derivative is within 3e-36 of 0 or 1, so x is kept to
+// that range and z above 2^-126.
 __device__ __forceinline__ float gelu_grad(float x) {
-  const float x2 = mul_rn(x, x);
-  const float u2 = mul_rn(mul_rn(1.59576912f, x), __builtin_fmaf(0.044715f, x2, 1.0f));
-  const float z = exp_neg(-fabsf(u2));
-  const float d = div_rn(1.0f, 1.0f + z);
-  const float p = u2 < 0.0f ? z * d : d;
-  const float du2 = mul_rn(1.59576912f, __builtin_fmaf(0.134145f, x2, 1.0f));
-  const float t = mul_rn(mul_rn(x, du2), mul_rn(z * d, d));
-  return z == 0.0f ? p : p + t;                           // far out x * du2 may be infinite, and z is 0
+  x = __builtin_amdgcn_fmed3f(x, -10.0f, 10.0f);
+  const float x2 = x * x, cx = 1.59576912f * x;
+  const float v = cx * __builtin_fmaf(0.044715f, x2, 1.0f);
+  const float z = exp_small(-fabsf(v));
+  const float d = recip_1_2(1.0f + z), zd = z * d;
+  const float xv = cx * __builtin_fmaf(0.134145f, x2, 1.0f);
+  return __builtin_fmaf(xv, zd * d, v < 0.0f ? zd : d);
 }
 
 template <class T, int ACT>
@@ -90,12 +90,13 @@ __global__ void __launch_bounds__(kBlock) checkpoint_read_kernel(Checkpoint c, c
   const float s = c.scale[row * c.lds + (col >> c.gshift)];
   float y[N];
   if constexpr (ACT != ACT_NONE) load_row<T, N>(dY + row * lddy, col, c.cols, 0.0f, y);
+  const float nan = s - s;                                // 0, or NaN with the scale
 #pragma unroll
   for (int e = 0; e < N; ++e) {
     const float x = mul_rn((float)q[e], s);
     if constexpr (ACT == ACT_NONE) y[e] = x;
-    if constexpr (ACT == ACT_RELU) y[e] = x > 0.0f ? y[e] : (x <= 0.0f ? 0.0f : x);
-    if constexpr (ACT == ACT_GELU) y[e] = mul_rn(y[e], gelu_grad(x));
+    if constexpr (ACT == ACT_RELU) y[e] = x > 0.0f ? y[e] : nan;
+    if constexpr (ACT == ACT_GELU) y[e] = y[e] * (gelu_grad(x) + nan);
   }
   store_row<T, N>(Y + row * ldy, col, c.cols, y);
 }

@@ -56,6 +56,22 @@ __device__ __forceinline__ void store_row(T* __restrict__ row, int64_t c, int64_
   }
 }
 
+// The same in two steps, for a load issued ahead of its use: the N values as
+// they are stored (those beyond `cols` are 0), then as floats.
+template <class T, int N>
+struct RawRow {
+  T t[N];
+  __device__ __forceinline__ void load(const T* __restrict__ row, int64_t c, int64_t cols) {
+    if (c + N <= cols) {
+      __builtin_memcpy(t, row + c, sizeof(t));
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) t[e] = c + e < cols ? row[c + e] : T{};
+    }
+  }
+  __device__ __forceinline__ float operator[](int e) const { return to_f32(t[e]); }
+};
+
 // N int8 codes at row[c ...]; those beyond `cols` are 0.
 template <int N>
 __device__ __forceinline__ void load_codes(const int8_t* __restrict__ row, int64_t c, int64_t cols,
@@ -88,35 +104,52 @@ __device__ __forceinline__ void store_codes(int8_t* __restrict__ row, int64_t c,
   }
 }
 
-// A lane's value exchanged with the lane at the given distance inside its
-// aligned group of 2 * distance lanes; the groups below it must already hold
-// one value (a reduction's steps 1, 2, 4, ..., 32 in this order).
+// Reductions over aligned groups of lanes: the lanes at distance 1, 2, 4, 8
+// are reached with DPP (a group that already holds one value may be mirrored
+// instead), those at 16 and 32 with the row swaps of gfx950, which leave the
+// two values of a pair in two registers.  All of it stays in the vector ALU;
+// a butterfly through LDS (ds_bpermute) takes several times as long a step.
 template <int STEP>
 __device__ __forceinline__ uint32_t lane_partner(uint32_t v) {
-  if constexpr (STEP == 1) return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);    // quad 1,0,3,2
-  if constexpr (STEP == 2) return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);    // quad 2,3,0,1
-  if constexpr (STEP == 4) return __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true);   // row_half_mirror
-  if constexpr (STEP == 8) return __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, true);   // row_mirror
-  if constexpr (STEP == 16 || STEP == 32) return __shfl_xor((int)v, STEP, 64);
+  constexpr int ctrl = STEP == 1 ? 0xB1 : STEP == 2 ? 0x4E : STEP == 4 ? 0x141 : 0x140;   // quad_perm, quad_perm,
+  return __builtin_amdgcn_update_dpp(0, v, ctrl, 0xF, 0xF, true);                         // half mirror, mirror
+}
+
+struct Pair32 {
+  uint32_t a, b;
+};
+template <int STEP>
+__device__ __forceinline__ Pair32 lane_pair(uint32_t v) {
+  if constexpr (STEP == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return Pair32{r[0], r[1]};
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return Pair32{r[0], r[1]};
+  }
 }
 
 template <int STEP>
-__device__ __forceinline__ double lane_partner_f64(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = lane_partner<STEP>((uint32_t)b), hi = lane_partner<STEP>((uint32_t)(b >> 32));
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+__device__ __forceinline__ double lane_add_f64(double v) {
+  const uint64_t x = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)x, hi = (uint32_t)(x >> 32);
+  if constexpr (STEP < 16) {
+    return v + __builtin_bit_cast(double, (uint64_t)lane_partner<STEP>(hi) << 32 | lane_partner<STEP>(lo));
+  } else {
+    const Pair32 l = lane_pair<STEP>(lo), h = lane_pair<STEP>(hi);
+    return __builtin_bit_cast(double, (uint64_t)h.a << 32 | l.a) + __builtin_bit_cast(double, (uint64_t)h.b << 32 | l.b);
+  }
 }
 
-// Sum over the wavefront in binary64, the same value in every lane (each
-// step adds a pair in either order, which gives the same bits).
+// Sum over the wavefront in binary64, the same value in every lane (both
+// lanes of a pair add the same two values).
 __device__ __forceinline__ double wave_sum_f64(double v) {
-  v += lane_partner_f64<1>(v);
-  v += lane_partner_f64<2>(v);
-  v += lane_partner_f64<4>(v);
-  v += lane_partner_f64<8>(v);
-  v += lane_partner_f64<16>(v);
-  v += lane_partner_f64<32>(v);
-  return v;
+  v = lane_add_f64<1>(v);
+  v = lane_add_f64<2>(v);
+  v = lane_add_f64<4>(v);
+  v = lane_add_f64<8>(v);
+  v = lane_add_f64<16>(v);
+  return lane_add_f64<32>(v);
 }
 
 // Maximum over aligned groups of LANES lanes (a power of two).
@@ -126,8 +159,14 @@ __device__ __forceinline__ uint32_t lanes_max_u32(uint32_t v) {
   if constexpr (LANES > 2) v = max(v, lane_partner<2>(v));
   if constexpr (LANES > 4) v = max(v, lane_partner<4>(v));
   if constexpr (LANES > 8) v = max(v, lane_partner<8>(v));
-  if constexpr (LANES > 16) v = max(v, lane_partner<16>(v));
-  if constexpr (LANES > 32) v = max(v, lane_partner<32>(v));
+  if constexpr (LANES > 16) {
+    const Pair32 p = lane_pair<16>(v);
+    v = max(p.a, p.b);
+  }
+  if constexpr (LANES > 32) {
+    const Pair32 p = lane_pair<32>(v);
+    v = max(p.a, p.b);
+  }
   return v;
 }
 
@@ -141,24 +180,46 @@ __device__ __forceinline__ float scale_of_bits(uint32_t a) {
   return a < kInfBits ? scale_of_absmax(__uint_as_float(a)) : __uint_as_float(0x7FC00000u);
 }
 
-// exp(x), for x up to about 80; +0 below -104; in IEEE operations: x = k
-// ln2 + r with |r| <= ln2/2 (ln2 in two parts, the fused steps exact enough
-// that r is off by less than an ulp), the Taylor polynomial of degree 7 (its
-// remainder is below 2^-28), scaled by 2^k.
-__device__ __forceinline__ float exp_neg(float x) {
-  x = x < -104.0f ? -104.0f : x;                          // (a NaN stays)
-  const float k = __builtin_rintf(x * 1.44269504f);
-  float r = __builtin_fmaf(k, -0.693145752f, x);          // 0x3F317200: 9 trailing zeros, k * ln2hi is exact
+// exp(x) 2^-k, with k in the low bits of t: x = k ln2 + r with k the nearest
+// integer to x / ln2 (found by adding 1.5 * 2^23) and |r| <= ln2/2, ln2 in two parts of which the first has 9
+// trailing zeros, so that its product is exact; then 1 + r + r^2 q(r), q of
+// degree 4 fitted to e^r with relative error 3.1e-9.  IEEE operations
+// throughout; the result is off by less than 1.3 * 2^-24 relative.
+__device__ __forceinline__ float exp_reduced(float x, uint32_t& t) {
+  const float big = __builtin_fmaf(x, 1.44269504f, 12582912.0f);
+  t = __float_as_uint(big);
+  const float k = big - 12582912.0f;
+  float r = __builtin_fmaf(k, -0.693145752f, x);
   r = __builtin_fmaf(k, -1.42860677e-6f, r);
-  float p = 1.98412698e-4f;
-  p = __builtin_fmaf(p, r, 1.38888889e-3f);
-  p = __builtin_fmaf(p, r, 8.33333333e-3f);
-  p = __builtin_fmaf(p, r, 4.16666667e-2f);
-  p = __builtin_fmaf(p, r, 1.66666667e-1f);
-  p = __builtin_fmaf(p, r, 0.5f);
+  float p = 0.00138145988f;
+  p = __builtin_fmaf(p, r, 0.00836871658f);
+  p = __builtin_fmaf(p, r, 0.041668389f);
+  p = __builtin_fmaf(p, r, 0.166665211f);
+  p = __builtin_fmaf(p, r, 0.49999994f);
   p = __builtin_fmaf(p, r, 1.0f);
-  p = __builtin_fmaf(p, r, 1.0f);
-  return __builtin_ldexpf(p, (int)k);
+  return __builtin_fmaf(p, r, 1.0f);
+}
+
+// exp(x) for x up to 88: +0 from -104 down, NaN for a NaN (v_maximum3 keeps it).
+__device__ __forceinline__ float exp_f32(float x) {
+  uint32_t t;
+  const float p = exp_reduced(__builtin_elementwise_maximum(x, -104.0f), t);
+  return __builtin_ldexpf(p, (int)(t - 0x4B400000u));
+}
+
+// exp(x) for -87.4 < x <= 0 (a result below 2^-126 is not exact).
+__device__ __forceinline__ float exp_small(float x) {
+  uint32_t t;
+  const float p = exp_reduced(x, t);
+  return __uint_as_float(__float_as_uint(p) + (t << 23));
+}
+
+// 1 / a for 1 <= a <= 2: the quadratic whose error T3(2a-3)/99 is the least
+// (1% relative), and two Newton steps; off by less than 1.2 * 2^-24 relative.
+__device__ __forceinline__ float recip_1_2(float a) {
+  float y = __builtin_fmaf(__builtin_fmaf(32.0f / 99.0f, a, -144.0f / 99.0f), a, 210.0f / 99.0f);
+  y = __builtin_fmaf(y, __builtin_fmaf(-a, y, 1.0f), y);
+  return __builtin_fmaf(y, __builtin_fmaf(-a, y, 1.0f), y);
 }
 
 }  // namespace i8g

@@ -47,9 +47,8 @@ __device__ __forceinline__ uint64_t candidate(uint32_t key, uint32_t index) {
 
 // (s, t) against the maximum `from`, rescaled to the larger maximum `to`.
 __device__ __forceinline__ void rescale(float& s, float& t, float from, float to) {
-  float d = from - to;
-  d = d < -104.0f ? -104.0f : d;
-  const float f = exp_neg(d);
+  const float d = __builtin_elementwise_maximum(from - to, -104.0f);
+  const float f = exp_f32(d);
   t = f * (t + s * d);
   s = f * s;
 }
@@ -255,9 +254,8 @@ __global__ void __launch_bounds__(kThreads) lp_part_kernel(LpArgs a) {
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          float d = v[u][e] - m;
-          d = d < -104.0f ? -104.0f : d;
-          const float p = exp_neg(d);
+          const float d = __builtin_elementwise_maximum(v[u][e] - m, -104.0f);   // (a NaN stays)
+          const float p = exp_f32(d);
           s += p;
           t = __builtin_fmaf(p, d, t);
         }
@@ -383,9 +381,8 @@ __global__ void __launch_bounds__(256) lp_bwd_kernel(LpBwdArgs a) {
       const int64_t c = c0 + u * 256 * N;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        float lp = v[u][e] - lse;
-        lp = lp < -104.0f ? -104.0f : lp;     // p is 0 there, and p * lp as well
-        const float p = exp_neg(lp);
+        const float lp = __builtin_elementwise_maximum(v[u][e] - lse, -104.0f);   // p is 0 there, and p * lp as well
+        const float p = exp_f32(lp);
         float d = -p * (g + gh * (lp + h));
         if (c + e == t) d += g;
         v[u][e] = empty ? 0.0f : d;

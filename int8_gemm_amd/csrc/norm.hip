@@ -38,8 +38,8 @@ __device__ __forceinline__ double rsqrt_f64(double a) {
   return y + y * e * (0.5 + 0.375 * e);
 }
 
-// Row sums of two binary64 values over the W waves that share a row; the
-// result is in every lane.  `red` has two halves used in turn, so one
+// Row sums of two binary64 values over the W waves (consecutive ones of the
+// workgroup) that share a row; the result is in every lane.  `red` has two halves used in turn, so one
 // barrier per call is enough: a wave can reach the call after the next one
 // only when every wave has read this one's half.
 template <int W>
@@ -49,7 +49,7 @@ __device__ __forceinline__ void row_sum2(double& a, double& b, double (*red)[2 *
   if constexpr (W > 1) {
     double* half = red[turn];
     turn ^= 1;
-    const int wave = threadIdx.x >> 6;
+    const int wave = (threadIdx.x >> 6) % W;
     if ((threadIdx.x & 63) == 0) {
       half[wave] = a;
       half[W + wave] = b;
@@ -71,7 +71,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (*red)[W], int&
   if constexpr (W > 1) {
     uint32_t* half = red[turn];
     turn ^= 1;
-    if ((threadIdx.x & 63) == 0) half[threadIdx.x >> 6] = v;
+    if ((threadIdx.x & 63) == 0) half[(threadIdx.x >> 6) % W] = v;
     __syncthreads();
     v = 0;
 #pragma unroll
@@ -242,63 +242,44 @@ __global__ void __launch_bounds__(1024) ln_fwd_long_kernel(LnFwdArgs a) {
 // Backward.  The input's values come from X, or are RN(q*s) of its 8-bit
 // checkpoint (CK).
 // ---------------------------------------------------------------------------
-template <class T, bool CK>
-struct Input {
-  const T* row;
-  const int8_t* codes;
-  const float* scale;
-  int gshift;
-  __device__ __forceinline__ Input(const LnBwdArgs& a, int64_t r) {
-    if constexpr (CK) {
-      codes = static_cast<const int8_t*>(a.X) + r * a.ldx;
-      scale = a.scale + r * a.lds;
-      gshift = a.gshift;
-    } else {
-      row = static_cast<const T*>(a.X) + r * a.ldx;
-    }
-  }
-  template <int N>
-  __device__ __forceinline__ void load(int64_t c, int64_t cols, float (&v)[N]) const {
-    if constexpr (CK) {
-      int q[N];
-      load_codes<N>(codes, c, cols, q);
-      const float s = c < cols ? scale[c >> gshift] : 0.0f;
-#pragma unroll
-      for (int e = 0; e < N; ++e) v[e] = mul_rn((float)q[e], s);
-    } else {
-      load_row<T, N>(row, c, cols, 0.0f, v);
-    }
+// N of them as they are stored.
+template <class T, bool CK, int N>
+struct Input : RawRow<T, N> {
+  __device__ __forceinline__ void load(const LnBwdArgs& a, int64_t r, int64_t c) {
+    RawRow<T, N>::load(static_cast<const T*>(a.X) + r * a.ldx, c, a.cols);
   }
 };
-
-// One row's terms: xh and w in place of x and dy.
-template <int N>
-__device__ __forceinline__ void bwd_terms(float (&x)[N], float (&dy)[N], const float (&g)[N], float mean,
-                                          float rstd) {
-#pragma unroll
-  for (int e = 0; e < N; ++e) {
-    x[e] = mul_rn(add_rn(x[e], -mean), rstd);
-    dy[e] = mul_rn(dy[e], g[e]);
+template <class T, int N>
+struct Input<T, true, N> {
+  RawRow<int8_t, N> q;
+  float s;
+  __device__ __forceinline__ void load(const LnBwdArgs& a, int64_t r, int64_t c) {
+    q.load(static_cast<const int8_t*>(a.X) + r * a.ldx, c, a.cols);
+    s = c < a.cols ? a.scale[r * a.lds + (c >> a.gshift)] : 0.0f;
   }
-}
+  __device__ __forceinline__ float operator[](int e) const { return mul_rn(q[e], s); }
+};
 
+__device__ __forceinline__ float bwd_xhat(float x, float mean, float rstd) { return mul_rn(add_rn(x, -mean), rstd); }
 __device__ __forceinline__ float bwd_dx(float w, float xh, float rstd, float c1, float c2) {
   return mul_rn(rstd, add_rn(add_rn(w, -c1), -mul_rn(xh, c2)));
 }
 
-// Rows held in registers.  The workgroups walk the rows with a fixed stride;
-// with PARTS each lane adds its columns' terms of dgamma and dbeta in
-// binary64, and the workgroup leaves one partial sum per column in
+// Rows held in registers, by workgroups of 8 waves that hold 8/W rows at a
+// time (16 waves and one row for W = 16) and walk the rows with a fixed
+// stride, the next row's values on their way while one is worked on.  With
+// PARTS each lane adds its columns' terms of dgamma and dbeta in binary64,
+// and the workgroup leaves one partial sum per column in
 // parts[block][2][cols] for ln_bwd_cols_kernel.
 template <class T, bool CK, int NV, int W, bool PARTS>
-__global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) ln_bwd_kernel(LnBwdArgs a) {
+__global__ void __launch_bounds__(W == 16 ? 1024 : 512) ln_bwd_kernel(LnBwdArgs a) {
   constexpr int N = kVec<T>;
-  constexpr int S = W == 1 ? 4 : 1;                 // rows of a workgroup at a time
-  __shared__ double red[2][2 * W];
-  __shared__ double part[W == 1 && PARTS ? 2 : 1][W == 1 && PARTS ? NV * N : 1][64];
+  constexpr int S = W == 16 ? 1 : 8 / W;
+  __shared__ double red[S][2][2 * W];
+  __shared__ double part[PARTS && S > 1 ? S : 1][PARTS && S > 1 ? NV * N * W * 64 : 1];
   int turn = 0;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c0 = (W == 1 ? 0 : (int64_t)wave * 64 * N * NV) + lane * N;
+  const int lane = threadIdx.x & 63, slot = (threadIdx.x >> 6) / W, wave = (threadIdx.x >> 6) % W;
+  const int64_t c0 = (int64_t)wave * 64 * N * NV + lane * N;
   float g[NV][N];
   double ag[PARTS ? NV : 1][N], ab[PARTS ? NV : 1][N];
 #pragma unroll
@@ -310,77 +291,93 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) ln_bwd_kernel(LnBwdArgs
     }
     if (a.gamma) load_row<float, N>(a.gamma, c0 + i * 64 * N, a.cols, 0.0f, g[i]);
   }
-  for (int64_t r = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x; r < a.rows;
-       r += (int64_t)gridDim.x * S) {
-    const Input<T, CK> in(a, r);
-    const T* dyr = static_cast<const T*>(a.dY) + r * a.lddy;
+  struct Row {
+    Input<T, CK, N> x[NV];
+    RawRow<T, N> dy[NV];
+    float mean, rstd;
+  } cur;
+  auto fetch = [&](Row& w, int64_t r) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      w.x[i].load(a, r, c0 + i * 64 * N);
+      w.dy[i].load(static_cast<const T*>(a.dY) + r * a.lddy, c0 + i * 64 * N, a.cols);
+    }
+    w.mean = a.mean[r];
+    w.rstd = a.rstd[r];
+  };
+  const int64_t step = (int64_t)gridDim.x * S;
+  int64_t first = (int64_t)blockIdx.x * S;               // the row of slot 0: the same for the workgroup
+  if (first + slot < a.rows) fetch(cur, first + slot);
+  for (; first < a.rows; first += step) {
+    const int64_t r = first + slot;
+    const bool live = r < a.rows;
     float x[NV][N], w[NV][N];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      in.template load<N>(c0 + i * 64 * N, a.cols, x[i]);
-      load_row<T, N>(dyr, c0 + i * 64 * N, a.cols, 0.0f, w[i]);
-    }
-    const float mean = a.mean[r], rstd = a.rstd[r];
     double s1 = 0.0, s2 = 0.0;
+    const float rstd = cur.rstd;
+    if (live) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float xh = mul_rn(add_rn(x[i][e], -mean), rstd);
-        if constexpr (PARTS) {
-          ag[i][e] += (double)w[i][e] * (double)xh;
-          ab[i][e] += (double)w[i][e];
+        for (int e = 0; e < N; ++e) {
+          const float dy = cur.dy[i][e], xh = bwd_xhat(cur.x[i][e], cur.mean, rstd);
+          if constexpr (PARTS) {
+            ag[i][e] += (double)dy * (double)xh;
+            ab[i][e] += (double)dy;
+          }
+          x[i][e] = xh;
+          w[i][e] = mul_rn(dy, g[i][e]);
+          s1 += (double)w[i][e];                          // (dy and so w are 0 behind the row's end)
+          s2 += (double)w[i][e] * (double)xh;
         }
-        x[i][e] = xh;
-        w[i][e] = mul_rn(w[i][e], g[i][e]);
-        s1 += (double)w[i][e];                        // (dy and so w are 0 behind the row's end)
-        s2 += (double)w[i][e] * (double)xh;
-      }
+      if (r + step < a.rows) fetch(cur, r + step);
     }
-    if (a.dX) {                                       // (the same for the whole grid)
-      row_sum2<W>(s1, s2, red, turn);
-      const float c1 = (float)(s1 * a.inv_n), c2 = (float)(s2 * a.inv_n);
-      T* dxr = static_cast<T*>(a.dX) + r * a.lddx;
+    if (a.dX) {                                           // (the same for the whole grid)
+      row_sum2<W>(s1, s2, red[slot], turn);
+      if (live) {
+        const float c1 = (float)(s1 * a.inv_n), c2 = (float)(s2 * a.inv_n);
+        T* dxr = static_cast<T*>(a.dX) + r * a.lddx;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
+        for (int i = 0; i < NV; ++i) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) w[i][e] = bwd_dx(w[i][e], x[i][e], rstd, c1, c2);
-        store_row<T, N>(dxr, c0 + i * 64 * N, a.cols, w[i]);
+          for (int e = 0; e < N; ++e) w[i][e] = bwd_dx(w[i][e], x[i][e], rstd, c1, c2);
+          store_row<T, N>(dxr, c0 + i * 64 * N, a.cols, w[i]);
+        }
       }
     }
   }
   if constexpr (PARTS) {
-    // the four waves of a workgroup add up in wave order
-    if constexpr (W == 1) {
-      for (int k = 0; k < 4; ++k) {
-        if (wave == k) {
+    double* out = a.parts + (int64_t)blockIdx.x * 2 * a.cols;
+    if constexpr (S > 1) {
+      // the slots' sums through LDS, added in the order of the slots; a column
+      // per thread, first of dgamma, then of dbeta
 #pragma unroll
-          for (int i = 0; i < NV; ++i)
+      for (int k = 0; k < 2; ++k) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-              if (k > 0) {
-                ag[i][e] += part[0][i * N + e][lane];
-                ab[i][e] += part[1][i * N + e][lane];
-              }
-              part[0][i * N + e][lane] = ag[i][e];
-              part[1][i * N + e][lane] = ab[i][e];
-            }
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int e = 0; e < N; ++e) part[slot][((wave * NV + i) * N + e) * 64 + lane] = k ? ab[i][e] : ag[i][e];
+        __syncthreads();
+        for (int j = threadIdx.x; j < NV * N * W * 64; j += 512) {
+          double s = part[0][j];
+#pragma unroll
+          for (int q = 1; q < S; ++q) s += part[q][j];
+          const int64_t c = (int64_t)(j / (64 * N)) * 64 * N + (j % 64) * N + j / 64 % N;
+          if (c < a.cols) out[k * a.cols + c] = s;
         }
         __syncthreads();
       }
-      if (wave != 3) return;
-    }
-    double* out = a.parts + (int64_t)blockIdx.x * 2 * a.cols;
+    } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const int64_t c = c0 + i * 64 * N + e;
-        if (c < a.cols) {
-          out[c] = ag[i][e];
-          out[a.cols + c] = ab[i][e];
+        for (int e = 0; e < N; ++e) {
+          const int64_t c = c0 + i * 64 * N + e;
+          if (c < a.cols) {
+            out[c] = ag[i][e];
+            out[a.cols + c] = ab[i][e];
+          }
         }
-      }
+    }
   }
 }
 
@@ -393,17 +390,21 @@ __global__ void __launch_bounds__(1024) ln_bwd_long_kernel(LnBwdArgs a) {
   int turn = 0;
   const int64_t c0 = (int64_t)threadIdx.x * N;
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    const Input<T, CK> in(a, r);
     const T* dyr = static_cast<const T*>(a.dY) + r * a.lddy;
     const float mean = a.mean[r], rstd = a.rstd[r];
     auto terms = [&](int64_t c, float (&x)[N], float (&w)[N]) __attribute__((always_inline)) {
       float g[N];
 #pragma unroll
       for (int e = 0; e < N; ++e) g[e] = 1.0f;
-      in.template load<N>(c, a.cols, x);
+      Input<T, CK, N> in;
+      in.load(a, r, c);
       load_row<T, N>(dyr, c, a.cols, 0.0f, w);
       if (a.gamma) load_row<float, N>(a.gamma, c, a.cols, 0.0f, g);
-      bwd_terms<N>(x, w, g, mean, rstd);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        x[e] = bwd_xhat(in[e], mean, rstd);
+        w[e] = mul_rn(w[e], g[e]);
+      }
     };
     double s1 = 0.0, s2 = 0.0;
     for (int64_t c = c0; c < a.cols; c += STEP) {
@@ -439,14 +440,14 @@ __global__ void __launch_bounds__(64) ln_bwd_long_parts_kernel(LnBwdArgs a) {
 #pragma unroll
   for (int e = 0; e < N; ++e) ag[e] = ab[e] = 0.0;
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
-    const Input<T, CK> in(a, r);
-    float x[N], dy[N];
-    in.template load<N>(c, a.cols, x);
+    Input<T, CK, N> x;
+    float dy[N];
+    x.load(a, r, c);
     load_row<T, N>(static_cast<const T*>(a.dY) + r * a.lddy, c, a.cols, 0.0f, dy);
     const float mean = a.mean[r], rstd = a.rstd[r];
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      ag[e] += (double)dy[e] * (double)mul_rn(add_rn(x[e], -mean), rstd);
+      ag[e] += (double)dy[e] * (double)bwd_xhat(x[e], mean, rstd);
       ab[e] += (double)dy[e];
     }
   }
@@ -459,24 +460,28 @@ __global__ void __launch_bounds__(64) ln_bwd_long_parts_kernel(LnBwdArgs a) {
     }
 }
 
-// The partial sums of 64 columns (of dgamma, then of dbeta) added up by a
-// workgroup of 16 waves, each over every 16th partial.
-__global__ void __launch_bounds__(1024) ln_bwd_cols_kernel(const double* __restrict__ parts, int n_parts,
-                                                           int64_t cols, float* __restrict__ dgamma,
-                                                           float* __restrict__ dbeta) {
-  __shared__ double red[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+// The partial sums of 16 columns (of dgamma, or with blockIdx.y of dbeta): a
+// thread adds every 16th of one column (the 16 columns are one cache line of
+// a partial), then the 16 threads of a column join.
+__global__ void __launch_bounds__(256) ln_bwd_cols_kernel(const double* __restrict__ parts, int n_parts,
+                                                          int64_t cols, float* __restrict__ dgamma,
+                                                          float* __restrict__ dbeta) {
+  __shared__ double red[16][17];
+  const int col = threadIdx.x & 15, slice = threadIdx.x >> 4;
+  const int64_t c = (int64_t)blockIdx.x * 16 + col;
   float* const out = blockIdx.y ? dbeta : dgamma;
   if (!out) return;
   double s = 0.0;
-  if (c < cols)
-    for (int p = wave; p < n_parts; p += 16) s += parts[((int64_t)p * 2 + blockIdx.y) * cols + c];
-  red[wave][lane] = s;
+  if (c < cols) {
+    const double* p = parts + blockIdx.y * cols + c;
+#pragma unroll 8
+    for (int i = slice; i < n_parts; i += 16) s += p[(int64_t)i * 2 * cols];
+  }
+  red[slice][col] = s;
   __syncthreads();
-  if (wave == 0 && c < cols) {
+  if (slice == 0 && c < cols) {
 #pragma unroll
-    for (int w = 1; w < 16; ++w) s += red[w][lane];
+    for (int w = 1; w < 16; ++w) s += red[w][col];
     out[c] = (float)s;
   }
 }
@@ -533,11 +538,10 @@ hipError_t ln_fwd(const LnFwdArgs& a, hipStream_t stream) {
 
 template <class T, bool CK, int NV, int W>
 void ln_bwd_held(const LnBwdArgs& a, int groups, hipStream_t stream) {
-  const dim3 block(W == 1 ? 256 : 64 * W);
   if (a.parts)
-    hipLaunchKernelGGL((ln_bwd_kernel<T, CK, NV, W, true>), dim3(groups), block, 0, stream, a);
+    hipLaunchKernelGGL((ln_bwd_kernel<T, CK, NV, W, true>), dim3(groups), dim3(512), 0, stream, a);
   else
-    hipLaunchKernelGGL((ln_bwd_kernel<T, CK, NV, W, false>), dim3(groups), block, 0, stream, a);
+    hipLaunchKernelGGL((ln_bwd_kernel<T, CK, NV, W, false>), dim3(row_grid(a.rows, 8 / W, 512)), dim3(512), 0, stream, a);
 }
 
 template <class T, bool CK>
@@ -545,14 +549,21 @@ hipError_t ln_bwd(const LnBwdArgs& a, float* dgamma, float* dbeta, hipStream_t s
   constexpr int N = kVec<T>, M = 16 / N;
   const int groups = ln_bwd_groups(a.rows, a.cols);
   const RowShape s = row_shape(a.cols, N);
+  // Rows of 16 waves leave no registers for the sums over the rows, and
+  // longer ones are not held: the sums are a pass of their own, before dX,
+  // which may be dY's memory.
+  if (a.parts && (s.waves == 0 || s.waves == 16))
+    hipLaunchKernelGGL((ln_bwd_long_parts_kernel<T, CK>), dim3((unsigned int)((a.cols + 64 * N - 1) / (64 * N)), groups),
+                       dim3(64), 0, stream, a);
   switch (s.waves) {
     case 0:
-      if (a.parts)   // before dX, which may be dY's memory
-        hipLaunchKernelGGL((ln_bwd_long_parts_kernel<T, CK>), dim3((unsigned int)((a.cols + 64 * N - 1) / (64 * N)), groups),
-                           dim3(64), 0, stream, a);
       if (a.dX && a.rows > 0)
         hipLaunchKernelGGL((ln_bwd_long_kernel<T, CK>), dim3(row_grid(a.rows, 1, int64_t(1) << 20)), dim3(1024), 0,
                            stream, a);
+      break;
+    case 16:
+      if (a.dX && a.rows > 0)
+        hipLaunchKernelGGL((ln_bwd_kernel<T, CK, M, 16, false>), dim3(row_grid(a.rows, 1, 256)), dim3(1024), 0, stream, a);
       break;
     case 1:
       if (s.nv == 1) ln_bwd_held<T, CK, 1, 1>(a, groups, stream);
@@ -562,11 +573,10 @@ hipError_t ln_bwd(const LnBwdArgs& a, float* dgamma, float* dbeta, hipStream_t s
       break;
     case 2: ln_bwd_held<T, CK, M, 2>(a, groups, stream); break;
     case 4: ln_bwd_held<T, CK, M, 4>(a, groups, stream); break;
-    case 8: ln_bwd_held<T, CK, M, 8>(a, groups, stream); break;
-    default: ln_bwd_held<T, CK, M, 16>(a, groups, stream); break;
+    default: ln_bwd_held<T, CK, M, 8>(a, groups, stream); break;
   }
   if (a.parts)
-    hipLaunchKernelGGL(ln_bwd_cols_kernel, dim3((unsigned int)((a.cols + 63) / 64), 2), dim3(1024), 0, stream, a.parts,
+    hipLaunchKernelGGL(ln_bwd_cols_kernel, dim3((unsigned int)((a.cols + 15) / 16), 2), dim3(256), 0, stream, a.parts,
                        groups, a.cols, dgamma, dbeta);
   return hipGetLastError();
 }
@@ -574,10 +584,9 @@ hipError_t ln_bwd(const LnBwdArgs& a, float* dgamma, float* dbeta, hipStream_t s
 }  // namespace
 
 int ln_bwd_groups(int64_t rows, int64_t cols) {
-  const int per_group = cols <= 1024 ? 4 : 1;
+  const int per_group = cols <= 1024 ? 8 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1;
   const int64_t g = (rows + per_group - 1) / per_group;
-  const int most = 512;
-  return (int)(g < 1 ? 1 : g < most ? g : most);
+  return (int)(g < 1 ? 1 : g < 256 ? g : 256);
 }
 
 hipError_t launch_ln_fwd(const LnFwdArgs& a, int dtype, bool quant, hipStream_t stream) {
