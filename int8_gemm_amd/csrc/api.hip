@@ -300,7 +300,7 @@ int layer_norm_quantize_rows(const void* X, uint32_t dtype, int64_t rows, int64_
 
 size_t layer_norm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
   if (rows < 0 || cols <= 0 || bad_sizes(rows, cols)) return 256;
-  return ((size_t)ln_bwd_groups(rows, cols) * 2 * (size_t)cols * sizeof(double) + 255) / 256 * 256;
+  return ((size_t)ln_bwd_groups(rows, cols) * 2 * (size_t)ln_bwd_held_max(cols) * sizeof(double) + 255) / 256 * 256;
 }
 
 // group -> shift of a checkpoint's column index; -1 for a size that is none.

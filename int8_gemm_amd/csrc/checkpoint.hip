@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kBlock) checkpoint_store_kernel(const T* __res
   float v[N];
   uint32_t m = 0;
   if (live) {
-    load_row<T, N>(X + row * ldx, col, c.cols, 0.0f, v);
+    load_row<T>(X + row * ldx, col, c.cols, 0.0f, v);
 #pragma unroll
     for (int e = 0; e < N; ++e) m = max(m, abs_bits(v[e]));
   }
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kBlock) checkpoint_store_kernel(const T* __res
   int q[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) q[e] = fine ? quantize1(v[e], inv) : 0;
-  store_codes<N>(c.Q + row * c.ldq, col, c.cols, q);
+  store_codes(c.Q + row * c.ldq, col, c.cols, q);
   if (unit % LANES == 0) c.scale[row * c.lds + unit / LANES] = s;
 }
 
@@ -86,10 +86,10 @@ __global__ void __launch_bounds__(kBlock) checkpoint_read_kernel(Checkpoint c, c
   if (row >= c.rows) return;
   const int64_t col = (int64_t)(at - row * units.per_row) * N;
   int q[N];
-  load_codes<N>(c.Q + row * c.ldq, col, c.cols, q);
+  load_codes(c.Q + row * c.ldq, col, c.cols, q);
   const float s = c.scale[row * c.lds + (col >> c.gshift)];
   float y[N];
-  if constexpr (ACT != ACT_NONE) load_row<T, N>(dY + row * lddy, col, c.cols, 0.0f, y);
+  if constexpr (ACT != ACT_NONE) load_row<T>(dY + row * lddy, col, c.cols, 0.0f, y);
   const float nan = s - s;                                // 0, or NaN with the scale
 #pragma unroll
   for (int e = 0; e < N; ++e) {
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kBlock) checkpoint_read_kernel(Checkpoint c, c
     if constexpr (ACT == ACT_RELU) y[e] = x > 0.0f ? y[e] : nan;
     if constexpr (ACT == ACT_GELU) y[e] = y[e] * (gelu_grad(x) + nan);
   }
-  store_row<T, N>(Y + row * ldy, col, c.cols, y);
+  store_row<T>(Y + row * ldy, col, c.cols, y);
 }
 
 // ---------------------------------------------------------------------------
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(256) checkpoint_cols_scale_kernel(Checkpoint c
       const int64_t end = r0 + kColRows < c.rows ? r0 + kColRows : c.rows;
       for (int64_t r = r0 + wave; r < end; r += 4) {
         int q[4];
-        load_codes<4>(c.Q + r * c.ldq, col, c.cols, q);
+        load_codes(c.Q + r * c.ldq, col, c.cols, q);
         const float s = c.scale[r * c.lds + (col >> c.gshift)];
 #pragma unroll
         for (int e = 0; e < 4; ++e) m[e] = max(m[e], abs_bits(mul_rn((float)q[e], s)));
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(256) checkpoint_cols_quant_kernel(Checkpoint c
       const int64_t k = k0 + rr * 4 + i;
       if (k < c.rows && col < c.cols) {
         int q[4];
-        load_codes<4>(c.Q + k * c.ldq, col, c.cols, q);
+        load_codes(c.Q + k * c.ldq, col, c.cols, q);
         const float s = c.scale[k * c.lds + (col >> c.gshift)];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {

@@ -180,10 +180,12 @@ struct LnBwdArgs {
   double inv_n;
   void* dX;                    // may be null
   int64_t lddx;
-  double* parts;               // [ln_bwd_groups][2][cols], null without dgamma and dbeta
+  double* parts;               // [ln_bwd_groups][2][up to ln_bwd_held_max], null without dgamma and dbeta
 };
-// Partial sums (= workgroups) of the backward pass.
+// Workgroups of the backward pass that leave partial sums, and the most sums
+// of one kind that each leaves.
 int ln_bwd_groups(int64_t rows, int64_t cols);
+int64_t ln_bwd_held_max(int64_t cols);
 hipError_t launch_ln_bwd(const LnBwdArgs& a, int dtype, bool from_codes, float* dgamma, float* dbeta,
                          hipStream_t stream);
 

@@ -28,9 +28,10 @@ template <class T> constexpr int kVec = 16 / (int)sizeof(T);
 // N consecutive values at row[c ...] as floats; values at and beyond `cols`
 // read as `fill` (nothing outside the row is touched).  A full vector is one
 // load of any alignment (gfx950 code objects run with unaligned access on).
-template <class T, int N>
-__device__ __forceinline__ void load_row(const T* __restrict__ row, int64_t c, int64_t cols, float fill,
-                                         float (&v)[N]) {
+// I: the type of column indexes, int where a row's length allows (32-bit
+// compares, and a row base in scalar registers with a 32-bit offset).
+template <class T, int N, class I>
+__device__ __forceinline__ void load_row(const T* __restrict__ row, I c, I cols, float fill, float (&v)[N]) {
   if (c + N <= cols) {
     T t[N];
     __builtin_memcpy(t, row + c, sizeof(t));
@@ -42,8 +43,8 @@ __device__ __forceinline__ void load_row(const T* __restrict__ row, int64_t c, i
   }
 }
 
-template <class T, int N>
-__device__ __forceinline__ void store_row(T* __restrict__ row, int64_t c, int64_t cols, const float (&v)[N]) {
+template <class T, int N, class I>
+__device__ __forceinline__ void store_row(T* __restrict__ row, I c, I cols, const float (&v)[N]) {
   if (c + N <= cols) {
     T t[N];
 #pragma unroll
@@ -57,25 +58,25 @@ __device__ __forceinline__ void store_row(T* __restrict__ row, int64_t c, int64_
 }
 
 // The same in two steps, for a load issued ahead of its use: the N values as
-// they are stored (those beyond `cols` are 0), then as floats.
+// they are stored (those beyond `cols` are `fill`), then as floats.
 template <class T, int N>
 struct RawRow {
   T t[N];
-  __device__ __forceinline__ void load(const T* __restrict__ row, int64_t c, int64_t cols) {
+  template <class I>
+  __device__ __forceinline__ void load(const T* __restrict__ row, I c, I cols, T fill = T{}) {
     if (c + N <= cols) {
       __builtin_memcpy(t, row + c, sizeof(t));
     } else {
 #pragma unroll
-      for (int e = 0; e < N; ++e) t[e] = c + e < cols ? row[c + e] : T{};
+      for (int e = 0; e < N; ++e) t[e] = c + e < cols ? row[c + e] : fill;
     }
   }
   __device__ __forceinline__ float operator[](int e) const { return to_f32(t[e]); }
 };
 
 // N int8 codes at row[c ...]; those beyond `cols` are 0.
-template <int N>
-__device__ __forceinline__ void load_codes(const int8_t* __restrict__ row, int64_t c, int64_t cols,
-                                           int (&q)[N]) {
+template <int N, class I>
+__device__ __forceinline__ void load_codes(const int8_t* __restrict__ row, I c, I cols, int (&q)[N]) {
   int8_t t[N];
   if (c + N <= cols) {
     __builtin_memcpy(t, row + c, N);
@@ -87,9 +88,8 @@ __device__ __forceinline__ void load_codes(const int8_t* __restrict__ row, int64
   for (int e = 0; e < N; ++e) q[e] = t[e];
 }
 
-template <int N>
-__device__ __forceinline__ void store_codes(int8_t* __restrict__ row, int64_t c, int64_t cols,
-                                            const int (&q)[N]) {
+template <int N, class I>
+__device__ __forceinline__ void store_codes(int8_t* __restrict__ row, I c, I cols, const int (&q)[N]) {
   if (c + N <= cols) {
     uint32_t w[N / 4];
 #pragma unroll

@@ -146,7 +146,7 @@ __device__ __forceinline__ void find_best(TopLds& l, const T* row, int lo, int h
     const int c = lo + (l.lane_of[i] + kThreads * (tid % NV)) * N;
     if (c >= hi) continue;
     float v[N];
-    load_row<T, N>(row, c, hi, 0.0f, v);
+    load_row<T>(row, c, hi, 0.0f, v);
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       if (c + e >= hi) continue;
@@ -171,7 +171,7 @@ __device__ __forceinline__ void find_best(TopLds& l, const T* row, int lo, int h
       float v[N];
       unsigned int hit = 0;
       if (c < hi) {
-        load_row<T, N>(row, c, hi, 0.0f, v);
+        load_row<T>(row, c, hi, 0.0f, v);
 #pragma unroll
         for (int e = 0; e < N; ++e)
           if (c + e < hi && rank_key(v[e]) == bar) hit |= 1u << e;
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads) lp_part_kernel(LpArgs a) {
     for (int base = lo; base < hi; base += kThreads * N * U) {
       float v[U][N];
 #pragma unroll
-      for (int u = 0; u < U; ++u) load_row<T, N>(row, base + (u * kThreads + tid) * N, hi, -__builtin_inff(), v[u]);
+      for (int u = 0; u < U; ++u) load_row<T>(row, base + (u * kThreads + tid) * N, hi, -__builtin_inff(), v[u]);
       float b = -__builtin_inff();
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(256) lp_bwd_kernel(LpBwdArgs a) {
     const bool empty = fabsf(lse) >= 16777216.0f;   // -inf, or so far out that lse is off by 1 and more
     float v[U][N];
 #pragma unroll
-    for (int u = 0; u < U; ++u) load_row<T, N>(x, c0 + u * 256 * N, a.cols, 0.0f, v[u]);
+    for (int u = 0; u < U; ++u) load_row<T>(x, c0 + u * 256 * N, a.cols, 0.0f, v[u]);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t c = c0 + u * 256 * N;
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(256) lp_bwd_kernel(LpBwdArgs a) {
         if (c + e == t) d += g;
         v[u][e] = empty ? 0.0f : d;
       }
-      store_row<T, N>(dx, c, a.cols, v[u]);
+      store_row<T>(dx, c, a.cols, v[u]);
     }
   }
 }

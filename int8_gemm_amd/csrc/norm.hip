@@ -34,8 +34,8 @@ constexpr int kHeldMax = 16384;      // longest row held in registers: 16 waves 
 __device__ __forceinline__ double rsqrt_f64(double a) {
   if (a == 0.0) return __builtin_huge_val();
   const double y = __builtin_amdgcn_rsq(a);
-  const double e = 1.0 - a * y * y;
-  return y + y * e * (0.5 + 0.375 * e);
+  const double e = __builtin_fma(-a * y, y, 1.0);
+  return __builtin_fma(y * e, __builtin_fma(0.375, e, 0.5), y);
 }
 
 // Row sums of two binary64 values over the W waves (consecutive ones of the
@@ -94,32 +94,59 @@ __device__ __forceinline__ RowStats stats_of(double x0, double s1, double s2, do
   return RowStats{(float)(x0 + d), (float)rsqrt_f64(var + eps)};
 }
 
+// Rows held in registers; the workgroups walk the rows with a fixed stride,
+// the next row's values on their way while one is worked on, gamma and beta
+// held throughout.
 template <class T, int NV, int W, bool QUANT>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) ln_fwd_kernel(LnFwdArgs a) {
   constexpr int N = kVec<T>;
   __shared__ double red[2][2 * W];
   __shared__ uint32_t redm[2][W];
   int turn = 0, turnm = 0;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cols = (int)a.cols;
   const int64_t step = W == 1 ? (int64_t)gridDim.x * 4 : gridDim.x;
-  const int64_t c0 = (W == 1 ? 0 : (int64_t)wave * 64 * N * NV) + lane * N;
+  const int c0 = (W == 1 ? 0 : wave * 64 * N * NV) + lane * N;
   const T* X = static_cast<const T*>(a.X);
-  for (int64_t r = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x; r < a.rows; r += step) {
-    const T* xr = X + r * a.ldx;
-    const float x0f = to_f32(xr[0]);
-    float v[NV][N];
+  int64_t r = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+  struct Row {
+    RawRow<T, N> v[NV];
+    T first;
+  } cur;
+  auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+    const T* xr = X + row * a.ldx;
+    cur.first = xr[0];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) load_row<T, N>(xr, c0 + i * 64 * N, a.cols, x0f, v[i]);
-    const double x0 = x0f;
+    for (int i = 0; i < NV; ++i) cur.v[i].load(xr, c0 + i * 64 * N, cols, cur.first);
+  };
+  if (r < a.rows) fetch(r);
+  float g[NV][N], b[NV][N];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = c0 + i * 64 * N;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      g[i][e] = c + e < cols ? 1.0f : 0.0f;             // behind the row's end y is 0
+      b[i][e] = 0.0f;
+    }
+    if (a.gamma) load_row<float>(a.gamma, c, cols, 0.0f, g[i]);
+    if (a.beta) load_row<float>(a.beta, c, cols, 0.0f, b[i]);
+  }
+  for (; r < a.rows; r += step) {
+    float v[NV][N];
+    const double x0 = to_f32(cur.first);
     double s1 = 0.0, s2 = 0.0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const double d = (double)v[i][e] - x0;      // 0 behind the row's end
+        v[i][e] = cur.v[i][e];
+        const double d = (double)v[i][e] - x0;            // 0 behind the row's end
         s1 += d;
-        s2 += d * d;
+        s2 = __builtin_fma(d, d, s2);
       }
+    }
+    if (r + step < a.rows) fetch(r + step);
     row_sum2<W>(s1, s2, red, turn);
     const RowStats st = stats_of(x0, s1, s2, a.inv_n, a.eps);
     if ((W == 1 || wave == 0) && lane == 0) {
@@ -129,22 +156,14 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) ln_fwd_kernel(LnFwdArgs
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t c = c0 + i * 64 * N;
-      float g[N], b[N];
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        g[e] = 1.0f;
-        b[e] = 0.0f;
-      }
-      if (a.gamma) load_row<float, N>(a.gamma, c, a.cols, 0.0f, g);
-      if (a.beta) load_row<float, N>(a.beta, c, a.cols, 0.0f, b);
+      const int c = c0 + i * 64 * N;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const float xh = mul_rn(add_rn(v[i][e], -st.mean), st.rstd);
-        v[i][e] = add_rn(mul_rn(xh, g[e]), b[e]);
-        if (QUANT && c + e < a.cols) m = max(m, abs_bits(v[i][e]));
+        v[i][e] = add_rn(mul_rn(xh, g[i][e]), b[i][e]);
+        if constexpr (QUANT) m = max(m, abs_bits(v[i][e]));
       }
-      if (!QUANT) store_row<T, N>(static_cast<T*>(a.Y) + r * a.ldy, c, a.cols, v[i]);
+      if (!QUANT) store_row<T>(static_cast<T*>(a.Y) + r * a.ldy, c, cols, v[i]);
     }
     if constexpr (QUANT) {
       m = row_max<W>(m, redm, turnm);
@@ -158,7 +177,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) ln_fwd_kernel(LnFwdArgs
         int q[N];
 #pragma unroll
         for (int e = 0; e < N; ++e) q[e] = fine ? quantize1(v[i][e], inv) : 0;
-        store_codes<N>(qr, c0 + i * 64 * N, a.cols, q);
+        store_codes(qr, c0 + i * 64 * N, cols, q);
       }
     }
   }
@@ -181,12 +200,12 @@ __global__ void __launch_bounds__(1024) ln_fwd_long_kernel(LnFwdArgs a) {
     double s1 = 0.0, s2 = 0.0;
     for (int64_t c = c0; c < a.cols; c += STEP) {
       float v[N];
-      load_row<T, N>(xr, c, a.cols, x0f, v);
+      load_row<T>(xr, c, a.cols, x0f, v);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const double d = (double)v[e] - x0;
         s1 += d;
-        s2 += d * d;
+        s2 = __builtin_fma(d, d, s2);
       }
     }
     row_sum2<16>(s1, s2, red, turn);
@@ -202,9 +221,9 @@ __global__ void __launch_bounds__(1024) ln_fwd_long_kernel(LnFwdArgs a) {
         g[e] = 1.0f;
         b[e] = 0.0f;
       }
-      load_row<T, N>(xr, c, a.cols, x0f, v);
-      if (a.gamma) load_row<float, N>(a.gamma, c, a.cols, 0.0f, g);
-      if (a.beta) load_row<float, N>(a.beta, c, a.cols, 0.0f, b);
+      load_row<T>(xr, c, a.cols, x0f, v);
+      if (a.gamma) load_row<float>(a.gamma, c, a.cols, 0.0f, g);
+      if (a.beta) load_row<float>(a.beta, c, a.cols, 0.0f, b);
 #pragma unroll
       for (int e = 0; e < N; ++e)
         v[e] = add_rn(mul_rn(mul_rn(add_rn(v[e], -st.mean), st.rstd), g[e]), b[e]);
@@ -230,9 +249,9 @@ __global__ void __launch_bounds__(1024) ln_fwd_long_kernel(LnFwdArgs a) {
         int q[N];
 #pragma unroll
         for (int e = 0; e < N; ++e) q[e] = fine ? quantize1(v[e], inv) : 0;
-        store_codes<N>(static_cast<int8_t*>(a.Y) + r * a.ldy, c, a.cols, q);
+        store_codes(static_cast<int8_t*>(a.Y) + r * a.ldy, c, a.cols, q);
       } else {
-        store_row<T, N>(static_cast<T*>(a.Y) + r * a.ldy, c, a.cols, v);
+        store_row<T>(static_cast<T*>(a.Y) + r * a.ldy, c, a.cols, v);
       }
     }
   }
@@ -245,17 +264,19 @@ __global__ void __launch_bounds__(1024) ln_fwd_long_kernel(LnFwdArgs a) {
 // N of them as they are stored.
 template <class T, bool CK, int N>
 struct Input : RawRow<T, N> {
-  __device__ __forceinline__ void load(const LnBwdArgs& a, int64_t r, int64_t c) {
-    RawRow<T, N>::load(static_cast<const T*>(a.X) + r * a.ldx, c, a.cols);
+  template <class I>
+  __device__ __forceinline__ void load(const LnBwdArgs& a, int64_t r, I c) {
+    RawRow<T, N>::load(static_cast<const T*>(a.X) + r * a.ldx, c, (I)a.cols);
   }
 };
 template <class T, int N>
 struct Input<T, true, N> {
   RawRow<int8_t, N> q;
   float s;
-  __device__ __forceinline__ void load(const LnBwdArgs& a, int64_t r, int64_t c) {
-    q.load(static_cast<const int8_t*>(a.X) + r * a.ldx, c, a.cols);
-    s = c < a.cols ? a.scale[r * a.lds + (c >> a.gshift)] : 0.0f;
+  template <class I>
+  __device__ __forceinline__ void load(const LnBwdArgs& a, int64_t r, I c) {
+    q.load(static_cast<const int8_t*>(a.X) + r * a.ldx, c, (I)a.cols);
+    s = c < (I)a.cols ? a.scale[r * a.lds + (c >> a.gshift)] : 0.0f;
   }
   __device__ __forceinline__ float operator[](int e) const { return mul_rn(q[e], s); }
 };
@@ -270,7 +291,8 @@ __device__ __forceinline__ float bwd_dx(float w, float xh, float rstd, float c1,
 // stride, the next row's values on their way while one is worked on.  With
 // PARTS each lane adds its columns' terms of dgamma and dbeta in binary64,
 // and the workgroup leaves one partial sum per column in
-// parts[block][2][cols] for ln_bwd_cols_kernel.
+// parts[block][2][held] for ln_bwd_cols_kernel, in the order of the lanes
+// (column_of), which makes whole cache lines of them.
 template <class T, bool CK, int NV, int W, bool PARTS>
 __global__ void __launch_bounds__(W == 16 ? 1024 : 512) ln_bwd_kernel(LnBwdArgs a) {
   constexpr int N = kVec<T>;
@@ -278,8 +300,10 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 512) ln_bwd_kernel(LnBwdArgs 
   __shared__ double red[S][2][2 * W];
   __shared__ double part[PARTS && S > 1 ? S : 1][PARTS && S > 1 ? NV * N * W * 64 : 1];
   int turn = 0;
-  const int lane = threadIdx.x & 63, slot = (threadIdx.x >> 6) / W, wave = (threadIdx.x >> 6) % W;
-  const int64_t c0 = (int64_t)wave * 64 * N * NV + lane * N;
+  const int lane = threadIdx.x & 63, cols = (int)a.cols;
+  const int slot = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) / W);
+  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) % W);
+  const int c0 = wave * 64 * N * NV + lane * N;
   float g[NV][N];
   double ag[PARTS ? NV : 1][N], ab[PARTS ? NV : 1][N];
 #pragma unroll
@@ -289,7 +313,7 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 512) ln_bwd_kernel(LnBwdArgs 
       g[i][e] = 1.0f;
       if constexpr (PARTS) ag[i][e] = ab[i][e] = 0.0;
     }
-    if (a.gamma) load_row<float, N>(a.gamma, c0 + i * 64 * N, a.cols, 0.0f, g[i]);
+    if (a.gamma) load_row<float>(a.gamma, c0 + i * 64 * N, cols, 0.0f, g[i]);
   }
   struct Row {
     Input<T, CK, N> x[NV];
@@ -300,7 +324,7 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 512) ln_bwd_kernel(LnBwdArgs 
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       w.x[i].load(a, r, c0 + i * 64 * N);
-      w.dy[i].load(static_cast<const T*>(a.dY) + r * a.lddy, c0 + i * 64 * N, a.cols);
+      w.dy[i].load(static_cast<const T*>(a.dY) + r * a.lddy, c0 + i * 64 * N, cols);
     }
     w.mean = a.mean[r];
     w.rstd = a.rstd[r];
@@ -321,13 +345,13 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 512) ln_bwd_kernel(LnBwdArgs 
         for (int e = 0; e < N; ++e) {
           const float dy = cur.dy[i][e], xh = bwd_xhat(cur.x[i][e], cur.mean, rstd);
           if constexpr (PARTS) {
-            ag[i][e] += (double)dy * (double)xh;
+            ag[i][e] = __builtin_fma((double)dy, (double)xh, ag[i][e]);   // (an exact product)
             ab[i][e] += (double)dy;
           }
           x[i][e] = xh;
           w[i][e] = mul_rn(dy, g[i][e]);
           s1 += (double)w[i][e];                          // (dy and so w are 0 behind the row's end)
-          s2 += (double)w[i][e] * (double)xh;
+          s2 = __builtin_fma((double)w[i][e], (double)xh, s2);
         }
       if (r + step < a.rows) fetch(cur, r + step);
     }
@@ -340,13 +364,14 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 512) ln_bwd_kernel(LnBwdArgs 
         for (int i = 0; i < NV; ++i) {
 #pragma unroll
           for (int e = 0; e < N; ++e) w[i][e] = bwd_dx(w[i][e], x[i][e], rstd, c1, c2);
-          store_row<T, N>(dxr, c0 + i * 64 * N, a.cols, w[i]);
+          store_row<T>(dxr, c0 + i * 64 * N, cols, w[i]);
         }
       }
     }
   }
   if constexpr (PARTS) {
-    double* out = a.parts + (int64_t)blockIdx.x * 2 * a.cols;
+    constexpr int HELD = W * NV * N * 64;
+    double* out = a.parts + (int64_t)blockIdx.x * 2 * HELD;
     if constexpr (S > 1) {
       // the slots' sums through LDS, added in the order of the slots; a column
       // per thread, first of dgamma, then of dbeta
@@ -357,12 +382,11 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 512) ln_bwd_kernel(LnBwdArgs 
 #pragma unroll
           for (int e = 0; e < N; ++e) part[slot][((wave * NV + i) * N + e) * 64 + lane] = k ? ab[i][e] : ag[i][e];
         __syncthreads();
-        for (int j = threadIdx.x; j < NV * N * W * 64; j += 512) {
+        for (int j = threadIdx.x; j < HELD; j += 512) {
           double s = part[0][j];
 #pragma unroll
           for (int q = 1; q < S; ++q) s += part[q][j];
-          const int64_t c = (int64_t)(j / (64 * N)) * 64 * N + (j % 64) * N + j / 64 % N;
-          if (c < a.cols) out[k * a.cols + c] = s;
+          out[k * HELD + j] = s;
         }
         __syncthreads();
       }
@@ -371,11 +395,9 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 512) ln_bwd_kernel(LnBwdArgs 
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          const int64_t c = c0 + i * 64 * N + e;
-          if (c < a.cols) {
-            out[c] = ag[i][e];
-            out[a.cols + c] = ab[i][e];
-          }
+          const int j = ((wave * NV + i) * N + e) * 64 + lane;
+          out[j] = ag[i][e];
+          out[HELD + j] = ab[i][e];
         }
     }
   }
@@ -398,8 +420,8 @@ __global__ void __launch_bounds__(1024) ln_bwd_long_kernel(LnBwdArgs a) {
       for (int e = 0; e < N; ++e) g[e] = 1.0f;
       Input<T, CK, N> in;
       in.load(a, r, c);
-      load_row<T, N>(dyr, c, a.cols, 0.0f, w);
-      if (a.gamma) load_row<float, N>(a.gamma, c, a.cols, 0.0f, g);
+      load_row<T>(dyr, c, a.cols, 0.0f, w);
+      if (a.gamma) load_row<float>(a.gamma, c, a.cols, 0.0f, g);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         x[e] = bwd_xhat(in[e], mean, rstd);
@@ -414,7 +436,7 @@ __global__ void __launch_bounds__(1024) ln_bwd_long_kernel(LnBwdArgs a) {
       for (int e = 0; e < N; ++e)
         if (c + e < a.cols) {
           s1 += (double)w[e];
-          s2 += (double)w[e] * (double)x[e];
+          s2 = __builtin_fma((double)w[e], (double)x[e], s2);
         }
     }
     row_sum2<16>(s1, s2, red, turn);
@@ -424,7 +446,7 @@ __global__ void __launch_bounds__(1024) ln_bwd_long_kernel(LnBwdArgs a) {
       terms(c, x, w);
 #pragma unroll
       for (int e = 0; e < N; ++e) w[e] = bwd_dx(w[e], x[e], rstd, c1, c2);
-      store_row<T, N>(static_cast<T*>(a.dX) + r * a.lddx, c, a.cols, w);
+      store_row<T>(static_cast<T*>(a.dX) + r * a.lddx, c, a.cols, w);
     }
   }
 }
@@ -443,11 +465,11 @@ __global__ void __launch_bounds__(64) ln_bwd_long_parts_kernel(LnBwdArgs a) {
     Input<T, CK, N> x;
     float dy[N];
     x.load(a, r, c);
-    load_row<T, N>(static_cast<const T*>(a.dY) + r * a.lddy, c, a.cols, 0.0f, dy);
+    load_row<T>(static_cast<const T*>(a.dY) + r * a.lddy, c, a.cols, 0.0f, dy);
     const float mean = a.mean[r], rstd = a.rstd[r];
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      ag[e] += (double)dy[e] * (double)bwd_xhat(x[e], mean, rstd);
+      ag[e] = __builtin_fma((double)dy[e], (double)bwd_xhat(x[e], mean, rstd), ag[e]);
       ab[e] += (double)dy[e];
     }
   }
@@ -460,22 +482,29 @@ __global__ void __launch_bounds__(64) ln_bwd_long_parts_kernel(LnBwdArgs a) {
     }
 }
 
-// The partial sums of 16 columns (of dgamma, or with blockIdx.y of dbeta): a
-// thread adds every 16th of one column (the 16 columns are one cache line of
-// a partial), then the 16 threads of a column join.
-__global__ void __launch_bounds__(256) ln_bwd_cols_kernel(const double* __restrict__ parts, int n_parts,
+// The column of the j-th partial sum, lanes holding vectors of n values
+// (n = 1: the sums are in the order of the columns).
+__device__ __forceinline__ int64_t column_of(int64_t j, int n) {
+  return n == 1 ? j : j / (64 * n) * (64 * n) + j % 64 * n + j / 64 % n;
+}
+
+// 16 of the `held` partial sums (of dgamma, or with blockIdx.y of dbeta): a
+// thread adds every 16th of one column (16 of them are one cache line of a
+// partial), then the 16 threads of a column join.
+template <int N>
+__global__ void __launch_bounds__(256) ln_bwd_cols_kernel(const double* __restrict__ parts, int n_parts, int64_t held,
                                                           int64_t cols, float* __restrict__ dgamma,
                                                           float* __restrict__ dbeta) {
   __shared__ double red[16][17];
   const int col = threadIdx.x & 15, slice = threadIdx.x >> 4;
-  const int64_t c = (int64_t)blockIdx.x * 16 + col;
+  const int64_t j = (int64_t)blockIdx.x * 16 + col, c = column_of(j, N);
   float* const out = blockIdx.y ? dbeta : dgamma;
   if (!out) return;
   double s = 0.0;
   if (c < cols) {
-    const double* p = parts + blockIdx.y * cols + c;
+    const double* p = parts + blockIdx.y * held + j;
 #pragma unroll 8
-    for (int i = slice; i < n_parts; i += 16) s += p[(int64_t)i * 2 * cols];
+    for (int i = slice; i < n_parts; i += 16) s += p[(int64_t)i * 2 * held];
   }
   red[slice][col] = s;
   __syncthreads();
@@ -508,7 +537,7 @@ unsigned int row_grid(int64_t rows, int per_group, int64_t most) {
 
 template <class T, bool QUANT, int NV, int W>
 void ln_fwd_held(const LnFwdArgs& a, hipStream_t stream) {
-  const unsigned int grid = row_grid(a.rows, W == 1 ? 4 : 1, int64_t(1) << 20);
+  const unsigned int grid = row_grid(a.rows, W == 1 ? 4 : 1, W == 1 ? 1024 : 4096 / W);
   hipLaunchKernelGGL((ln_fwd_kernel<T, NV, W, QUANT>), dim3(grid), dim3(W == 1 ? 256 : 64 * W), 0, stream, a);
 }
 
@@ -575,9 +604,15 @@ hipError_t ln_bwd(const LnBwdArgs& a, float* dgamma, float* dbeta, hipStream_t s
     case 4: ln_bwd_held<T, CK, M, 4>(a, groups, stream); break;
     default: ln_bwd_held<T, CK, M, 8>(a, groups, stream); break;
   }
-  if (a.parts)
-    hipLaunchKernelGGL(ln_bwd_cols_kernel, dim3((unsigned int)((a.cols + 15) / 16), 2), dim3(256), 0, stream, a.parts,
-                       groups, a.cols, dgamma, dbeta);
+  if (a.parts) {
+    const bool by_lane = s.waves >= 1 && s.waves <= 8;
+    const int64_t held = by_lane ? (int64_t)s.waves * (s.waves == 1 ? s.nv : M) * 64 * N : a.cols;
+    const dim3 grid((unsigned int)((held + 15) / 16), 2);
+    if (by_lane)
+      hipLaunchKernelGGL(ln_bwd_cols_kernel<N>, grid, dim3(256), 0, stream, a.parts, groups, held, a.cols, dgamma, dbeta);
+    else
+      hipLaunchKernelGGL(ln_bwd_cols_kernel<1>, grid, dim3(256), 0, stream, a.parts, groups, held, a.cols, dgamma, dbeta);
+  }
   return hipGetLastError();
 }
 
@@ -587,6 +622,16 @@ int ln_bwd_groups(int64_t rows, int64_t cols) {
   const int per_group = cols <= 1024 ? 8 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1;
   const int64_t g = (rows + per_group - 1) / per_group;
   return (int)(g < 1 ? 1 : g < 256 ? g : 256);
+}
+
+// Partial sums of a workgroup of the backward pass, of one kind: the columns
+// that its lanes hold (whole vectors of 8 values in 64 lanes, 1, 2, 4 or 8
+// times 1024 of them in longer rows).
+int64_t ln_bwd_held_max(int64_t cols) {
+  if (cols <= 1024) return (cols + 511) / 512 * 512;
+  for (int64_t held = 2048; held <= 8192; held *= 2)
+    if (cols <= held) return held;
+  return cols;
 }
 
 hipError_t launch_ln_fwd(const LnFwdArgs& a, int dtype, bool quant, hipStream_t stream) {
