@@ -40,6 +40,8 @@ __device__ __forceinline__ float rank_value(uint32_t key) {
   const int o = (int)(key ^ 0x80000000u);
   return __uint_as_float(o < 0 ? (uint32_t)(-o) | 0x80000000u : (uint32_t)o);
 }
+// The largest of a wave's (never NaN) values.
+__device__ __forceinline__ float wave_max(float x) { return rank_value(lanes_max_u32<64>(rank_key(x))); }
 // Larger for the larger value, then for the lower index.
 __device__ __forceinline__ uint64_t candidate(uint32_t key, uint32_t index) {
   return (uint64_t)key << 32 | (0xFFFFFFFFu - index);
@@ -77,13 +79,20 @@ __device__ __forceinline__ void write_row(const LpArgs& a, int64_t r, const Part
   }
 }
 
-// The k best of n candidates in LDS, best first: a candidate's place is the
-// number of better ones.
-__device__ __forceinline__ void place_best(const unsigned long long* list, int n, int k, unsigned long long* best) {
+// The k best of n candidates in LDS (with room for up to 7 more behind them,
+// which are set to 0), best first: a candidate's place is the number of
+// better ones, counted 8 at a time so that the reads overlap.
+__device__ __forceinline__ void place_best(unsigned long long* list, int n, int k, unsigned long long* best) {
+  const int padded = (n + 7) & ~7;
+  if ((int)threadIdx.x < padded - n) list[n + threadIdx.x] = 0;
+  __syncthreads();
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     const unsigned long long mine = list[i];
     int above = 0;
-    for (int j = 0; j < n && above < k; ++j) above += list[j] > mine ? 1 : 0;
+    for (int j = 0; j < padded && above < k; j += 8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) above += list[j + e] > mine ? 1 : 0;
+    }
     if (above < k && mine != 0) best[above] = mine;
   }
 }
@@ -91,7 +100,7 @@ __device__ __forceinline__ void place_best(const unsigned long long* list, int n
 // LDS of the search for the best alternatives.
 struct TopLds {
   uint32_t key[kThreads];                     // the largest key of each thread
-  unsigned long long list[(kTopMax - 1) * kValues + 1024];
+  unsigned long long list[(kTopMax - 1) * kValues + 1024 + 8];
   unsigned long long best[kTopMax];
   int lane_of[kTopMax - 1 + 32];
   int wave_count[kThreads / 64];
@@ -110,7 +119,7 @@ template <class T>
 __device__ __forceinline__ void find_best(TopLds& l, const T* row, int lo, int hi, float mx, int k) {
   constexpr int N = kVec<T>, NV = kValues / N;
   constexpr int kAbove = (kTopMax - 1) * kValues;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t mine = rank_key(mx);
   l.key[tid] = mine;
   if (tid < kTopMax) l.best[tid] = 0;
@@ -126,7 +135,10 @@ __device__ __forceinline__ void find_best(TopLds& l, const T* row, int lo, int h
       int n = 0;
 #pragma unroll
       for (int j = 0; j < kThreads / 64; ++j) n += __popcll(__ballot(key[j] >= b));
-      if (n >= k) bar = b;
+      if (n >= k) {
+        bar = b;
+        if (n == k) break;
+      }
     }
     if (lane == 0) l.bar = bar;
   }
@@ -215,8 +227,7 @@ __device__ __forceinline__ void find_best(TopLds& l, const T* row, int lo, int h
     const int at = tid + i * kThreads;
     if (at < n_eq) l.list[n + at] = moved[i];
   }
-  __syncthreads();
-  place_best(l.list, n + n_eq, k, l.best);
+  place_best(l.list, n + n_eq, k, l.best);      // (begins with a barrier)
   __syncthreads();
 }
 
@@ -229,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) lp_part_kernel(LpArgs a) {
   TopLds& top = *reinterpret_cast<TopLds*>(top_bytes);
   __shared__ double row_m, row_l;
   __shared__ int row_empty;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int part = blockIdx.x, lo = part * a.seg;
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
     const int64_t task = r * a.parts + part;
@@ -261,9 +272,7 @@ __global__ void __launch_bounds__(kThreads) lp_part_kernel(LpArgs a) {
         }
     }
     // join the threads
-    float mm = m;
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) mm = fmaxf(mm, __shfl_xor(mm, off, 64));
+    float mm = wave_max(m);
     if (lane == 0) red_m[wave] = mm;
     __syncthreads();
 #pragma unroll
@@ -312,7 +321,7 @@ __global__ void __launch_bounds__(kThreads) lp_part_kernel(LpArgs a) {
 // Joins the parts of a row.
 template <class T>
 __global__ void __launch_bounds__(256) lp_join_kernel(LpArgs a) {
-  __shared__ unsigned long long list[kMaxParts * kTopMax];
+  __shared__ unsigned long long list[kMaxParts * kTopMax + 8];
   __shared__ unsigned long long best[kTopMax];
   __shared__ double row_m, row_l;
   __shared__ int row_empty;
@@ -321,9 +330,7 @@ __global__ void __launch_bounds__(256) lp_join_kernel(LpArgs a) {
     if (tid < 64) {
       LpPart q{0.0, 0.0, kLowest, 0.0f};
       if (tid < a.parts) q = a.sums[r * a.parts + tid];
-      float mm = q.m;
-#pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) mm = fmaxf(mm, __shfl_xor(mm, off, 64));
+      const float mm = wave_max(q.m);
       double d = (double)q.m - (double)mm;
       d = d < -800.0 ? -800.0 : d;
       const double f = exp(d);
@@ -342,7 +349,6 @@ __global__ void __launch_bounds__(256) lp_join_kernel(LpArgs a) {
     if (a.topk > 0) {
       const int n = a.parts * a.topk;
       for (int i = tid; i < n; i += 256) list[i] = a.cands[r * n + i];
-      __syncthreads();
       place_best(list, n, a.topk, best);
       __syncthreads();
       if (tid < a.topk) {
