@@ -57,7 +57,26 @@ __device__ __forceinline__ void store_row(T* __restrict__ row, I c, I cols, cons
   }
 }
 
-// The same in two steps, for a load issued ahead of its use: the N values as
+// store_row with nontemporal stores.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+template <class T, int N, class I>
+__device__ __forceinline__ void stream_row(T* __restrict__ row, I c, I cols, const float (&v)[N]) {
+  if (c + N <= cols) {
+    T t[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) t[e] = from_f32<T>(v[e]);
+    u32x4_any u;
+    static_assert(sizeof(u) == sizeof(t), "a 16-byte vector");
+    __builtin_memcpy(&u, t, sizeof(t));
+    __builtin_nontemporal_store(u, reinterpret_cast<u32x4_any*>(row + c));
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (c + e < cols) row[c + e] = from_f32<T>(v[e]);
+  }
+}
+
+// load_row in two steps, for a load issued ahead of its use: the N values as
 // they are stored (those beyond `cols` are `fill`), then as floats.
 template <class T, int N>
 struct RawRow {

@@ -79,28 +79,34 @@ __device__ __forceinline__ void write_row(const LpArgs& a, int64_t r, const Part
   }
 }
 
-// The k best of n candidates in LDS (with room for up to 7 more behind them,
-// which are set to 0), best first: a candidate's place is the number of
-// better ones, counted 8 at a time so that the reads overlap.
-__device__ __forceinline__ void place_best(unsigned long long* list, int n, int k, unsigned long long* best) {
-  const int padded = (n + 7) & ~7;
-  if ((int)threadIdx.x < padded - n) list[n + threadIdx.x] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+// The k best of n candidates in LDS, best first: a candidate's place is the
+// number of better ones.  Four lanes count for each, 8 at a time so that the
+// reads overlap, until they know that it is not among the best.  `list` has
+// room for kPad more, which the caller has set to 0 (pad_list).
+constexpr int kPad = 31;
+__device__ __forceinline__ void pad_list(unsigned long long* list, int n) {
+  if (threadIdx.x < kPad) list[n + threadIdx.x] = 0;
+}
+__device__ __forceinline__ void place_best(const unsigned long long* list, int n, int k, unsigned long long* best,
+                                           int thread, int threads) {
+  const int part = thread & 3;
+  for (int i = thread >> 2; i < n; i += threads >> 2) {
     const unsigned long long mine = list[i];
     int above = 0;
-    for (int j = 0; j < padded && above < k; j += 8) {
+    for (int j = part * 8; j < n && above < k; j += 32) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) above += list[j + e] > mine ? 1 : 0;
     }
-    if (above < k && mine != 0) best[above] = mine;
+    above += lane_partner<1>(above);
+    above += lane_partner<2>(above);
+    if (part == 0 && above < k && mine != 0) best[above] = mine;
   }
 }
 
 // LDS of the search for the best alternatives.
 struct TopLds {
   uint32_t key[kThreads];                     // the largest key of each thread
-  unsigned long long list[(kTopMax - 1) * kValues + 1024 + 8];
+  unsigned long long list[(kTopMax - 1) * kValues + 1024 + kPad];
   unsigned long long best[kTopMax];
   int lane_of[kTopMax - 1 + 32];
   int wave_count[kThreads / 64];
@@ -227,7 +233,9 @@ __device__ __forceinline__ void find_best(TopLds& l, const T* row, int lo, int h
     const int at = tid + i * kThreads;
     if (at < n_eq) l.list[n + at] = moved[i];
   }
-  place_best(l.list, n + n_eq, k, l.best);      // (begins with a barrier)
+  pad_list(l.list, n + n_eq);
+  __syncthreads();
+  place_best(l.list, n + n_eq, k, l.best, tid, kThreads);
   __syncthreads();
 }
 
@@ -318,15 +326,19 @@ __global__ void __launch_bounds__(kThreads) lp_part_kernel(LpArgs a) {
   }
 }
 
-// Joins the parts of a row.
+// Joins the parts of a row: wave 0 their sums, the other waves their best.
+constexpr int kJoinThreads = 1024;
 template <class T>
-__global__ void __launch_bounds__(256) lp_join_kernel(LpArgs a) {
-  __shared__ unsigned long long list[kMaxParts * kTopMax + 8];
+__global__ void __launch_bounds__(kJoinThreads) lp_join_kernel(LpArgs a) {
+  __shared__ unsigned long long list[kMaxParts * kTopMax + kPad];
   __shared__ unsigned long long best[kTopMax];
   __shared__ double row_m, row_l;
   __shared__ int row_empty;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, n = a.parts * a.topk;
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
+    for (int i = tid; i < n; i += kJoinThreads) list[i] = a.cands[r * n + i];
+    pad_list(list, n);
+    __syncthreads();
     if (tid < 64) {
       LpPart q{0.0, 0.0, kLowest, 0.0f};
       if (tid < a.parts) q = a.sums[r * a.parts + tid];
@@ -345,26 +357,23 @@ __global__ void __launch_bounds__(256) lp_join_kernel(LpArgs a) {
         row_l = o.log_s;
         row_empty = o.empty;
       }
-    }
-    if (a.topk > 0) {
-      const int n = a.parts * a.topk;
-      for (int i = tid; i < n; i += 256) list[i] = a.cands[r * n + i];
-      place_best(list, n, a.topk, best);
-      __syncthreads();
-      if (tid < a.topk) {
-        const unsigned long long c = best[tid];
-        const float v = rank_value((uint32_t)(c >> 32));
-        a.top_index[r * a.topk + tid] = (int32_t)(0xFFFFFFFFu - (uint32_t)c);
-        a.top_logprob[r * a.topk + tid] = row_empty ? -__builtin_inff() : (float)((double)v - row_m - row_l);
-      }
+    } else {
+      place_best(list, n, a.topk, best, tid - 64, kJoinThreads - 64);
     }
     __syncthreads();
+    if (tid < a.topk) {
+      const unsigned long long c = best[tid];
+      const float v = rank_value((uint32_t)(c >> 32));
+      a.top_index[r * a.topk + tid] = (int32_t)(0xFFFFFFFFu - (uint32_t)c);
+      a.top_logprob[r * a.topk + tid] = row_empty ? -__builtin_inff() : (float)((double)v - row_m - row_l);
+    }
+    __syncthreads();                          // LDS is used again
   }
 }
 
 constexpr int kGradVecs = 4;                  // vectors of a thread of the backward pass
 
-template <class T>
+template <class T, bool STREAM>
 __global__ void __launch_bounds__(256) lp_bwd_kernel(LpBwdArgs a) {
   constexpr int N = kVec<T>, U = kGradVecs;
   constexpr int CHUNK = 256 * N * U;
@@ -393,7 +402,10 @@ __global__ void __launch_bounds__(256) lp_bwd_kernel(LpBwdArgs a) {
         if (c + e == t) d += g;
         v[u][e] = empty ? 0.0f : d;
       }
-      store_row<T>(dx, c, a.cols, v[u]);
+      if constexpr (STREAM)
+        stream_row<T>(dx, c, a.cols, v[u]);
+      else
+        store_row<T>(dx, c, a.cols, v[u]);
     }
   }
 }
@@ -408,25 +420,30 @@ hipError_t forward(const LpArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((lp_part_kernel<T, true>), grid, block, 0, stream, a);
   else
     hipLaunchKernelGGL((lp_part_kernel<T, false>), grid, block, 0, stream, a);
-  if (a.parts > 1) hipLaunchKernelGGL((lp_join_kernel<T>), dim3(1, row_grid(a.rows)), dim3(256), 0, stream, a);
+  if (a.parts > 1) hipLaunchKernelGGL((lp_join_kernel<T>), dim3(1, row_grid(a.rows)), dim3(kJoinThreads), 0, stream, a);
   return hipGetLastError();
 }
 
 template <class T>
 hipError_t backward(const LpBwdArgs& a, hipStream_t stream) {
   constexpr int CHUNK = 256 * kVec<T> * kGradVecs;
-  hipLaunchKernelGGL((lp_bwd_kernel<T>), dim3((unsigned int)((a.cols + CHUNK - 1) / CHUNK), row_grid(a.rows)), dim3(256), 0, stream, a);
+  const dim3 grid((unsigned int)((a.cols + CHUNK - 1) / CHUNK), row_grid(a.rows));
+  // a gradient larger than half the last-level cache is stored around it
+  if ((double)a.rows * (double)a.cols * sizeof(T) > kStreamOutBytes)
+    hipLaunchKernelGGL((lp_bwd_kernel<T, true>), grid, dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((lp_bwd_kernel<T, false>), grid, dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 // Parts of a row: as many as its length needs, and with few rows as many as
-// fill the chip, each of 4096 columns or more.
+// fill the chip, each of a batch of 16 values a thread (8192 columns) or more.
 LpSplit lp_split(int64_t rows, int64_t cols) {
   int64_t parts = (cols + kSegMax - 1) / kSegMax;
   const int64_t fill = rows >= 512 ? 1 : (512 + rows - 1) / rows;
-  int64_t most = (cols + 4095) / 4096;
+  int64_t most = (cols + 16 * kThreads - 1) / (16 * kThreads);
   most = most < kMaxParts ? most : kMaxParts;
   if (parts < fill) parts = fill < most ? fill : most > parts ? most : parts;
   const int64_t seg = ((cols + parts - 1) / parts + 63) / 64 * 64;
