@@ -432,12 +432,16 @@ int checkpoint_act_bwd(const int8_t* Q, int64_t ldq, const float* scale, int64_t
  * quantize_cols(checkpoint_restore(...)) byte for byte; a column that holds a
  * NaN gets a NaN scale and codes 0.
  *   Qt     cols x rows int8, leading dimension ldqt >= rows.
- *   scale_out  cols f32 (also scratch while the call runs).
- * Errors: as checkpoint_i8.
+ *   scale_out  cols f32.
+ *   workspace  device scratch of checkpoint_quantize_cols_workspace_bytes(rows,
+ *          cols), 256-byte aligned, any contents (not needed without rows).
+ * Errors: as checkpoint_i8, and I8G_EWORKSPACE.
  */
+size_t checkpoint_quantize_cols_workspace_bytes(int64_t rows, int64_t cols);
 int checkpoint_quantize_cols(const int8_t* Q, int64_t ldq, const float* scale, int64_t lds,
                              int32_t group, int64_t rows, int64_t cols, int8_t* Qt, int64_t ldqt,
-                             float* scale_out, void* stream);
+                             float* scale_out, void* workspace, size_t workspace_bytes,
+                             void* stream);
 
 /*
  * layer_norm_bwd_checkpoint -- layer_norm_bwd with the input's values taken

@@ -62,7 +62,8 @@ EXPORTED = ("quantize_rows", "quantize_cols", "gemm_i8_blockscaled", "gemm_i8_wo
             "gemm_i8_workspace_bytes_flags", "i8g_audit_quantize_fmt", "i8g_set_test_overrides",
             "i8g_plan_query", "gemm_i8_blockscaled_noalloc", "layer_norm", "layer_norm_quantize_rows",
             "layer_norm_bwd", "layer_norm_bwd_workspace_bytes", "layer_norm_bwd_checkpoint", "checkpoint_i8",
-            "checkpoint_restore", "checkpoint_act_bwd", "checkpoint_quantize_cols", "token_logprobs",
+            "checkpoint_restore", "checkpoint_act_bwd", "checkpoint_quantize_cols",
+            "checkpoint_quantize_cols_workspace_bytes", "token_logprobs",
             "token_logprobs_workspace_bytes", "token_logprobs_bwd")
 
 _lib = None
@@ -157,7 +158,7 @@ def load():
             ("checkpoint_i8", [c_vp, c_u32, c_i64, c_i64, c_i64, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp]),
             ("checkpoint_restore", [*ckpt, c_vp, c_u32, c_i64, c_vp]),
             ("checkpoint_act_bwd", [*ckpt, c_u32, c_vp, c_i64, c_vp, c_i64, c_u32, c_vp]),
-            ("checkpoint_quantize_cols", [*ckpt, c_vp, c_i64, c_vp, c_vp]),
+            ("checkpoint_quantize_cols", [*ckpt, c_vp, c_i64, c_vp, c_vp, c_sz, c_vp]),
             ("token_logprobs", [c_vp, c_u32, c_i64, c_i64, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                                 c_sz, c_vp]),
             ("token_logprobs_bwd", [c_vp, c_u32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64,
@@ -166,6 +167,8 @@ def load():
         getattr(lib, name).restype = ctypes.c_int
     lib.layer_norm_bwd_workspace_bytes.argtypes = [c_i64, c_i64]
     lib.layer_norm_bwd_workspace_bytes.restype = c_sz
+    lib.checkpoint_quantize_cols_workspace_bytes.argtypes = [c_i64, c_i64]
+    lib.checkpoint_quantize_cols_workspace_bytes.restype = c_sz
     lib.token_logprobs_workspace_bytes.argtypes = [c_i64, c_i64, c_i32]
     lib.token_logprobs_workspace_bytes.restype = c_sz
     _lib = lib
@@ -732,7 +735,9 @@ def checkpoint_quantize_cols(Q, scale, group):
     rows, cols = Q.shape
     Qt = _int8_padded(cols, rows, Q.device)
     s = torch.empty(cols, dtype=torch.float32, device=Q.device)
-    _enqueue(load().checkpoint_quantize_cols, Q, *ck, Qt.data_ptr(), Qt.stride(0), s.data_ptr())
+    nbytes = load().checkpoint_quantize_cols_workspace_bytes(rows, cols)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=Q.device)
+    _enqueue(load().checkpoint_quantize_cols, Q, *ck, Qt.data_ptr(), Qt.stride(0), s.data_ptr(), ws.data_ptr(), nbytes)
     return Qt, s
 
 

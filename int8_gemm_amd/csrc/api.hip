@@ -402,14 +402,23 @@ int checkpoint_act_bwd(const int8_t* Q, int64_t ldq, const float* scale, int64_t
   return hip_status(launch_checkpoint_read(c, (int)act, dY, lddy, dX, lddx, (int)dtype, as_stream(stream)));
 }
 
+size_t checkpoint_quantize_cols_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0 || bad_sizes(rows, cols)) return 256;
+  return ((size_t)checkpoint_cols_parts(rows) * (size_t)cols * 4 + 255) / 256 * 256;
+}
+
 int checkpoint_quantize_cols(const int8_t* Q, int64_t ldq, const float* scale, int64_t lds, int32_t group, int64_t rows,
-                             int64_t cols, int8_t* Qt, int64_t ldqt, float* scale_out, void* stream) {
+                             int64_t cols, int8_t* Qt, int64_t ldqt, float* scale_out, void* workspace,
+                             size_t workspace_bytes, void* stream) {
   Checkpoint c;
   if (bad_checkpoint(Q, ldq, scale, lds, group, rows, cols, false, &c)) return I8G_EINVAL;
   if (bad_matrix(Qt, cols, rows, ldqt, 1)) return I8G_EINVAL;
   if (cols == 0) return I8G_OK;
   if (!scale_out || bad_f32(scale_out)) return I8G_EINVAL;
-  return hip_status(launch_checkpoint_cols(c, Qt, ldqt, scale_out, as_stream(stream)));
+  if (rows > 0 && (!workspace || (uintptr_t)workspace % 256 != 0 ||
+                   workspace_bytes < checkpoint_quantize_cols_workspace_bytes(rows, cols)))
+    return I8G_EWORKSPACE;
+  return hip_status(launch_checkpoint_cols(c, Qt, ldqt, scale_out, workspace, as_stream(stream)));
 }
 
 static bool bad_i64(const void* p) { return (uintptr_t)p % 8 != 0; }

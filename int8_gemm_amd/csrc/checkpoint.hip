@@ -102,98 +102,140 @@ __global__ void __launch_bounds__(kBlock) checkpoint_read_kernel(Checkpoint c, c
 }
 
 // ---------------------------------------------------------------------------
-// quantize_cols of a checkpoint's values: a pass for the column scales (the
-// largest partial scale is the scale of the column's maximum, as rounding is
-// monotone, so atomicMax on the bits of the scales is exact in any order; a
-// NaN is the largest), then a pass that quantizes and transposes.
+// quantize_cols of a checkpoint's values: a pass that leaves the column maxima
+// of up to kColParts ranges of rows in the workspace, then a pass that takes
+// the largest of them, quantizes and transposes.  Both work on tiles of 64
+// columns x 128 rows, a thread on 8 columns (one 8-byte load a row, inside
+// one group) of 4 rows.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) checkpoint_cols_init_kernel(float* scale, int64_t n) {
+constexpr int kTileCols = 64, kTileRows = 128;
+constexpr int kColParts = 64;
+
+// The values of row r, columns col .. col+7; 0 outside the matrix.
+__device__ __forceinline__ void tile_row(const Checkpoint& c, int64_t r, int64_t col, float (&v)[8]) {
+  int q[8];
+  float s = 0.0f;
+  if (r < c.rows && col < c.cols) {
+    load_codes(c.Q + r * c.ldq, col, c.cols, q);
+    s = c.scale[r * c.lds + (col >> c.gshift)];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = 0;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = mul_rn((float)q[e], s);
+}
+
+// The largest of x over the lanes of equal number mod 8.
+__device__ __forceinline__ uint32_t max_mod8(uint32_t x) {
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, x, 0x128, 0xF, 0xF, true));   // rotated by 8 lanes of 16
+  Pair32 p = lane_pair<16>(x);
+  p = lane_pair<32>(max(p.a, p.b));
+  return max(p.a, p.b);
+}
+
+// Column maxima, as the bits of |x| (a NaN is above all), of the row tiles
+// blockIdx.y, blockIdx.y + gridDim.y, ...
+__global__ void __launch_bounds__(256) checkpoint_cols_max_kernel(Checkpoint c, uint32_t* __restrict__ parts) {
+  __shared__ uint32_t red[4][kTileCols];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t col = (int64_t)blockIdx.x * kTileCols + (threadIdx.x & 7) * 8;
+  uint32_t m[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int64_t r0 = (int64_t)blockIdx.y * kTileRows; r0 < c.rows; r0 += (int64_t)gridDim.y * kTileRows) {
+    float v[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tile_row(c, r0 + i * 32 + (threadIdx.x >> 3), col, v[i]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      m[e] = max(max(m[e], max(abs_bits(v[0][e]), abs_bits(v[1][e]))), max(abs_bits(v[2][e]), abs_bits(v[3][e])));
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    m[e] = max_mod8(m[e]);
+    if (lane < 8) red[wave][lane * 8 + e] = m[e];
+  }
+  __syncthreads();
+  const int64_t j = (int64_t)blockIdx.x * kTileCols + threadIdx.x;
+  if (threadIdx.x < kTileCols && j < c.cols)
+    parts[blockIdx.y * c.cols + j] = max(max(red[0][threadIdx.x], red[1][threadIdx.x]),
+                                         max(red[2][threadIdx.x], red[3][threadIdx.x]));
+}
+
+// Quantized, transposed through LDS (4 rows of a column to a word; a row of
+// 33 words puts the 64 lanes of a wave on 64 banks) and stored as 64 rows of
+// 128 bytes.  The workgroups of the first row tile write the scales.
+__global__ void __launch_bounds__(256) checkpoint_cols_quant_kernel(Checkpoint c, int8_t* __restrict__ Qt,
+                                                                    int64_t ldqt, float* __restrict__ scale,
+                                                                    const uint32_t* __restrict__ parts, int n_parts) {
+  __shared__ uint32_t red[4][kTileCols];
+  __shared__ float s_inv[kTileCols];
+  __shared__ unsigned int tile[kTileCols][kTileRows / 4 + 1];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t j0 = (int64_t)blockIdx.x * kTileCols;
+  const int cg = tid & 7, rr = tid >> 3;
+  const int64_t col = j0 + cg * 8;
+  int64_t r0 = (int64_t)blockIdx.y * kTileRows;
+  float v[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tile_row(c, r0 + rr * 4 + i, col, v[i]);   // on their way while the scales are found
+  uint32_t m = 0;
+  if (j0 + lane < c.cols) {
+#pragma unroll 4
+    for (int i = wave; i < n_parts; i += 4) m = max(m, parts[i * c.cols + j0 + lane]);
+  }
+  red[wave][lane] = m;
+  __syncthreads();
+  if (tid < kTileCols) {
+    m = max(max(red[0][tid], red[1][tid]), max(red[2][tid], red[3][tid]));
+    const float s = scale_of_bits(m);
+    s_inv[tid] = m < kInfBits ? recip_rn(s) : 0.0f;       // a NaN column: codes 0
+    if (blockIdx.y == 0 && j0 + tid < c.cols) scale[j0 + tid] = s;
+  }
+  __syncthreads();
+  float inv[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) inv[e] = s_inv[cg * 8 + e];
+  while (r0 < c.rows) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      unsigned int w = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w |= (unsigned int)(quantize1(v[i][e], inv[e]) & 0xFF) << (8 * i);
+      tile[cg * 8 + e][rr] = inv[e] > 0.0f ? w : 0u;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {                         // 8 threads store a column's 128 bytes
+      const int jl = i * 32 + (tid >> 3), part = tid & 7;
+      const int64_t j = j0 + jl, k = r0 + part * 16;
+      if (j < c.cols && k < c.rows) {
+        int8_t* dst = Qt + j * ldqt + k;
+        unsigned int w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = tile[jl][part * 4 + e];
+        if (k + 16 <= c.rows) {
+          __builtin_memcpy(dst, w, 16);
+        } else {
+          for (int e = 0; e < 16 && k + e < c.rows; ++e) dst[e] = (int8_t)((w[e >> 2] >> (8 * (e & 3))) & 0xFF);
+        }
+      }
+    }
+    r0 += (int64_t)gridDim.y * kTileRows;
+    if (r0 < c.rows) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tile_row(c, r0 + rr * 4 + i, col, v[i]);
+    }
+    __syncthreads();
+  }
+}
+
+// The scales of columns without rows: the floor.
+__global__ void __launch_bounds__(256) checkpoint_cols_floor_kernel(float* scale, int64_t n) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i < n) scale[i] = scale_floor();
 }
 
-constexpr int kColRows = 64;     // rows of a workgroup of the scale pass
-
-__global__ void __launch_bounds__(256) checkpoint_cols_scale_kernel(Checkpoint c, unsigned int* __restrict__ scale) {
-  __shared__ uint32_t red[4][256];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t col = (int64_t)blockIdx.x * 256 + lane * 4;
-  for (int64_t r0 = (int64_t)blockIdx.y * kColRows; r0 < c.rows; r0 += (int64_t)gridDim.y * kColRows) {
-    uint32_t m[4] = {0, 0, 0, 0};
-    if (col < c.cols) {
-      const int64_t end = r0 + kColRows < c.rows ? r0 + kColRows : c.rows;
-      for (int64_t r = r0 + wave; r < end; r += 4) {
-        int q[4];
-        load_codes(c.Q + r * c.ldq, col, c.cols, q);
-        const float s = c.scale[r * c.lds + (col >> c.gshift)];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m[e] = max(m[e], abs_bits(mul_rn((float)q[e], s)));
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) red[wave][lane * 4 + e] = m[e];
-    __syncthreads();
-    const int t = threadIdx.x;
-    const uint32_t a = max(max(red[0][t], red[1][t]), max(red[2][t], red[3][t]));
-    if ((int64_t)blockIdx.x * 256 + t < c.cols)
-      atomicMax(scale + (int64_t)blockIdx.x * 256 + t, __float_as_uint(scale_of_bits(a)));
-    __syncthreads();
-  }
-}
-
-// 64 rows x 64 columns: quantized, transposed through LDS, stored as 64 rows
-// of 64 bytes.
-__global__ void __launch_bounds__(256) checkpoint_cols_quant_kernel(Checkpoint c, int8_t* __restrict__ Qt,
-                                                                    int64_t ldqt, const float* __restrict__ scale) {
-  __shared__ float s_inv[64];
-  __shared__ unsigned int tile[64][17];
-  const int tid = threadIdx.x;
-  const int64_t j0 = (int64_t)blockIdx.x * 64;
-  if (tid < 64) {
-    const float s = j0 + tid < c.cols ? scale[j0 + tid] : 1.0f;
-    s_inv[tid] = s == s ? recip_rn(s) : 0.0f;             // a NaN column: codes 0
-  }
-  __syncthreads();
-  const int cg = tid & 15, rr = tid >> 4;
-  const int64_t col = j0 + cg * 4;
-  float inv[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) inv[e] = s_inv[cg * 4 + e];
-  for (int64_t k0 = (int64_t)blockIdx.y * 64; k0 < c.rows; k0 += (int64_t)gridDim.y * 64) {
-    unsigned int w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t k = k0 + rr * 4 + i;
-      if (k < c.rows && col < c.cols) {
-        int q[4];
-        load_codes(c.Q + k * c.ldq, col, c.cols, q);
-        const float s = c.scale[k * c.lds + (col >> c.gshift)];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int v = inv[e] > 0.0f ? quantize1(mul_rn((float)q[e], s), inv[e]) : 0;
-          w[e] |= (unsigned int)(v & 0xFF) << (8 * i);
-        }
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) tile[cg * 4 + e][rr] = w[e];
-    __syncthreads();
-    const int jl = tid >> 2, ch = tid & 3;
-    const int64_t j = j0 + jl, k = k0 + ch * 16;
-    if (j < c.cols && k < c.rows) {
-      int8_t* dst = Qt + j * ldqt + k;
-      unsigned int t[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) t[e] = tile[jl][ch * 4 + e];
-      if (k + 16 <= c.rows) {
-        __builtin_memcpy(dst, t, 16);
-      } else {
-        for (int e = 0; e < 16 && k + e < c.rows; ++e) dst[e] = (int8_t)((t[e >> 2] >> (8 * (e & 3))) & 0xFF);
-      }
-    }
-    __syncthreads();
-  }
-}
+int64_t row_tiles(int64_t rows) { return (rows + kTileRows - 1) / kTileRows; }
 
 // Calls launch(first row, rows, grid) for slabs of rows of fewer than 2^31 units.
 template <class F>
@@ -273,17 +315,25 @@ hipError_t launch_checkpoint_read(const Checkpoint& c, int act, const void* dY, 
   }
 }
 
-hipError_t launch_checkpoint_cols(const Checkpoint& c, int8_t* Qt, int64_t ldqt, float* scale, hipStream_t stream) {
-  hipLaunchKernelGGL(checkpoint_cols_init_kernel, dim3((unsigned int)((c.cols + 255) / 256)), dim3(256), 0, stream,
-                     scale, c.cols);
-  if (c.rows > 0) {
-    const int64_t by = (c.rows + 63) / 64;
-    const unsigned int gy = (unsigned int)(by < 4096 ? by : 4096);
-    hipLaunchKernelGGL(checkpoint_cols_scale_kernel, dim3((unsigned int)((c.cols + 255) / 256), gy), dim3(256), 0,
-                       stream, c, reinterpret_cast<unsigned int*>(scale));
-    hipLaunchKernelGGL(checkpoint_cols_quant_kernel, dim3((unsigned int)((c.cols + 63) / 64), gy), dim3(256), 0,
-                       stream, c, Qt, ldqt, scale);
+int checkpoint_cols_parts(int64_t rows) {
+  const int64_t n = row_tiles(rows);
+  return (int)(n < kColParts ? n : kColParts);
+}
+
+hipError_t launch_checkpoint_cols(const Checkpoint& c, int8_t* Qt, int64_t ldqt, float* scale, void* parts,
+                                  hipStream_t stream) {
+  if (c.rows == 0) {
+    hipLaunchKernelGGL(checkpoint_cols_floor_kernel, dim3((unsigned int)((c.cols + 255) / 256)), dim3(256), 0, stream,
+                       scale, c.cols);
+    return hipGetLastError();
   }
+  uint32_t* p = static_cast<uint32_t*>(parts);
+  const unsigned int bx = (unsigned int)((c.cols + kTileCols - 1) / kTileCols);
+  const int n = checkpoint_cols_parts(c.rows);
+  const int64_t tiles = row_tiles(c.rows);
+  hipLaunchKernelGGL(checkpoint_cols_max_kernel, dim3(bx, n), dim3(256), 0, stream, c, p);
+  hipLaunchKernelGGL(checkpoint_cols_quant_kernel, dim3(bx, (unsigned int)(tiles < 4096 ? tiles : 4096)), dim3(256), 0, stream,
+                     c, Qt, ldqt, scale, p, n);
   return hipGetLastError();
 }
 

@@ -200,8 +200,10 @@ def test_writes_nothing_else(g, rows, cols):
         assert untouched(Y, rows, cols, ymark) and torch.isfinite(Y[:rows, :cols].float()).all()
     Qt, qmark = guarded(cols, rows + 7, torch.int8)
     s = torch.full((cols + 4,), 5.0, device="cuda")
-    assert lib.checkpoint_quantize_cols(*ck, Qt.data_ptr(), rows + 7, s.data_ptr(), st) == 0
-    assert untouched(Qt, cols, rows, qmark) and (s[cols:] == 5.0).all()
+    nbytes = lib.checkpoint_quantize_cols_workspace_bytes(rows, cols)
+    ws = torch.full((nbytes + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    assert lib.checkpoint_quantize_cols(*ck, Qt.data_ptr(), rows + 7, s.data_ptr(), ws.data_ptr(), nbytes, st) == 0
+    assert untouched(Qt, cols, rows, qmark) and (s[cols:] == 5.0).all() and (ws[nbytes:] == 0xFF).all()
 
 
 def test_far_rows(g):

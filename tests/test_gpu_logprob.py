@@ -205,6 +205,21 @@ def test_gradient(g, rows, vocab, dtype):
     same_bits(Z, got, "in place")
 
 
+def test_large_gradient(g):
+    """A gradient of more than 128 MiB is stored another way: the same bytes
+    as in two halves."""
+    rows, vocab = 1400, 50257
+    say("logprobs large gradient", rows, vocab)
+    X = torch.randn((rows, vocab), generator=torch.Generator("cuda").manual_seed(1), device="cuda").to(torch.bfloat16)
+    t = torch.arange(rows, device="cuda") * 31 % vocab
+    _, h, lse, _, _ = g.token_logprobs(X, t)
+    one = torch.ones(rows, device="cuda")
+    whole = g.token_logprobs_bwd(X, t, lse, h, one, one)
+    for sl in (slice(0, 700), slice(700, 1400)):
+        half = g.token_logprobs_bwd(X[sl], t[sl], lse[sl], h[sl], one[sl], one[sl])
+        assert torch.equal(whole[sl].view(torch.int16), half.view(torch.int16))
+
+
 def test_gradient_of_masked_rows(g):
     say("logprobs gradient, masked rows")
     for dt in DTYPES.values():

@@ -72,9 +72,12 @@ def test_checkpoint(lib):
     refused(lib.checkpoint_restore, ck + [A, 1, 70, None], {**bad, 7: [None, ODD], 8: [3], 9: [69]})
     refused(lib.checkpoint_act_bwd, ck + [1, A, 70, A, 70, 1, None],
             {**bad, 7: [0, 3], 8: [None, ODD], 9: [69], 10: [None, ODD], 11: [69], 12: [3]})
-    refused(lib.checkpoint_quantize_cols, ck + [A, 4, A, None], {**bad, 7: [None], 8: [3], 9: [None, ODD]})
+    need = lib.checkpoint_quantize_cols_workspace_bytes(4, 70)
+    good = ck + [A, 4, A, WS, need, None]
+    refused(lib.checkpoint_quantize_cols, good, {**bad, 7: [None], 8: [3], 9: [None, ODD]})
+    refused(lib.checkpoint_quantize_cols, good, {10: [None, P((1 << 24) + 64)], 11: [0, need - 1]}, EWORKSPACE)
     assert lib.checkpoint_restore(A, 70, A, 0, 0, 4, 70, A, 1, 70, None) == EINVAL                 # lds 0 for row scales
-    assert lib.checkpoint_quantize_cols(A, 0, A, 0, 32, 4, 0, A, 4, A, None) == OK                 # no columns
+    assert lib.checkpoint_quantize_cols(A, 0, A, 0, 32, 4, 0, A, 4, A, None, 0, None) == OK                 # no columns
 
 
 def test_token_logprobs(lib):
