@@ -210,7 +210,8 @@ def _round16(n):
 def _int8_padded(rows, cols, device):
     """rows x cols int8 view of a buffer whose rows are padded to 16 bytes."""
     ld = max(_round16(cols), 16)
-    return torch.empty((rows, ld), dtype=torch.int8, device=device)[:, :cols]
+    buf = torch.empty((rows, ld), dtype=torch.int8, device=device)
+    return buf if ld == cols else buf[:, :cols]
 
 
 def quantize_rows(X):
@@ -557,7 +558,7 @@ def _values(x, name, like=None):
 def _layout(x, name, like=None):
     if not x.is_cuda:
         raise ValueError(f"{name} must be on a GPU")
-    if like is not None and x.device != like.device:
+    if like is not None and x.get_device() != like.get_device():
         raise ValueError(f"{name} must be on {like.device}, got {x.device}")
     rows, cols = x.shape
     if cols > 1 and rows > 0 and x.stride(1) != 1:
@@ -573,7 +574,7 @@ def _vector(x, n, name, like, optional=False):
         return None
     if not isinstance(x, torch.Tensor) or x.dtype != torch.float32 or x.dim() != 1 or x.numel() != n:
         raise ValueError(f"{name} must be a 1-D float32 tensor of {n} values")
-    if x.device != like.device:
+    if x.get_device() != like.get_device():
         raise ValueError(f"{name} must be on {like.device}, got {x.device}")
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -665,12 +666,12 @@ def _checkpoint(Q, scale, group, shape=None, like=None):
         raise ValueError("group must be 32, 64, 128 or 256, or 0 for one scale per row")
     groups = -(-cols // group) if group else min(cols, 1)
     if not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32 or \
-            not (tuple(scale.shape) == (rows, groups) or (group == 0 and tuple(scale.shape) == (rows,))):
+            not (scale.shape == (rows, groups) or (group == 0 and scale.shape == (rows,))):
         raise ValueError(f"scale must be a float32 tensor of shape ({rows}, {groups})"
                          + (f" or ({rows},)" if group == 0 else ""))
-    if scale.device != Q.device:
+    if scale.get_device() != Q.get_device():
         raise ValueError(f"scale must be on {Q.device}, got {scale.device}")
-    if scale.dim() == 2 and groups > 1 and scale.stride(1) != 1:
+    if groups > 1 and scale.stride(1) != 1:
         raise ValueError("scale must be row-major (unit column stride)")
     lds = scale.stride(0) if rows > 1 else max(groups, 1)
     if lds < groups:
@@ -744,7 +745,7 @@ def checkpoint_quantize_cols(Q, scale, group):
 def _targets(t, rows, like):
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int64 or t.dim() != 1 or t.numel() != rows:
         raise ValueError(f"targets must be a 1-D int64 tensor of {rows} token numbers")
-    if t.device != like.device:
+    if t.get_device() != like.get_device():
         raise ValueError(f"targets must be on {like.device}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError("targets must be contiguous")
@@ -765,9 +766,9 @@ def token_logprobs(logits, targets, topk=0):
     index = torch.empty((rows, topk), dtype=torch.int32, device=dev) if topk else None
     top = torch.empty((rows, topk), dtype=torch.float32, device=dev) if topk else None
     nbytes = load().token_logprobs_workspace_bytes(rows, vocab, topk)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     _enqueue(load().token_logprobs, logits, logits.data_ptr(), _DTYPES[logits.dtype], rows, vocab, ld, t, topk,
-             logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), _addr(index), _addr(top), ws.data_ptr(), nbytes)
+             logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), _addr(index), _addr(top), _addr(ws), nbytes)
     return logprob, entropy, lse, index, top
 
 

@@ -429,9 +429,9 @@ static size_t lp_sums_bytes(int64_t rows, int parts) {
 }
 
 size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int32_t topk) {
-  if (rows <= 0 || rows > INT32_MAX || vocab <= 0 || vocab > I8G_VOCAB_MAX || topk < 0 || topk > I8G_TOPK_MAX) return 256;
+  if (rows <= 0 || rows > INT32_MAX || vocab <= 0 || vocab > I8G_VOCAB_MAX || topk < 0 || topk > I8G_TOPK_MAX) return 0;
   const LpSplit sp = lp_split(rows, vocab);
-  if (sp.parts == 1) return 256;
+  if (sp.parts == 1) return 0;
   return lp_sums_bytes(rows, sp.parts) + ((size_t)rows * sp.parts * topk * 8 + 255) / 256 * 256;
 }
 
@@ -446,8 +446,8 @@ int token_logprobs(const void* logits, uint32_t dtype, int64_t rows, int64_t voc
   if (rows > 0 && ((logprob && !targets) || (topk > 0 && (!top_index || !top_logprob)))) return I8G_EINVAL;
   if (rows == 0) return I8G_OK;
   const LpSplit sp = lp_split(rows, vocab);
-  if (!workspace || (uintptr_t)workspace % 256 != 0 || workspace_bytes < token_logprobs_workspace_bytes(rows, vocab, topk))
-    return I8G_EWORKSPACE;
+  const size_t need = token_logprobs_workspace_bytes(rows, vocab, topk);
+  if (need > 0 && (!workspace || (uintptr_t)workspace % 256 != 0 || workspace_bytes < need)) return I8G_EWORKSPACE;
   char* ws = static_cast<char*>(workspace);
   LpArgs a{logits, rows, vocab, ld, targets, sp.parts, sp.seg, topk, logprob, entropy, lse, top_index, top_logprob,
            reinterpret_cast<LpPart*>(ws), reinterpret_cast<unsigned long long*>(ws + lp_sums_bytes(rows, sp.parts))};

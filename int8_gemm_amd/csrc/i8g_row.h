@@ -93,6 +93,11 @@ struct RawRow {
   __device__ __forceinline__ float operator[](int e) const { return to_f32(t[e]); }
 };
 
+// The low bytes of four integers as one word.
+__device__ __forceinline__ uint32_t pack_bytes(int a, int b, int c, int d) {
+  return __builtin_amdgcn_perm(b, a, 0x0C0C0400u) | __builtin_amdgcn_perm(d, c, 0x04000C0Cu);
+}
+
 // N int8 codes at row[c ...]; those beyond `cols` are 0.
 template <int N, class I>
 __device__ __forceinline__ void load_codes(const int8_t* __restrict__ row, I c, I cols, int (&q)[N]) {
@@ -113,8 +118,7 @@ __device__ __forceinline__ void store_codes(int8_t* __restrict__ row, I c, I col
     uint32_t w[N / 4];
 #pragma unroll
     for (int i = 0; i < N / 4; ++i)
-      w[i] = (uint32_t)(q[4 * i] & 0xFF) | (uint32_t)(q[4 * i + 1] & 0xFF) << 8 |
-             (uint32_t)(q[4 * i + 2] & 0xFF) << 16 | (uint32_t)(q[4 * i + 3] & 0xFF) << 24;
+      w[i] = pack_bytes(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
     __builtin_memcpy(row + c, w, N);
   } else {
 #pragma unroll

@@ -82,7 +82,7 @@ def test_checkpoint(lib):
 
 def test_token_logprobs(lib):
     need = lib.token_logprobs_workspace_bytes(2, 50257, 4)
-    assert need > 256
+    assert need >= 256
     #       x dtype rows vocab ld targets topk logprob entropy lse index top ws bytes stream
     good = [A, 0, 2, 50257, 50257, A, 4, A, A, A, A, A, WS, need, None]
     bad = {0: [None, ODD], 1: [3], 2: [-1, 1 << 31], 3: [-1, 0, (1 << 22) + 1, 1 << 31], 4: [50256],
@@ -108,7 +108,7 @@ def test_workspace_sizes(lib):
         sizes = [lib.layer_norm_bwd_workspace_bytes(r, cols) for r in (1, 2, 4, 5, 100, 8192, 1 << 30)]
         assert sizes == sorted(sizes)
     for args in ((0, 5, 1), (5, 0, 1), (-1, 5, 1), (5, 5, -1), (5, 5, 33), (5, 1 << 30, 1)):
-        assert lib.token_logprobs_workspace_bytes(*args) == 256
+        assert lib.token_logprobs_workspace_bytes(*args) == 0
 
 
 def test_python_arguments():
