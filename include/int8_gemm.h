@@ -466,8 +466,9 @@ int layer_norm_bwd_checkpoint(const void* dY, int64_t lddy, uint32_t dtype, cons
  *   logprob, entropy, lse   rows f32 each, any may be NULL.
  *   top_index, top_logprob  rows x topk int32 / f32 (not used for topk 0).
  *   workspace  device scratch of token_logprobs_workspace_bytes(rows, vocab,
- *            topk), 256-byte aligned, any contents; NULL where that is 0 (many
- *            rows, or short ones).
+ *            topk), 256-byte aligned, any contents; NULL where that is 0
+ *            (topk 0 with many rows, or short ones).  With topk it holds 256
+ *            bytes for each 8192 columns of a row.
  * Sums are held against the row's maximum, in binary32 over at most 128
  * values and binary64 beyond.  A logit of -inf has probability 0 and adds
  * nothing to the entropy.  A row of -inf only has lse and every log

@@ -423,16 +423,18 @@ int checkpoint_quantize_cols(const int8_t* Q, int64_t ldq, const float* scale, i
 
 static bool bad_i64(const void* p) { return (uintptr_t)p % 8 != 0; }
 
-// Bytes of the parts' sums, rounded so that the candidates behind them are aligned.
+// Bytes of the parts' sums, rounded so that what is behind them is aligned.
 static size_t lp_sums_bytes(int64_t rows, int parts) {
   return ((size_t)rows * (size_t)parts * sizeof(LpPart) + 255) / 256 * 256;
 }
 
+// The workspace: the parts' sums, then (with topk) the maxima of the batches.
 size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int32_t topk) {
   if (rows <= 0 || rows > INT32_MAX || vocab <= 0 || vocab > I8G_VOCAB_MAX || topk < 0 || topk > I8G_TOPK_MAX) return 0;
   const LpSplit sp = lp_split(rows, vocab);
-  if (sp.parts == 1) return 0;
-  return lp_sums_bytes(rows, sp.parts) + ((size_t)rows * sp.parts * topk * 8 + 255) / 256 * 256;
+  if (sp.parts == 1 && topk == 0) return 0;
+  const size_t tops = topk > 0 ? (size_t)rows * sp.tops * sizeof(float) : 0;
+  return lp_sums_bytes(rows, sp.parts) + (tops + 255) / 256 * 256;
 }
 
 int token_logprobs(const void* logits, uint32_t dtype, int64_t rows, int64_t vocab, int64_t ld, const int64_t* targets,
@@ -449,8 +451,9 @@ int token_logprobs(const void* logits, uint32_t dtype, int64_t rows, int64_t voc
   const size_t need = token_logprobs_workspace_bytes(rows, vocab, topk);
   if (need > 0 && (!workspace || (uintptr_t)workspace % 256 != 0 || workspace_bytes < need)) return I8G_EWORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  LpArgs a{logits, rows, vocab, ld, targets, sp.parts, sp.seg, topk, logprob, entropy, lse, top_index, top_logprob,
-           reinterpret_cast<LpPart*>(ws), reinterpret_cast<unsigned long long*>(ws + lp_sums_bytes(rows, sp.parts))};
+  LpArgs a{logits, rows, vocab, ld, targets, sp.parts, sp.seg, sp.batches, topk,
+           logprob, entropy, lse, top_index, top_logprob, reinterpret_cast<LpPart*>(ws),
+           reinterpret_cast<float*>(ws + lp_sums_bytes(rows, sp.parts))};
   return hip_status(launch_token_logprobs(a, (int)dtype, as_stream(stream)));
 }
 

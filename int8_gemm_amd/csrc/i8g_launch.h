@@ -208,24 +208,27 @@ int checkpoint_cols_parts(int64_t rows);
 hipError_t launch_checkpoint_cols(const Checkpoint& c, int8_t* Qt, int64_t ldqt, float* scale, void* parts,
                                   hipStream_t stream);
 
-struct LpPart {                // sums of one part of a row (see logprob.hip)
-  double s, t;
-  float m, unused;
+struct LpPart {                // sums of one part of a row (see logprob.hip); of a row of one part, for its best
+  double s, t;                 // tokens, its maximum and log S, and whether it is empty
+  float m;
+  int empty;
 };
 struct LpSplit {
   int parts, seg;              // parts of a row and columns of a part
+  int batches;                 // batches of a row
+  size_t tops;                 // maxima that a row leaves, with topk
 };
 LpSplit lp_split(int64_t rows, int64_t cols);
 struct LpArgs {
   const void* X;
   int64_t rows, cols, ldx;
   const int64_t* targets;
-  int parts, seg, topk;
+  int parts, seg, batches, topk;
   float *logprob, *entropy, *lse;   // may be null
   int32_t* top_index;
   float* top_logprob;
-  LpPart* sums;                // [rows][parts], with more than one part
-  unsigned long long* cands;   // [rows][parts][topk], with more than one part
+  LpPart* sums;                // [rows][parts], with topk or more than one part
+  float* tops;                 // [rows][LpSplit::tops], with topk
 };
 hipError_t launch_token_logprobs(const LpArgs& a, int dtype, hipStream_t stream);
 struct LpBwdArgs {

@@ -10,6 +10,7 @@
 // are rescaled when the maximum grows; threads and parts are joined in
 // binary64.  Both directions are bound by reading the logits (and writing the
 // gradient); the exponential's ~20 operations a value are next.
+#include "../../include/int8_gemm.h"
 #include "i8g_launch.h"
 #include "i8g_row.h"
 
@@ -17,9 +18,11 @@ namespace i8g {
 namespace {
 
 constexpr int kThreads = 512;                 // of a workgroup of the forward pass
-constexpr int kValues = 128;                  // values of a thread at most
-constexpr int kSegMax = kThreads * kValues;   // columns of a part at most
+constexpr int kBatch = kThreads * 16;         // columns of a batch: 16 values a thread
+constexpr int kPartBatches = 8;               // batches of a part at most: 128 values a thread
 constexpr int kMaxParts = 64;                 // parts of a row at most (a wave joins them)
+constexpr int kTops = kThreads / 8;           // maxima that a batch leaves, of 8 threads each (kGroup values)
+constexpr int kGroup = 128;
 constexpr int kTopMax = 32;
 constexpr float kLowest = -3.40282347e38f;    // the running maximum's start: finite, so x - m is never NaN for finite x or -inf
 
@@ -42,6 +45,12 @@ __device__ __forceinline__ float rank_value(uint32_t key) {
 }
 // The largest of a wave's (never NaN) values.
 __device__ __forceinline__ float wave_max(float x) { return rank_value(lanes_max_u32<64>(rank_key(x))); }
+// The largest of 8 lanes' values, NaN aside.
+__device__ __forceinline__ float lanes8_max(float x) {
+  x = fmaxf(x, __uint_as_float(lane_partner<1>(__float_as_uint(x))));
+  x = fmaxf(x, __uint_as_float(lane_partner<2>(__float_as_uint(x))));
+  return fmaxf(x, __uint_as_float(lane_partner<4>(__float_as_uint(x))));
+}
 // Larger for the larger value, then for the lower index.
 __device__ __forceinline__ uint64_t candidate(uint32_t key, uint32_t index) {
   return (uint64_t)key << 32 | (0xFFFFFFFFu - index);
@@ -79,182 +88,32 @@ __device__ __forceinline__ void write_row(const LpArgs& a, int64_t r, const Part
   }
 }
 
-// The k best of n candidates in LDS, best first: a candidate's place is the
-// number of better ones.  Four lanes count for each, 8 at a time so that the
-// reads overlap, until they know that it is not among the best.  `list` has
-// room for kPad more, which the caller has set to 0 (pad_list).
-constexpr int kPad = 31;
-__device__ __forceinline__ void pad_list(unsigned long long* list, int n) {
-  if (threadIdx.x < kPad) list[n + threadIdx.x] = 0;
-}
-__device__ __forceinline__ void place_best(const unsigned long long* list, int n, int k, unsigned long long* best,
-                                           int thread, int threads) {
-  const int part = thread & 3;
-  for (int i = thread >> 2; i < n; i += threads >> 2) {
-    const unsigned long long mine = list[i];
-    int above = 0;
-    for (int j = part * 8; j < n && above < k; j += 32) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) above += list[j + e] > mine ? 1 : 0;
-    }
-    above += lane_partner<1>(above);
-    above += lane_partner<2>(above);
-    if (part == 0 && above < k && mine != 0) best[above] = mine;
-  }
-}
-
-// LDS of the search for the best alternatives.
-struct TopLds {
-  uint32_t key[kThreads];                     // the largest key of each thread
-  unsigned long long list[(kTopMax - 1) * kValues + 1024 + kPad];
-  unsigned long long best[kTopMax];
-  int lane_of[kTopMax - 1 + 32];
-  int wave_count[kThreads / 64];
-  uint32_t bar;
-  int n_above, n_equal, n_cand, n_cand_equal;
+// The sum over a workgroup of the waves' (s, t) against their maxima.
+template <int WAVES>
+struct SumLds {
+  double s[WAVES], t[WAVES];
+  float m[WAVES];
 };
 
-// The min(k, values) best of a part's values into l.best (unused places 0).
-// The k-th largest of the threads' maxima is a bar that at least k values
-// reach, and values above it are only in the fewer than k threads whose
-// maximum is above it: those threads' values are read again (from cache),
-// with those of the threads whose maximum is the bar itself.  If that many
-// values equal the bar that they would not fit (masked rows), the ones of
-// lowest index are found by a scan from the part's start.
-template <class T>
-__device__ __forceinline__ void find_best(TopLds& l, const T* row, int lo, int hi, float mx, int k) {
-  constexpr int N = kVec<T>, NV = kValues / N;
-  constexpr int kAbove = (kTopMax - 1) * kValues;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const uint32_t mine = rank_key(mx);
-  l.key[tid] = mine;
-  if (tid < kTopMax) l.best[tid] = 0;
-  if (tid == 0) l.n_above = l.n_equal = l.n_cand = l.n_cand_equal = 0;
-  __syncthreads();
-  if (wave == 0) {                            // the largest bar that k threads reach, bit by bit
-    uint32_t key[kThreads / 64];
-#pragma unroll
-    for (int j = 0; j < kThreads / 64; ++j) key[j] = l.key[lane + 64 * j];
-    uint32_t bar = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t b = bar | 1u << bit;
-      int n = 0;
-#pragma unroll
-      for (int j = 0; j < kThreads / 64; ++j) n += __popcll(__ballot(key[j] >= b));
-      if (n >= k) {
-        bar = b;
-        if (n == k) break;
-      }
-    }
-    if (lane == 0) l.bar = bar;
-  }
-  __syncthreads();
-  const uint32_t bar = l.bar;
-  if (mine > bar) l.lane_of[atomicAdd(&l.n_above, 1)] = tid;      // fewer than k
-  __syncthreads();
-  const int n_above = l.n_above;
-  if (mine == bar) {
-    const int i = atomicAdd(&l.n_equal, 1);
-    if (i < 32) l.lane_of[n_above + i] = tid;
-  }
-  __syncthreads();
-  const bool few = l.n_equal <= 32;
-  const int n_lanes = n_above + (few ? l.n_equal : 0);
-  for (int i = tid / NV; i < n_lanes; i += kThreads / NV) {       // NV lanes read a thread's vectors
-    const int c = lo + (l.lane_of[i] + kThreads * (tid % NV)) * N;
-    if (c >= hi) continue;
-    float v[N];
-    load_row<T>(row, c, hi, 0.0f, v);
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      if (c + e >= hi) continue;
-      const uint32_t key = rank_key(v[e]);
-      if (key > bar) {
-        l.list[atomicAdd(&l.n_cand, 1)] = candidate(key, c + e);
-      } else if (key == bar) {
-        const int at = atomicAdd(&l.n_cand_equal, 1);
-        if (at < 1024) l.list[kAbove + at] = candidate(key, c + e);
-      }
-    }
-  }
-  __syncthreads();
-  int n = l.n_cand, n_eq = l.n_cand_equal;
-  if (n >= k) n_eq = 0;
-  if (n < k && (!few || n_eq > 1024)) {
-    // the values that equal the bar, from the part's start
-    const int need = k - n;
-    n_eq = 0;
-    for (int base = lo; base < hi && n_eq < need; base += kThreads * N) {
-      const int c = base + tid * N;
-      float v[N];
-      unsigned int hit = 0;
-      if (c < hi) {
-        load_row<T>(row, c, hi, 0.0f, v);
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-          if (c + e < hi && rank_key(v[e]) == bar) hit |= 1u << e;
-      }
-      int before = __popc(hit);               // inclusive sum over the lanes, then exclusive
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int o = __shfl_up(before, off, 64);
-        if (lane >= off) before += o;
-      }
-      if (lane == 63) l.wave_count[wave] = before;
-      before -= __popc(hit);
-      __syncthreads();
-      int total = 0;
-      for (int w = 0; w < kThreads / 64; ++w) {
-        if (w < wave) before += l.wave_count[w];
-        total += l.wave_count[w];
-      }
-      before += n_eq;
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (hit >> e & 1u) {
-          if (before < need) l.list[kAbove + before] = candidate(bar, c + e);
-          ++before;
-        }
-      n_eq += total;
-      __syncthreads();
-    }
-    n_eq = n_eq < need ? n_eq : need;
-  }
-  // one list: the equal ones behind the ones above
-  unsigned long long moved[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int at = tid + i * kThreads;
-    moved[i] = at < n_eq ? l.list[kAbove + at] : 0;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int at = tid + i * kThreads;
-    if (at < n_eq) l.list[n + at] = moved[i];
-  }
-  pad_list(l.list, n + n_eq);
-  __syncthreads();
-  place_best(l.list, n + n_eq, k, l.best, tid, kThreads);
-  __syncthreads();
-}
-
+// A pass over the logits: the sums of each part of a row, and with TOP the
+// maxima of every 8 threads' values of a batch, from which lp_find_kernel or
+// lp_join_kernel find the best.  (The values of 8 threads are whole cache
+// lines; with a maximum for each thread over all its batches, which are as
+// many, reading the best threads' values again took 33 us of 8192 x 50304 f32
+// with 4 alternatives, and finding them inside this kernel, whose registers
+// and LDS then leave a third of the waves, 50 us, in bf16 117 us.)
 template <class T, bool TOP>
 __global__ void __launch_bounds__(kThreads) lp_part_kernel(LpArgs a) {
   constexpr int N = kVec<T>, U = 16 / N;      // vectors of a batch: 16 values
-  __shared__ double red_s[kThreads / 64], red_t[kThreads / 64];
-  __shared__ float red_m[kThreads / 64];
-  __shared__ __attribute__((aligned(16))) char top_bytes[TOP ? sizeof(TopLds) : 16];
-  TopLds& top = *reinterpret_cast<TopLds*>(top_bytes);
-  __shared__ double row_m, row_l;
-  __shared__ int row_empty;
+  constexpr int WAVES = kThreads / 64;
+  __shared__ SumLds<WAVES> red;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int part = blockIdx.x, lo = part * a.seg;
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
     const int64_t task = r * a.parts + part;
     const int hi = lo + a.seg < a.cols ? lo + a.seg : (int)a.cols;
     const T* row = static_cast<const T*>(a.X) + r * a.ldx;
-    float m = kLowest, mx = -__builtin_inff(), s = 0.0f, t = 0.0f;
+    float m = kLowest, s = 0.0f, t = 0.0f;
     for (int base = lo; base < hi; base += kThreads * N * U) {
       float v[U][N];
 #pragma unroll
@@ -264,7 +123,10 @@ __global__ void __launch_bounds__(kThreads) lp_part_kernel(LpArgs a) {
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int e = 0; e < N; ++e) b = fmaxf(b, v[u][e]);
-      mx = fmaxf(mx, b);
+      if constexpr (TOP) {
+        const float top = lanes8_max(b);
+        if ((tid & 7) == 0) a.tops[(r * a.batches + base / kBatch) * kTops + (tid >> 3)] = top;
+      }
       if (b > m) {
         rescale(s, t, m, b);
         m = b;
@@ -281,66 +143,294 @@ __global__ void __launch_bounds__(kThreads) lp_part_kernel(LpArgs a) {
     }
     // join the threads
     float mm = wave_max(m);
-    if (lane == 0) red_m[wave] = mm;
+    if (lane == 0) red.m[wave] = mm;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) mm = fmaxf(mm, red_m[w]);
+    for (int w = 0; w < WAVES; ++w) mm = fmaxf(mm, red.m[w]);
     rescale(s, t, m, mm);
     const double ws = wave_sum_f64((double)s), wt = wave_sum_f64((double)t);
     if (lane == 0) {
-      red_s[wave] = ws;
-      red_t[wave] = wt;
+      red.s[wave] = ws;
+      red.t[wave] = wt;
     }
     __syncthreads();
-    PartSum p{0.0, 0.0, mm};
+    if (tid == 0) {
+      PartSum p{0.0, 0.0, mm};
 #pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) {
-      p.s += red_s[w];
-      p.t += red_t[w];
-    }
-    if (a.parts > 1) {
-      if (tid == 0) a.sums[task] = LpPart{p.s, p.t, p.m, 0.0f};
-      if constexpr (TOP) {
-        find_best<T>(top, row, lo, hi, mx, a.topk);
-        if (tid < a.topk) a.cands[task * a.topk + tid] = top.best[tid];
+      for (int w = 0; w < WAVES; ++w) {
+        p.s += red.s[w];
+        p.t += red.t[w];
       }
-    } else {
-      if (tid == 0) {
+      if (a.parts > 1) {
+        a.sums[task] = LpPart{p.s, p.t, p.m, 0};
+      } else {
         const RowOut o(p);
         write_row<T>(a, r, p, o);
-        row_m = o.m;
-        row_l = o.log_s;
-        row_empty = o.empty;
-      }
-      if constexpr (TOP) {
-        find_best<T>(top, row, lo, hi, mx, a.topk);
-        if (tid < a.topk) {
-          const unsigned long long c = top.best[tid];
-          const float v = rank_value((uint32_t)(c >> 32));
-          a.top_index[r * a.topk + tid] = (int32_t)(0xFFFFFFFFu - (uint32_t)c);
-          a.top_logprob[r * a.topk + tid] = row_empty ? -__builtin_inff() : (float)((double)v - row_m - row_l);
-        }
+        if constexpr (TOP) a.sums[task] = LpPart{o.m, o.log_s, 0.0f, o.empty};
       }
     }
     __syncthreads();                          // LDS is used again
   }
 }
 
-// Joins the parts of a row: wave 0 their sums, the other waves their best.
-constexpr int kJoinThreads = 1024;
+// The k best of n candidates in LDS, best first: a candidate's place is the
+// number of better ones.  Four lanes count for each, 8 at a time so that the
+// reads overlap, until they know that it is not among the best.  `list` has
+// room for kPad more, which hold 0.
+constexpr int kPad = 31;
+__device__ __forceinline__ void place_best(const unsigned long long* list, int n, int k, unsigned long long* best,
+                                           int thread, int threads) {
+  const int part = thread & 3;
+  for (int i = thread >> 2; i < n; i += threads >> 2) {
+    const unsigned long long mine = list[i];
+    int above = 0;
+    for (int j = part * 8; j < n && above < k; j += 32) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) above += list[j + e] > mine ? 1 : 0;
+    }
+    above += lane_partner<1>(above);
+    above += lane_partner<2>(above);
+    if (part == 0 && above < k && mine != 0) best[above] = mine;
+  }
+}
+
+// What one wave wrote to LDS may be read by its other lanes behind this.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// The number of the lane among the set bits of a ballot.
+__device__ __forceinline__ int lane_rank(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+}
+
+// LDS of one wave's search.
+constexpr int kAbove = 256;                   // values above the bar
+constexpr int kEqual = 64;                    // and values that equal it, before they are scanned for
+constexpr int kSame = 32;                     // groups whose maximum equals the bar, likewise
+struct FindLds {
+  unsigned long long list[kAbove + kEqual + kPad];
+  unsigned short again[kTopMax + kSame];      // groups to read again
+  int n_above, n_equal;                       // values noted, above the bar and equal to it
+};
+constexpr int kChunk = 8 * kBatch;            // columns that one wave searches: 512 groups, 8 a lane
+
+// The min(k, columns) best of columns [lo, lo + kChunk) of a row by one wave,
+// into best[0 .. k) (unused places 0), from the maxima of its groups.  The
+// k-th largest of the maxima is a bar that at least k values reach, and values
+// above it are only in the at most k groups whose maximum is above it: those
+// groups are read again, with those whose maximum is the bar itself.  If more
+// values are above the bar than fit (many in few groups), the bar is raised;
+// if so many equal it that they do not fit (masked rows), the ones of lowest
+// index are found by a scan from `lo`.
 template <class T>
-__global__ void __launch_bounds__(kJoinThreads) lp_join_kernel(LpArgs a) {
-  __shared__ unsigned long long list[kMaxParts * kTopMax + kPad];
+__device__ __forceinline__ void wave_best(const LpArgs& a, const T* row, const float* tops, int lo, FindLds& l,
+                                          unsigned long long* best) {
+  constexpr int N = kVec<T>, K = 8;
+  constexpr int VECS = kGroup / N;            // vectors of a group, 8 side by side
+  constexpr int U = 16 / N;                   // of a lane in flight
+  const int lane = threadIdx.x & 63, k = a.topk;
+  const int hi = lo + kChunk < a.cols ? lo + kChunk : (int)a.cols;
+  const int n_tops = (hi - lo + kBatch - 1) / kBatch * kTops;   // 64 to 512: at least k
+  unsigned long long* const equal = l.list + kAbove;
+  if (lane < k) best[lane] = 0;
+  uint32_t key[K], top = 0;
+#pragma unroll
+  for (int j = 0; j < K; ++j) key[j] = 64 * j < n_tops ? rank_key(tops[lane + 64 * j]) : 0;
+#pragma unroll
+  for (int j = 0; j < K; ++j) top = max(top, key[j]);
+  top = lanes_max_u32<64>(top);
+  // The largest bar that k groups reach, or one that exactly k reach: steps
+  // down from the largest key, 4 times as far each, then halving.  (A group
+  // without values has the key of -inf, so 1 is reached by all.)
+  uint32_t bar = 0, over = top + 1;           // reached by at least k, by fewer
+  int n = 0;
+  auto reach = [&](uint32_t b) __attribute__((always_inline)) {
+    int c = 0;
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (64 * j < n_tops) c += __popcll(__ballot(key[j] >= b));
+    return c;
+  };
+  for (int shift = 20; shift < 32; shift += 2) {
+    const uint32_t b = top > 1u << shift ? top - (1u << shift) : 1;
+    n = reach(b);
+    if (n >= k) {
+      bar = b;
+      break;
+    }
+    over = b;
+  }
+  while (n != k && over - bar > 1) {
+    const uint32_t b = bar + (over - bar) / 2;
+    const int nb = reach(b);
+    if (nb >= k) {
+      bar = b;
+      n = nb;
+    } else {
+      over = b;
+    }
+  }
+  // the groups to read again: above the bar (at most k), then at it
+  int n_again = 0, n_same = 0;
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    const uint64_t mask = __ballot(key[j] > bar);
+    if (key[j] > bar) l.again[n_again + lane_rank(mask)] = (unsigned short)(lane + 64 * j);
+    n_again += __popcll(mask);
+    n_same += __popcll(__ballot(key[j] == bar));
+  }
+  const bool few = n_same <= kSame;
+  if (few) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      const uint64_t mask = __ballot(key[j] == bar);
+      if (key[j] == bar) l.again[n_again + lane_rank(mask)] = (unsigned short)(lane + 64 * j);
+      n_again += __popcll(mask);
+    }
+  }
+  wave_sync();
+  // Their values: those above b counted (n_above), and those equal to it
+  // (n_equal); with `keep` noted as well, as many as fit, in any order.
+  int n_above = 0, n_equal = 0;
+  auto scan = [&](uint32_t b, bool keep) __attribute__((always_inline)) {
+    if (lane == 0) l.n_above = l.n_equal = 0;
+    wave_sync();
+    const int vecs = n_again * VECS;
+    const float low = rank_value(b);
+    for (int base = 0; base < vecs; base += 64 * U) {
+      float v[U][N];
+      int c[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = base + u * 64 + lane;
+        c[u] = hi;                            // (nothing is read there)
+        if (i < vecs) {
+          const int g = l.again[i / VECS], s = i % VECS;
+          c[u] = lo + g / kTops * kBatch + ((s >> 3) * kThreads + g % kTops * 8 + (s & 7)) * N;
+        }
+        load_row<T>(row, c[u], hi, -__builtin_inff(), v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          if (v[u][e] < low || c[u] + e >= hi) continue;          // (a NaN may count as -inf)
+          const uint32_t x = rank_key(v[u][e]);
+          if (x > b) {
+            const int i = atomicAdd(&l.n_above, 1);
+            if (keep && i < kAbove) l.list[i] = candidate(x, c[u] + e);
+          } else if (x == b) {
+            const int i = atomicAdd(&l.n_equal, 1);
+            if (keep && i < kEqual) equal[i] = candidate(x, c[u] + e);
+          }
+        }
+    }
+    wave_sync();
+    n_above = __builtin_amdgcn_readfirstlane(l.n_above);
+    n_equal = __builtin_amdgcn_readfirstlane(l.n_equal);
+    wave_sync();
+  };
+  scan(bar, true);
+  if (n_above > kAbove) {                     // halving up to a bar with at least k values at or above it
+    over = top + 1;
+    while (n_above > kAbove && over - bar > 1) {
+      const uint32_t b = bar + (over - bar) / 2;
+      const int was = n_above;
+      scan(b, false);
+      if (n_above + n_equal >= k) {
+        bar = b;
+      } else {
+        over = b;
+        n_above = was;                        // (of the bar that stays)
+      }
+    }
+    scan(bar, true);
+  }
+  wave_sync();
+  n = n_above;
+  int n_eq = n < k ? n_equal : 0;
+  if (n < k && (!few || n_eq > kEqual)) {
+    const int need = k - n;
+    n_eq = 0;
+    for (int base = lo; base < hi && n_eq < need; base += 64 * N) {
+      const int c = base + lane * N;
+      float v[N];
+      load_row<T>(row, c, hi, 0.0f, v);
+      unsigned int hit = 0;
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (c + e < hi && rank_key(v[e]) == bar) hit |= 1u << e;
+      int before = __popc(hit);               // inclusive sum over the lanes
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(before, off, 64);
+        if (lane >= off) before += o;
+      }
+      const int total = __shfl(before, 63, 64);
+      before += n_eq - __popc(hit);
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (hit >> e & 1u) {
+          if (before < need) equal[before] = candidate(bar, c + e);
+          ++before;
+        }
+      n_eq += total;
+    }
+    n_eq = n_eq < need ? n_eq : need;
+    wave_sync();
+  }
+  // one list: the equal ones behind the ones above, and padding
+  static_assert(kEqual == 64, "one of them a lane");
+  const unsigned long long moved = lane < n_eq ? equal[lane] : 0;
+  wave_sync();
+  if (lane < n_eq) l.list[n + lane] = moved;
+  n += n_eq;
+  if (lane < kPad) l.list[n + lane] = 0;
+  wave_sync();
+  place_best(l.list, n, k, best, lane, 64);
+  wave_sync();
+}
+
+// The best of a row in their order, by `tid` < topk.
+__device__ __forceinline__ void write_best(const LpArgs& a, int64_t r, int tid, unsigned long long c, double m,
+                                           double log_s, bool empty) {
+  const float v = rank_value((uint32_t)(c >> 32));
+  a.top_index[r * a.topk + tid] = (int32_t)(0xFFFFFFFFu - (uint32_t)c);
+  a.top_logprob[r * a.topk + tid] = empty ? -__builtin_inff() : (float)((double)v - m - log_s);
+}
+
+// Rows of one part: a wave a row.
+template <class T>
+__global__ void __launch_bounds__(64, 8) lp_find_kernel(LpArgs a) {
+  __shared__ FindLds lds;
+  __shared__ unsigned long long best[kTopMax];
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const LpPart q = a.sums[r];                 // the row's maximum and log S
+    wave_best<T>(a, static_cast<const T*>(a.X) + r * a.ldx, a.tops + r * a.batches * kTops, 0, lds, best);
+    if ((int)threadIdx.x < a.topk) write_best(a, r, threadIdx.x, best[threadIdx.x], q.s, q.t, q.empty != 0);
+    wave_sync();
+  }
+}
+
+// Rows of several parts: wave 0 joins the sums while the others find the best
+// of each chunk, and all of them the best of those.
+constexpr int kFinders = 15;
+constexpr int kMaxChunks = I8G_VOCAB_MAX / kChunk;
+template <class T>
+__global__ void __launch_bounds__(64 * (kFinders + 1)) lp_join_kernel(LpArgs a) {
+  __shared__ FindLds lds[kFinders];
+  __shared__ unsigned long long list[kMaxChunks * kTopMax + kPad];
   __shared__ unsigned long long best[kTopMax];
   __shared__ double row_m, row_l;
   __shared__ int row_empty;
-  const int tid = threadIdx.x, n = a.parts * a.topk;
+  static_assert(sizeof(lds) + sizeof(list) + sizeof(best) + 64 <= 65536, "a workgroup's LDS");
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int chunks = (a.batches + 7) / 8, n = chunks * a.topk;
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
-    for (int i = tid; i < n; i += kJoinThreads) list[i] = a.cands[r * n + i];
-    pad_list(list, n);
-    __syncthreads();
-    if (tid < 64) {
-      LpPart q{0.0, 0.0, kLowest, 0.0f};
+    if (wave == 0) {
+      LpPart q{0.0, 0.0, kLowest, 0};
       if (tid < a.parts) q = a.sums[r * a.parts + tid];
       const float mm = wave_max(q.m);
       double d = (double)q.m - (double)mm;
@@ -357,15 +447,17 @@ __global__ void __launch_bounds__(kJoinThreads) lp_join_kernel(LpArgs a) {
         row_l = o.log_s;
         row_empty = o.empty;
       }
-    } else {
-      place_best(list, n, a.topk, best, tid - 64, kJoinThreads - 64);
+      if (lane < kPad) list[n + lane] = 0;
+    } else if (a.topk > 0) {
+      for (int c = wave - 1; c < chunks; c += kFinders)
+        wave_best<T>(a, static_cast<const T*>(a.X) + r * a.ldx, a.tops + (r * a.batches + c * 8) * kTops, c * kChunk,
+                     lds[wave - 1], list + c * a.topk);
     }
     __syncthreads();
-    if (tid < a.topk) {
-      const unsigned long long c = best[tid];
-      const float v = rank_value((uint32_t)(c >> 32));
-      a.top_index[r * a.topk + tid] = (int32_t)(0xFFFFFFFFu - (uint32_t)c);
-      a.top_logprob[r * a.topk + tid] = row_empty ? -__builtin_inff() : (float)((double)v - row_m - row_l);
+    if (a.topk > 0) {
+      place_best(list, n, a.topk, best, tid, 64 * (kFinders + 1));
+      __syncthreads();
+      if (tid < a.topk) write_best(a, r, tid, best[tid], row_m, row_l, row_empty);
     }
     __syncthreads();                          // LDS is used again
   }
@@ -377,35 +469,45 @@ template <class T, bool STREAM>
 __global__ void __launch_bounds__(256) lp_bwd_kernel(LpBwdArgs a) {
   constexpr int N = kVec<T>, U = kGradVecs;
   constexpr int CHUNK = 256 * N * U;
-  const int64_t c0 = (int64_t)blockIdx.x * CHUNK + (int64_t)threadIdx.x * N;
+  const int cols = (int)a.cols, c0 = (int)blockIdx.x * CHUNK + (int)threadIdx.x * N;
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
     const T* x = static_cast<const T*>(a.X) + r * a.ldx;
     T* dx = static_cast<T*>(a.dX) + r * a.lddx;
-    const float lse = a.lse[r];
-    int64_t t = a.g_logprob ? a.targets[r] : -1;
-    if (t >= a.cols) t = -1;
-    const float g = t >= 0 ? a.g_logprob[r] : 0.0f;
-    const float gh = a.g_entropy ? a.g_entropy[r] : 0.0f;
-    const float h = a.g_entropy ? a.entropy[r] : 0.0f;
-    const bool empty = fabsf(lse) >= 16777216.0f;   // -inf, or so far out that lse is off by 1 and more
     float v[U][N];
 #pragma unroll
-    for (int u = 0; u < U; ++u) load_row<T>(x, c0 + u * 256 * N, a.cols, 0.0f, v[u]);
+    for (int u = 0; u < U; ++u) load_row<T>(x, c0 + u * 256 * N, cols, 0.0f, v[u]);
+    // dx_j = -p_j (g + gh (log p_j + H)) = p_j (nh log p_j + n0), and + g for the token
+    float lse = a.lse[r], g = 0.0f, n0 = 0.0f, nh = 0.0f;
+    int t = -1;
+    if (fabsf(lse) >= 16777216.0f) {          // -inf, or so far out that lse is off by 1 and more: p = 0
+      lse = __builtin_inff();
+    } else {
+      if (a.g_logprob) {
+        const int64_t token = a.targets[r];
+        if (token >= 0 && token < a.cols) {
+          t = (int)token;
+          g = a.g_logprob[r];
+        }
+      }
+      if (a.g_entropy) nh = -a.g_entropy[r];
+      n0 = a.g_entropy ? __builtin_fmaf(nh, a.entropy[r], -g) : -g;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t c = c0 + u * 256 * N;
+      const int c = c0 + u * 256 * N;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const float lp = __builtin_elementwise_maximum(v[u][e] - lse, -104.0f);   // p is 0 there, and p * lp as well
-        const float p = exp_f32(lp);
-        float d = -p * (g + gh * (lp + h));
-        if (c + e == t) d += g;
-        v[u][e] = empty ? 0.0f : d;
+        v[u][e] = exp_f32(lp) * __builtin_fmaf(nh, lp, n0);
+      }
+      if (t >= c && t < c + N) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[u][e] += t == c + e ? g : 0.0f;
       }
       if constexpr (STREAM)
-        stream_row<T>(dx, c, a.cols, v[u]);
+        stream_row<T>(dx, c, cols, v[u]);
       else
-        store_row<T>(dx, c, a.cols, v[u]);
+        store_row<T>(dx, c, cols, v[u]);
     }
   }
 }
@@ -420,7 +522,12 @@ hipError_t forward(const LpArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((lp_part_kernel<T, true>), grid, block, 0, stream, a);
   else
     hipLaunchKernelGGL((lp_part_kernel<T, false>), grid, block, 0, stream, a);
-  if (a.parts > 1) hipLaunchKernelGGL((lp_join_kernel<T>), dim3(1, row_grid(a.rows)), dim3(kJoinThreads), 0, stream, a);
+  if (a.parts > 1) {
+    hipLaunchKernelGGL((lp_join_kernel<T>), dim3(1, row_grid(a.rows)), dim3(64 * (kFinders + 1)), 0, stream, a);
+  } else if (a.topk > 0) {
+    const int64_t most = int64_t(1) << 20;
+    hipLaunchKernelGGL((lp_find_kernel<T>), dim3((unsigned int)(a.rows < most ? a.rows : most)), dim3(64), 0, stream, a);
+  }
   return hipGetLastError();
 }
 
@@ -438,16 +545,16 @@ hipError_t backward(const LpBwdArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// Parts of a row: as many as its length needs, and with few rows as many as
-// fill the chip, each of a batch of 16 values a thread (8192 columns) or more.
+// Parts of a row, of whole batches: as many as its length needs, and with few
+// rows as many as fill the chip.
 LpSplit lp_split(int64_t rows, int64_t cols) {
-  int64_t parts = (cols + kSegMax - 1) / kSegMax;
+  const int64_t batches = (cols + kBatch - 1) / kBatch;
+  const int64_t need = (batches + kPartBatches - 1) / kPartBatches;
   const int64_t fill = rows >= 512 ? 1 : (512 + rows - 1) / rows;
-  int64_t most = (cols + 16 * kThreads - 1) / (16 * kThreads);
-  most = most < kMaxParts ? most : kMaxParts;
-  if (parts < fill) parts = fill < most ? fill : most > parts ? most : parts;
-  const int64_t seg = ((cols + parts - 1) / parts + 63) / 64 * 64;
-  return LpSplit{(int)((cols + seg - 1) / seg), (int)seg};
+  int64_t parts = fill < need ? need : fill < batches ? fill : batches;
+  if (parts > kMaxParts) parts = kMaxParts;
+  const int64_t each = (batches + parts - 1) / parts;
+  return LpSplit{(int)((batches + each - 1) / each), (int)(each * kBatch), (int)batches, (size_t)batches * kTops};
 }
 
 hipError_t launch_token_logprobs(const LpArgs& a, int dtype, hipStream_t stream) {

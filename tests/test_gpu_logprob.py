@@ -106,6 +106,12 @@ def hard_rows(vocab, dt, rng):
     v = normal()
     v[(np.arange(vocab) // (16 // dt.itemsize)) % 512 < 3] += 20
     rows["one thread's columns"] = v
+    v = normal()
+    v[(np.arange(vocab) // (16 // dt.itemsize)) % 512 // 8 < 2] += 30
+    rows["few groups' columns"] = v
+    v = normal()
+    v[(np.arange(vocab) // (16 // dt.itemsize)) % 512 // 8 < 2] = 30
+    rows["few groups' columns equal"] = v
     v = rng.standard_normal(vocab) * 0.01
     v[(np.arange(vocab) // (16 // dt.itemsize)) % 512 == 511] = 4.0
     rows["one thread's columns equal"] = v

@@ -107,7 +107,7 @@ def test_workspace_sizes(lib):
     for cols in (5, 768, 5000):
         sizes = [lib.layer_norm_bwd_workspace_bytes(r, cols) for r in (1, 2, 4, 5, 100, 8192, 1 << 30)]
         assert sizes == sorted(sizes)
-    for args in ((0, 5, 1), (5, 0, 1), (-1, 5, 1), (5, 5, -1), (5, 5, 33), (5, 1 << 30, 1)):
+    for args in ((0, 5, 1), (5, 0, 1), (-1, 5, 1), (5, 5, -1), (5, 5, 33), (5, 1 << 30, 1), (5, 5, 0), (5000, 50257, 0)):
         assert lib.token_logprobs_workspace_bytes(*args) == 0
 
 
