@@ -1,6 +1,7 @@
 """Python binding of libint8_gemm.so (bit-reproducible block-scaled int8 GEMM).
 
-Argument marshalling only: every step of the method runs in the library's
+Argument marshalling only (with ctypes, for the operators between the GEMMs
+in rowops_bind.so): every step of the method runs in the library's
 HIP kernels.  PyTorch provides device memory and the current stream.  The
 entry points have the names of the C ABI in ``include/int8_gemm.h``:
 
@@ -538,256 +539,93 @@ def blockscaled_gemm(A, B, relu=False, want_hash=False):
 
 
 # ---- the operators between the GEMMs --------------------------------------
+# Their statements (checks, outputs, scratch, the C call on torch's current
+# stream of the first tensor's device) are in csrc/rowops_bind.cpp: made in
+# Python they took longer than the kernels.  Matrices are 2-D with unit column
+# stride and rows that do not overlap; vectors are contiguous f32.
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _ACTS = {"relu": 1, "gelu": 2}
+_ROWOPS = ("layer_norm", "layer_norm_quantize_rows", "layer_norm_bwd", "layer_norm_bwd_workspace_bytes",
+           "layer_norm_bwd_checkpoint", "checkpoint_i8", "checkpoint_restore", "checkpoint_act_bwd",
+           "checkpoint_quantize_cols", "checkpoint_quantize_cols_workspace_bytes", "token_logprobs",
+           "token_logprobs_workspace_bytes", "token_logprobs_bwd")
+_bind = None
 
 
-def _values(x, name, like=None):
-    """(rows, cols, ld) of a 2-D matrix of f32, bf16 or f16 values (of the
-    dtype and device of `like`, if given)."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D tensor")
-    if x.dtype not in _DTYPES:
-        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {x.dtype}")
-    if like is not None and (x.dtype != like.dtype or x.shape != like.shape):
-        raise ValueError(f"{name} must have the dtype and shape of the other values: "
-                         f"{like.dtype} {tuple(like.shape)}, got {x.dtype} {tuple(x.shape)}")
-    return _layout(x, name, like)
-
-
-def _layout(x, name, like=None):
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be on a GPU")
-    if like is not None and x.get_device() != like.get_device():
-        raise ValueError(f"{name} must be on {like.device}, got {x.device}")
-    rows, cols = x.shape
-    if cols > 1 and rows > 0 and x.stride(1) != 1:
-        raise ValueError(f"{name} must be row-major (unit column stride)")
-    if rows > 1 and x.stride(0) < cols:
-        raise ValueError(f"{name} has overlapping rows (expanded?): call .contiguous() first")
-    return rows, cols, x.stride(0) if rows > 1 else max(cols, 1)
-
-
-def _vector(x, n, name, like, optional=False):
-    """The address of a contiguous f32 vector of n values."""
-    if x is None and optional:
-        return None
-    if not isinstance(x, torch.Tensor) or x.dtype != torch.float32 or x.dim() != 1 or x.numel() != n:
-        raise ValueError(f"{name} must be a 1-D float32 tensor of {n} values")
-    if x.get_device() != like.get_device():
-        raise ValueError(f"{name} must be on {like.device}, got {x.device}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return x.data_ptr()
-
-
-def _enqueue(fn, like, *args):
-    """fn(*args, stream) on torch's current stream of like's device.  The
-    stream's handle is read without making a Stream object (1.9 us of a call
-    that takes 10)."""
-    dev = like.get_device()
-    stream = torch._C._cuda_getCurrentRawStream(dev)
-    if dev == torch.cuda.current_device():
-        rc = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, stream)
-    if rc:
-        _check(rc)
-
-
-def _like(x):
-    """An uninitialized contiguous matrix of x's shape and dtype."""
-    return torch.empty_like(x, memory_format=torch.contiguous_format)
+def _rowops():
+    """The binding of these operators, with the library's addresses (once)."""
+    global _bind
+    if _bind is None:
+        lib = load()
+        try:
+            from . import rowops_bind
+        except ImportError as e:
+            raise RuntimeError("rowops_bind.so is not built or cannot be loaded; run "
+                               "`python -m int8_gemm_amd.build`") from e
+        rowops_bind.init({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _ROWOPS},
+                         torch._C._cuda_getCurrentRawStream, _check)
+        _bind = rowops_bind
+    return _bind
 
 
 def layer_norm(X, weight=None, bias=None, eps=1e-5):
     """Layer norm of the rows of X: (Y, mean, rstd), Y of X's dtype; weight
     and bias are f32 (None: ones, zeros)."""
-    rows, cols, ldx = _values(X, "X")
-    w, b = _vector(weight, cols, "weight", X, True), _vector(bias, cols, "bias", X, True)
-    Y = _like(X)
-    stats = torch.empty((2, rows), dtype=torch.float32, device=X.device)
-    mean, rstd = stats.unbind(0)
-    _enqueue(load().layer_norm, X, X.data_ptr(), _DTYPES[X.dtype], rows, cols, ldx, w, b, eps, Y.data_ptr(),
-             max(cols, 1), mean.data_ptr(), rstd.data_ptr())
-    return Y, mean, rstd
+    return _rowops().layer_norm(X, weight, bias, eps)
 
 
 def layer_norm_quantize_rows(X, weight=None, bias=None, eps=1e-5):
     """quantize_rows of layer_norm's binary32 output: (Q, scale, mean, rstd)."""
-    rows, cols, ldx = _values(X, "X")
-    w, b = _vector(weight, cols, "weight", X, True), _vector(bias, cols, "bias", X, True)
-    Q = _int8_padded(rows, cols, X.device)
-    stats = torch.empty((3, rows), dtype=torch.float32, device=X.device)
-    scale, mean, rstd = stats.unbind(0)
-    _enqueue(load().layer_norm_quantize_rows, X, X.data_ptr(), _DTYPES[X.dtype], rows, cols, ldx, w, b, eps,
-             Q.data_ptr(), Q.stride(0), scale.data_ptr(), mean.data_ptr(), rstd.data_ptr())
-    return Q, scale, mean, rstd
-
-
-def _ln_grads(dY, cols, weight_grad):
-    """dX, dweight, dbias and their scratch (which lives as long as torch's
-    current stream needs it)."""
-    dX = _like(dY)
-    if not weight_grad:
-        return dX, None, None, None, 0
-    nbytes = load().layer_norm_bwd_workspace_bytes(dY.shape[0], cols)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dY.device)
-    dw, db = torch.empty((2, cols), dtype=torch.float32, device=dY.device).unbind(0)
-    return dX, dw, db, ws, nbytes
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
+    return _rowops().layer_norm_quantize_rows(X, weight, bias, eps)
 
 
 def layer_norm_bwd(dY, X, mean, rstd, weight=None, weight_grad=True):
     """(dX, dweight, dbias) for the gradient dY of layer_norm's output; the
     last two are None without weight_grad."""
-    rows, cols, lddy = _values(dY, "dY")
-    _, _, ldx = _values(X, "X", dY)
-    m, r, w = (_vector(mean, rows, "mean", dY), _vector(rstd, rows, "rstd", dY),
-               _vector(weight, cols, "weight", dY, True))
-    dX, dw, db, ws, nbytes = _ln_grads(dY, cols, weight_grad)
-    _enqueue(load().layer_norm_bwd, dY, dY.data_ptr(), lddy, X.data_ptr(), ldx, _DTYPES[dY.dtype], rows, cols, w,
-             m, r, dX.data_ptr(), max(cols, 1), _addr(dw), _addr(db), _addr(ws), nbytes)
-    return dX, dw, db
-
-
-def _checkpoint(Q, scale, group, shape=None, like=None):
-    """The leading arguments of the calls that read a checkpoint."""
-    if not isinstance(Q, torch.Tensor) or Q.dim() != 2 or Q.dtype != torch.int8:
-        raise ValueError("Q must be a 2-D int8 tensor")
-    if shape is not None and tuple(Q.shape) != tuple(shape):
-        raise ValueError(f"Q must have the shape {tuple(shape)}, got {tuple(Q.shape)}")
-    rows, cols, ldq = _layout(Q, "Q", like)
-    if group not in (0, 32, 64, 128, 256):
-        raise ValueError("group must be 32, 64, 128 or 256, or 0 for one scale per row")
-    groups = -(-cols // group) if group else min(cols, 1)
-    if not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32 or \
-            not (scale.shape == (rows, groups) or (group == 0 and scale.shape == (rows,))):
-        raise ValueError(f"scale must be a float32 tensor of shape ({rows}, {groups})"
-                         + (f" or ({rows},)" if group == 0 else ""))
-    if scale.get_device() != Q.get_device():
-        raise ValueError(f"scale must be on {Q.device}, got {scale.device}")
-    if groups > 1 and scale.stride(1) != 1:
-        raise ValueError("scale must be row-major (unit column stride)")
-    lds = scale.stride(0) if rows > 1 else max(groups, 1)
-    if lds < groups:
-        raise ValueError("scale has overlapping rows (expanded?): call .contiguous() first")
-    return Q.data_ptr(), ldq, scale.data_ptr(), lds, group, rows, cols
+    return _rowops().layer_norm_bwd(dY, X, mean, rstd, weight, weight_grad)
 
 
 def layer_norm_bwd_checkpoint(dY, Q, scale, group, mean, rstd, weight=None, weight_grad=True):
     """layer_norm_bwd with the input taken from its 8-bit checkpoint."""
-    rows, cols, lddy = _values(dY, "dY")
-    ck = _checkpoint(Q, scale, group, dY.shape, dY)
-    m, r, w = (_vector(mean, rows, "mean", dY), _vector(rstd, rows, "rstd", dY),
-               _vector(weight, cols, "weight", dY, True))
-    dX, dw, db, ws, nbytes = _ln_grads(dY, cols, weight_grad)
-    _enqueue(load().layer_norm_bwd_checkpoint, dY, dY.data_ptr(), lddy, _DTYPES[dY.dtype], *ck, w, m, r,
-             dX.data_ptr(), max(cols, 1), _addr(dw), _addr(db), _addr(ws), nbytes)
-    return dX, dw, db
+    return _rowops().layer_norm_bwd_checkpoint(dY, Q, scale, group, mean, rstd, weight, weight_grad)
 
 
 def checkpoint_i8(X, group=128):
     """An activation in 8 bits: (Q, scale) with one scale for each row and
     group of 32, 64, 128 or 256 columns."""
-    rows, cols, ldx = _values(X, "X")
-    if group not in (32, 64, 128, 256):
-        raise ValueError("group must be 32, 64, 128 or 256")
-    Q = _int8_padded(rows, cols, X.device)
-    groups = -(-cols // group)
-    scale = torch.empty((rows, groups), dtype=torch.float32, device=X.device)
-    _enqueue(load().checkpoint_i8, X, X.data_ptr(), _DTYPES[X.dtype], rows, cols, ldx, group, Q.data_ptr(),
-             Q.stride(0), scale.data_ptr(), max(groups, 1))
-    return Q, scale
+    return _rowops().checkpoint_i8(X, group)
 
 
 def checkpoint_restore(Q, scale, group, dtype=torch.float32):
     """The values of a checkpoint.  group 0: one scale per row, as
     quantize_rows and layer_norm_quantize_rows give them."""
-    ck = _checkpoint(Q, scale, group)
     if dtype not in _DTYPES:
         raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-    Y = torch.empty(Q.shape, dtype=dtype, device=Q.device)
-    _enqueue(load().checkpoint_restore, Q, *ck, Y.data_ptr(), _DTYPES[dtype], max(Q.shape[1], 1))
-    return Y
+    return _rowops().checkpoint_restore(Q, scale, group, _DTYPES[dtype])
 
 
 def checkpoint_act_bwd(dY, Q, scale, group, act="gelu"):
     """dX = dY * act'(x) at the checkpoint's values x; act is "relu" or
     "gelu" (the tanh form)."""
-    _, cols, lddy = _values(dY, "dY")
-    ck = _checkpoint(Q, scale, group, dY.shape, dY)
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
-    dX = _like(dY)
-    _enqueue(load().checkpoint_act_bwd, dY, *ck, _ACTS[act], dY.data_ptr(), lddy, dX.data_ptr(), max(cols, 1),
-             _DTYPES[dY.dtype])
-    return dX
+    return _rowops().checkpoint_act_bwd(dY, Q, scale, group, _ACTS[act])
 
 
 def checkpoint_quantize_cols(Q, scale, group):
     """quantize_cols of the checkpoint's values: (Qt, scale), the transposed
     operand of a weight gradient's GEMM."""
-    ck = _checkpoint(Q, scale, group)
-    rows, cols = Q.shape
-    Qt = _int8_padded(cols, rows, Q.device)
-    s = torch.empty(cols, dtype=torch.float32, device=Q.device)
-    nbytes = load().checkpoint_quantize_cols_workspace_bytes(rows, cols)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=Q.device)
-    _enqueue(load().checkpoint_quantize_cols, Q, *ck, Qt.data_ptr(), Qt.stride(0), s.data_ptr(), ws.data_ptr(), nbytes)
-    return Qt, s
-
-
-def _targets(t, rows, like):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int64 or t.dim() != 1 or t.numel() != rows:
-        raise ValueError(f"targets must be a 1-D int64 tensor of {rows} token numbers")
-    if t.get_device() != like.get_device():
-        raise ValueError(f"targets must be on {like.device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError("targets must be contiguous")
-    return t.data_ptr()
+    return _rowops().checkpoint_quantize_cols(Q, scale, group)
 
 
 def token_logprobs(logits, targets, topk=0):
     """(logprob, entropy, lse, top_index, top_logprob) of each row of logits:
     the log probability of its target (0 for a target outside the
     vocabulary), and its topk best tokens (None, None for topk 0)."""
-    rows, vocab, ld = _values(logits, "logits")
-    t = _targets(targets, rows, logits)
-    if topk < 0 or topk > 32 or (rows > 0 and topk > vocab):
-        raise ValueError(f"topk must be between 0 and min(32, {vocab}), got {topk}")
-    dev = logits.device
-    out = torch.empty((3, rows), dtype=torch.float32, device=dev)
-    logprob, entropy, lse = out.unbind(0)
-    index = torch.empty((rows, topk), dtype=torch.int32, device=dev) if topk else None
-    top = torch.empty((rows, topk), dtype=torch.float32, device=dev) if topk else None
-    nbytes = load().token_logprobs_workspace_bytes(rows, vocab, topk)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-    _enqueue(load().token_logprobs, logits, logits.data_ptr(), _DTYPES[logits.dtype], rows, vocab, ld, t, topk,
-             logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), _addr(index), _addr(top), _addr(ws), nbytes)
-    return logprob, entropy, lse, index, top
+    return _rowops().token_logprobs(logits, targets, topk)
 
 
 def token_logprobs_bwd(logits, targets, lse, entropy=None, g_logprob=None, g_entropy=None, out=None):
     """The gradient of the logits for those of the log probabilities and the
     entropies of token_logprobs (either may be None); out may be logits."""
-    rows, vocab, ld = _values(logits, "logits")
-    t = _targets(targets, rows, logits) if targets is not None else None
-    if g_logprob is None and g_entropy is None:
-        raise ValueError("g_logprob or g_entropy is needed")
-    if g_logprob is not None and t is None:
-        raise ValueError("targets are needed with g_logprob")
-    if g_entropy is not None and entropy is None:
-        raise ValueError("entropy is needed with g_entropy")
-    vecs = [_vector(lse, rows, "lse", logits), _vector(entropy, rows, "entropy", logits, True),
-            _vector(g_logprob, rows, "g_logprob", logits, True), _vector(g_entropy, rows, "g_entropy", logits, True)]
-    if out is None:
-        out = _like(logits)
-    _, _, ldo = _values(out, "out", logits)
-    _enqueue(load().token_logprobs_bwd, logits, logits.data_ptr(), _DTYPES[logits.dtype], rows, vocab, ld, t, *vecs,
-             out.data_ptr(), ldo)
-    return out
+    return _rowops().token_logprobs_bwd(logits, targets, lse, entropy, g_logprob, g_entropy, out)

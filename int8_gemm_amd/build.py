@@ -1,4 +1,6 @@
-"""Build libint8_gemm.so (the HIP kernels and the C ABI) for gfx950, in-tree.
+"""Build libint8_gemm.so (the HIP kernels and the C ABI) for gfx950, and
+rowops_bind.so (the host-only binding of the operators between the GEMMs to
+torch tensors), in-tree.
 
     python -m int8_gemm_amd.build            # build the library
     python -m int8_gemm_amd.build --asm DIR  # also write the gfx950 assembly
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -23,6 +26,8 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "hash.hip", "verify.hip", "norm.hip", "checkpoint.hip",
            "logprob.hip"]
 ARCH = "gfx950"
+BIND_SOURCE = "rowops_bind.cpp"
+BIND_PATH = os.path.join(HERE, "rowops_bind.so")
 
 
 def hipcc() -> str:
@@ -40,6 +45,32 @@ def common_flags():
         "-Wall", "-Wno-unused-function", "-Wno-unused-command-line-argument",
         "-I", os.path.join(ROOT, "include"),
     ]
+
+
+def bind_command(out: str):
+    """The host compiler's command for the binding (torch's C++ interface and
+    the C ABI's header; the C ABI itself is reached by address)."""
+    import torch
+    from torch.utils import cpp_extension
+    cxx = shutil.which(os.environ.get("CXX", "g++")) or "g++"
+    includes = [a for p in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"]) for a in ("-isystem", p)]
+    libs = [a for p in cpp_extension.library_paths() for a in ("-L", p)]
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *includes, "-o", out,
+            os.path.join(CSRC, BIND_SOURCE), *libs, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
+def build_bind(verbose: bool = False) -> str:
+    tmp = BIND_PATH + ".tmp"
+    cmd = bind_command(tmp)
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError(f"the binding's compiler failed with status {res.returncode}")
+    os.replace(tmp, BIND_PATH)
+    return BIND_PATH
 
 
 def build(verbose: bool = False, asm_dir: str = None) -> str:
@@ -62,6 +93,7 @@ def build(verbose: bool = False, asm_dir: str = None) -> str:
         if stubs:
             raise RuntimeError("undefined kernel launch stubs in the built library: " + ", ".join(stubs))
     os.replace(tmp, LIB_PATH)
+    build_bind(verbose)
     if asm_dir:
         os.makedirs(asm_dir, exist_ok=True)
         for s in srcs:

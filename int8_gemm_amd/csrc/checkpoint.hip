@@ -207,9 +207,8 @@ __global__ void __launch_bounds__(256) checkpoint_cols_quant_kernel(Checkpoint c
   while (r0 < c.rows) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      unsigned int w = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w |= (unsigned int)(quantize1(v[i][e], inv[e]) & 0xFF) << (8 * i);
+      const unsigned int w = pack_bytes(quantize1(v[0][e], inv[e]), quantize1(v[1][e], inv[e]),
+                                        quantize1(v[2][e], inv[e]), quantize1(v[3][e], inv[e]));
       tile[cg * 8 + e][rr] = inv[e] > 0.0f ? w : 0u;
     }
     __syncthreads();
