@@ -216,25 +216,25 @@ struct FindLds {
 };
 constexpr int kChunk = 8 * kBatch;            // columns that one wave searches: 512 groups, 8 a lane
 
-// The min(k, columns) best of columns [lo, lo + kChunk) of a row by one wave,
-// into best[0 .. k) (unused places 0), from the maxima of its groups.  The
-// k-th largest of the maxima is a bar that at least k values reach, and values
-// above it are only in the at most k groups whose maximum is above it: those
-// groups are read again, with those whose maximum is the bar itself.  If more
-// values are above the bar than fit (many in few groups), the bar is raised;
-// if so many equal it that they do not fit (masked rows), the ones of lowest
-// index are found by a scan from `lo`.
-template <class T>
-__device__ __forceinline__ void wave_best(const LpArgs& a, const T* row, const float* tops, int lo, FindLds& l,
-                                          unsigned long long* best) {
-  constexpr int N = kVec<T>, K = 8;
-  constexpr int VECS = kGroup / N;            // vectors of a group, 8 side by side
-  constexpr int U = 16 / N;                   // of a lane in flight
+// The end of a chunk that starts at column lo.
+__device__ __forceinline__ int chunk_end(const LpArgs& a, int lo) {
+  return lo + kChunk < a.cols ? lo + kChunk : (int)a.cols;
+}
+
+// What the maxima of a chunk's groups say of its best values.
+struct Groups {
+  uint32_t bar;                               // a key that at least topk values reach
+  int n_again;                                // groups to read again, noted in FindLds::again
+  bool few;                                   // whether the groups whose maximum is the bar are among them
+};
+
+// By one wave.  The k-th largest of the maxima is a bar that at least k
+// values reach, and values above it are only in the at most k groups whose
+// maximum is above it.
+__device__ __forceinline__ Groups pick_groups(const LpArgs& a, const float* tops, int lo, FindLds& l) {
+  constexpr int K = 8;
   const int lane = threadIdx.x & 63, k = a.topk;
-  const int hi = lo + kChunk < a.cols ? lo + kChunk : (int)a.cols;
-  const int n_tops = (hi - lo + kBatch - 1) / kBatch * kTops;   // 64 to 512: at least k
-  unsigned long long* const equal = l.list + kAbove;
-  if (lane < k) best[lane] = 0;
+  const int n_tops = (chunk_end(a, lo) - lo + kBatch - 1) / kBatch * kTops;   // 64 to 512: at least k
   uint32_t key[K], top = 0;
 #pragma unroll
   for (int j = 0; j < K; ++j) key[j] = 64 * j < n_tops ? rank_key(tops[lane + 64 * j]) : 0;
@@ -272,7 +272,7 @@ __device__ __forceinline__ void wave_best(const LpArgs& a, const T* row, const f
       over = b;
     }
   }
-  // the groups to read again: above the bar (at most k), then at it
+  // the groups above the bar (at most k), then those at it
   int n_again = 0, n_same = 0;
 #pragma unroll
   for (int j = 0; j < K; ++j) {
@@ -290,68 +290,90 @@ __device__ __forceinline__ void wave_best(const LpArgs& a, const T* row, const f
       n_again += __popcll(mask);
     }
   }
-  wave_sync();
-  // Their values: those above b counted (n_above), and those equal to it
-  // (n_equal); with `keep` noted as well, as many as fit, in any order.
+  return Groups{bar, n_again, few};
+}
+
+// The values of the groups to read again, by `threads` threads: those above b
+// and those equal to it counted in l.n_above and l.n_equal (0 before), and
+// with `keep` noted as well, as many as fit, in any order.
+template <class T>
+__device__ __forceinline__ void scan_groups(const LpArgs& a, const T* row, int lo, FindLds& l, int n_again, uint32_t b,
+                                            bool keep, int thread, int threads) {
+  constexpr int N = kVec<T>, U = 16 / N;      // vectors of a thread in flight
+  constexpr int VECS = kGroup / N;            // of a group, 8 side by side
+  const int hi = chunk_end(a, lo), vecs = n_again * VECS;
+  const float low = rank_value(b);
+  for (int base = 0; base < vecs; base += threads * U) {
+    float v[U][N];
+    int c[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = base + u * threads + thread;
+      c[u] = hi;                              // (nothing is read there)
+      if (i < vecs) {
+        const int g = l.again[i / VECS], s = i % VECS;
+        c[u] = lo + g / kTops * kBatch + ((s >> 3) * kThreads + g % kTops * 8 + (s & 7)) * N;
+      }
+      load_row<T>(row, c[u], hi, -__builtin_inff(), v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        if (v[u][e] < low || c[u] + e >= hi) continue;            // (a NaN may count as -inf)
+        const uint32_t x = rank_key(v[u][e]);
+        if (x > b) {
+          const int i = atomicAdd(&l.n_above, 1);
+          if (keep && i < kAbove) l.list[i] = candidate(x, c[u] + e);
+        } else if (x == b) {
+          const int i = atomicAdd(&l.n_equal, 1);
+          if (keep && i < kEqual) l.list[kAbove + i] = candidate(x, c[u] + e);
+        }
+      }
+  }
+}
+
+// The min(k, columns) best of the chunk from column lo by one wave, into
+// best[0 .. k) (unused places 0): the groups above the bar and at it are read
+// again.  If more values are above the bar than fit (many in few groups), the
+// bar is raised; if so many equal it that they do not fit (masked rows), the
+// ones of lowest index are found by a scan from `lo`.
+template <class T>
+__device__ __forceinline__ void wave_best(const LpArgs& a, const T* row, const float* tops, int lo, FindLds& l,
+                                          unsigned long long* best) {
+  constexpr int N = kVec<T>;
+  const int lane = threadIdx.x & 63, k = a.topk, hi = chunk_end(a, lo);
+  unsigned long long* const equal = l.list + kAbove;
+  if (lane < k) best[lane] = 0;
+  Groups g = pick_groups(a, tops, lo, l);
   int n_above = 0, n_equal = 0;
   auto scan = [&](uint32_t b, bool keep) __attribute__((always_inline)) {
     if (lane == 0) l.n_above = l.n_equal = 0;
     wave_sync();
-    const int vecs = n_again * VECS;
-    const float low = rank_value(b);
-    for (int base = 0; base < vecs; base += 64 * U) {
-      float v[U][N];
-      int c[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = base + u * 64 + lane;
-        c[u] = hi;                            // (nothing is read there)
-        if (i < vecs) {
-          const int g = l.again[i / VECS], s = i % VECS;
-          c[u] = lo + g / kTops * kBatch + ((s >> 3) * kThreads + g % kTops * 8 + (s & 7)) * N;
-        }
-        load_row<T>(row, c[u], hi, -__builtin_inff(), v[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          if (v[u][e] < low || c[u] + e >= hi) continue;          // (a NaN may count as -inf)
-          const uint32_t x = rank_key(v[u][e]);
-          if (x > b) {
-            const int i = atomicAdd(&l.n_above, 1);
-            if (keep && i < kAbove) l.list[i] = candidate(x, c[u] + e);
-          } else if (x == b) {
-            const int i = atomicAdd(&l.n_equal, 1);
-            if (keep && i < kEqual) equal[i] = candidate(x, c[u] + e);
-          }
-        }
-    }
+    scan_groups<T>(a, row, lo, l, g.n_again, b, keep, lane, 64);
     wave_sync();
     n_above = __builtin_amdgcn_readfirstlane(l.n_above);
     n_equal = __builtin_amdgcn_readfirstlane(l.n_equal);
     wave_sync();
   };
-  scan(bar, true);
+  scan(g.bar, true);
   if (n_above > kAbove) {                     // halving up to a bar with at least k values at or above it
-    over = top + 1;
-    while (n_above > kAbove && over - bar > 1) {
-      const uint32_t b = bar + (over - bar) / 2;
+    uint32_t over = 0xFFFFFFFFu;
+    while (n_above > kAbove && over - g.bar > 1) {
+      const uint32_t b = g.bar + (over - g.bar) / 2;
       const int was = n_above;
       scan(b, false);
       if (n_above + n_equal >= k) {
-        bar = b;
+        g.bar = b;
       } else {
         over = b;
         n_above = was;                        // (of the bar that stays)
       }
     }
-    scan(bar, true);
+    scan(g.bar, true);
   }
-  wave_sync();
-  n = n_above;
-  int n_eq = n < k ? n_equal : 0;
-  if (n < k && (!few || n_eq > kEqual)) {
+  int n = n_above, n_eq = n < k ? n_equal : 0;
+  if (n < k && (!g.few || n_eq > kEqual)) {
     const int need = k - n;
     n_eq = 0;
     for (int base = lo; base < hi && n_eq < need; base += 64 * N) {
@@ -361,7 +383,7 @@ __device__ __forceinline__ void wave_best(const LpArgs& a, const T* row, const f
       unsigned int hit = 0;
 #pragma unroll
       for (int e = 0; e < N; ++e)
-        if (c + e < hi && rank_key(v[e]) == bar) hit |= 1u << e;
+        if (c + e < hi && rank_key(v[e]) == g.bar) hit |= 1u << e;
       int before = __popc(hit);               // inclusive sum over the lanes
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
@@ -373,7 +395,7 @@ __device__ __forceinline__ void wave_best(const LpArgs& a, const T* row, const f
 #pragma unroll
       for (int e = 0; e < N; ++e)
         if (hit >> e & 1u) {
-          if (before < need) equal[before] = candidate(bar, c + e);
+          if (before < need) equal[before] = candidate(g.bar, c + e);
           ++before;
         }
       n_eq += total;
@@ -414,21 +436,28 @@ __global__ void __launch_bounds__(64, 8) lp_find_kernel(LpArgs a) {
   }
 }
 
-// Rows of several parts: wave 0 joins the sums while the others find the best
-// of each chunk, and all of them the best of those.
+// Rows of several parts.  Wave 0 joins the sums; of a row of one chunk wave 1
+// picks the groups meanwhile, and all waves read them again and rank the
+// values (1 x 50257 with 20 alternatives: 11.6 us by one wave alone); of
+// longer rows each of the other waves finds the best of a chunk, and all of
+// them the best of those.
 constexpr int kFinders = 15;
 constexpr int kMaxChunks = I8G_VOCAB_MAX / kChunk;
 template <class T>
 __global__ void __launch_bounds__(64 * (kFinders + 1)) lp_join_kernel(LpArgs a) {
+  constexpr int ALL = 64 * (kFinders + 1);
   __shared__ FindLds lds[kFinders];
   __shared__ unsigned long long list[kMaxChunks * kTopMax + kPad];
   __shared__ unsigned long long best[kTopMax];
   __shared__ double row_m, row_l;
   __shared__ int row_empty;
+  __shared__ Groups groups;
   static_assert(sizeof(lds) + sizeof(list) + sizeof(best) + 64 <= 65536, "a workgroup's LDS");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int chunks = (a.batches + 7) / 8, n = chunks * a.topk;
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
+    const T* row = static_cast<const T*>(a.X) + r * a.ldx;
+    const float* tops = a.tops + r * a.batches * kTops;
     if (wave == 0) {
       LpPart q{0.0, 0.0, kLowest, 0};
       if (tid < a.parts) q = a.sums[r * a.parts + tid];
@@ -448,17 +477,36 @@ __global__ void __launch_bounds__(64 * (kFinders + 1)) lp_join_kernel(LpArgs a) 
         row_empty = o.empty;
       }
       if (lane < kPad) list[n + lane] = 0;
-    } else if (a.topk > 0) {
+    } else if (a.topk > 0 && chunks > 1) {
       for (int c = wave - 1; c < chunks; c += kFinders)
-        wave_best<T>(a, static_cast<const T*>(a.X) + r * a.ldx, a.tops + (r * a.batches + c * 8) * kTops, c * kChunk,
-                     lds[wave - 1], list + c * a.topk);
+        wave_best<T>(a, row, tops + c * 8 * kTops, c * kChunk, lds[wave - 1], list + c * a.topk);
+    } else if (a.topk > 0 && wave == 1) {
+      const Groups g = pick_groups(a, tops, 0, lds[0]);
+      if (lane == 0) {
+        groups = g;
+        lds[0].n_above = lds[0].n_equal = 0;
+      }
     }
     __syncthreads();
-    if (a.topk > 0) {
-      place_best(list, n, a.topk, best, tid, 64 * (kFinders + 1));
+    if (a.topk > 0 && chunks > 1) {
+      place_best(list, n, a.topk, best, tid, ALL);
+    } else if (a.topk > 0) {
+      FindLds& l = lds[0];
+      scan_groups<T>(a, row, 0, l, groups.n_again, groups.bar, true, tid, ALL);
       __syncthreads();
-      if (tid < a.topk) write_best(a, r, tid, best[tid], row_m, row_l, row_empty);
+      const int above = l.n_above, equal = above < a.topk ? l.n_equal : 0;
+      if (above <= kAbove && (above >= a.topk || (groups.few && equal <= kEqual))) {
+        // both kinds into one list, and padding
+        for (int i = tid; i < above + equal + kPad; i += ALL)
+          list[i] = i < above ? l.list[i] : i < above + equal ? l.list[kAbove + i - above] : 0;
+        __syncthreads();
+        place_best(list, above + equal, a.topk, best, tid, ALL);
+      } else if (wave == 1) {
+        wave_best<T>(a, row, tops, 0, lds[1], best);
+      }
     }
+    __syncthreads();
+    if (tid < a.topk) write_best(a, r, tid, best[tid], row_m, row_l, row_empty);
     __syncthreads();                          // LDS is used again
   }
 }
