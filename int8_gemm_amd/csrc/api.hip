@@ -404,7 +404,7 @@ int checkpoint_act_bwd(const int8_t* Q, int64_t ldq, const float* scale, int64_t
 
 size_t checkpoint_quantize_cols_workspace_bytes(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0 || bad_sizes(rows, cols)) return 256;
-  return ((size_t)checkpoint_cols_parts(rows) * (size_t)cols * 4 + 255) / 256 * 256;
+  return (checkpoint_cols_words(rows, cols) * 4 + 255) / 256 * 256;
 }
 
 int checkpoint_quantize_cols(const int8_t* Q, int64_t ldq, const float* scale, int64_t lds, int32_t group, int64_t rows,

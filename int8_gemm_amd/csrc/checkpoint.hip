@@ -47,10 +47,14 @@ struct Place {
   }
 };
 
+// Values of a lane of the store: its group's two divisions serve 8 values in
+// f32 too (two 16-byte loads; 4 take 24.4 us for 8192 x 3072, 8 take 20.8).
+constexpr int kStoreUnit = 8;
+
 template <class T, int GROUP>
 __global__ void __launch_bounds__(kBlock) checkpoint_store_kernel(const T* __restrict__ X, int64_t ldx, Checkpoint c,
                                                                   Divisor units) {
-  constexpr int N = kVec<T>, LANES = GROUP / N;           // a group's lanes are one aligned run of lanes
+  constexpr int N = kStoreUnit, LANES = GROUP / N;        // a group's lanes are one aligned run of lanes
   const Place<N> at(units);
   const bool live = at.row < c.rows;
   float v[N];
@@ -164,10 +168,9 @@ __global__ void __launch_bounds__(256) checkpoint_cols_max_kernel(Checkpoint c, 
     if (lane < 8) red[wave][lane * 8 + e] = m[e];
   }
   __syncthreads();
-  const int64_t j = (int64_t)blockIdx.x * kTileCols + threadIdx.x;
-  if (threadIdx.x < kTileCols && j < c.cols)
-    parts[blockIdx.y * c.cols + j] = max(max(red[0][threadIdx.x], red[1][threadIdx.x]),
-                                         max(red[2][threadIdx.x], red[3][threadIdx.x]));
+  if (threadIdx.x < kTileCols)                            // rows of parts are whole tiles
+    parts[((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kTileCols + threadIdx.x] =
+        max(max(red[0][threadIdx.x], red[1][threadIdx.x]), max(red[2][threadIdx.x], red[3][threadIdx.x]));
 }
 
 // Quantized, transposed through LDS (4 rows of a column to a word; a row of
@@ -187,17 +190,25 @@ __global__ void __launch_bounds__(256) checkpoint_cols_quant_kernel(Checkpoint c
   float v[4][8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) tile_row(c, r0 + rr * 4 + i, col, v[i]);   // on their way while the scales are found
-  uint32_t m = 0;
-  if (j0 + lane < c.cols) {
-#pragma unroll 4
-    for (int i = wave; i < n_parts; i += 4) m = max(m, parts[i * c.cols + j0 + lane]);
+  // the maxima of the row ranges, 4 columns a lane and 4 ranges a wave at a time
+  uint32_t m[4] = {0, 0, 0, 0};
+  for (int p = wave * 4 + (lane >> 4); p < n_parts; p += 16) {
+    uint32_t x[4];
+    __builtin_memcpy(x, parts + ((int64_t)p * gridDim.x + blockIdx.x) * kTileCols + (lane & 15) * 4, 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = max(m[e], x[e]);
   }
-  red[wave][lane] = m;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    Pair32 p = lane_pair<16>(m[e]);
+    p = lane_pair<32>(max(p.a, p.b));
+    if (lane < 16) red[wave][lane * 4 + e] = max(p.a, p.b);
+  }
   __syncthreads();
   if (tid < kTileCols) {
-    m = max(max(red[0][tid], red[1][tid]), max(red[2][tid], red[3][tid]));
-    const float s = scale_of_bits(m);
-    s_inv[tid] = m < kInfBits ? recip_rn(s) : 0.0f;       // a NaN column: codes 0
+    const uint32_t a = max(max(red[0][tid], red[1][tid]), max(red[2][tid], red[3][tid]));
+    const float s = scale_of_bits(a);
+    s_inv[tid] = a < kInfBits ? recip_rn(s) : 0.0f;       // a NaN column: codes 0
     if (blockIdx.y == 0 && j0 + tid < c.cols) scale[j0 + tid] = s;
   }
   __syncthreads();
@@ -266,7 +277,7 @@ Checkpoint slab_of(Checkpoint c, int64_t first, int64_t rows) {
 
 template <class T, int GROUP>
 hipError_t store(const T* x, int64_t ldx, const Checkpoint& c, hipStream_t stream) {
-  const int64_t units = (c.cols + GROUP - 1) / GROUP * (GROUP / kVec<T>);     // whole groups
+  const int64_t units = (c.cols + GROUP - 1) / GROUP * (GROUP / kStoreUnit);  // whole groups
   for_slabs(c.rows, units, [&](int64_t first, int64_t rows, dim3 grid, const Divisor& d) {
     hipLaunchKernelGGL((checkpoint_store_kernel<T, GROUP>), grid, dim3(kBlock), 0, stream, x + first * ldx, ldx,
                        slab_of(c, first, rows), d);
@@ -324,9 +335,13 @@ hipError_t launch_checkpoint_read(const Checkpoint& c, int act, const void* dY, 
   }
 }
 
-int checkpoint_cols_parts(int64_t rows) {
+static int cols_parts(int64_t rows) {
   const int64_t n = row_tiles(rows);
   return (int)(n < kColParts ? n : kColParts);
+}
+
+size_t checkpoint_cols_words(int64_t rows, int64_t cols) {
+  return (size_t)cols_parts(rows) * ((cols + kTileCols - 1) / kTileCols * kTileCols);
 }
 
 hipError_t launch_checkpoint_cols(const Checkpoint& c, int8_t* Qt, int64_t ldqt, float* scale, void* parts,
@@ -338,7 +353,7 @@ hipError_t launch_checkpoint_cols(const Checkpoint& c, int8_t* Qt, int64_t ldqt,
   }
   uint32_t* p = static_cast<uint32_t*>(parts);
   const unsigned int bx = (unsigned int)((c.cols + kTileCols - 1) / kTileCols);
-  const int n = checkpoint_cols_parts(c.rows);
+  const int n = cols_parts(c.rows);
   const int64_t tiles = row_tiles(c.rows);
   hipLaunchKernelGGL(checkpoint_cols_max_kernel, dim3(bx, n), dim3(256), 0, stream, c, p);
   hipLaunchKernelGGL(checkpoint_cols_quant_kernel, dim3(bx, (unsigned int)(tiles < 4096 ? tiles : 4096)), dim3(256), 0, stream,

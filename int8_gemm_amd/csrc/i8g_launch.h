@@ -203,8 +203,8 @@ hipError_t launch_checkpoint_store(const void* X, int64_t ldx, int dtype, const 
 // Y = RN(q*s) (ACT_NONE), or Y = dY * act'(RN(q*s)).
 hipError_t launch_checkpoint_read(const Checkpoint& c, int act, const void* dY, int64_t lddy, void* Y, int64_t ldy,
                                   int dtype, hipStream_t stream);
-// Column maxima that the first pass leaves: checkpoint_cols_parts(rows) x cols words at `parts`.
-int checkpoint_cols_parts(int64_t rows);
+// Words of `parts`: the column maxima of row ranges that the first pass leaves.
+size_t checkpoint_cols_words(int64_t rows, int64_t cols);
 hipError_t launch_checkpoint_cols(const Checkpoint& c, int8_t* Qt, int64_t ldqt, float* scale, void* parts,
                                   hipStream_t stream);
 
