@@ -98,15 +98,15 @@ __global__ void __launch_bounds__(kBlock) checkpoint_read_kernel(Checkpoint c, c
   constexpr int N = kVec<T>;
   const Place<N> at(units);
   if (at.row >= c.rows) return;
-  int q[N];
-  load_codes(c.Q + at.row * c.ldq, at.col, c.cols, q);
+  CodeWords<N> q;
+  q.load(c.Q + at.row * c.ldq, at.col, c.cols);
   const float s = c.scale[at.row * c.lds + (at.col >> c.gshift)];
   float y[N];
   if constexpr (ACT != ACT_NONE) load_row<T>(dY + at.row * lddy, at.col, c.cols, 0.0f, y);
   const float nan = s - s;                                // 0, or NaN with the scale
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    const float x = mul_rn((float)q[e], s);
+    const float x = mul_rn(q[e], s);
     if constexpr (ACT == ACT_NONE) y[e] = x;
     if constexpr (ACT == ACT_RELU) y[e] = x > 0.0f ? y[e] : nan;
     if constexpr (ACT == ACT_GELU) y[e] = y[e] * (gelu_grad(x) + nan);
@@ -124,19 +124,32 @@ __global__ void __launch_bounds__(kBlock) checkpoint_read_kernel(Checkpoint c, c
 constexpr int kTileCols = 64, kTileRows = 128;
 constexpr int kColParts = 64;
 
-// The values of row r, columns col .. col+7; 0 outside the matrix.
-__device__ __forceinline__ void tile_row(const Checkpoint& c, int64_t r, int64_t col, float (&v)[8]) {
-  int q[8];
-  float s = 0.0f;
-  if (r < c.rows && col < c.cols) {
-    load_codes(c.Q + r * c.ldq, col, c.cols, q);
-    s = c.scale[r * c.lds + (col >> c.gshift)];
+// The values of columns col .. col+7 of 4 rows from `row`; 0 outside the
+// matrix.  `inside`: the whole tile lies in the matrix.
+__device__ __forceinline__ void tile_rows(const Checkpoint& c, int64_t row, int64_t col, bool inside,
+                                          float (&v)[4][8]) {
+  CodeWords<8> q[4];
+  float s[4];
+  const int8_t* Q = c.Q + row * c.ldq + col;
+  const float* S = c.scale + row * c.lds + (col >> c.gshift);
+  if (inside) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __builtin_memcpy(q[i].w, Q + i * c.ldq, 8);
+      s[i] = S[i * c.lds];
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = 0;
+    for (int i = 0; i < 4; ++i) {
+      const bool some = row + i < c.rows && col < c.cols;
+      q[i].load(Q + i * c.ldq, (int64_t)0, some ? c.cols - col : (int64_t)0);
+      s[i] = some ? S[i * c.lds] : 0.0f;
+    }
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = mul_rn((float)q[e], s);
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] = mul_rn(q[i][e], s[i]);
 }
 
 // The largest of x over the lanes of equal number mod 8.
@@ -153,11 +166,11 @@ __global__ void __launch_bounds__(256) checkpoint_cols_max_kernel(Checkpoint c, 
   __shared__ uint32_t red[4][kTileCols];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t col = (int64_t)blockIdx.x * kTileCols + (threadIdx.x & 7) * 8;
+  const bool wide = ((int64_t)blockIdx.x + 1) * kTileCols <= c.cols;
   uint32_t m[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   for (int64_t r0 = (int64_t)blockIdx.y * kTileRows; r0 < c.rows; r0 += (int64_t)gridDim.y * kTileRows) {
     float v[4][8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) tile_row(c, r0 + i * 32 + (threadIdx.x >> 3), col, v[i]);
+    tile_rows(c, r0 + (threadIdx.x >> 3) * 4, col, wide && r0 + kTileRows <= c.rows, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       m[e] = max(max(m[e], max(abs_bits(v[0][e]), abs_bits(v[1][e]))), max(abs_bits(v[2][e]), abs_bits(v[3][e])));
@@ -188,8 +201,8 @@ __global__ void __launch_bounds__(256) checkpoint_cols_quant_kernel(Checkpoint c
   const int64_t col = j0 + cg * 8;
   int64_t r0 = (int64_t)blockIdx.y * kTileRows;
   float v[4][8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) tile_row(c, r0 + rr * 4 + i, col, v[i]);   // on their way while the scales are found
+  const bool wide = j0 + kTileCols <= c.cols;
+  tile_rows(c, r0 + rr * 4, col, wide && r0 + kTileRows <= c.rows, v);   // on their way while the scales are found
   // the maxima of the row ranges, 4 columns a lane and 4 ranges a wave at a time
   uint32_t m[4] = {0, 0, 0, 0};
   for (int p = wave * 4 + (lane >> 4); p < n_parts; p += 16) {
@@ -240,10 +253,7 @@ __global__ void __launch_bounds__(256) checkpoint_cols_quant_kernel(Checkpoint c
       }
     }
     r0 += (int64_t)gridDim.y * kTileRows;
-    if (r0 < c.rows) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tile_row(c, r0 + rr * 4 + i, col, v[i]);
-    }
+    if (r0 < c.rows) tile_rows(c, r0 + rr * 4, col, wide && r0 + kTileRows <= c.rows, v);
     __syncthreads();
   }
 }

@@ -98,19 +98,30 @@ __device__ __forceinline__ uint32_t pack_bytes(int a, int b, int c, int d) {
   return __builtin_amdgcn_perm(b, a, 0x0C0C0400u) | __builtin_amdgcn_perm(d, c, 0x04000C0Cu);
 }
 
-// N int8 codes at row[c ...]; those beyond `cols` are 0.
-template <int N, class I>
-__device__ __forceinline__ void load_codes(const int8_t* __restrict__ row, I c, I cols, int (&q)[N]) {
-  int8_t t[N];
-  if (c + N <= cols) {
-    __builtin_memcpy(t, row + c, N);
-  } else {
+// N int8 codes at row[c ...], four to a word; those beyond `cols` are 0.
+// (Kept as words, a code becomes a float in one instruction; as bytes, every
+// one is moved on its own.)
+template <int N>
+struct CodeWords {
+  uint32_t w[N / 4];
+  template <class I>
+  __device__ __forceinline__ void load(const int8_t* __restrict__ row, I c, I cols) {
+    if (c + N <= cols) {
+      __builtin_memcpy(w, row + c, N);
+    } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) t[e] = c + e < cols ? row[c + e] : (int8_t)0;
+      for (int i = 0; i < N / 4; ++i) {
+        w[i] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + 4 * i + e < cols) w[i] |= (uint32_t)(uint8_t)row[c + 4 * i + e] << (8 * e);
+      }
+    }
   }
-#pragma unroll
-  for (int e = 0; e < N; ++e) q[e] = t[e];
-}
+  __device__ __forceinline__ float operator[](int e) const {
+    return (float)(int)(int8_t)(w[e / 4] >> (8 * (e % 4)));
+  }
+};
 
 template <int N, class I>
 __device__ __forceinline__ void store_codes(int8_t* __restrict__ row, I c, I cols, const int (&q)[N]) {

@@ -271,7 +271,7 @@ struct Input : RawRow<T, N> {
 };
 template <class T, int N>
 struct Input<T, true, N> {
-  RawRow<int8_t, N> q;
+  CodeWords<N> q;
   float s;
   template <class I>
   __device__ __forceinline__ void load(const LnBwdArgs& a, int64_t r, I c) {
