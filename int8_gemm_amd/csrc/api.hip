@@ -165,7 +165,7 @@ const char* i8g_status_string(int status) {
     case I8G_EINVAL: return "invalid argument (null pointer, negative size or leading dimension too small)";
     case I8G_EKRANGE: return "K exceeds 133144: exact int32 accumulation is not guaranteed";
     case I8G_EALIGN: return "operand not 16-byte aligned, or its leading dimension not a multiple of 16 covering a whole row (K rounded up to 16 bytes; int4: 16 bytes per 32 values)";
-    case I8G_EWORKSPACE: return "workspace missing, misaligned or smaller than gemm_i8_workspace_bytes()";
+    case I8G_EWORKSPACE: return "workspace missing, misaligned or smaller than the call's *_workspace_bytes()";
     case I8G_EHIP: return "HIP runtime error while enqueueing a kernel";
     case I8G_EGATE: return "self-check failed: a device output differs from the exact host mirror";
     case I8G_ESCRATCH: return "the shape needs more scratch than the 64 MiB static buffer of gemm_i8_blockscaled_noalloc holds (a split K of a large output): use gemm_i8_blockscaled with a workspace";

@@ -142,7 +142,7 @@ def test_activation_gradient(g, rows, cols, group, act, dtype):
 
 @pytest.mark.parametrize("group", [32, 64, 128, 256])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 768), (3, 33), (63, 64), (64, 65), (65, 1001), (200, 300),
-                                       (1000, 768), (4099, 70), (17, 5000), (8192, 96), (20001, 33)])
+                                       (1000, 768), (4099, 70), (17, 5000), (8192, 96), (20001, 33), (600001, 17)])
 def test_quantize_cols(g, rows, cols, group):
     say("checkpoint columns", rows, cols, group)
     rng = np.random.default_rng(rows + cols + group)

@@ -69,7 +69,7 @@ def tokens(rng, rows, vocab):
 @pytest.mark.parametrize("rows,vocab,topk", [
     (1, 1, 1), (3, 2, 2), (2, 7, 0), (5, 64, 32), (3, 1000, 5), (2, 4096, 8), (2, 4097, 8), (1, 50257, 20),
     (3, 50304, 32), (600, 777, 3), (520, 8193, 4), (2, 65536, 7), (1, 65537, 32), (1, 131075, 20), (515, 65600, 2),
-    (1, 1000003, 32)])
+    (1, 1000003, 32), (70000, 65, 3)])
 def test_forward(g, rows, vocab, topk, dtype):
     say("logprobs", rows, vocab, topk, dtype)
     rng = np.random.default_rng(rows + vocab)
@@ -184,7 +184,7 @@ def grad_bound(X64, lse, h, g, gh, want, dt):
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
-@pytest.mark.parametrize("rows,vocab", [(1, 1), (3, 2), (2, 65), (600, 100), (5, 4097), (3, 50257), (2, 131075)])
+@pytest.mark.parametrize("rows,vocab", [(1, 1), (3, 2), (2, 65), (600, 100), (5, 4097), (3, 50257), (2, 131075), (70000, 33)])
 def test_gradient(g, rows, vocab, dtype):
     say("logprobs gradient", rows, vocab, dtype)
     rng = np.random.default_rng(rows + vocab)

@@ -14,7 +14,8 @@ pytestmark = pytest.mark.gpu
 U = R.U
 
 SHAPES = [(1, 1), (1, 768), (5, 3), (9, 64), (3, 255), (7, 256), (2, 257), (130, 511), (3, 769), (4, 1000),
-          (2, 1024), (3, 1025), (2, 2047), (3, 4097), (2, 8200), (2, 16384), (2, 16387), (1, 40001)]
+          (2, 1024), (3, 1025), (2, 2047), (3, 4097), (2, 8200), (2, 16384), (2, 16387), (1, 40001),
+          (9001, 40), (5003, 1100), (1100, 4200), (600, 8193)]   # (more rows than workgroups hold at a time)
 
 
 @pytest.fixture(scope="module")
@@ -119,7 +120,8 @@ def test_forward_hard_rows(g):
 
 
 BWD_SHAPES = [(1, 1), (1, 768), (3, 5), (2, 255), (37, 256), (6, 513), (700, 768), (9, 1000), (5, 1024), (3, 1025),
-              (601, 1600), (4, 3000), (2, 4097), (3, 8193), (2, 16384), (3, 16390), (2, 33001)]
+              (601, 1600), (4, 3000), (2, 4097), (3, 8193), (2, 16384), (3, 16390), (2, 33001),
+             (9001, 40), (2500, 1100), (1300, 2100), (600, 4200), (300, 8193), (300, 16390)]   # (several rounds of rows)
 
 
 def grads_input(rng, rows, cols, dt, pad, shift):
