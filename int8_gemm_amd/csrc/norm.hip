@@ -21,6 +21,8 @@
 // once, a row staying in registers in between.  A row of up to 1024 values is
 // held by one wave, 16 values a lane; a longer one by 2 to 16 waves of one
 // workgroup; rows beyond 16384 values are read again instead of held.
+#include <type_traits>
+
 #include "i8g_launch.h"
 #include "i8g_row.h"
 
@@ -97,9 +99,8 @@ __device__ __forceinline__ RowStats stats_of(double x0, double s1, double s2, do
 // Rows held in registers; the workgroups walk the rows with a fixed stride,
 // the next row's values on their way while one is worked on, gamma and beta
 // held throughout.
-template <class T, int NV, int W, bool QUANT>
+template <class T, int N, int NV, int W, bool QUANT>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) ln_fwd_kernel(LnFwdArgs a) {
-  constexpr int N = kVec<T>;
   __shared__ double red[2][2 * W];
   __shared__ uint32_t redm[2][W];
   int turn = 0, turnm = 0;
@@ -293,9 +294,8 @@ __device__ __forceinline__ float bwd_dx(float w, float xh, float rstd, float c1,
 // and the workgroup leaves one partial sum per column in
 // parts[block][2][held] for ln_bwd_cols_kernel, in the order of the lanes
 // (column_of), which makes whole cache lines of them.
-template <class T, bool CK, int NV, int W, bool PARTS>
+template <class T, bool CK, int N, int NV, int W, bool PARTS>
 __global__ void __launch_bounds__(W == 16 ? 1024 : 512) ln_bwd_kernel(LnBwdArgs a) {
-  constexpr int N = kVec<T>;
   constexpr int S = W == 16 ? 1 : 8 / W;
   __shared__ double red[S][2][2 * W];
   __shared__ double part[PARTS && S > 1 ? S : 1][PARTS && S > 1 ? NV * N * W * 64 : 1];
@@ -485,19 +485,20 @@ __global__ void __launch_bounds__(64) ln_bwd_long_parts_kernel(LnBwdArgs a) {
 // The column of the j-th partial sum, lanes holding vectors of n values
 // (n = 1: the sums are in the order of the columns).
 __device__ __forceinline__ int64_t column_of(int64_t j, int n) {
-  return n == 1 ? j : j / (64 * n) * (64 * n) + j % 64 * n + j / 64 % n;
+  if (n == 1) return j;
+  const int i = (int)j;                                   // (rows held by lanes are short)
+  return n == 4 ? i / 256 * 256 + i % 64 * 4 + i / 64 % 4 : i / 512 * 512 + i % 64 * 8 + i / 64 % 8;
 }
 
 // 16 of the `held` partial sums (of dgamma, or with blockIdx.y of dbeta): a
 // thread adds every 16th of one column (16 of them are one cache line of a
 // partial), then the 16 threads of a column join.
-template <int N>
 __global__ void __launch_bounds__(256) ln_bwd_cols_kernel(const double* __restrict__ parts, int n_parts, int64_t held,
-                                                          int64_t cols, float* __restrict__ dgamma,
+                                                          int order, int64_t cols, float* __restrict__ dgamma,
                                                           float* __restrict__ dbeta) {
   __shared__ double red[16][17];
   const int col = threadIdx.x & 15, slice = threadIdx.x >> 4;
-  const int64_t j = (int64_t)blockIdx.x * 16 + col, c = column_of(j, N);
+  const int64_t j = (int64_t)blockIdx.x * 16 + col, c = column_of(j, order);
   float* const out = blockIdx.y ? dbeta : dgamma;
   if (!out) return;
   double s = 0.0;
@@ -515,18 +516,25 @@ __global__ void __launch_bounds__(256) ln_bwd_cols_kernel(const double* __restri
   }
 }
 
-// Waves of a row and vectors of a lane (of N values each, 16 at most): the
-// shortest that hold the row.
+// How a row is held: n values a vector, nv vectors a lane (16 values at most),
+// in `waves` waves; the fewest that hold it.  Vectors are 16 bytes, but 8 in
+// the 2-byte types for a row of one wave that whole vectors of 8 values would
+// fill to less.  8192 x 768 bf16: into codes and restored 16.2 us with 4
+// values a vector and 18.5 with 8, backward 14.3 and 18.1; 8192 x 1024, which
+// both fill: 8.2 us with 8 and 10.9 with 4.
 struct RowShape {
-  int waves, nv;   // waves == 0: too long to hold
+  int waves, n, nv;   // waves == 0: too long to hold
 };
-RowShape row_shape(int64_t cols, int n) {
-  const int per = 64 * n, most = 16 / n;
-  if (cols > kHeldMax) return RowShape{0, 0};
-  int w = 1;
-  while ((int64_t)w * per * most < cols) w *= 2;
-  const int nv = (int)((cols + (int64_t)w * per - 1) / ((int64_t)w * per));
-  return RowShape{w, nv};
+RowShape row_shape(int64_t cols, int vec) {
+  if (cols > kHeldMax) return RowShape{0, vec, 0};
+  const int64_t quarters = (cols + 255) / 256;           // of 64 lanes x 16 values
+  if (quarters <= 4) {
+    const int n = vec == 8 && quarters % 2 == 0 ? 8 : 4;
+    return RowShape{1, n, (int)quarters * 4 / n};
+  }
+  int w = 2;
+  while (w * 1024 < cols) w *= 2;
+  return RowShape{w, vec, 16 / vec};
 }
 
 // Workgroups of a kernel whose workgroups walk the rows.
@@ -535,83 +543,87 @@ unsigned int row_grid(int64_t rows, int per_group, int64_t most) {
   return (unsigned int)(g < most ? g : most);
 }
 
-template <class T, bool QUANT, int NV, int W>
-void ln_fwd_held(const LnFwdArgs& a, hipStream_t stream) {
-  const unsigned int grid = row_grid(a.rows, W == 1 ? 4 : 1, W == 1 ? 1024 : 4096 / W);
-  hipLaunchKernelGGL((ln_fwd_kernel<T, NV, W, QUANT>), dim3(grid), dim3(W == 1 ? 256 : 64 * W), 0, stream, a);
+// Calls f with the shape's N, NV and W as compile-time constants; V is the
+// type's whole vector.  (A whole vector of 8 takes 1 or 2, a vector of 4 up to
+// 4 in f32, and 1 or 3 where it is half of a whole one.)
+template <int I>
+using Int = std::integral_constant<int, I>;
+template <int V, class F>
+void with_shape(const RowShape& s, F f) {
+  constexpr int M = 16 / V;
+  switch (s.waves) {
+    case 1:
+      if constexpr (V == 8) {
+        if (s.n == 8 && s.nv == 1) return f(Int<8>{}, Int<1>{}, Int<1>{});
+        if (s.n == 8) return f(Int<8>{}, Int<2>{}, Int<1>{});
+        if (s.nv == 1) return f(Int<4>{}, Int<1>{}, Int<1>{});
+        return f(Int<4>{}, Int<3>{}, Int<1>{});
+      } else {
+        if (s.nv == 1) return f(Int<4>{}, Int<1>{}, Int<1>{});
+        if (s.nv == 2) return f(Int<4>{}, Int<2>{}, Int<1>{});
+        if (s.nv == 3) return f(Int<4>{}, Int<3>{}, Int<1>{});
+        return f(Int<4>{}, Int<4>{}, Int<1>{});
+      }
+    case 2: return f(Int<V>{}, Int<M>{}, Int<2>{});
+    case 4: return f(Int<V>{}, Int<M>{}, Int<4>{});
+    case 8: return f(Int<V>{}, Int<M>{}, Int<8>{});
+    default: return f(Int<V>{}, Int<M>{}, Int<16>{});
+  }
 }
 
 template <class T, bool QUANT>
 hipError_t ln_fwd(const LnFwdArgs& a, hipStream_t stream) {
-  constexpr int M = 16 / kVec<T>;                    // vectors of a full lane
   const RowShape s = row_shape(a.cols, kVec<T>);
-  switch (s.waves) {
-    case 0: {
-      const unsigned int grid = row_grid(a.rows, 1, int64_t(1) << 20);
-      hipLaunchKernelGGL((ln_fwd_long_kernel<T, QUANT>), dim3(grid), dim3(1024), 0, stream, a);
-      break;
-    }
-    case 1:
-      if (s.nv == 1) ln_fwd_held<T, QUANT, 1, 1>(a, stream);
-      else if (s.nv == 2) ln_fwd_held<T, QUANT, 2, 1>(a, stream);
-      else if (s.nv == 3) ln_fwd_held<T, QUANT, M < 3 ? M : 3, 1>(a, stream);
-      else ln_fwd_held<T, QUANT, M, 1>(a, stream);
-      break;
-    case 2: ln_fwd_held<T, QUANT, M, 2>(a, stream); break;
-    case 4: ln_fwd_held<T, QUANT, M, 4>(a, stream); break;
-    case 8: ln_fwd_held<T, QUANT, M, 8>(a, stream); break;
-    default: ln_fwd_held<T, QUANT, M, 16>(a, stream); break;
+  if (s.waves == 0) {
+    const unsigned int grid = row_grid(a.rows, 1, int64_t(1) << 20);
+    hipLaunchKernelGGL((ln_fwd_long_kernel<T, QUANT>), dim3(grid), dim3(1024), 0, stream, a);
+  } else {
+    with_shape<kVec<T>>(s, [&](auto n, auto nv, auto w) {
+      constexpr int W = decltype(w)::value;
+      const unsigned int grid = row_grid(a.rows, W == 1 ? 4 : 1, W == 1 ? 1024 : 4096 / W);
+      hipLaunchKernelGGL((ln_fwd_kernel<T, decltype(n)::value, decltype(nv)::value, W, QUANT>), dim3(grid),
+                         dim3(W == 1 ? 256 : 64 * W), 0, stream, a);
+    });
   }
   return hipGetLastError();
 }
 
-template <class T, bool CK, int NV, int W>
-void ln_bwd_held(const LnBwdArgs& a, int groups, hipStream_t stream) {
-  if (a.parts)
-    hipLaunchKernelGGL((ln_bwd_kernel<T, CK, NV, W, true>), dim3(groups), dim3(512), 0, stream, a);
-  else
-    hipLaunchKernelGGL((ln_bwd_kernel<T, CK, NV, W, false>), dim3(row_grid(a.rows, 8 / W, 512)), dim3(512), 0, stream, a);
-}
-
 template <class T, bool CK>
 hipError_t ln_bwd(const LnBwdArgs& a, float* dgamma, float* dbeta, hipStream_t stream) {
-  constexpr int N = kVec<T>, M = 16 / N;
+  constexpr int V = kVec<T>;
   const int groups = ln_bwd_groups(a.rows, a.cols);
-  const RowShape s = row_shape(a.cols, N);
+  const RowShape s = row_shape(a.cols, V);
   // Rows of 16 waves leave no registers for the sums over the rows, and
   // longer ones are not held: the sums are a pass of their own, before dX,
   // which may be dY's memory.
-  if (a.parts && (s.waves == 0 || s.waves == 16))
-    hipLaunchKernelGGL((ln_bwd_long_parts_kernel<T, CK>), dim3((unsigned int)((a.cols + 64 * N - 1) / (64 * N)), groups),
+  const bool apart = s.waves == 0 || s.waves == 16;
+  if (a.parts && apart)
+    hipLaunchKernelGGL((ln_bwd_long_parts_kernel<T, CK>), dim3((unsigned int)((a.cols + 64 * V - 1) / (64 * V)), groups),
                        dim3(64), 0, stream, a);
-  switch (s.waves) {
-    case 0:
-      if (a.dX && a.rows > 0)
-        hipLaunchKernelGGL((ln_bwd_long_kernel<T, CK>), dim3(row_grid(a.rows, 1, int64_t(1) << 20)), dim3(1024), 0,
+  if (s.waves == 0) {
+    if (a.dX && a.rows > 0)
+      hipLaunchKernelGGL((ln_bwd_long_kernel<T, CK>), dim3(row_grid(a.rows, 1, int64_t(1) << 20)), dim3(1024), 0,
+                         stream, a);
+  } else {
+    with_shape<V>(s, [&](auto n, auto nv, auto w) {
+      constexpr int N = decltype(n)::value, NV = decltype(nv)::value, W = decltype(w)::value;
+      if constexpr (W == 16) {
+        if (a.dX && a.rows > 0)
+          hipLaunchKernelGGL((ln_bwd_kernel<T, CK, N, NV, 16, false>), dim3(row_grid(a.rows, 1, 256)), dim3(1024), 0,
+                             stream, a);
+      } else if (a.parts) {
+        hipLaunchKernelGGL((ln_bwd_kernel<T, CK, N, NV, W, true>), dim3(groups), dim3(512), 0, stream, a);
+      } else {
+        hipLaunchKernelGGL((ln_bwd_kernel<T, CK, N, NV, W, false>), dim3(row_grid(a.rows, 8 / W, 512)), dim3(512), 0,
                            stream, a);
-      break;
-    case 16:
-      if (a.dX && a.rows > 0)
-        hipLaunchKernelGGL((ln_bwd_kernel<T, CK, M, 16, false>), dim3(row_grid(a.rows, 1, 256)), dim3(1024), 0, stream, a);
-      break;
-    case 1:
-      if (s.nv == 1) ln_bwd_held<T, CK, 1, 1>(a, groups, stream);
-      else if (s.nv == 2) ln_bwd_held<T, CK, 2, 1>(a, groups, stream);
-      else if (s.nv == 3) ln_bwd_held<T, CK, M < 3 ? M : 3, 1>(a, groups, stream);
-      else ln_bwd_held<T, CK, M, 1>(a, groups, stream);
-      break;
-    case 2: ln_bwd_held<T, CK, M, 2>(a, groups, stream); break;
-    case 4: ln_bwd_held<T, CK, M, 4>(a, groups, stream); break;
-    default: ln_bwd_held<T, CK, M, 8>(a, groups, stream); break;
+      }
+    });
   }
   if (a.parts) {
-    const bool by_lane = s.waves >= 1 && s.waves <= 8;
-    const int64_t held = by_lane ? (int64_t)s.waves * (s.waves == 1 ? s.nv : M) * 64 * N : a.cols;
-    const dim3 grid((unsigned int)((held + 15) / 16), 2);
-    if (by_lane)
-      hipLaunchKernelGGL(ln_bwd_cols_kernel<N>, grid, dim3(256), 0, stream, a.parts, groups, held, a.cols, dgamma, dbeta);
-    else
-      hipLaunchKernelGGL(ln_bwd_cols_kernel<1>, grid, dim3(256), 0, stream, a.parts, groups, held, a.cols, dgamma, dbeta);
+    const int64_t held = apart ? a.cols : (int64_t)s.waves * 64 * s.n * s.nv;
+    const int order = apart ? 1 : s.n;
+    hipLaunchKernelGGL(ln_bwd_cols_kernel, dim3((unsigned int)((held + 15) / 16), 2), dim3(256), 0, stream, a.parts,
+                       groups, held, order, a.cols, dgamma, dbeta);
   }
   return hipGetLastError();
 }
