@@ -511,19 +511,21 @@ __global__ void __launch_bounds__(64 * (kFinders + 1)) lp_join_kernel(LpArgs a) 
   }
 }
 
-constexpr int kGradVecs = 4;                  // vectors of a thread of the backward pass
-
-template <class T, bool STREAM>
-__global__ void __launch_bounds__(256) lp_bwd_kernel(LpBwdArgs a) {
-  constexpr int N = kVec<T>, U = kGradVecs;
-  constexpr int CHUNK = 256 * N * U;
-  const int cols = (int)a.cols, c0 = (int)blockIdx.x * CHUNK + (int)threadIdx.x * N;
-  for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
+// The gradient: a row by `per_row` threads (whole waves, 256 at most) of a
+// workgroup of 256, U vectors a thread.
+template <class T, int U, bool STREAM>
+__global__ void __launch_bounds__(256) lp_bwd_kernel(LpBwdArgs a, int per_row) {
+  constexpr int N = kVec<T>;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = per_row >> 6;
+  const int slot = wave / waves, slots = 4 / waves;
+  const int cols = (int)a.cols;
+  const int c0 = ((int)blockIdx.x * per_row * U + (int)threadIdx.x - slot * per_row) * N;
+  for (int64_t r = (int64_t)blockIdx.y * slots + slot; r < a.rows; r += (int64_t)gridDim.y * slots) {
     const T* x = static_cast<const T*>(a.X) + r * a.ldx;
     T* dx = static_cast<T*>(a.dX) + r * a.lddx;
     float v[U][N];
 #pragma unroll
-    for (int u = 0; u < U; ++u) load_row<T>(x, c0 + u * 256 * N, cols, 0.0f, v[u]);
+    for (int u = 0; u < U; ++u) load_row<T>(x, c0 + u * per_row * N, cols, 0.0f, v[u]);
     // dx_j = -p_j (g + gh (log p_j + H)) = p_j (nh log p_j + n0), and + g for the token
     float lse = a.lse[r], g = 0.0f, n0 = 0.0f, nh = 0.0f;
     int t = -1;
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(256) lp_bwd_kernel(LpBwdArgs a) {
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * 256 * N;
+      const int c = c0 + u * per_row * N;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const float lp = __builtin_elementwise_maximum(v[u][e] - lse, -104.0f);   // p is 0 there, and p * lp as well
@@ -579,16 +581,26 @@ hipError_t forward(const LpArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <class T>
-hipError_t backward(const LpBwdArgs& a, hipStream_t stream) {
-  constexpr int CHUNK = 256 * kVec<T> * kGradVecs;
-  const dim3 grid((unsigned int)((a.cols + CHUNK - 1) / CHUNK), row_grid(a.rows));
+template <class T, int U>
+hipError_t backward(const LpBwdArgs& a, int per_row, hipStream_t stream) {
+  const int chunk = per_row * kVec<T> * U, slots = 256 / per_row;
+  const dim3 grid((unsigned int)((a.cols + chunk - 1) / chunk), row_grid((a.rows + slots - 1) / slots));
   // a gradient larger than half the last-level cache is stored around it
   if ((double)a.rows * (double)a.cols * sizeof(T) > kStreamOutBytes)
-    hipLaunchKernelGGL((lp_bwd_kernel<T, true>), grid, dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((lp_bwd_kernel<T, U, true>), grid, dim3(256), 0, stream, a, per_row);
   else
-    hipLaunchKernelGGL((lp_bwd_kernel<T, false>), grid, dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((lp_bwd_kernel<T, U, false>), grid, dim3(256), 0, stream, a, per_row);
   return hipGetLastError();
+}
+
+// Two vectors a thread (4096 x 50304 f32 272 us; 301 with four, 327 with one);
+// one where 256 threads then hold the row, and one or two waves where they do
+// (32768 x 1000 bf16 by 128 threads 28.6 us; by 256 41 us, with two vectors 60).
+template <class T>
+hipError_t backward(const LpBwdArgs& a, hipStream_t stream) {
+  const int64_t vecs = (a.cols + kVec<T> - 1) / kVec<T>;
+  if (vecs > 256) return backward<T, 2>(a, 256, stream);
+  return backward<T, 1>(a, vecs <= 64 ? 64 : vecs <= 128 ? 128 : 256, stream);
 }
 
 }  // namespace
