@@ -205,6 +205,39 @@ __device__ __forceinline__ int lane_rank(uint64_t mask) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
 }
 
+// The largest bar that at least k keys reach, or one that exactly k reach,
+// where at least k reach 1: steps down from the largest key, 4 times as far
+// each, then halving.
+struct Bar {
+  uint32_t bar;
+  int n;                                      // keys that reach it
+};
+template <class F>
+__device__ __forceinline__ Bar find_bar(uint32_t top, int k, F reach) {
+  uint32_t bar = 0, over = top + 1;           // reached by at least k, by fewer
+  int n = 0;
+  for (int shift = 20; shift < 32; shift += 2) {
+    const uint32_t b = top > 1u << shift ? top - (1u << shift) : 1;
+    n = reach(b);
+    if (n >= k) {
+      bar = b;
+      break;
+    }
+    over = b;
+  }
+  while (n != k && over - bar > 1) {
+    const uint32_t b = bar + (over - bar) / 2;
+    const int nb = reach(b);
+    if (nb >= k) {
+      bar = b;
+      n = nb;
+    } else {
+      over = b;
+    }
+  }
+  return Bar{bar, n};
+}
+
 // LDS of one wave's search.
 constexpr int kAbove = 256;                   // values above the bar
 constexpr int kEqual = 64;                    // and values that equal it, before they are scanned for
@@ -241,11 +274,6 @@ __device__ __forceinline__ Groups pick_groups(const LpArgs& a, const float* tops
 #pragma unroll
   for (int j = 0; j < K; ++j) top = max(top, key[j]);
   top = lanes_max_u32<64>(top);
-  // The largest bar that k groups reach, or one that exactly k reach: steps
-  // down from the largest key, 4 times as far each, then halving.  (A group
-  // without values has the key of -inf, so 1 is reached by all.)
-  uint32_t bar = 0, over = top + 1;           // reached by at least k, by fewer
-  int n = 0;
   auto reach = [&](uint32_t b) __attribute__((always_inline)) {
     int c = 0;
 #pragma unroll
@@ -253,25 +281,8 @@ __device__ __forceinline__ Groups pick_groups(const LpArgs& a, const float* tops
       if (64 * j < n_tops) c += __popcll(__ballot(key[j] >= b));
     return c;
   };
-  for (int shift = 20; shift < 32; shift += 2) {
-    const uint32_t b = top > 1u << shift ? top - (1u << shift) : 1;
-    n = reach(b);
-    if (n >= k) {
-      bar = b;
-      break;
-    }
-    over = b;
-  }
-  while (n != k && over - bar > 1) {
-    const uint32_t b = bar + (over - bar) / 2;
-    const int nb = reach(b);
-    if (nb >= k) {
-      bar = b;
-      n = nb;
-    } else {
-      over = b;
-    }
-  }
+  // (a group without values has the key of -inf, so 1 is reached by all)
+  const uint32_t bar = find_bar(top, k, reach).bar;
   // the groups above the bar (at most k), then those at it
   int n_again = 0, n_same = 0;
 #pragma unroll
@@ -511,6 +522,106 @@ __global__ void __launch_bounds__(64 * (kFinders + 1)) lp_join_kernel(LpArgs a) 
   }
 }
 
+// Short rows: a wave holds a whole row, C values a lane, and finds the best in
+// its registers.
+constexpr int kShort = 64 * 32;               // columns that one wave takes
+constexpr int kShortRows = 4;                 // of a workgroup
+
+template <class T, int C, bool TOP>
+__global__ void __launch_bounds__(64 * kShortRows, C <= 32 ? 4 : 1) lp_short_kernel(LpArgs a) {
+  constexpr int N = kVec<T>, U = C / N;
+  __shared__ unsigned long long lists[TOP ? kShortRows : 1][kTopMax + kPad];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cols = (int)a.cols, k = a.topk;
+  for (int64_t r = (int64_t)blockIdx.x * kShortRows + wave; r < a.rows; r += (int64_t)gridDim.x * kShortRows) {
+    const T* row = static_cast<const T*>(a.X) + r * a.ldx;
+    float v[U][N], m = kLowest, s = 0.0f, t = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_row<T>(row, (u * 64 + lane) * N, cols, -__builtin_inff(), v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < N; ++e) m = fmaxf(m, v[u][e]);
+    m = wave_max(m);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float d = __builtin_elementwise_maximum(v[u][e] - m, -104.0f);   // (a NaN stays)
+        const float p = exp_f32(d);
+        s += p;
+        t = __builtin_fmaf(p, d, t);
+      }
+    const PartSum p{wave_sum_f64((double)s), wave_sum_f64((double)t), m};
+    const RowOut o(p);
+    if (lane == 0) write_row<T>(a, r, p, o);
+    if constexpr (TOP) {
+      // The largest bar that k values reach, or one that exactly k reach.
+      uint32_t key[U][N], top = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          key[u][e] = (u * 64 + lane) * N + e < cols ? rank_key(v[u][e]) : 0;
+          top = max(top, key[u][e]);
+        }
+      top = lanes_max_u32<64>(top);
+      auto reach = [&](uint32_t b) __attribute__((always_inline)) {
+        int c = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 0; e < N; ++e) c += __popcll(__ballot(key[u][e] >= b));
+        return c;
+      };
+      const Bar bar = find_bar(top, k, reach);
+      // Those that reach it if they are k; else those above it, and of those
+      // that equal it the ones of lowest index.
+      const uint32_t least = bar.n == k ? bar.bar : bar.bar + 1;
+      unsigned long long* const list = lists[wave];
+      int n = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const uint64_t mask = __ballot(key[u][e] >= least);
+          if (key[u][e] >= least) list[n + lane_rank(mask)] = candidate(key[u][e], (u * 64 + lane) * N + e);
+          n += __popcll(mask);
+        }
+      for (int u = 0; u < U && n < k; ++u) {
+        int before = n, own = 0;
+        uint32_t hit = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          uint32_t x = 0;                     // (registers are not indexed by u)
+#pragma unroll
+          for (int i = 0; i < U; ++i) x = i == u ? key[i][e] : x;
+          const uint64_t mask = __ballot(x == bar.bar);
+          before += lane_rank(mask);
+          n += __popcll(mask);
+          hit |= (x == bar.bar ? 1u : 0u) << e;
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (hit >> e & 1u) {
+            if (before + own < k) list[before + own] = candidate(bar.bar, (u * 64 + lane) * N + e);
+            ++own;
+          }
+      }
+      if (lane < kPad) list[k + lane] = 0;
+      wave_sync();
+      // each of the k counts the better ones
+      const unsigned long long mine = lane < k ? list[lane] : 0;
+      int above = 0;
+      for (int j = 0; j < k; j += 8)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) above += list[j + e] > mine ? 1 : 0;
+      if (lane < k) write_best(a, r, above, mine, o.m, o.log_s, o.empty);
+      wave_sync();                            // the list is used again
+    }
+  }
+}
+
 // The gradient: a row by `per_row` threads (whole waves, 256 at most) of a
 // workgroup of 256, U vectors a thread.
 template <class T, int U, bool STREAM>
@@ -565,8 +676,31 @@ __global__ void __launch_bounds__(256) lp_bwd_kernel(LpBwdArgs a, int per_row) {
 // Rows are the grid's y; the workgroups walk on where there are more.
 unsigned int row_grid(int64_t rows) { return (unsigned int)(rows < 65535 ? rows : 65535); }
 
+template <class T, int C, bool TOP>
+hipError_t forward_short(const LpArgs& a, hipStream_t stream) {
+  const int64_t most = int64_t(1) << 20, groups = (a.rows + kShortRows - 1) / kShortRows;
+  const dim3 grid((unsigned int)(groups < most ? groups : most)), block(64 * kShortRows);
+  if constexpr (TOP)
+    if (a.topk > 0) {
+      hipLaunchKernelGGL((lp_short_kernel<T, C, true>), grid, block, 0, stream, a);
+      return hipGetLastError();
+    }
+  hipLaunchKernelGGL((lp_short_kernel<T, C, false>), grid, block, 0, stream, a);
+  return hipGetLastError();
+}
+
+// Rows of up to 2048 columns by a wave each (by the kernels of longer rows in
+// parentheses, bf16): 32768 x 1000 29.6 us (148), with 5 alternatives 63 (160);
+// 128 x 1500 with 20 alternatives 20.0 (18.2), with 32 21.0 (39.2), where a
+// batch leaves fewer maxima than that; 1 x 1000 3.3 (3.8).  Up to 4096 where
+// nothing is searched for and there are rows for every SIMD: 8192 x 4096 22.5
+// (37.4), 1024 x 4096 6.3 (7.2), 128 x 4096 6.3 (4.3); 8192 x 8192 53 (48).
 template <class T>
 hipError_t forward(const LpArgs& a, hipStream_t stream) {
+  if (a.cols <= 64 * 8) return forward_short<T, 8, true>(a, stream);
+  if (a.cols <= 64 * 16) return forward_short<T, 16, true>(a, stream);
+  if (a.cols <= kShort) return forward_short<T, 32, true>(a, stream);
+  if (a.cols <= 2 * kShort && a.topk == 0 && a.rows >= 1024) return forward_short<T, 64, false>(a, stream);
   const dim3 grid(a.parts, row_grid(a.rows)), block(kThreads);
   if (a.topk > 0)
     hipLaunchKernelGGL((lp_part_kernel<T, true>), grid, block, 0, stream, a);
@@ -606,8 +740,9 @@ hipError_t backward(const LpBwdArgs& a, hipStream_t stream) {
 }  // namespace
 
 // Parts of a row, of whole batches: as many as its length needs, and with few
-// rows as many as fill the chip.
+// rows as many as fill the chip.  (None of a row that a wave holds.)
 LpSplit lp_split(int64_t rows, int64_t cols) {
+  if (cols <= kShort) return LpSplit{0, 0, 0, 0};
   const int64_t batches = (cols + kBatch - 1) / kBatch;
   const int64_t need = (batches + kPartBatches - 1) / kPartBatches;
   const int64_t fill = rows >= 512 ? 1 : (512 + rows - 1) / rows;

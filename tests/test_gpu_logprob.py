@@ -119,6 +119,21 @@ def hard_rows(vocab, dt, rng):
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,vocab,topk", [
+    (5, 512, 32), (5, 513, 9), (6, 1024, 32), (6, 1025, 32), (7, 2048, 20), (7, 2049, 20), (1030, 2050, 0), (1025, 4096, 0)])
+def test_forward_rows_of_a_wave(g, rows, vocab, topk, dtype):
+    """The lengths around which rows are held by one wave, in 8, 16, 32 or 64 values a lane."""
+    test_forward(g, rows, vocab, topk, dtype)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("vocab,topk", [(513, 32), (2047, 20)])
+@pytest.mark.parametrize("copies", [1, 40])
+def test_hard_rows_of_a_wave(g, vocab, topk, dtype, copies):
+    test_hard_rows(g, vocab, topk, dtype, copies)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("vocab,topk", [(40, 32), (5000, 20), (50257, 32), (70001, 20)])
 @pytest.mark.parametrize("copies", [1, 40])
 def test_hard_rows(g, vocab, topk, dtype, copies):
