@@ -521,7 +521,9 @@ __global__ void __launch_bounds__(256) ln_bwd_cols_kernel(const double* __restri
 // the 2-byte types for a row of one wave that whole vectors of 8 values would
 // fill to less.  8192 x 768 bf16: into codes and restored 16.2 us with 4
 // values a vector and 18.5 with 8, backward 14.3 and 18.1; 8192 x 1024, which
-// both fill: 8.2 us with 8 and 10.9 with 4.
+// both fill: 8.2 us with 8 and 10.9 with 4.  Longer rows take 3 vectors of 4
+// where those hold them: 8192 x 1280 bf16 13.2 us and backward 23.7 (14.5 and
+// 31.9 with 16 values a lane), 8192 x 6144 bf16 39.0 and 80.4 (46.0 and 80.2).
 struct RowShape {
   int waves, n, nv;   // waves == 0: too long to hold
 };
@@ -534,7 +536,8 @@ RowShape row_shape(int64_t cols, int vec) {
   }
   int w = 2;
   while (w * 1024 < cols) w *= 2;
-  return RowShape{w, vec, 16 / vec};
+  const int n = cols <= w * 768 ? 4 : vec;
+  return RowShape{w, n, cols <= w * 768 ? 3 : 16 / vec};
 }
 
 // Workgroups of a kernel whose workgroups walk the rows.
@@ -564,10 +567,10 @@ void with_shape(const RowShape& s, F f) {
         if (s.nv == 3) return f(Int<4>{}, Int<3>{}, Int<1>{});
         return f(Int<4>{}, Int<4>{}, Int<1>{});
       }
-    case 2: return f(Int<V>{}, Int<M>{}, Int<2>{});
-    case 4: return f(Int<V>{}, Int<M>{}, Int<4>{});
-    case 8: return f(Int<V>{}, Int<M>{}, Int<8>{});
-    default: return f(Int<V>{}, Int<M>{}, Int<16>{});
+    case 2: return s.nv == 3 ? f(Int<4>{}, Int<3>{}, Int<2>{}) : f(Int<V>{}, Int<M>{}, Int<2>{});
+    case 4: return s.nv == 3 ? f(Int<4>{}, Int<3>{}, Int<4>{}) : f(Int<V>{}, Int<M>{}, Int<4>{});
+    case 8: return s.nv == 3 ? f(Int<4>{}, Int<3>{}, Int<8>{}) : f(Int<V>{}, Int<M>{}, Int<8>{});
+    default: return s.nv == 3 ? f(Int<4>{}, Int<3>{}, Int<16>{}) : f(Int<V>{}, Int<M>{}, Int<16>{});
   }
 }
 

@@ -260,3 +260,13 @@ def test_far_rows(g):
     _, mean, rstd = g.layer_norm(values)
     for a, b in zip(g.layer_norm_bwd(X, X, mean, rstd), g.layer_norm_bwd(values, values, mean, rstd)):
         same_bits(a, b, "gradients of far rows")
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,cols", [(3, 1280), (517, 1536), (3, 1537), (2, 3071), (259, 6144), (2, 6145), (2, 12287)])
+def test_rows_of_three_vectors_a_lane(g, rows, cols, dtype):
+    """The widths around which several waves hold a row in 12 or in 16 values a lane."""
+    test_forward(g, rows, cols, dtype)
+    test_forward_into_codes(g, rows, cols, dtype)
+    test_backward(g, rows, cols, dtype)
+    test_backward_from_checkpoint(g, rows, cols, 64, dtype)
