@@ -393,8 +393,9 @@ int layer_norm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ldx, uin
  *   scale  rows x ceil(cols/group) f32, leading dimension lds.
  * A value is off by at most half its group's scale, a(group)/254, and the
  * roundings of s and RN(q*s): RN(127*s) may be above a by 2^-23 of it, which
- * overflows for |a| within 2^-22 of the largest binary32 value.  A group with an infinity or a NaN gets a NaN scale
- * and codes 0, so that it restores as NaN.
+ * overflows for |a| within 2^-22 of the largest binary32 value.  A group with
+ * an infinity or a NaN gets a NaN scale and codes 0, so that it restores as
+ * NaN.
  * The calls that read a checkpoint also take group = 0, one scale per row,
  * scale[i * lds]: with lds = 1 that is the output of quantize_rows or of
  * layer_norm_quantize_rows, so the codes a GEMM has read serve as the saved
@@ -467,8 +468,8 @@ int layer_norm_bwd_checkpoint(const void* dY, int64_t lddy, uint32_t dtype, cons
  *   top_index, top_logprob  rows x topk int32 / f32 (not used for topk 0).
  *   workspace  device scratch of token_logprobs_workspace_bytes(rows, vocab,
  *            topk), 256-byte aligned, any contents; NULL where that is 0
- *            (topk 0 with many rows, or short ones).  With topk it holds 256
- *            bytes for each 8192 columns of a row.
+ *            (rows of up to 2048 columns; topk 0 with many rows).  With topk
+ *            it holds 256 bytes for each 8192 columns of a row.
  * Sums are held against the row's maximum, in binary32 over at most 128
  * values and binary64 beyond.  A logit of -inf has probability 0 and adds
  * nothing to the entropy.  A row of -inf only has lse and every log

@@ -362,12 +362,20 @@ hipError_t launch_checkpoint_cols(const Checkpoint& c, int8_t* Qt, int64_t ldqt,
     return hipGetLastError();
   }
   uint32_t* p = static_cast<uint32_t*>(parts);
-  const unsigned int bx = (unsigned int)((c.cols + kTileCols - 1) / kTileCols);
   const int n = cols_parts(c.rows);
   const int64_t tiles = row_tiles(c.rows);
-  hipLaunchKernelGGL(checkpoint_cols_max_kernel, dim3(bx, n), dim3(256), 0, stream, c, p);
-  hipLaunchKernelGGL(checkpoint_cols_quant_kernel, dim3(bx, (unsigned int)(tiles < 4096 ? tiles : 4096)), dim3(256), 0, stream,
-                     c, Qt, ldqt, scale, p, n);
+  // a launch holds fewer than 2^32 threads, 4 a column; slabs of columns are whole groups
+  const int64_t slab = int64_t(1) << 29;
+  for (int64_t j = 0; j < c.cols; j += slab) {
+    Checkpoint part = c;
+    part.Q += j;
+    part.scale += j >> c.gshift;
+    part.cols = c.cols - j < slab ? c.cols - j : slab;
+    const unsigned int bx = (unsigned int)((part.cols + kTileCols - 1) / kTileCols);
+    hipLaunchKernelGGL(checkpoint_cols_max_kernel, dim3(bx, n), dim3(256), 0, stream, part, p);
+    hipLaunchKernelGGL(checkpoint_cols_quant_kernel, dim3(bx, (unsigned int)(tiles < 4096 ? tiles : 4096)), dim3(256),
+                       0, stream, part, Qt + j * ldqt, ldqt, scale + j, p, n);
+  }
   return hipGetLastError();
 }
 

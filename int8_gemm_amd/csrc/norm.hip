@@ -625,8 +625,15 @@ hipError_t ln_bwd(const LnBwdArgs& a, float* dgamma, float* dbeta, hipStream_t s
   if (a.parts) {
     const int64_t held = apart ? a.cols : (int64_t)s.waves * 64 * s.n * s.nv;
     const int order = apart ? 1 : s.n;
-    hipLaunchKernelGGL(ln_bwd_cols_kernel, dim3((unsigned int)((held + 15) / 16), 2), dim3(256), 0, stream, a.parts,
-                       groups, held, order, a.cols, dgamma, dbeta);
+    // a launch holds fewer than 2^32 threads, 16 a column; a slab starts where
+    // the columns are in order (only long rows take more than one)
+    const int64_t slab = int64_t(1) << 27;
+    for (int64_t j = 0; j < held; j += slab) {
+      const int64_t n = held - j < slab ? held - j : slab;
+      const int64_t cols = a.cols - j < slab ? a.cols - j : slab;
+      hipLaunchKernelGGL(ln_bwd_cols_kernel, dim3((unsigned int)((n + 15) / 16), 2), dim3(256), 0, stream, a.parts + j,
+                         groups, held, order, cols, dgamma ? dgamma + j : dgamma, dbeta ? dbeta + j : dbeta);
+    }
   }
   return hipGetLastError();
 }

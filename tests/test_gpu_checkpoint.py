@@ -225,3 +225,23 @@ def test_far_rows(g):
     same_bits(g.checkpoint_restore(far, S, 128), g.checkpoint_restore(Q, S, 128), "restored")
     for a, b in zip(g.checkpoint_quantize_cols(far, S, 128), g.checkpoint_quantize_cols(Q, S, 128)):
         same_bits(a, b, "columns")
+
+
+def test_quantize_cols_of_2_30_columns(g):
+    """More columns than one launch takes, against calls on some of them."""
+    rows, cols, group = 2, (1 << 30) + 70, 128
+    say("ckpt quantize_cols", rows, cols)
+    lib, st = g.load(), torch.cuda.current_stream().cuda_stream
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    Q = torch.randint(-127, 128, (rows, cols), generator=gen, device="cuda", dtype=torch.int8)
+    s = torch.rand((rows, -(-cols // group)), generator=gen, device="cuda") + 0.01
+    Qt = torch.empty((cols, rows), dtype=torch.int8, device="cuda")
+    scale = torch.empty(cols, device="cuda")
+    ws = torch.empty(lib.checkpoint_quantize_cols_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    assert lib.checkpoint_quantize_cols(Q.data_ptr(), cols, s.data_ptr(), s.shape[1], group, rows, cols, Qt.data_ptr(),
+                                        rows, scale.data_ptr(), ws.data_ptr(), ws.numel(), st) == 0
+    for lo, hi in ((0, 300), ((1 << 29) - 256, (1 << 29) + 300), ((1 << 30) - 128, cols)):
+        part = Q[:, lo:hi]
+        qt, sc = g.checkpoint_quantize_cols(part, s[:, lo // group:-(-hi // group)], group)
+        same_bits(Qt[lo:hi], qt, f"codes from {lo}")
+        same_bits(scale[lo:hi], sc, f"scales from {lo}")

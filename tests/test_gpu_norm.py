@@ -270,3 +270,17 @@ def test_rows_of_three_vectors_a_lane(g, rows, cols, dtype):
     test_forward_into_codes(g, rows, cols, dtype)
     test_backward(g, rows, cols, dtype)
     test_backward_from_checkpoint(g, rows, cols, 64, dtype)
+
+
+def test_weight_gradient_of_a_row_of_2_28_columns(g):
+    """More columns than one launch sums.  With mean 0 and rstd 1 and one row
+    dbeta is dY and dgamma the product of two bf16 values, exact in f32; a sum
+    starts from +0, and +0 + -0 is +0."""
+    cols = (1 << 28) + 100
+    say("ln weight gradient", cols)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    dY, X = (torch.randn((1, cols), generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    mean, rstd = torch.zeros(1, device="cuda"), torch.ones(1, device="cuda")
+    _, dw, db = g.layer_norm_bwd(dY, X, mean, rstd)
+    same_bits(db, dY[0].float() + 0.0, "dbeta")
+    same_bits(dw, dY[0].float() * X[0].float() + 0.0, "dgamma")
