@@ -21,6 +21,12 @@
 // once, a row staying in registers in between.  A row of up to 1024 values is
 // held by one wave, 16 values a lane; a longer one by 2 to 16 waves of one
 // workgroup; rows beyond 16384 values are read again instead of held.
+//
+// 8192 x 768 f32, which the 256 MB cache holds (a copy there moves 6.9 TB/s):
+// forward 10.2 us (50 MB, 4.9 TB/s), into codes 10.8 us (31 MB), backward 15.6 us
+// (75 MB, 4.8 TB/s) and 3.9 us for the columns' sums.  About 2 us of each are
+// the launch and the first load; in codes the row's second reduction and the
+// quantizing are most of the rest.
 #include <type_traits>
 
 #include "i8g_launch.h"
@@ -41,9 +47,9 @@ __device__ __forceinline__ double rsqrt_f64(double a) {
 }
 
 // Row sums of two binary64 values over the W waves (consecutive ones of the
-// workgroup) that share a row; the result is in every lane.  `red` has two halves used in turn, so one
-// barrier per call is enough: a wave can reach the call after the next one
-// only when every wave has read this one's half.
+// workgroup) that share a row; the result is in every lane.  `red` has two
+// halves used in turn, so one barrier per call is enough: a wave can reach the
+// call after the next one only when every wave has read this one's half.
 template <int W>
 __device__ __forceinline__ void row_sum2(double& a, double& b, double (*red)[2 * W], int& turn) {
   a = wave_sum_f64(a);

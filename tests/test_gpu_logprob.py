@@ -310,3 +310,20 @@ def test_far_rows(g):
     want = g.token_logprobs_bwd(values, t, a[2], a[1], one, one)
     same_bits(g.token_logprobs_bwd(X, t, a[2], a[1], one, one), want, "gradient of far rows")
     same_bits(g.token_logprobs_bwd(X, t, a[2], a[1], one, one, out=X).contiguous(), want, "in place")
+
+
+@pytest.mark.parametrize("rows,vocab,topk", [(5, 300, 0), (5, 2000, 4), (1100, 4000, 0), (5, 50257, 4), (600, 8200, 2)])
+def test_nan_of_any_payload(g, rows, vocab, topk):
+    """A NaN makes its row's outputs NaN whatever bits it has, and no other row's."""
+    say("logprobs NaN payloads", rows, vocab, topk)
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    X = torch.randn((rows, vocab), generator=gen, device="cuda")
+    words = X.view(torch.int32)
+    for r, w in enumerate((0x7F800001, 0x7FC00001, 0x7FFFFFFF, 0x7FC001FF - (1 << 32) + 0x80000000)):
+        words[r, (r * 77 + 5) % vocab] = w
+    t = torch.zeros(rows, dtype=torch.int64, device="cuda")
+    out = g.token_logprobs(X, t, topk)
+    for name, o in zip(("logprob", "entropy", "lse"), out):
+        assert torch.isnan(o[:4]).all() and not torch.isnan(o[4:]).any(), name
+    if topk:
+        assert torch.isnan(out[4][:4]).all() and not torch.isnan(out[4][4:]).any()
