@@ -323,7 +323,9 @@ int output_hash(const float* C, int64_t M, int64_t N, int64_t ldc,
  * are allowed here: they make their own row (for a checkpoint their own
  * group, for a column sum or column scale their own column) NaN and nothing
  * else.  Results depend on sizes and values only, never on timing: no sum is
- * taken with atomics, and two calls give the same bytes.
+ * taken with atomics, and two calls give the same bytes.  Outputs and the
+ * workspace overlap nothing else, except where a call names an input that an
+ * output may be.
  * ------------------------------------------------------------------------ */
 #define I8G_F32  0u
 #define I8G_BF16 1u

@@ -17,6 +17,8 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -73,17 +75,25 @@ def build_bind(verbose: bool = False) -> str:
     return BIND_PATH
 
 
-def build(verbose: bool = False, asm_dir: str = None) -> str:
-    cc = hipcc()
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    tmp = LIB_PATH + ".tmp"
-    cmd = [cc, *common_flags(), "-shared", "-o", tmp, *srcs]
+def _run(cmd, verbose: bool):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError(f"hipcc failed with status {res.returncode}")
+
+
+def build(verbose: bool = False, asm_dir: str = None) -> str:
+    cc = hipcc()
+    srcs = [os.path.join(CSRC, s) for s in SOURCES]
+    tmp = LIB_PATH + ".tmp"
+    with tempfile.TemporaryDirectory() as objs:
+        out = [os.path.join(objs, os.path.basename(s) + ".o") for s in srcs]
+        cmds = [[cc, *common_flags(), "-c", "-o", o, s] for o, s in zip(out, srcs)]
+        with ThreadPoolExecutor(min(len(srcs), os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda cmd: _run(cmd, verbose), cmds))
+        _run([cc, *common_flags(), "-shared", "-o", tmp, *out], verbose)
     # A kernel template whose host-side instantiation fails leaves its launch
     # stub undefined: the link succeeds, but loading the library would not.
     nm = shutil.which("nm")

@@ -9,7 +9,7 @@
 // they would have read a value.  All are bound by memory: 8192 x 3072 f32 in
 // groups of 128 is stored in 20.8 us and restored in 19.9 (126 MB each, 6.1
 // and 6.3 TB/s; a copy within the 256 MB cache moves 6.9), the gradient of GELU
-// in bf16 takes 23.7 us (126 MB, 5.3 TB/s; its 27 operations a value are next),
+// in bf16 takes 23.7 us (126 MB, 5.3 TB/s; its 42 instructions a value are next),
 // the columns of 8192 x 768 5.2 and 8.0 us (two passes over 6.3 MB, 2 us of
 // each the launch and the first load).
 #include "i8g_launch.h"
