@@ -356,8 +356,12 @@ __global__ void __launch_bounds__(W == 16 ? 1024 : 512) ln_bwd_kernel(LnBwdArgs 
           }
           x[i][e] = xh;
           w[i][e] = mul_rn(dy, g[i][e]);
-          s1 += (double)w[i][e];                          // (dy and so w are 0 behind the row's end)
-          s2 = __builtin_fma((double)w[i][e], (double)xh, s2);
+          s1 += (double)w[i][e];                          // (0 behind the row's end)
+          // Behind the row's end dy and w are 0, but RN(0 - mean) * rstd may be infinite where no value of the row
+          // has such an xh (equal ones, far out), and 0 times that is a NaN.  (Up to 2.5% of the pass; xh
+          // itself set to 0 takes up to 5%, vectors that end and those that do not told apart 10%.)
+          const bool inside = c0 + i * 64 * N + e < cols;
+          s2 = __builtin_fma((double)w[i][e], (double)(inside ? xh : 0.0f), s2);
         }
       if (r + step < a.rows) fetch(cur, r + step);
     }

@@ -284,3 +284,35 @@ def test_weight_gradient_of_a_row_of_2_28_columns(g):
     _, dw, db = g.layer_norm_bwd(dY, X, mean, rstd)
     same_bits(db, dY[0].float() + 0.0, "dbeta")
     same_bits(dw, dY[0].float() * X[0].float() + 0.0, "dgamma")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [5, 768, 1000, 1024, 1280, 1500, 1600, 2500, 5000, 9000, 12000, 16390])
+def test_backward_of_equal_rows(g, cols, dtype):
+    """Rows of equal values: x - mean is 0 and so is xh, however large the
+    values and rstd are; the rows are as finite as any, whether the lanes that
+    hold them are full (768, 1024) or not.  |mean| * rstd is beyond binary32 in
+    four of them, the type's lowest value among those."""
+    say("ln backward of equal rows", cols, dtype)
+    rows, dt = 9, DTYPES[dtype]
+    rng = np.random.default_rng(cols)
+    w, _, wt, _ = affine(rng, cols)
+    X, dY, mean, rstd = grads_input(rng, rows, cols, dt, cols % 3, cols % 2)
+    r5, r12 = np.float32(1 / np.sqrt(1e-5)), np.float32(1 / np.sqrt(1e-12))
+    # 127 * 2^k: its 8-bit checkpoint restores it exactly
+    for r, value, rs in ((0, 127 * 2.0 ** 114, r5), (2, -127 * 2.0 ** 114, r5), (4, 127 * 2.0 ** 104, r12), (6, 1.0, r12)):
+        X[r], mean[r], rstd[r] = value, value, rs
+    mt, rt = torch.from_numpy(mean).cuda(), torch.from_numpy(rstd).cuda()
+    for group in (0, 64):
+        Q, S = g.checkpoint_i8(X, group) if group else g.quantize_rows(X.float())
+        restored = R.checkpoint_restore(Q.cpu().numpy(), S.cpu().numpy(), group)
+        got = g.layer_norm_bwd_checkpoint(dY, Q, S, group, mt, rt, wt)
+        check_grads(got, R.ln_bwd64(host(dY), restored, mean, rstd, w), dt, "equal rows from a checkpoint")
+    lowest = torch.finfo(dt).min
+    X[8], mt[8], rt[8] = lowest, lowest, float(r5)
+    mean[8], rstd[8] = lowest, r5
+    for weight in (True, False):
+        got = g.layer_norm_bwd(dY, X, mt, rt, wt if weight else None)
+        check_grads(got, R.ln_bwd64(host(dY), host(X), mean, rstd, w if weight else None), dt, "equal rows")
+        alone = g.layer_norm_bwd(dY, X, mt, rt, wt if weight else None, weight_grad=False)
+        same_bits(alone[0], got[0], "dX alone")
