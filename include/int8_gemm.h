@@ -320,12 +320,13 @@ int output_hash(const float* C, int64_t M, int64_t N, int64_t ldc,
  * dimension >= cols and the alignment of their element type; every matrix of
  * values in one call has the same dtype.  Statistics, scales, weights and
  * their gradients are f32.  Sizes are at most 2^31 - 1.  Infinities and NaN
- * are allowed here: they make their own row (for a checkpoint their own
- * group, for a column sum or column scale their own column) NaN and nothing
- * else.  Results depend on sizes and values only, never on timing: no sum is
- * taken with atomics, and two calls give the same bytes.  Outputs and the
- * workspace overlap nothing else, except where a call names an input that an
- * output may be.
+ * are allowed here: one in X makes its row NaN (in a checkpoint its group of
+ * the row, and in a checkpoint's column codes its column) and nothing else,
+ * one in dY of checkpoint_act_bwd its own value; layer_norm_bwd and the log
+ * probabilities say what becomes of theirs.  Results depend on sizes and
+ * values only, never on timing: no sum is taken with atomics, and two calls
+ * give the same bytes.  Outputs and the workspace overlap nothing else, except
+ * where a call names an input that an output may be.
  * ------------------------------------------------------------------------ */
 #define I8G_F32  0u
 #define I8G_BF16 1u
@@ -341,7 +342,9 @@ int output_hash(const float* C, int64_t M, int64_t N, int64_t ldc,
  *   X, Y   rows x cols of `dtype`; Y may be X itself (with ldy = ldx).
  *   gamma, beta  cols f32 each, or NULL for ones / zeros.
  *   mean, rstd   rows f32 each (inputs of the backward pass), or NULL.
- * A row of one value or of equal values has var = 0 and gives beta.
+ * A row of one value or of equal values has var = 0 and rstd = RN(1 / sqrt(eps)),
+ * and gives beta; where that rstd is infinite in binary32 (eps 0, or below
+ * 8.6e-78) it gives NaN.
  * Errors: I8G_EINVAL (null pointer, unknown dtype, negative size, cols == 0
  * with rows > 0, leading dimension < cols, misaligned element pointer, eps
  * negative or not finite), I8G_EHIP.
@@ -378,6 +381,11 @@ int layer_norm_quantize_rows(const void* X, uint32_t dtype, int64_t rows, int64_
  *   workspace  device scratch of layer_norm_bwd_workspace_bytes(rows, cols),
  *          256-byte aligned, any contents; not needed (may be NULL) when
  *          dgamma and dbeta are both NULL.
+ * A row of X with an infinity or a NaN (layer_norm gives it a NaN rstd), or of
+ * equal values with an infinite rstd, has dX NaN and makes every column of
+ * dgamma NaN; dbeta does not depend on it.  An infinity or a NaN in dY leaves
+ * its row of dX and its column of dgamma and of dbeta without finite values
+ * (infinite or NaN).  Other rows of dX and other columns are as without them.
  * Errors: as layer_norm, and I8G_EWORKSPACE.
  */
 size_t layer_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
@@ -449,7 +457,8 @@ int checkpoint_quantize_cols(const int8_t* Q, int64_t ldq, const float* scale, i
 /*
  * layer_norm_bwd_checkpoint -- layer_norm_bwd with the input's values taken
  * from its checkpoint, x = RN(q * s); mean and rstd are those of the input
- * that the forward pass saw.  Arguments otherwise as layer_norm_bwd.
+ * that the forward pass saw.  Arguments otherwise as layer_norm_bwd; a NaN
+ * scale makes its row of dX and the group's columns of dgamma NaN.
  */
 int layer_norm_bwd_checkpoint(const void* dY, int64_t lddy, uint32_t dtype, const int8_t* Q,
                               int64_t ldq, const float* scale, int64_t lds, int32_t group,

@@ -316,3 +316,82 @@ def test_backward_of_equal_rows(g, cols, dtype):
         check_grads(got, R.ln_bwd64(host(dY), host(X), mean, rstd, w if weight else None), dt, "equal rows")
         alone = g.layer_norm_bwd(dY, X, mt, rt, wt if weight else None, weight_grad=False)
         same_bits(alone[0], got[0], "dX alone")
+
+
+@pytest.mark.parametrize("cols", [1, 300, 5000, 20000])
+def test_equal_values_give_beta(g, cols):
+    """var is 0: beta where 1 / sqrt(eps) is finite in binary32, NaN where not."""
+    say("ln equal values", cols)
+    rng = np.random.default_rng(cols)
+    w, b, wt, bt = affine(rng, cols)
+    for dt in DTYPES.values():
+        X = torch.tensor([0.0, 3.25, -1e-3, torch.finfo(dt).min, torch.finfo(dt).max]).to(dt).cuda()[:, None].repeat(1, cols)
+        for eps in (1e-5, 1e-30, 8.7e-78, 8.6e-78, 0.0):
+            Y, mean, rstd = g.layer_norm(X, wt, bt, eps)
+            same_bits(mean, X[:, 0].float(), "mean")
+            Q, s, _, _ = g.layer_norm_quantize_rows(X, wt, bt, eps)
+            if eps > 8.65e-78:
+                # (rstd is half a step off at most, and the root's own 2^-50)
+                within(host(rstd), np.full(5, 1 / np.sqrt(eps)), 1.001 * U / np.sqrt(eps), "rstd")
+                same_bits(Y, bt.to(dt).expand(5, cols), "Y")
+                q, sc = ref.quantize_rows(np.tile(b, (5, 1)))
+                assert np.array_equal(Q.cpu().numpy(), q) and np.array_equal(s.cpu().numpy(), sc)
+            else:
+                assert torch.isinf(rstd).all() and torch.isnan(Y).all() and torch.isnan(s).all() and (Q == 0).all()
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("cols", [7, 768, 1000, 1600, 5000, 9000, 17000])
+def test_backward_of_rows_that_are_not_finite(g, cols, dtype):
+    """What an infinity or a NaN in X, in dY or in a checkpoint's scale reaches,
+    and the rest as without it."""
+    say("ln backward not finite", cols, dtype)
+    rows, dt = 19, DTYPES[dtype]
+    rng = np.random.default_rng(cols)
+    w, _, wt, _ = affine(rng, cols)
+    X, dY, _, _ = grads_input(rng, rows, cols, dt, cols % 3, cols % 2)
+    _, mean, rstd = g.layer_norm(X)
+    clean = g.layer_norm_bwd(dY, X, mean, rstd, wt)
+    last = cols - 1
+    # in X: its row of dX and all of dgamma
+    Z = X.clone()
+    Z[3, last], Z[8, 0], Z[8, 2], Z[10, cols // 2] = float("inf"), float("inf"), -float("inf"), float("nan")
+    bad, good = [3, 8, 10], [r for r in range(rows) if r not in (3, 8, 10)]
+    _, zm, zr = g.layer_norm(Z)
+    assert torch.isnan(zr[bad]).all()
+    dX, dw, db = g.layer_norm_bwd(dY, Z, zm, zr, wt)
+    assert torch.isnan(dX[bad]).all() and torch.isnan(dw).all()
+    same_bits(dX[good], clean[0][good], "dX of the other rows")
+    same_bits(db, clean[2], "dbeta")
+    # a row of equal values with an infinite rstd
+    Z = X.clone()
+    Z[5] = 1.5
+    _, zm, zr = g.layer_norm(Z, eps=0.0)
+    assert torch.isinf(zr[5])
+    dX, dw, db = g.layer_norm_bwd(dY, Z, zm, zr, wt)
+    assert torch.isnan(dX[5]).all() and torch.isnan(dw).all() and torch.isfinite(dX[[4, 6]]).all()
+    same_bits(db, clean[2], "dbeta of a row without a norm")
+    # in dY: its row of dX, its columns of dgamma and dbeta
+    D = dY.clone()
+    D[2, 1], D[6, last], D[18, 3] = float("inf"), float("nan"), -float("inf")
+    bad, good = [2, 6, 18], [r for r in range(rows) if r not in (2, 6, 18)]
+    hit = torch.zeros(cols, dtype=torch.bool, device="cuda")
+    hit[[1, 3, last]] = True
+    dX, dw, db = g.layer_norm_bwd(D, X, mean, rstd, wt)
+    assert not torch.isfinite(dX[bad].float()).any()
+    same_bits(dX[good], clean[0][good], "dX of the other rows")
+    for got, want, name in ((dw, clean[1], "dgamma"), (db, clean[2], "dbeta")):
+        assert not torch.isfinite(got[hit]).any(), name
+        same_bits(got[~hit], want[~hit], name + " of the other columns")
+    # a checkpoint's scale: its row of dX, its group's columns of dgamma
+    Q, S = g.checkpoint_i8(X, 32)
+    clean = g.layer_norm_bwd_checkpoint(dY, Q, S, 32, mean, rstd, wt)
+    S[4, 0] = S[11, -1] = float("nan")
+    group = torch.arange(cols, device="cuda") // 32
+    hit = (group == 0) | (group == group[-1])
+    good = [r for r in range(rows) if r not in (4, 11)]
+    dX, dw, db = g.layer_norm_bwd_checkpoint(dY, Q, S, 32, mean, rstd, wt)
+    assert torch.isnan(dX[[4, 11]]).all() and torch.isnan(dw[hit]).all()
+    same_bits(dX[good], clean[0][good], "dX of the other rows")
+    same_bits(dw[~hit], clean[1][~hit], "dgamma of the other groups")
+    same_bits(db, clean[2], "dbeta")
