@@ -326,7 +326,8 @@ int output_hash(const float* C, int64_t M, int64_t N, int64_t ldc,
  * probabilities say what becomes of theirs.  Results depend on sizes and
  * values only, never on timing: no sum is taken with atomics, and two calls
  * give the same bytes.  Outputs and the workspace overlap nothing else, except
- * where a call names an input that an output may be.
+ * where a call names an input that an output may be: with the same leading
+ * dimension, never a part of it or a shifted view (I8G_EINVAL).
  * ------------------------------------------------------------------------ */
 #define I8G_F32  0u
 #define I8G_BF16 1u
@@ -511,7 +512,8 @@ int token_logprobs(const void* logits, uint32_t dtype, int64_t rows, int64_t voc
  * more than a factor e (a row of -inf only, one masked by the type's lowest
  * value throughout), gets 0.
  *   dlogits  rows x vocab of dtype; it may be logits itself (lddl = ld).
- * Errors: as token_logprobs.
+ * Errors: as token_logprobs; I8G_EINVAL also where dlogits overlaps logits
+ * otherwise, or any of the vectors.
  */
 int token_logprobs_bwd(const void* logits, uint32_t dtype, int64_t rows, int64_t vocab, int64_t ld,
                        const int64_t* targets, const float* lse, const float* entropy,

@@ -627,5 +627,6 @@ def token_logprobs(logits, targets, topk=0):
 
 def token_logprobs_bwd(logits, targets, lse, entropy=None, g_logprob=None, g_entropy=None, out=None):
     """The gradient of the logits for those of the log probabilities and the
-    entropies of token_logprobs (either may be None); out may be logits."""
+    entropies of token_logprobs (either may be None); out may be logits, but
+    not overlap them or the vectors otherwise."""
     return _rowops().token_logprobs_bwd(logits, targets, lse, entropy, g_logprob, g_entropy, out)

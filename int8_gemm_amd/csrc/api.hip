@@ -10,6 +10,7 @@
 #include "../../include/int8_gemm.h"
 #include "i8g_device.h"
 #include "i8g_launch.h"
+#include "i8g_overlap.h"
 
 using namespace i8g;
 
@@ -267,6 +268,14 @@ static bool bad_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, in
   if (ld < cols) return true;
   return rows > 0 && cols > 0 && (!p || (uintptr_t)p % (uintptr_t)bytes != 0);
 }
+static ByteRows byte_rows(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t bytes) {
+  return ByteRows{(uintptr_t)p, rows, cols * bytes, rows > 1 ? ld * bytes : 0};
+}
+// An output that may be the input of the same shape and type, but not part of it.
+static bool bad_in_place(const void* out, int64_t ldo, const void* in, int64_t ldi, int64_t rows, int64_t cols,
+                         int64_t bytes) {
+  return !itself_or_apart(byte_rows(out, rows, cols, ldo, bytes), byte_rows(in, rows, cols, ldi, bytes));
+}
 static bool bad_f32(const void* p) { return (uintptr_t)p % 4 != 0; }   // (null is aligned)
 
 static bool bad_sizes(int64_t rows, int64_t cols) {
@@ -282,6 +291,7 @@ static int layer_norm_fwd(const void* X, uint32_t dtype, int64_t rows, int64_t c
   if (bad_f32(gamma) || bad_f32(beta) || bad_f32(scale) || bad_f32(mean) || bad_f32(rstd)) return I8G_EINVAL;
   if (!(eps >= 0.0 && eps <= 1.7976931348623157e308)) return I8G_EINVAL;
   if (y_bytes && rows > 0 && !scale) return I8G_EINVAL;
+  if (!y_bytes && bad_in_place(Y, ldy, X, ldx, rows, cols, bytes)) return I8G_EINVAL;
   if (rows == 0) return I8G_OK;
   LnFwdArgs a{X, rows, cols, ldx, gamma, beta, eps, 1.0 / (double)cols, Y, ldy, scale, mean, rstd};
   return hip_status(launch_ln_fwd(a, (int)dtype, y_bytes != 0, as_stream(stream)));
@@ -333,7 +343,8 @@ static int layer_norm_backward(const void* dY, int64_t lddy, uint32_t dtype, con
   const int64_t bytes = dtype_bytes(dtype);
   if (bytes == 0 || bad_sizes(rows, cols) || (cols == 0 && rows > 0)) return I8G_EINVAL;
   if (bad_matrix(dY, rows, cols, lddy, bytes) || (!c && bad_matrix(X, rows, cols, ldx, bytes))) return I8G_EINVAL;
-  if (dX && bad_matrix(dX, rows, cols, lddx, bytes)) return I8G_EINVAL;
+  if (dX && (bad_matrix(dX, rows, cols, lddx, bytes) || bad_in_place(dX, lddx, dY, lddy, rows, cols, bytes)))
+    return I8G_EINVAL;
   if (rows > 0 && (!mean || !rstd)) return I8G_EINVAL;
   if (bad_f32(gamma) || bad_f32(mean) || bad_f32(rstd) || bad_f32(dgamma) || bad_f32(dbeta)) return I8G_EINVAL;
   const bool sums = cols > 0 && (dgamma || dbeta);
@@ -398,6 +409,7 @@ int checkpoint_act_bwd(const int8_t* Q, int64_t ldq, const float* scale, int64_t
   if (bytes == 0 || bad_checkpoint(Q, ldq, scale, lds, group, rows, cols, false, &c)) return I8G_EINVAL;
   if (act != I8G_ACT_RELU && act != I8G_ACT_GELU) return I8G_EINVAL;
   if (bad_matrix(dY, rows, cols, lddy, bytes) || bad_matrix(dX, rows, cols, lddx, bytes)) return I8G_EINVAL;
+  if (bad_in_place(dX, lddx, dY, lddy, rows, cols, bytes)) return I8G_EINVAL;
   if (rows == 0 || cols == 0) return I8G_OK;
   return hip_status(launch_checkpoint_read(c, (int)act, dY, lddy, dX, lddx, (int)dtype, as_stream(stream)));
 }
@@ -466,6 +478,11 @@ int token_logprobs_bwd(const void* logits, uint32_t dtype, int64_t rows, int64_t
   if (bad_i64(targets) || bad_f32(lse) || bad_f32(entropy) || bad_f32(g_logprob) || bad_f32(g_entropy)) return I8G_EINVAL;
   if (rows == 0) return I8G_OK;
   if (!lse || (!g_logprob && !g_entropy) || (g_logprob && !targets) || (g_entropy && !entropy)) return I8G_EINVAL;
+  if (bad_in_place(dlogits, lddl, logits, ld, rows, vocab, bytes)) return I8G_EINVAL;
+  const ByteRows out = byte_rows(dlogits, rows, vocab, lddl, bytes);
+  if (share_bytes(out, byte_rows(targets, targets ? 1 : 0, rows, 0, 8))) return I8G_EINVAL;
+  for (const float* v : {lse, entropy, g_logprob, g_entropy})
+    if (share_bytes(out, byte_rows(v, v ? 1 : 0, rows, 0, 4))) return I8G_EINVAL;
   LpBwdArgs a{logits, rows, vocab, ld, targets, lse, entropy, g_logprob, g_entropy, dlogits, lddl};
   return hip_status(launch_token_logprobs_bwd(a, (int)dtype, as_stream(stream)));
 }

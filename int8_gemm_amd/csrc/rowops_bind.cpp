@@ -21,6 +21,7 @@
 #include <string>
 
 #include "../../include/int8_gemm.h"
+#include "i8g_overlap.h"
 
 namespace {
 
@@ -77,6 +78,16 @@ Matrix layout(const at::Tensor& t, const char* name, const at::Tensor* like) {
   if (m.rows > 1 && t.stride(0) < m.cols) refuse("%s has overlapping rows (expanded?): call .contiguous() first", name);
   m.ld = m.rows > 1 ? t.stride(0) : m.cols > 1 ? m.cols : 1;
   return m;
+}
+
+// Where the elements of a matrix, and of a contiguous vector, are.
+i8g::ByteRows bytes_of(const Matrix& m) {
+  const int64_t size = (int64_t)m.t->element_size();
+  return i8g::ByteRows{(uintptr_t)m.data(), m.rows, m.cols * size, m.ld * size};
+}
+i8g::ByteRows bytes_of(const at::Tensor& v) {
+  const int64_t size = (int64_t)v.nbytes();
+  return i8g::ByteRows{(uintptr_t)v.data_ptr(), 1, size, size};
 }
 
 uint32_t dtype_code(at::ScalarType s) {
@@ -364,6 +375,12 @@ PyObject* token_logprobs_bwd_(Args a) {   // logits, targets, lse, entropy, g_lo
   } else {
     out = values(a[6], "out", x.t);
     dx = *out.t;
+    if (!i8g::itself_or_apart(bytes_of(out), bytes_of(x)))
+      refuse("out must be the logits themselves or not overlap them");
+    static const char* const names[] = {"targets", "lse", "entropy", "g_logprob", "g_entropy"};
+    for (int i = 0; i < 5; ++i)
+      if (a[i + 1] != Py_None && i8g::share_bytes(bytes_of(out), bytes_of(THPVariable_Unpack(a[i + 1]))))
+        refuse("out must not overlap %s", names[i]);
   }
   enqueue(api.token_logprobs_bwd, *x.t, x.data(), dtype_code(x.t->scalar_type()), x.rows, x.cols, x.ld, t, lse, h, g, gh,
           out.data(), out.ld);

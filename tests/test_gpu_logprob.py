@@ -327,3 +327,49 @@ def test_nan_of_any_payload(g, rows, vocab, topk):
         assert torch.isnan(o[:4]).all() and not torch.isnan(o[4:]).any(), name
     if topk:
         assert torch.isnan(out[4][:4]).all() and not torch.isnan(out[4][4:]).any()
+
+
+def test_gradient_out(g):
+    """out is the logits themselves, or memory apart from them and the
+    vectors; what overlaps is refused before anything is written."""
+    say("logprobs gradient out")
+    rows, vocab = 5, 300
+    for dt in DTYPES.values():
+        buf = torch.randn((rows + 1, 2 * vocab), generator=torch.Generator("cuda").manual_seed(2), device="cuda").to(dt)
+        X, beside = buf[:rows, :vocab], buf[:rows, vocab:]
+        t = torch.arange(rows, device="cuda")
+        _, h, lse, _, _ = g.token_logprobs(X, t)
+        one = torch.ones(rows, device="cuda")
+        want = g.token_logprobs_bwd(X, t, lse, h, one, one)
+        keep = buf.clone()
+        for out in (buf[:rows, 1:vocab + 1], buf[:rows, vocab - 1:2 * vocab - 1], buf[1:, :vocab],
+                    buf.as_strided((rows, vocab), (2 * vocab - 8, 1))):
+            with pytest.raises(ValueError, match="overlap"):
+                g.token_logprobs_bwd(X, t, lse, h, one, one, out=out)
+        one_row = buf.view(-1)[:vocab][None]
+        with pytest.raises(ValueError, match="overlap"):
+            g.token_logprobs_bwd(one_row, t[:1], lse[:1], None, one[:1], out=buf.view(-1)[8:vocab + 8][None])
+        same_bits(buf, keep, "the buffer")
+        # between the logits' rows, where nothing is shared
+        got = g.token_logprobs_bwd(X, t, lse, h, one, one, out=beside)
+        assert got.data_ptr() == beside.data_ptr()
+        same_bits(got.contiguous(), want, "beside the logits")
+        same_bits(X.contiguous(), keep[:rows, :vocab].contiguous(), "the logits")
+    # vectors inside out's memory, and in the gap between its rows
+    buf = torch.zeros((rows, 400), device="cuda")
+    out = buf[:, :vocab]
+    X = torch.randn((rows, vocab), generator=torch.Generator("cuda").manual_seed(3), device="cuda")
+    _, h, lse, _, _ = g.token_logprobs(X, t)
+    want = g.token_logprobs_bwd(X, t, lse, h, one, one)
+    for v in (buf[1, 100:105], buf[0, 296:301]):
+        for i in range(4):
+            args = [lse, h, one, one]
+            args[i] = v
+            with pytest.raises(ValueError, match="overlap"):
+                g.token_logprobs_bwd(X, t, *args, out=out)
+    tt = buf[2, 40:50].view(torch.int64)
+    with pytest.raises(ValueError, match="overlap"):
+        g.token_logprobs_bwd(X, tt, lse, h, one, one, out=out)
+    gap = buf[3, 300:305]
+    gap.copy_(lse)
+    same_bits(g.token_logprobs_bwd(X, t, gap, h, one, one, out=out).contiguous(), want, "a vector in the gap")

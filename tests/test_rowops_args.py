@@ -1,11 +1,15 @@
 """Refusals of the operators between the GEMMs (CPU only: every call fails
 its checks on the host, so its addresses are never used)."""
 import ctypes
+import random
+import shutil
+import subprocess
 
 import pytest
 import torch
 
 import int8_gemm_amd as g
+from int8_gemm_amd import build as B
 
 OK, EINVAL, EWORKSPACE = 0, 1, 4
 P = ctypes.c_void_p
@@ -132,3 +136,56 @@ def test_python_arguments():
         g.token_logprobs(x, torch.zeros(4, dtype=torch.int64))
     with pytest.raises(ValueError, match="2-D"):
         g.token_logprobs_bwd(None, None, None)
+
+
+def test_outputs_in_place_or_apart(lib):
+    """An output that may be an input is that input or apart from it: a shifted
+    view, or the same address with other rows, would be read where another
+    workgroup has written."""
+    at = lambda n: P((1 << 20) + n)  # noqa: E731
+    for rows, shifts in ((4, (4, 28, 36, 64, -4, -100)), (1, (4, 28, -4, -28))):      # rows of 8 f32 with ld 9
+        for n in shifts:
+            assert lib.layer_norm(A, 0, rows, 8, 9, None, None, 1e-5, at(n), 9, None, None, None) == EINVAL, n
+            assert lib.layer_norm_bwd(A, 9, P(1 << 22), 9, 0, rows, 8, None, P(1 << 23), P(1 << 23), at(n), 9, None, None,
+                                      None, 0, None) == EINVAL, n
+            assert lib.checkpoint_act_bwd(P(1 << 22), 8, P(1 << 23), 1, 32, rows, 8, 1, A, 9, at(n), 9, 0, None) == EINVAL, n
+            assert lib.token_logprobs_bwd(A, 0, rows, 8, 9, P(1 << 22), P(1 << 23), None, P(1 << 23), None, at(n), 9,
+                                          None) == EINVAL, n
+    assert lib.layer_norm(A, 0, 4, 8, 9, None, None, 1e-5, A, 10, None, None, None) == EINVAL
+    assert lib.token_logprobs_bwd(A, 1, 4, 8, 9, P(1 << 22), P(1 << 23), None, P(1 << 23), None, A, 16, None) == EINVAL
+    # the vectors of the log probabilities' gradient: targets, lse, entropy, g_logprob, g_entropy
+    far = [P(1 << (22 + i)) for i in range(5)]
+    for i in range(5):
+        # 4 rows of 32 bytes in 64; 4 targets are 32 bytes, 4 f32 are 16 and from -16 would end where the rows start
+        for n in (-16 if i == 0 else -8, 0, 16, 64 * 3 + 24):
+            v = list(far)
+            v[i] = at(n)
+            assert lib.token_logprobs_bwd(P(1 << 30), 0, 4, 8, 8, *v, A, 16, None) == EINVAL, (i, n)
+
+
+def test_sharing_of_bytes(tmp_path):
+    """The rule on overlaps against counting the bytes of small matrices."""
+    cxx = shutil.which("g++")
+    if not cxx:
+        pytest.skip("a host compiler is needed")
+    src, out = tmp_path / "o.cpp", tmp_path / "o.so"
+    src.write_text('#include "i8g_overlap.h"\n'
+                   'extern "C" int share(long a, long ra, long wa, long la, long b, long rb, long wb, long lb) {\n'
+                   '  return i8g::share_bytes({(uintptr_t)a, ra, wa, la}, {(uintptr_t)b, rb, wb, lb});\n}\n')
+    subprocess.run([cxx, "-std=c++17", "-shared", "-fPIC", "-I", B.CSRC, "-o", str(out), str(src)], check=True)
+    share = ctypes.CDLL(str(out)).share
+    share.argtypes = [ctypes.c_long] * 8
+    rng = random.Random(1)
+    seen = [0, 0]
+    for _ in range(20000):
+        m = []
+        for _ in range(2):
+            w = rng.randint(0, 7)
+            m.append((1000 + rng.randint(0, 60), rng.randint(0, 6), w, max(w, 1) + rng.choice([0, 1, 5, 9, 16])))
+        if rng.random() < 0.4:
+            m[1] = (*m[1][:3], max(m[0][3], m[1][2]))
+        (a, b) = [{at + i * ld + j for i in range(rows) for j in range(w)} for at, rows, w, ld in m]
+        want = bool(a & b)
+        assert bool(share(*m[0], *m[1])) == want, m
+        seen[want] += 1
+    assert min(seen) > 2000
