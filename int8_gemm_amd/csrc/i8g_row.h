@@ -28,10 +28,11 @@ template <class T> constexpr int kVec = 16 / (int)sizeof(T);
 // N consecutive values at row[c ...] as floats; values at and beyond `cols`
 // read as `fill` (nothing outside the row is touched).  A full vector is one
 // load of any alignment (gfx950 code objects run with unaligned access on).
+// (No pointer here is declared apart from others: outputs may be inputs.)
 // I: the type of column indexes, int where a row's length allows (32-bit
 // compares, and a row base in scalar registers with a 32-bit offset).
 template <class T, int N, class I>
-__device__ __forceinline__ void load_row(const T* __restrict__ row, I c, I cols, float fill, float (&v)[N]) {
+__device__ __forceinline__ void load_row(const T* row, I c, I cols, float fill, float (&v)[N]) {
   if (c + N <= cols) {
     T t[N];
     __builtin_memcpy(t, row + c, sizeof(t));
@@ -44,7 +45,7 @@ __device__ __forceinline__ void load_row(const T* __restrict__ row, I c, I cols,
 }
 
 template <class T, int N, class I>
-__device__ __forceinline__ void store_row(T* __restrict__ row, I c, I cols, const float (&v)[N]) {
+__device__ __forceinline__ void store_row(T* row, I c, I cols, const float (&v)[N]) {
   if (c + N <= cols) {
     T t[N];
 #pragma unroll
@@ -60,7 +61,7 @@ __device__ __forceinline__ void store_row(T* __restrict__ row, I c, I cols, cons
 // store_row with nontemporal stores.
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 template <class T, int N, class I>
-__device__ __forceinline__ void stream_row(T* __restrict__ row, I c, I cols, const float (&v)[N]) {
+__device__ __forceinline__ void stream_row(T* row, I c, I cols, const float (&v)[N]) {
   if (c + N <= cols) {
     T t[N];
 #pragma unroll
@@ -82,7 +83,7 @@ template <class T, int N>
 struct RawRow {
   T t[N];
   template <class I>
-  __device__ __forceinline__ void load(const T* __restrict__ row, I c, I cols, T fill = T{}) {
+  __device__ __forceinline__ void load(const T* row, I c, I cols, T fill = T{}) {
     if (c + N <= cols) {
       __builtin_memcpy(t, row + c, sizeof(t));
     } else {
@@ -105,7 +106,7 @@ template <int N>
 struct CodeWords {
   uint32_t w[N / 4];
   template <class I>
-  __device__ __forceinline__ void load(const int8_t* __restrict__ row, I c, I cols) {
+  __device__ __forceinline__ void load(const int8_t* row, I c, I cols) {
     if (c + N <= cols) {
       __builtin_memcpy(w, row + c, N);
     } else {
@@ -124,7 +125,7 @@ struct CodeWords {
 };
 
 template <int N, class I>
-__device__ __forceinline__ void store_codes(int8_t* __restrict__ row, I c, I cols, const int (&q)[N]) {
+__device__ __forceinline__ void store_codes(int8_t* row, I c, I cols, const int (&q)[N]) {
   if (c + N <= cols) {
     uint32_t w[N / 4];
 #pragma unroll

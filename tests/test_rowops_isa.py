@@ -56,3 +56,20 @@ def test_float_instructions(functions):
                 if c[op] != n:
                     bad.append((fn, op, c[op], n))
     assert not bad, bad[:10]
+
+
+@pytest.mark.timeout(600)
+def test_in_place_kernels_promise_no_apartness(tmp_path):
+    """The kernels for an output that is the input, which take both as
+    arguments, must not declare them apart (__restrict__, the compiler's
+    noalias): a load could then move behind another value's store."""
+    out = str(tmp_path / "checkpoint.ll")
+    p = compile_asm(os.path.join(B.CSRC, "checkpoint.hip"), out, ("-emit-llvm",))
+    _, err = p.communicate()
+    assert p.returncode == 0, err[-2000:]
+    with open(out) as f:
+        heads = [line for line in f if line.startswith("define ") and "checkpoint_read_kernel" in line]
+    apart = [h for h in heads if re.search(r"checkpoint_read_kernel\w*Li[012]ELb1E", h)]
+    in_place = [h for h in heads if h not in apart]
+    assert len(in_place) == 6 and len(apart) == 9         # 3 types; 2 uses in place, and the restoring one
+    assert not [h[:200] for h in in_place if "noalias" in h.split("(", 1)[1]]
