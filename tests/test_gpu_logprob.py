@@ -373,3 +373,33 @@ def test_gradient_out(g):
     gap = buf[3, 300:305]
     gap.copy_(lse)
     same_bits(g.token_logprobs_bwd(X, t, gap, h, one, one, out=out).contiguous(), want, "a vector in the gap")
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("vocab,topk", [(40, 32), (513, 32), (2047, 20), (5000, 20), (50257, 32), (70001, 20)])
+@pytest.mark.parametrize("copies", [1, 40])
+def test_log_probabilities_of_hard_rows(g, vocab, topk, dtype, copies):
+    """The log probabilities of the given and of the best tokens: x - max is
+    exact in binary64, log S is off by what S is off relative (bounds), and the
+    result is rounded once.  A row of -inf only gives -inf, without a token 0."""
+    say("logprobs of hard rows, values", vocab, topk, dtype, copies)
+    rng = np.random.default_rng(vocab + 1)
+    dt = DTYPES[dtype]
+    rows = hard_rows(vocab, dt, rng)
+    values = torch.from_numpy(np.stack(list(rows.values()))).to(dt)
+    n = len(rows)
+    empty = list(rows).index("all -inf")
+    for t in (rng.integers(0, vocab, n), np.where(np.arange(n) % 2 == empty % 2, -100, vocab // 2), np.full(n, vocab - 1)):
+        got = g.token_logprobs(values.cuda().repeat(copies, 1), torch.from_numpy(np.tile(t, copies)).cuda(), topk)
+        want = R.logprobs64(host(values), t, topk)
+        log_s = bounds(host(values), np.zeros(n), np.zeros(n))[0]
+        for c in (0, copies - 1):
+            sl = slice(c * n, (c + 1) * n)
+            fine = np.where(np.isfinite(want[0]), want[0], 0.0)
+            within(host(got[0][sl]), want[0], log_s + U * np.abs(fine), "log probabilities")
+            fine = np.where(np.isfinite(want[4]), want[4], 0.0)
+            within(host(got[4][sl]), want[4], log_s[:, None] + U * np.abs(fine), "the best tokens' log probabilities")
+            assert np.array_equal(got[3][sl].cpu().numpy(), want[3])
+        given = t[empty] >= 0
+        assert float(got[0][empty]) == (-np.inf if given else 0.0) and (got[4][empty] == -np.inf).all()
+        assert float(got[2][empty]) == -np.inf and float(got[1][empty]) == 0.0
