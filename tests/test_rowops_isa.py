@@ -73,3 +73,17 @@ def test_in_place_kernels_promise_no_apartness(tmp_path):
     in_place = [h for h in heads if h not in apart]
     assert len(in_place) == 6 and len(apart) == 9         # 3 types; 2 uses in place, and the restoring one
     assert not [h[:200] for h in in_place if "noalias" in h.split("(", 1)[1]]
+
+
+@pytest.mark.timeout(600)
+def test_every_declared_kernel_is_built(functions):
+    """No kernel of the sources is left out of the scanned code, and so none
+    stays in them that no call reaches (templates are built where they are used)."""
+    names, declared, found = " ".join(functions), set(), 0
+    for s in SOURCES:
+        with open(os.path.join(B.CSRC, s)) as f:
+            text = f.read()
+        found += text.count("__global__")
+        declared |= set(re.findall(r"__global__\s+void\s+(?:__launch_bounds__\((?:[^()]|\([^()]*\))*\)\s*)?(\w+)\s*\(", text))
+    assert len(declared) == found and set(KERNELS) <= declared, sorted(declared)
+    assert not [k for k in declared if not re.search(rf"\d+{k}(I|E|P|N)", names)]
