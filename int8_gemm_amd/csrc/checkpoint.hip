@@ -6,12 +6,14 @@
 //
 // Storing reads a value and writes a byte; restoring, the activation's
 // gradient and the column quantization of a checkpoint read that byte where
-// they would have read a value.  All are bound by memory: 8192 x 3072 f32 in
-// groups of 128 is stored in 20.8 us and restored in 19.9 (126 MB each, 6.1
-// and 6.3 TB/s; a copy within the 256 MB cache moves 6.9), the gradient of GELU
-// in bf16 takes 23.7 us (126 MB, 5.3 TB/s; its 42 instructions a value are next),
-// the columns of 8192 x 768 5.2 and 8.0 us (two passes over 6.3 MB, 2 us of
-// each the launch and the first load).
+// they would have read a value.  They are bound by memory: 8192 x 3072 f32 in
+// groups of 128 is stored in 20.4 us and restored in 19.8 (126 MB each, 6.2
+// and 6.4 TB/s; a copy within the 256 MB cache moves 6.9), the gradient of GELU
+// in bf16 takes 24.2 us (126 MB, 5.2 TB/s; its 42 instructions a value are next).
+// The column quantization's two passes are bound by latency, a thread having
+// four 8-byte loads in flight: 5.2 and 8.0 us for 8192 x 768, of which the
+// launch and the first load are 2 each, and 11.1 and 17.6 us for 8192 x 3072
+// (2.3 and 2.9 TB/s).
 #include <type_traits>
 
 #include "i8g_launch.h"

@@ -69,7 +69,7 @@ __device__ __forceinline__ void rescale(float& s, float& t, float from, float to
 
 // Adds a value d = x - m <= 0 to the sums.  2-byte logits are bound by these
 // operations, so exp(d) is made of fewer than exp_f32's: ln2 in one part (off
-// by 1.9e-9 k), 1 + r q(r) with q of degree 4 (relative error 9.2e-8 for |r| <=
+// by 1.9e-9 k), 1 + r q(r) with q of degree 4 (relative error 9.6e-8 for |r| <=
 // ln2/2), and an exponent set by one addition, for which d is kept above -87:
 // that adds less than 2^-96 to either sum of the longest row.  Off by less
 // than (2.6 + 0.05 |d|) 2^-24 relative, and exact for d = 0.  8192 x 50304

@@ -11,22 +11,26 @@
 //   c1 = RN(sum w / n)                c2 = RN(sum w*xh / n)
 //   dx = RN(rstd * RN(RN(w - c1) - RN(xh * c2)))
 //   dgamma_j = RN(sum over rows of dy*xh)     dbeta_j = RN(sum over rows of dy)
-// A product of two binary32 values is exact in binary64, and a binary64 sum
-// of them is off by less than 2^-40 of its terms' magnitude, so the rounded
-// sums do not depend on the order of addition except next to a rounding
-// border; the order is fixed by the sizes all the same (no atomics), so two
-// runs give the same bytes.
+// A product of two binary32 values is exact in binary64, and a binary64 sum of
+// k of them one after another is off by at most k 2^-53 of its terms'
+// magnitude, k being the values of a lane or the rows of a workgroup: less
+// than 2^-40 up to 2^20 rows, 2^-29 for 2^31.  So the rounded sums do not
+// depend on the order of addition except next to a rounding border; the order
+// is fixed by the sizes all the same (no atomics), so two runs give the same
+// bytes.
 //
-// Both directions are bound by memory: every value is read once and written
-// once, a row staying in registers in between.  A row of up to 1024 values is
-// held by one wave, 16 values a lane; a longer one by 2 to 16 waves of one
-// workgroup; rows beyond 16384 values are read again instead of held.
+// Both directions are bound by memory: a value is read once and written once,
+// a row staying in registers in between.  A row of up to 1024 values is held by
+// one wave, 16 values a lane; a longer one by 2 to 16 waves of one workgroup;
+// rows beyond 16384 values are read again instead of held.  The backward pass
+// reads rows beyond 8192 values twice: the sums over the rows do not fit the
+// registers beside them and are a pass of their own.
 //
 // 8192 x 768 f32, which the 256 MB cache holds (a copy there moves 6.9 TB/s):
-// forward 10.2 us (50 MB, 4.9 TB/s), into codes 10.8 us (31 MB), backward 15.6 us
-// (75 MB, 4.8 TB/s) and 3.9 us for the columns' sums.  About 2 us of each are
-// the launch and the first load; in codes the row's second reduction and the
-// quantizing are most of the rest.
+// forward 10.0 us (50 MB, 5.0 TB/s), into codes 10.6 us (31 MB), backward 15.5 us
+// (75 MB, 4.9 TB/s) and 3.9 us for the columns' sums.  About 2 us of each are
+// the launch and the first load; in codes the row's second reduction, which
+// waits for the first, and the quantizing are most of the rest.
 #include <type_traits>
 
 #include "i8g_launch.h"
