@@ -24,7 +24,7 @@ inline bool share_bytes(ByteRows a, ByteRows b) {
     a = b;
     b = t;
   }
-  const auto end = [](const ByteRows& m) { return m.at + (uintptr_t)((m.rows - 1) * m.ld + m.width); };
+  const auto end = [](const ByteRows& m) { return m.at + (uintptr_t)(m.rows - 1) * (uintptr_t)m.ld + (uintptr_t)m.width; };
   if (end(a) <= b.at || end(b) <= a.at) return false;
   if (a.rows > 1 && a.ld == b.ld) {
     // row i of a and row i + k of b start d + k ld bytes from each other, k from 1 - a.rows to b.rows - 1
