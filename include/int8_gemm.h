@@ -521,6 +521,119 @@ int token_logprobs_bwd(const void* logits, uint32_t dtype, int64_t rows, int64_t
                        void* stream);
 
 /* ------------------------------------------------------------------------
+ * The two ends of a training step, which share the token table: the log
+ * probabilities of the LM head from its int8 operands, and the embedding.
+ * Types, sizes, alignment, infinities, NaN, overlaps and the independence of
+ * timing are as for the operators between the GEMMs; operands in int8 are as
+ * for gemm_i8_blockscaled.
+ * ------------------------------------------------------------------------ */
+#define I8G_HEAD_ROWS_MAX 1073741824   /* 2^30 */
+
+/*
+ * gemm_i8_logprobs -- token_logprobs of the output of gemm_i8_blockscaled,
+ * which is never stored: with L = epilogue(QA . QBt^T) (the same bits),
+ *   lse[i] = log sum_j exp L[i,j],  logprob[i] = L[i,t] - lse[i],
+ * t = targets[i]; a target outside [0, N) is no token: its logprob is 0.
+ *   QA, lda, s_row   M tokens of K codes, M f32 scales.
+ *   QBt, ldb, s_col  N vocabulary rows of K codes (the table's rows, as
+ *            quantize_rows writes them), N f32 scales.
+ *   targets  M int64; may be NULL with logprob NULL.
+ *   logprob, lse   M f32 each, either may be NULL.
+ *   workspace  device scratch of gemm_i8_logprobs_workspace_bytes(M, N, K),
+ *            256-byte aligned, any contents.
+ * Sums are held in binary32 over at most 64 values a lane against their
+ * maximum, and in binary64 beyond a tile of 256 (128) columns; exponentials
+ * are the hardware's (1 ulp).  A row whose largest logit is 2^127 / log2(e) or
+ * more, or that holds a NaN, is NaN; one whose logits are all below -2e38 has
+ * lse and logprob -inf.
+ * Errors: I8G_EINVAL (null pointer, negative size, M above I8G_HEAD_ROWS_MAX,
+ * N above I8G_VOCAB_MAX, N == 0 with M > 0, misaligned vector), I8G_EKRANGE,
+ * I8G_EALIGN, I8G_EWORKSPACE, I8G_EHIP.
+ */
+size_t gemm_i8_logprobs_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int gemm_i8_logprobs(const int8_t* QA, int64_t lda, const float* s_row, const int8_t* QBt, int64_t ldb,
+                     const float* s_col, int64_t M, int64_t N, int64_t K, const int64_t* targets,
+                     float* logprob, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gemm_i8_logprobs_bwd -- the gradients of both operands' values (those that
+ * the codes stand for, s_row[i] QA[i,k] and s_col[j] QBt[j,k]) for the
+ * gradients g_logprob and g_lse of gemm_i8_logprobs' outputs (M f32 each;
+ * either may be NULL for 0, not both):
+ *   G[i,j]   = g_logprob[i] ([j = t] - p[i,j]) + g_lse[i] p[i,j],
+ *              p = exp(L - lse), g_logprob 0 for a row without a token
+ *   dA[i,k]  = sum_j G[i,j] s_col[j] QBt[j,k]       M x K of dtype
+ *   dBt[j,k] = sum_i G[i,j] s_row[i] QA[i,k]        N x K of dtype
+ *   lse      M f32, as gemm_i8_logprobs wrote them.
+ *   dA, dBt  either may be NULL.  With M == 0 dBt is 0.
+ *   workspace  device scratch of gemm_i8_logprobs_bwd_workspace_bytes(M, N, K,
+ *            dtype), 256-byte aligned, any contents (not needed with M == 0).
+ * The products run on the matrix cores in bf16 with binary32 sums, over pieces
+ * of the vocabulary whose G has at most 2^27 values (or 256 columns): codes are
+ * exact, s_row[i] G[i,j] s_col[j] is rounded to bf16 for bf16 gradients and to
+ * a sum of two bf16 (2^-18) for f32 and f16.  Scales have to be positive, as
+ * the quantize passes write them.  As in token_logprobs_bwd, a row with
+ * |lse| >= 2^24 gets 0 (and adds nothing to dBt).  A NaN in a row's lse,
+ * gradients or scale makes its row of dA and all of dBt NaN.
+ * Errors: as gemm_i8_logprobs; I8G_EINVAL for an unknown dtype, a leading
+ * dimension below K, a misaligned output.
+ */
+size_t gemm_i8_logprobs_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, uint32_t dtype);
+int gemm_i8_logprobs_bwd(const int8_t* QA, int64_t lda, const float* s_row, const int8_t* QBt, int64_t ldb,
+                         const float* s_col, int64_t M, int64_t N, int64_t K, const int64_t* targets,
+                         const float* lse, const float* g_logprob, const float* g_lse, void* dA, int64_t ldda,
+                         void* dBt, int64_t lddb, uint32_t dtype, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/*
+ * embedding -- Y[i] = alpha W[t], t = tokens[i], with P[positions[i]] added:
+ *   Y = RN(RN(alpha * w) + p) in binary32, rounded once more to `dtype`.
+ *   W, ldw   vocab x cols of dtype.
+ *   tokens   rows int64; one outside [0, vocab) is no token: its row is +0.
+ *   P, ldp   n_pos x cols of dtype, or NULL for none.
+ *   positions  rows int64 (not used without P); one outside [0, n_pos) adds
+ *            nothing.
+ *   Y, ldy   rows x cols of dtype; it overlaps no input.
+ * Errors: I8G_EINVAL (null pointer, unknown dtype, negative or too large size,
+ * leading dimension < cols, misaligned pointer), I8G_EHIP.
+ */
+int embedding(const void* W, uint32_t dtype, int64_t vocab, int64_t cols, int64_t ldw, const int64_t* tokens,
+              int64_t rows, float alpha, const void* P, int64_t n_pos, int64_t ldp, const int64_t* positions,
+              void* Y, int64_t ldy, void* stream);
+
+/*
+ * embedding_i8 -- embedding from the codes and row scales of a table (the
+ * operand that the head's product reads): w = RN(q * s).
+ *   Q, ldq, scale  vocab x cols int8, vocab f32.
+ *   P and Y are of dtype.
+ * Otherwise as embedding.
+ */
+int embedding_i8(const int8_t* Q, int64_t ldq, const float* scale, int64_t vocab, int64_t cols,
+                 const int64_t* tokens, int64_t rows, float alpha, const void* P, int64_t n_pos, int64_t ldp,
+                 const int64_t* positions, void* Y, uint32_t dtype, int64_t ldy, void* stream);
+
+/*
+ * embedding_bwd -- the gradient of embedding's table (or, with the positions
+ * as tokens, of P): dW[v] = alpha * sum of dY[i] over tokens[i] = v, plus
+ * add[v]; the sum and what is added in binary64, rounded to binary32 once.
+ *   dY       rows x cols of dtype.
+ *   tokens   rows int64; one outside [0, vocab) adds nothing.
+ *   add, ldadd  vocab x cols f32 or NULL for 0; it may be dW itself (then only
+ *            the rows of tokens that occur are written).
+ *   dW, lddw  vocab x cols f32, every row written; it overlaps no other input.
+ *   workspace  device scratch of embedding_bwd_workspace_bytes(rows, cols),
+ *            256-byte aligned, any contents (not needed with rows == 0).
+ * A dY with an infinity or a NaN leaves its column of its token's row without
+ * a finite value, and nothing else.
+ * Errors: as embedding, I8G_EINVAL where dW overlaps dY, tokens or part of
+ * add, and I8G_EWORKSPACE.
+ */
+size_t embedding_bwd_workspace_bytes(int64_t rows, int64_t cols);
+int embedding_bwd(const void* dY, uint32_t dtype, int64_t rows, int64_t cols, int64_t lddy, const int64_t* tokens,
+                  int64_t vocab, float alpha, const float* add, int64_t ldadd, float* dW, int64_t lddw,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Self-checks, after the defence layers of the page "Verification -- why
  * you can trust the numbers" ("Layer 1: exact init gates", "Layer 2:
  * continuous audit", "Layer 3: the kernel probe").  Where that page falls

@@ -28,6 +28,14 @@ and, between the GEMMs of a training step (f32, bf16 or f16 values):
     token_logprobs(logits, targets, topk)           -> (logprob, entropy, lse, top_index, top_logprob)
     token_logprobs_bwd(logits, targets, lse, entropy, g_logprob, g_entropy)  -> dlogits
 
+and at its two ends, which share the token table:
+
+    gemm_i8_logprobs(QA, s_row, QBt, s_col, targets)  -> (logprob, lse)   no logits are stored
+    gemm_i8_logprobs_bwd(QA, s_row, QBt, s_col, targets, lse, g_logprob, g_lse, dtype) -> (dA, dBt)
+    embedding(table, tokens, alpha, pos_table, positions)                 -> Y
+    embedding_i8(Q, scale, tokens, alpha, pos_table, positions, dtype)    -> Y
+    embedding_bwd(dY, tokens, vocab, alpha, add, out)                     -> dtable
+
 Hash tensors hold the 64-bit hash in an int64 element; ``hash_value``
 returns it as a Python int in [0, 2^64).  If the library is not built, or
 cannot be loaded, every entry point raises: there is no fallback.
@@ -44,7 +52,8 @@ __all__ = ["quantize_rows", "quantize_cols", "gemm_i8_blockscaled", "output_hash
            "FMT_POW2", "FMT_INT4", "int4_line_bytes", "gemm_i8_requant", "quantize_batch",
            "layer_norm", "layer_norm_quantize_rows", "layer_norm_bwd", "layer_norm_bwd_checkpoint",
            "checkpoint_i8", "checkpoint_restore", "checkpoint_act_bwd", "checkpoint_quantize_cols",
-           "token_logprobs", "token_logprobs_bwd"]
+           "token_logprobs", "token_logprobs_bwd", "gemm_i8_logprobs", "gemm_i8_logprobs_bwd", "embedding",
+           "embedding_i8", "embedding_bwd"]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libint8_gemm.so")
@@ -65,7 +74,9 @@ EXPORTED = ("quantize_rows", "quantize_cols", "gemm_i8_blockscaled", "gemm_i8_wo
             "layer_norm_bwd", "layer_norm_bwd_workspace_bytes", "layer_norm_bwd_checkpoint", "checkpoint_i8",
             "checkpoint_restore", "checkpoint_act_bwd", "checkpoint_quantize_cols",
             "checkpoint_quantize_cols_workspace_bytes", "token_logprobs",
-            "token_logprobs_workspace_bytes", "token_logprobs_bwd")
+            "token_logprobs_workspace_bytes", "token_logprobs_bwd", "gemm_i8_logprobs",
+            "gemm_i8_logprobs_workspace_bytes", "gemm_i8_logprobs_bwd", "gemm_i8_logprobs_bwd_workspace_bytes",
+            "embedding", "embedding_i8", "embedding_bwd", "embedding_bwd_workspace_bytes")
 
 _lib = None
 _ws = {}
@@ -149,6 +160,9 @@ def load():
     lib.i8g_plan_query.restype = ctypes.c_int
     c_f64 = ctypes.c_double
     ckpt = [c_vp, c_i64, c_vp, c_i64, c_i32, c_i64, c_i64]     # Q, ldq, scale, lds, group, rows, cols
+    head = [c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp]     # QA ... K, targets
+    c_f32 = ctypes.c_float
+    lookup = [c_vp, c_i64, c_f32, c_vp, c_i64, c_i64, c_vp, c_vp]                # tokens ... positions, Y
     ln_grad = [c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_vp, c_sz, c_vp]
     for name, args in (
             ("layer_norm", [c_vp, c_u32, c_i64, c_i64, c_i64, c_vp, c_vp, c_f64, c_vp, c_i64, c_vp, c_vp, c_vp]),
@@ -163,7 +177,13 @@ def load():
             ("token_logprobs", [c_vp, c_u32, c_i64, c_i64, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                                 c_sz, c_vp]),
             ("token_logprobs_bwd", [c_vp, c_u32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64,
-                                    c_vp])):
+                                    c_vp]),
+            ("gemm_i8_logprobs", [*head, c_vp, c_vp, c_vp, c_sz, c_vp]),
+            ("gemm_i8_logprobs_bwd", [*head, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_u32, c_vp, c_sz, c_vp]),
+            ("embedding", [c_vp, c_u32, c_i64, c_i64, c_i64, *lookup, c_i64, c_vp]),
+            ("embedding_i8", [c_vp, c_i64, c_vp, c_i64, c_i64, *lookup, c_u32, c_i64, c_vp]),
+            ("embedding_bwd", [c_vp, c_u32, c_i64, c_i64, c_i64, c_vp, c_i64, c_f32, c_vp, c_i64, c_vp, c_i64, c_vp,
+                               c_sz, c_vp])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = ctypes.c_int
     lib.layer_norm_bwd_workspace_bytes.argtypes = [c_i64, c_i64]
@@ -172,6 +192,12 @@ def load():
     lib.checkpoint_quantize_cols_workspace_bytes.restype = c_sz
     lib.token_logprobs_workspace_bytes.argtypes = [c_i64, c_i64, c_i32]
     lib.token_logprobs_workspace_bytes.restype = c_sz
+    lib.gemm_i8_logprobs_workspace_bytes.argtypes = [c_i64, c_i64, c_i64]
+    lib.gemm_i8_logprobs_workspace_bytes.restype = c_sz
+    lib.gemm_i8_logprobs_bwd_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, c_u32]
+    lib.gemm_i8_logprobs_bwd_workspace_bytes.restype = c_sz
+    lib.embedding_bwd_workspace_bytes.argtypes = [c_i64, c_i64]
+    lib.embedding_bwd_workspace_bytes.restype = c_sz
     _lib = lib
     return lib
 
@@ -548,7 +574,9 @@ _ACTS = {"relu": 1, "gelu": 2}
 _ROWOPS = ("layer_norm", "layer_norm_quantize_rows", "layer_norm_bwd", "layer_norm_bwd_workspace_bytes",
            "layer_norm_bwd_checkpoint", "checkpoint_i8", "checkpoint_restore", "checkpoint_act_bwd",
            "checkpoint_quantize_cols", "checkpoint_quantize_cols_workspace_bytes", "token_logprobs",
-           "token_logprobs_workspace_bytes", "token_logprobs_bwd")
+           "token_logprobs_workspace_bytes", "token_logprobs_bwd", "gemm_i8_logprobs",
+           "gemm_i8_logprobs_workspace_bytes", "gemm_i8_logprobs_bwd", "gemm_i8_logprobs_bwd_workspace_bytes",
+           "embedding", "embedding_i8", "embedding_bwd", "embedding_bwd_workspace_bytes")
 _bind = None
 
 
@@ -630,3 +658,42 @@ def token_logprobs_bwd(logits, targets, lse, entropy=None, g_logprob=None, g_ent
     entropies of token_logprobs (either may be None); out may be logits, but
     not overlap them or the vectors otherwise."""
     return _rowops().token_logprobs_bwd(logits, targets, lse, entropy, g_logprob, g_entropy, out)
+
+
+# ---- the two ends of a training step ---------------------------------------
+def _dtype_code(dtype):
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    return _DTYPES[dtype]
+
+
+def gemm_i8_logprobs(QA, s_row, QBt, s_col, targets):
+    """(logprob, lse) of the rows of L = gemm_i8_blockscaled(QA, s_row, QBt,
+    s_col), which is never stored: lse the log-sum-exp of each row, logprob
+    L[i, targets[i]] - lse[i] (0 for a target outside the vocabulary).  QBt's
+    rows are the vocabulary's."""
+    return _rowops().gemm_i8_logprobs(QA, s_row, QBt, s_col, targets)
+
+
+def gemm_i8_logprobs_bwd(QA, s_row, QBt, s_col, targets, lse, g_logprob, g_lse=None, dtype=torch.float32):
+    """(dA, dBt): the gradients of the values that QA and QBt stand for, for
+    those of gemm_i8_logprobs' outputs (either may be None)."""
+    return _rowops().gemm_i8_logprobs_bwd(QA, s_row, QBt, s_col, targets, lse, g_logprob, g_lse, _dtype_code(dtype))
+
+
+def embedding(table, tokens, alpha=1.0, pos_table=None, positions=None):
+    """Rows alpha * table[tokens] + pos_table[positions], of the table's
+    dtype; the row of a token outside the table is 0."""
+    return _rowops().embedding(table, tokens, alpha, pos_table, positions)
+
+
+def embedding_i8(Q, scale, tokens, alpha=1.0, pos_table=None, positions=None, dtype=torch.float32):
+    """embedding from a table's codes and row scales (quantize_rows)."""
+    return _rowops().embedding_i8(Q, scale, tokens, alpha, pos_table, positions, _dtype_code(dtype))
+
+
+def embedding_bwd(dY, tokens, vocab, alpha=1.0, add=None, out=None):
+    """The gradient of embedding's table (f32, vocab rows), plus `add`; out
+    may be `add` itself, which then grows in the rows of the tokens that
+    occur."""
+    return _rowops().embedding_bwd(dY, tokens, vocab, alpha, add, out)

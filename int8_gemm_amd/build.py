@@ -26,7 +26,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_NAME = "libint8_gemm.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "hash.hip", "verify.hip", "norm.hip", "checkpoint.hip",
-           "logprob.hip"]
+           "logprob.hip", "head.hip", "embedding.hip"]
 ARCH = "gfx950"
 BIND_SOURCE = "rowops_bind.cpp"
 BIND_PATH = os.path.join(HERE, "rowops_bind.so")

@@ -487,6 +487,108 @@ int token_logprobs_bwd(const void* logits, uint32_t dtype, int64_t rows, int64_t
   return hip_status(launch_token_logprobs_bwd(a, (int)dtype, as_stream(stream)));
 }
 
+// ---- the LM head without its logits, the embedding ----
+// The operands of a product of M tokens' codes by N vocabulary rows'.
+static int bad_head(const int8_t* QA, int64_t lda, const float* s_row, const int8_t* QBt, int64_t ldb, const float* s_col,
+                    int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || K < 0 || M > I8G_HEAD_ROWS_MAX || N > I8G_VOCAB_MAX || (N == 0 && M > 0)) return I8G_EINVAL;
+  if (K > I8G_K_MAX) return I8G_EKRANGE;
+  if ((M > 0 && !s_row) || (N > 0 && !s_col) || bad_f32(s_row) || bad_f32(s_col)) return I8G_EINVAL;
+  if (K > 0 && ((M > 0 && !QA) || (N > 0 && !QBt))) return I8G_EINVAL;
+  const int64_t k16 = (K + 15) / 16 * 16;
+  if (K > 0 && (((uintptr_t)QA % 16) || ((uintptr_t)QBt % 16) || (lda % 16) || (ldb % 16) || lda < k16 || ldb < k16))
+    return I8G_EALIGN;
+  return I8G_OK;
+}
+
+size_t gemm_i8_logprobs_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || M > I8G_HEAD_ROWS_MAX || N <= 0 || N > I8G_VOCAB_MAX || K < 0) return 256;
+  return head_fwd_bytes(M, N);
+}
+
+int gemm_i8_logprobs(const int8_t* QA, int64_t lda, const float* s_row, const int8_t* QBt, int64_t ldb, const float* s_col,
+                     int64_t M, int64_t N, int64_t K, const int64_t* targets, float* logprob, float* lse, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (const int bad = bad_head(QA, lda, s_row, QBt, ldb, s_col, M, N, K)) return bad;
+  if (bad_i64(targets) || bad_f32(logprob) || bad_f32(lse) || (M > 0 && logprob && !targets)) return I8G_EINVAL;
+  if (M == 0 || (!logprob && !lse)) return I8G_OK;
+  if (!workspace || (uintptr_t)workspace % 256 != 0 || workspace_bytes < head_fwd_bytes(M, N)) return I8G_EWORKSPACE;
+  return hip_status(launch_head_fwd(HeadArgs{QA, QBt, s_row, s_col, lda, ldb, M, N, K}, targets, logprob, lse, workspace,
+                                    as_stream(stream)));
+}
+
+size_t gemm_i8_logprobs_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, uint32_t dtype) {
+  if (M <= 0 || M > I8G_HEAD_ROWS_MAX || N <= 0 || N > I8G_VOCAB_MAX || K <= 0 || K > I8G_K_MAX || dtype > I8G_F16) return 256;
+  return head_bwd_bytes(M, N, K, (int)dtype);
+}
+
+int gemm_i8_logprobs_bwd(const int8_t* QA, int64_t lda, const float* s_row, const int8_t* QBt, int64_t ldb,
+                         const float* s_col, int64_t M, int64_t N, int64_t K, const int64_t* targets, const float* lse,
+                         const float* g_logprob, const float* g_lse, void* dA, int64_t ldda, void* dBt, int64_t lddb,
+                         uint32_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  const int64_t bytes = dtype_bytes(dtype);
+  if (bytes == 0) return I8G_EINVAL;
+  if (const int bad = bad_head(QA, lda, s_row, QBt, ldb, s_col, M, N, K)) return bad;
+  if (bad_i64(targets) || bad_f32(lse) || bad_f32(g_logprob) || bad_f32(g_lse)) return I8G_EINVAL;
+  if ((dA && bad_matrix(dA, M, K, ldda, bytes)) || (dBt && bad_matrix(dBt, N, K, lddb, bytes))) return I8G_EINVAL;
+  if (M > 0 && (!lse || (!g_logprob && !g_lse) || (g_logprob && !targets))) return I8G_EINVAL;
+  if (N == 0 || K == 0 || (!dA && !dBt) || (M == 0 && !dBt)) return I8G_OK;
+  const size_t need = M > 0 ? head_bwd_bytes(M, N, K, (int)dtype) : 0;
+  if (need > 0 && (!workspace || (uintptr_t)workspace % 256 != 0 || workspace_bytes < need)) return I8G_EWORKSPACE;
+  return hip_status(launch_head_bwd(HeadArgs{QA, QBt, s_row, s_col, lda, ldb, M, N, K},
+                                    HeadGradArgs{targets, lse, g_logprob, g_lse, dA, dBt, ldda, lddb, (int)dtype}, workspace,
+                                    as_stream(stream)));
+}
+
+static int embed(const void* W, int64_t w_bytes, const float* scale, uint32_t dtype, int64_t vocab, int64_t cols, int64_t ldw,
+                 const int64_t* tokens, int64_t rows, float alpha, const void* P, int64_t n_pos, int64_t ldp,
+                 const int64_t* positions, void* Y, int64_t ldy, void* stream) {
+  const int64_t bytes = dtype_bytes(dtype);
+  if (bytes == 0 || bad_sizes(rows, cols) || bad_sizes(vocab, n_pos)) return I8G_EINVAL;
+  if (bad_matrix(W, vocab, cols, ldw, w_bytes ? w_bytes : bytes) || bad_matrix(Y, rows, cols, ldy, bytes)) return I8G_EINVAL;
+  if (bad_i64(tokens) || bad_i64(positions) || bad_f32(scale) || (rows > 0 && !tokens)) return I8G_EINVAL;
+  if (P && (bad_matrix(P, n_pos, cols, ldp, bytes) || (rows > 0 && !positions))) return I8G_EINVAL;
+  if (w_bytes && vocab > 0 && !scale) return I8G_EINVAL;
+  if (rows == 0 || cols == 0) return I8G_OK;
+  return hip_status(launch_embedding(EmbedArgs{W, vocab, cols, ldw, scale, tokens, rows, alpha, P, n_pos, ldp, positions, Y, ldy, 0, 0},
+                                     (int)dtype, w_bytes != 0, as_stream(stream)));
+}
+
+int embedding(const void* W, uint32_t dtype, int64_t vocab, int64_t cols, int64_t ldw, const int64_t* tokens, int64_t rows,
+              float alpha, const void* P, int64_t n_pos, int64_t ldp, const int64_t* positions, void* Y, int64_t ldy,
+              void* stream) {
+  return embed(W, 0, nullptr, dtype, vocab, cols, ldw, tokens, rows, alpha, P, n_pos, ldp, positions, Y, ldy, stream);
+}
+
+int embedding_i8(const int8_t* Q, int64_t ldq, const float* scale, int64_t vocab, int64_t cols, const int64_t* tokens,
+                 int64_t rows, float alpha, const void* P, int64_t n_pos, int64_t ldp, const int64_t* positions, void* Y,
+                 uint32_t dtype, int64_t ldy, void* stream) {
+  return embed(Q, 1, scale, dtype, vocab, cols, ldq, tokens, rows, alpha, P, n_pos, ldp, positions, Y, ldy, stream);
+}
+
+size_t embedding_bwd_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0 || bad_sizes(rows, cols)) return 256;
+  return embedding_bwd_bytes(rows, cols);
+}
+
+int embedding_bwd(const void* dY, uint32_t dtype, int64_t rows, int64_t cols, int64_t lddy, const int64_t* tokens,
+                  int64_t vocab, float alpha, const float* add, int64_t ldadd, float* dW, int64_t lddw, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  const int64_t bytes = dtype_bytes(dtype);
+  if (bytes == 0 || bad_sizes(rows, cols) || bad_sizes(vocab, 0)) return I8G_EINVAL;
+  if (bad_matrix(dY, rows, cols, lddy, bytes) || bad_matrix(dW, vocab, cols, lddw, 4)) return I8G_EINVAL;
+  if (bad_i64(tokens) || (rows > 0 && !tokens)) return I8G_EINVAL;
+  if (add && (bad_matrix(add, vocab, cols, ldadd, 4) || bad_in_place(dW, lddw, add, ldadd, vocab, cols, 4))) return I8G_EINVAL;
+  if (share_bytes(byte_rows(dW, vocab, cols, lddw, 4), byte_rows(dY, rows, cols, lddy, bytes)) ||
+      share_bytes(byte_rows(dW, vocab, cols, lddw, 4), byte_rows(tokens, tokens ? 1 : 0, rows, 0, 8)))
+    return I8G_EINVAL;
+  if (vocab == 0 || cols == 0) return I8G_OK;
+  if (rows > 0 && (!workspace || (uintptr_t)workspace % 256 != 0 || workspace_bytes < embedding_bwd_bytes(rows, cols)))
+    return I8G_EWORKSPACE;
+  return hip_status(launch_embedding_bwd(EmbedBwdArgs{dY, rows, cols, lddy, tokens, vocab, alpha, add, ldadd, dW, lddw},
+                                         (int)dtype, workspace, as_stream(stream)));
+}
+
 size_t gemm_i8_workspace_bytes_flags(int64_t M, int64_t N, int64_t K, uint32_t flags) {
   if (M <= 0 || N <= 0) return 256;
   // the plan may depend on ldc (very wide rows exclude the persistent

@@ -1,0 +1,965 @@
+// head.hip -- log probabilities of given tokens straight from the int8
+// operands of the LM head's product, and the gradients of both operands.  The
+// logits are never stored.
+//
+// With L_ij = RN(RN(RN(acc_ij) s_row_i) s_col_j), acc = QA . QBt^T (the value
+// that gemm_i8_blockscaled writes):
+//   lse_i = log sum_j exp L_ij            logprob_i = L_it - lse_i
+//   G_ij = g_i ([j = t] - p_ij) + gl_i p_ij,   p_ij = exp(L_ij - lse_i)
+//   dA_ik = sum_j G_ij s_col_j QBt_jk     dBt_jk = sum_i G_ij s_row_i QA_ik
+// Both gradients read one matrix T_ij = s_row_i G_ij s_col_j:
+//   dA_ik = (1 / s_row_i) sum_j T_ij QBt_jk,  dBt_jk = (1 / s_col_j) sum_i T_ij QA_ik,
+// and the codes are exact in bf16, so T is all that is rounded for the matrix
+// cores: to bf16 for bf16 gradients (2^-9 of each value, what the outputs are
+// rounded by too), to a sum of two bf16 (2^-18) for f32 and f16 ones.
+//
+// Forward: a workgroup multiplies a tile of vocabulary rows by a tile of
+// tokens; the vocabulary is the accumulators' row dimension, so that a lane
+// holds one token's logits and a row's maximum and sum are in-lane work.  A
+// tile leaves (max, sum) of its part of every row; a second kernel joins them
+// and computes the given token's logit anew.
+// Backward: in pieces of the vocabulary.  A piece's tiles are multiplied again
+// and leave T in blocks of 32 tokens by 16 vocabulary rows, 1 KiB each, in the
+// register order of the matrix cores' operands: dA's product reads a block as
+// it is, dBt's through the transposing LDS read.  Both products of a piece run
+// in one launch.
+#include "../../include/int8_gemm.h"
+#include "i8g_launch.h"
+#include "i8g_row.h"
+
+#include <type_traits>
+
+namespace i8g {
+namespace {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v16i __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.44269502f;
+constexpr float kLowest = -2e38f;      // the least maximum of a row's part: its product with kLog2e is finite
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {   // all but the last N vector loads, and every LDS access
+  static_assert(N >= 0 && N < 64, "vmcnt is a 6-bit counter");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | (((N >> 4) & 3) << 14));
+}
+// Workgroup barrier without the memory fence of __syncthreads(), which would
+// wait for the loads in flight; callers wait for what they need first.
+__device__ __forceinline__ void barrier_nofence() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+// Direct loads of 16 bytes a lane to lds + 16 * lane.  The compiler makes LDS
+// reads wait for every direct load in flight that it knows of, and would empty
+// the pipeline at each stage, so these are not told to it: nothing returns to a
+// register, and the callers wait.  (m0, which holds the destination, has no
+// other use in these kernels: the compiler writes it for direct loads and
+// indexed registers only.)
+__device__ __forceinline__ uint32_t lds_address(const int8_t* lds) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const int8_t*)lds;
+}
+__device__ __forceinline__ void lds_load16(const int8_t* g, const int8_t* lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(lds_address(lds)), "v"(g)
+               : "memory");
+}
+__device__ __forceinline__ void lds_load16(const char* base, int offset, const int8_t* lds) {   // base: uniform
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds_address(lds)), "v"(offset), "s"(base)
+               : "memory");
+}
+// Asks for the READS fragment reads of the next k-step between this one's
+// MFMAs, one by one.
+template <int READS, int MFMAS>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int t = 0; t < (READS < MFMAS ? READS : MFMAS); ++t) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
+  }
+  if constexpr (READS < MFMAS) __builtin_amdgcn_sched_group_barrier(0x008, MFMAS - READS, 0);
+  __builtin_amdgcn_sched_barrier(0);
+}
+// Undoes the dealing of workgroups to the 8 XCDs: consecutive results share an L2.
+__device__ __forceinline__ int xcd_order(int wg, int total) {
+  const int xcd = wg & 7, per = total >> 3, rem = total & 7;
+  return xcd * per + (xcd < rem ? xcd : rem) + (wg >> 3);
+}
+__device__ __forceinline__ float other_half(float x) {   // the value of lane ^ 32
+  const Pair32 p = lane_pair<32>(__float_as_uint(x));
+  return __uint_as_float(threadIdx.x & 32 ? p.a : p.b);
+}
+
+// ---- the logits of a tile -----------------------------------------------------
+struct LogitArgs {
+  const int8_t *A, *B;         // tokens x K, vocab x K
+  const float *s_row, *s_col;
+  int64_t lda, ldb;
+  int M, N, K;
+};
+
+// BV vocabulary rows by BT tokens, WV x WT waves; stages of 128 bytes of K, two
+// in LDS, filled by direct loads (16-byte chunk c of row r at c ^ (r/2)%8, which
+// spreads a fragment's 32 rows over the banks).
+template <int BV, int BT, int WV, int WT>
+struct LogitTile {
+  static constexpr int NW = WV * WT, NT = NW * 64;
+  static constexpr int FV = BV / WV / 32, FT = BT / WT / 32;
+  static constexpr int STAGE = (BV + BT) * 128;
+  static constexpr int INS = (BV + BT) / (8 * NW), INS_V = BV / (8 * NW);
+  static_assert(INS * 8 * NW == BV + BT && INS_V * 8 * NW == BV && NW % 2 == 0, "whole loads");
+  static constexpr int LDS = 2 * STAGE;
+
+  static __device__ __forceinline__ void multiply(const LogitArgs& p, int8_t* smem, int v0, int t0,
+                                                  v16i (&acc)[FV][FT]) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wv = wave / WT, wt = wave % WT;
+    const int k16 = (p.K + 15) & ~15;
+    const int n = (p.K + 127) / 128;
+#pragma unroll
+    for (int i = 0; i < FV; ++i)
+#pragma unroll
+      for (int j = 0; j < FT; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+    if (n == 0) return;
+
+    // rows (q * NW + wave) * 8 + lane / 8; NW is even, so (row / 2) % 8 does not depend on q
+    const int chunk = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
+    const int8_t* src[INS];
+#pragma unroll
+    for (int q = 0; q < INS; ++q) {
+      const int r = (q * NW + wave) * 8 + (lane >> 3);
+      if (q < INS_V) {
+        const int v = min(v0 + r, p.N - 1);
+        src[q] = p.B + (int64_t)v * p.ldb;
+      } else {
+        const int t = min(t0 + r - BV, p.M - 1);
+        src[q] = p.A + (int64_t)t * p.lda;
+      }
+    }
+    auto issue = [&](int kt) {
+      int8_t* base = smem + (kt & 1) * STAGE + wave * 1024;
+      const int at = min(kt * 128 + chunk * 16, k16 - 16);   // (what lies beyond K is cleared below)
+#pragma unroll
+      for (int q = 0; q < INS; ++q) lds_load16(src[q] + at, base + q * NW * 1024);
+    };
+    // The last stage's bytes beyond K: cleared in the tokens' rows, which makes
+    // those products 0 whatever the other operand's bytes are.
+    auto clear_tail = [&](int kt) {
+      const int left = p.K - kt * 128;
+      if (left >= 128) return;
+      int8_t* base = smem + (kt & 1) * STAGE + BV * 128;
+      for (int c = tid; c < BT * 8; c += NT) {
+        const int r = c >> 3, first = (c & 7) * 16;
+        if (first + 16 <= left) continue;
+        uint32_t* w = reinterpret_cast<uint32_t*>(base + r * 128 + ((c & 7) ^ ((r >> 1) & 7)) * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int keep = left - first - 4 * i;             // bytes of this word that are kept
+          if (keep <= 0) w[i] = 0;
+          else if (keep < 4) w[i] &= (1u << (8 * keep)) - 1;
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);                    // lgkmcnt(0)
+      barrier_nofence();
+    };
+
+    int offv[4][FV], offt[4][FT];
+    const int half = lane >> 5;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+      for (int i = 0; i < FV; ++i) {
+        const int r = (wv * FV + i) * 32 + (lane & 31);
+        offv[s][i] = r * 128 + ((2 * s + half) ^ ((r >> 1) & 7)) * 16;
+      }
+#pragma unroll
+      for (int j = 0; j < FT; ++j) {
+        const int r = BV + (wt * FT + j) * 32 + (lane & 31);
+        offt[s][j] = r * 128 + ((2 * s + half) ^ ((r >> 1) & 7)) * 16;
+      }
+    }
+    auto read = [&](int kt, int s, v4i (&fv)[FV], v4i (&ft)[FT]) {
+      const int8_t* base = smem + (kt & 1) * STAGE;
+#pragma unroll
+      for (int i = 0; i < FV; ++i) fv[i] = *reinterpret_cast<const v4i*>(base + offv[s][i]);
+#pragma unroll
+      for (int j = 0; j < FT; ++j) ft[j] = *reinterpret_cast<const v4i*>(base + offt[s][j]);
+    };
+    auto mfma = [&](const v4i (&fv)[FV], const v4i (&ft)[FT]) {
+#pragma unroll
+      for (int i = 0; i < FV; ++i)
+#pragma unroll
+        for (int j = 0; j < FT; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fv[i], ft[j], acc[i][j], 0, 0, 0);
+    };
+    v4i fv0[FV], ft0[FT], fv1[FV], ft1[FT];
+    issue(0);
+    if (n > 1) {
+      issue(1);
+      wait_loads<INS>();
+    } else {
+      wait_loads<0>();
+    }
+    barrier_nofence();
+    if (n == 1) clear_tail(0);
+    read(0, 0, fv0, ft0);
+    // (the last stage stands apart: a branch around the products would move the
+    // accumulators)
+    for (int kt = 0; kt + 1 < n; ++kt) {
+      read(kt, 1, fv1, ft1);
+      mfma(fv0, ft0);
+      interleave<FV + FT, FV * FT>();
+      read(kt, 2, fv0, ft0);
+      mfma(fv1, ft1);
+      interleave<FV + FT, FV * FT>();
+      read(kt, 3, fv1, ft1);
+      mfma(fv0, ft0);
+      interleave<FV + FT, FV * FT>();
+      // the next stage has landed, and this one's last fragments are in
+      // registers: its buffer is free
+      wait_loads<0>();
+      barrier_nofence();
+      if (kt + 2 < n) issue(kt + 2);
+      else clear_tail(kt + 1);
+      read(kt + 1, 0, fv0, ft0);
+      mfma(fv1, ft1);
+      interleave<FV + FT, FV * FT>();
+    }
+    read(n - 1, 1, fv1, ft1);
+    mfma(fv0, ft0);
+    interleave<FV + FT, FV * FT>();
+    read(n - 1, 2, fv0, ft0);
+    mfma(fv1, ft1);
+    interleave<FV + FT, FV * FT>();
+    read(n - 1, 3, fv1, ft1);
+    mfma(fv0, ft0);
+    interleave<FV + FT, FV * FT>();
+    mfma(fv1, ft1);
+  }
+};
+
+// ---- forward --------------------------------------------------------------------
+struct FwdArgs {
+  LogitArgs l;
+  int tiles_v, tiles_t;
+  v2f* parts;                  // [tiles_v][M]: the maximum times kLog2e, and the sum against it
+};
+
+// Tiles of tokens that share a vocabulary tile in an L2 before the next one.
+constexpr int kGroupT = 8;
+__device__ __forceinline__ void tile_of(int w, int tiles_v, int tiles_t, int& tv, int& tt) {
+  const int group = w / (kGroupT * tiles_v), first = group * kGroupT;
+  const int wide = min(kGroupT, tiles_t - first), in = w - group * kGroupT * tiles_v;
+  tt = first + in % wide;
+  tv = in / wide;
+}
+
+template <int BV, int BT, int WV, int WT, int PER_CU>
+__global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_fwd_kernel(const FwdArgs p) {
+  using Tile = LogitTile<BV, BT, WV, WT>;
+  constexpr int FV = Tile::FV, FT = Tile::FT;
+  __shared__ __attribute__((aligned(1024))) int8_t smem[Tile::LDS];
+  __shared__ __attribute__((aligned(16))) float sc[BV];
+  __shared__ v2f part[WV][BT];
+  int tv, tt;
+  tile_of(xcd_order(blockIdx.x, gridDim.x), p.tiles_v, p.tiles_t, tv, tt);
+  const int v0 = tv * BV, t0 = tt * BT;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wv = wave / WT, wt = wave % WT;
+  for (int i = tid; i < BV; i += Tile::NT) sc[i] = p.l.s_col[min(v0 + i, p.l.N - 1)];
+  float sr[FT];
+#pragma unroll
+  for (int j = 0; j < FT; ++j) sr[j] = p.l.s_row[min(t0 + (wt * FT + j) * 32 + (lane & 31), p.l.M - 1)];
+  v16i acc[FV][FT];
+  Tile::multiply(p.l, smem, v0, t0, acc);
+  if (p.l.K == 0) __syncthreads();
+  const int half = lane >> 5;
+  const bool ragged = v0 + BV > p.l.N;
+#pragma unroll
+  for (int j = 0; j < FT; ++j) {
+    float x[FV][16];
+    float m = kLowest;
+#pragma unroll
+    for (int i = 0; i < FV; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = (wv * FV + i) * 32 + 8 * q + 4 * half;
+        const v4f s4 = *reinterpret_cast<const v4f*>(sc + r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float y = epilogue1(acc[i][j][4 * q + e], sr[j], s4[e]);
+          if (ragged && v0 + r + e >= p.l.N) y = -__builtin_inff();
+          x[i][4 * q + e] = y;
+          m = fmaxf(m, y);
+        }
+      }
+    m = fmaxf(m, other_half(m));
+    const float m2 = m * kLog2e;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < FV; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i][e], kLog2e, -m2));
+    s += other_half(s);
+    if (half == 0) part[wv][(wt * FT + j) * 32 + lane] = v2f{m2, s};
+  }
+  __syncthreads();
+  if (tid < BT && t0 + tid < p.l.M) {
+    v2f a = part[0][tid];
+#pragma unroll
+    for (int w = 1; w < WV; ++w) {
+      const v2f b = part[w][tid];
+      const float m2 = fmaxf(a.x, b.x);
+      a.y = a.y * __builtin_amdgcn_exp2f(a.x - m2) + b.y * __builtin_amdgcn_exp2f(b.x - m2);
+      a.x = m2;
+    }
+    p.parts[(size_t)tv * p.l.M + t0 + tid] = a;
+  }
+}
+
+struct JoinArgs {
+  LogitArgs l;
+  const int64_t* targets;
+  const v2f* parts;
+  int n_parts;
+  float *logprob, *lse;        // may be null
+};
+
+// R rows a workgroup: 256 / R threads a row join its parts, then a wave a row
+// computes the given token's logit.
+template <int R>
+__global__ void __launch_bounds__(256) head_join_kernel(const JoinArgs p) {
+  constexpr int S = 256 / R;
+  __shared__ double sum[S][R];
+  __shared__ float top[S][R];
+  __shared__ float out[R];
+  const int tid = threadIdx.x, r = tid % R, slot = tid / R;
+  const int row = blockIdx.x * R + r;
+  float m = -__builtin_inff();
+  double s = 0.0;
+  if (row < p.l.M)
+    for (int i = slot; i < p.n_parts; i += S) {
+      const v2f a = p.parts[(size_t)i * p.l.M + row];
+      // (a NaN maximum does not occur: maxima ignore NaN and their rows have a NaN sum)
+      if (a.x > m) {
+        s *= exp2((double)m - (double)a.x);
+        m = a.x;
+      }
+      s += (double)a.y * exp2((double)a.x - (double)m);
+    }
+  top[slot][r] = m;
+  sum[slot][r] = s;
+  __syncthreads();
+  if (tid < R) {
+    for (int i = 1; i < S; ++i) m = fmaxf(m, top[i][r]);
+    s = 0.0;
+    for (int i = 0; i < S; ++i)
+      if (top[i][r] > -__builtin_inff()) s += sum[i][r] * exp2((double)top[i][r] - (double)m);
+    const float lse = (float)(((double)m + log2(s)) / (double)kLog2e);
+    out[r] = lse;
+    if (row < p.l.M && p.lse) p.lse[row] = lse;
+  }
+  if (!p.logprob) return;
+  __syncthreads();
+  const int lane = tid & 63;
+  for (int i = tid >> 6; i < R; i += 4) {
+    const int at = blockIdx.x * R + i;
+    if (at >= p.l.M) return;
+    const int64_t t = p.targets[at];
+    float lp = 0.0f;
+    if (t >= 0 && t < p.l.N) {
+      const int8_t *a = p.l.A + (int64_t)at * p.l.lda, *b = p.l.B + t * p.l.ldb;
+      int acc = 0;
+      for (int k = lane * 16; k < p.l.K; k += 1024) {
+        v4i x = *reinterpret_cast<const v4i*>(a + k);
+        const v4i y = *reinterpret_cast<const v4i*>(b + k);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int keep = p.l.K - k - 4 * w;
+          if (keep < 4) x[w] = keep <= 0 ? 0 : x[w] & ((1 << (8 * keep)) - 1);
+          acc = __builtin_amdgcn_sdot4(x[w], y[w], acc, false);
+        }
+      }
+#pragma unroll
+      for (int d = 32; d >= 1; d >>= 1) acc += __shfl_xor(acc, d, 64);
+      const float x = epilogue1(acc, p.l.s_row[at], p.l.s_col[t]), lse = out[i];
+      lp = lse == -__builtin_inff() ? lse : x - lse;         // (every logit -inf: so is every log probability)
+    }
+    if (lane == 0) p.logprob[at] = lp;
+  }
+}
+
+// ---- backward ---------------------------------------------------------------------
+// Codes as bf16 blocks of 16 rows (the contraction) by 32 columns, 1 KiB in the
+// order of a fragment: lane l holds column l%32, rows 8 (l/32) ... + 7.  Zero
+// beyond `rows` and `cols`.
+struct PackArgs {
+  const int8_t* Q;
+  int64_t ld;
+  int rows, cols;
+  int row0;                    // first row of the piece
+  int blocks;                  // blocks of 16 rows
+  int KB;                      // blocks of 32 columns
+  v4i* out;                    // [blocks][KB][64]
+};
+__global__ void __launch_bounds__(256) head_pack_kernel(const PackArgs p) {
+  const int c4 = threadIdx.x & 7, half = (threadIdx.x >> 3) & 1;  // 16 threads a block, 4 columns and 8 rows each
+  for (int64_t block = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); block < (int64_t)p.blocks * p.KB; block += (int64_t)gridDim.x * 16) {
+    const int b16 = (int)(block / p.KB), kb = (int)(block % p.KB);
+    const int k = kb * 32 + c4 * 4;
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t r = (int64_t)p.row0 + b16 * 16 + half * 8 + e;
+      w[e] = 0;
+      if (r < p.rows && k < p.cols) {
+        w[e] = *reinterpret_cast<const uint32_t*>(p.Q + r * p.ld + k);
+        if (p.cols - k < 4) w[e] &= (1u << (8 * (p.cols - k))) - 1;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      v4i o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {      // |q| <= 128 has 8 bits: its binary32's upper half is the bf16
+        const uint32_t lo = __float_as_uint((float)(int8_t)(w[2 * e] >> (8 * c)));
+        const uint32_t hi = __float_as_uint((float)(int8_t)(w[2 * e + 1] >> (8 * c)));
+        o[e] = (int)(lo >> 16 | (hi & 0xFFFF0000u));
+      }
+      p.out[block * 64 + half * 32 + c4 * 4 + c] = o;
+    }  }
+}
+
+struct WeightArgs {            // T of a piece
+  LogitArgs l;
+  const int64_t* targets;
+  const float *lse, *g, *gl;   // g or gl may be null (0)
+  int v0;                      // the piece's first vocabulary row
+  int tiles_v, tiles_t;        // of the piece
+  int C16;                     // blocks of 16 vocabulary rows in a row of blocks
+  v4i* T;                      // [tokens / 32][C16][64]
+  size_t plane;                // from the first to the second bf16 of a value (v4i), TERMS 2
+};
+
+template <int TERMS>
+__global__ void __launch_bounds__(512, 2) head_weights_kernel(const WeightArgs p) {
+  using Tile = LogitTile<256, 256, 2, 4>;
+  constexpr int FV = Tile::FV, FT = Tile::FT;
+  __shared__ __attribute__((aligned(1024))) int8_t smem[Tile::LDS];
+  __shared__ __attribute__((aligned(16))) float sc[256];
+  int tv, tt;
+  tile_of(xcd_order(blockIdx.x, gridDim.x), p.tiles_v, p.tiles_t, tv, tt);
+  const int v0 = p.v0 + tv * 256, t0 = tt * 256;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wv = wave >> 2, wt = wave & 3;
+  if (tid < 256) sc[tid] = p.l.s_col[min(v0 + tid, p.l.N - 1)];
+  float sr[FT], lse2[FT], share[FT], given[FT];
+  int target[FT];              // in this tile, or -1
+#pragma unroll
+  for (int j = 0; j < FT; ++j) {
+    const int t = t0 + (wt * FT + j) * 32 + (lane & 31);
+    sr[j] = share[j] = given[j] = lse2[j] = 0.0f;
+    target[j] = -1;
+    if (t < p.l.M) {
+      sr[j] = p.l.s_row[t];
+      const float lse = p.lse[t];
+      int64_t at = -1;
+      float g = 0.0f;
+      if (p.g) {
+        at = p.targets[t];
+        if (at < 0 || at >= p.l.N) at = -1;
+        else g = p.g[t];
+      }
+      // a row whose log-sum-exp is off by a factor e or more in p has no gradient
+      if (!(fabsf(lse) >= 16777216.0f)) {
+        lse2[j] = lse * kLog2e;
+        const float rest = __builtin_fmaf(lse, kLog2e, -lse2[j]);       // exp2(-lse2 - rest) is the row's factor
+        share[j] = ((p.gl ? p.gl[t] : 0.0f) - g) * __builtin_amdgcn_exp2f(-rest) * sr[j];
+        given[j] = g * sr[j];
+        if (at >= v0 && at < v0 + 256) target[j] = (int)(at - v0);
+      }
+    }
+  }
+  v16i acc[FV][FT];
+  Tile::multiply(p.l, smem, v0, t0, acc);
+  if (p.l.K == 0) __syncthreads();
+  const int half = lane >> 5;
+  const bool ragged = v0 + 256 > p.l.N;
+#pragma unroll
+  for (int j = 0; j < FT; ++j) {
+    v4i* row = p.T + ((size_t)(tt * 8 + wt * FT + j) * p.C16 + (size_t)tv * 16) * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < FV; ++i) {
+      uint32_t hi[8], lo[8];
+      const int r0 = (wv * FV + i) * 32;
+      const bool here = __builtin_amdgcn_ballot_w64(target[j] >= r0 && target[j] < r0 + 32) != 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = r0 + 8 * q + 4 * half;
+        const v4f s4 = *reinterpret_cast<const v4f*>(sc + r);
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = epilogue1(acc[i][j][4 * q + e], sr[j], s4[e]);
+          float v = share[j] * __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2e, -lse2[j]));
+          if (here && target[j] == r + e) v += given[j];
+          v *= s4[e];
+          if (share[j] == 0.0f && !(here && target[j] == r + e)) v = 0.0f;
+          if (ragged && v0 + r + e >= p.l.N) v = 0.0f;
+          y[e] = v;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const v2b b = __builtin_convertvector(v2f{y[2 * e], y[2 * e + 1]}, v2b);
+          const uint32_t u = __builtin_bit_cast(uint32_t, b);
+          hi[2 * q + e] = u;
+          if (TERMS == 2) {
+            const v2f left = {y[2 * e] - __uint_as_float(u << 16), y[2 * e + 1] - __uint_as_float(u & 0xFFFF0000u)};
+            lo[2 * q + e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(left, v2b));
+          }
+        }
+      }
+      // lanes l and l ^ 32 hold rows 8q + 0..3 and 8q + 4..7: a fragment's lane
+      // holds 8 in a row
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        v4i* to = row + (size_t)((wv * FV + i) * 2 + s) * 64;
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term) {
+          const uint32_t* w = term ? lo : hi;
+          const auto a = __builtin_amdgcn_permlane32_swap(w[4 * s], w[4 * s + 2], false, false);
+          const auto b = __builtin_amdgcn_permlane32_swap(w[4 * s + 1], w[4 * s + 3], false, false);
+          to[term ? p.plane : 0] = v4i{(int)a[0], (int)b[0], (int)a[1], (int)b[1]};
+        }
+      }
+    }
+  }
+}
+
+// Both products of a piece.  A unit is a tile of 256 columns k (rows of the
+// accumulators) by CT tokens (dA) or vocabulary rows (dBt), over a range of the
+// contraction in stages of 64.
+struct GradArgs {
+  const v4i* T;
+  size_t plane;                // TERMS 2
+  int C16;
+  int KB, tiles_k;
+  struct Side {
+    const v4i* codes;          // [contraction / 16][KB][64]
+    int tiles, splits;         // tiles of CT, ranges of the contraction
+    int stages;                // of the whole contraction
+    int per;                   // stages of a range
+    float* planes;             // [splits][tiles][tiles_k][256 * CT] in register order, or null: write `out`
+    int add;                   // add to the planes
+  } a, b;                      // dA: contraction over the piece's vocabulary; dBt: over the tokens
+  int units_b;
+  int64_t first;               // unit of the launch
+  // dBt written here (without planes)
+  void* out;
+  int64_t ld;
+  int dtype, rows, cols;       // rows of the piece that exist
+  const float* scale;          // of its rows
+};
+
+template <class T>
+__device__ __forceinline__ void store4(T* to, int n, const float (&v)[4]) {
+  T t[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) t[e] = from_f32<T>(v[e]);
+  if (n >= 4) {
+    __builtin_memcpy(to, t, sizeof(t));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (e < n) to[e] = t[e];
+  }
+}
+// Values k ... k + 3 of a gradient's row, n of them.
+__device__ __forceinline__ void store_grad(void* out, int64_t ld, int dtype, int64_t row, int k, int n, v4f acc, float scale) {
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = acc[e] / scale;
+  if (dtype == DT_F32) store4(static_cast<float*>(out) + row * ld + k, n, v);
+  else if (dtype == DT_BF16) store4(static_cast<bf16_t*>(out) + row * ld + k, n, v);
+  else store4(static_cast<f16_t*>(out) + row * ld + k, n, v);
+}
+
+// DUAL: dBt, for which T is read transposed.
+template <int TERMS, bool DUAL>
+__device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Side& s, int u, int8_t* smem) {
+  constexpr int FC = 2 / TERMS, CT = 256 / TERMS, STAGE = 65536;
+  constexpr int READS = DUAL ? 8 : 6;                      // LDS reads of a k-step
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wk = wave >> 2, wc = wave & 3;
+  const int kt = u % p.tiles_k, ct = (u / p.tiles_k) % s.tiles, split = u / (p.tiles_k * s.tiles);
+  const int first = split * s.per, n = min(s.per, s.stages - first);
+
+  // sources of this wave's 4 + 4 loads of a stage: the same in every lane but
+  // for the lane's 16 bytes of a block
+  const char* ga = reinterpret_cast<const char*>(s.codes + ((size_t)(first * 4) * p.KB + kt * 8 + wave) * 64);
+  const char* gb = reinterpret_cast<const char*>(p.T);
+  const size_t row_a = (size_t)p.KB * 1024, row_b = (size_t)p.C16 * 1024, plane_b = p.plane * 16;
+  const int lane_a = lane * 16;
+  int lane_b = lane_a;
+  size_t step_b = 4096, q_b;   // from stage to stage, and from a wave's load to its next of the same term
+  if constexpr (!DUAL) {
+    // [32 tokens][16 of the contraction]: q takes two rows of blocks each
+    gb += (size_t)(ct * (CT / 32) + (wave >> 2)) * row_b + (size_t)(first * 4 + (wave & 3)) * 1024;
+    q_b = 2 * row_b;
+  } else {
+    // [32 tokens of the contraction][16 vocabulary rows]; the 16-byte pieces of a block (half h, token t) are
+    // placed at (h, t ^ (4h + 8 (block % 2))), so that a transposing read of 32 lanes covers all banks
+    lane_b = ((lane & 32) | ((lane & 31) ^ (4 * (lane >> 5) + 8 * (wave & 1)))) * 16;
+    gb += (size_t)(first * 2) * row_b + (size_t)(ct * (CT / 16) + wave) * 1024;
+    q_b = TERMS == 2 ? row_b : 8192;                     // TERMS 1: two loads a row of blocks
+    step_b = 2 * row_b;
+  }
+  auto issue = [&](int st) {
+    int8_t* base = smem + (st & 1) * STAGE + wave * 1024;
+    const char* a = ga + (size_t)st * 4 * row_a;
+    const char* b = gb + (size_t)st * step_b;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) lds_load16(a + q * row_a, lane_a, base + q * 8192);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      size_t at;
+      if (TERMS == 2) at = (q >> 1) * plane_b + (q & 1) * q_b;
+      else at = DUAL ? (q >> 1) * row_b + (q & 1) * q_b : q * q_b;
+      lds_load16(b + at, lane_b, base + 32768 + q * 8192);
+    }
+  };
+  // LDS: codes [k-step 4][32 columns 8]; T [term][32 tokens][k-step 4], or [term][32 tokens 2][16 vocabulary rows]
+  const int offa = wk * 4096 + lane * 16;
+  int offb, flip = 0;
+  if constexpr (!DUAL) {
+    offb = 32768 + wc * FC * 4096 + lane * 16;
+  } else {
+    const int g = lane >> 4, r = (lane & 15) >> 2, c = lane & 3, h = c >> 1;
+    const int t = ((8 * (g >> 1)) ^ (8 * (g & 1))) + 4 * h + r;
+    offb = 32768 + (wc * FC * 2 + (g & 1)) * 1024 + h * 512 + t * 16 + (c & 1) * 8;
+    flip = offb ^ 64;                                       // the fragment's other 4 tokens
+  }
+  v16f acc[4][FC];
+  // register order of a plane: [wave][i][j][q][lane] of 4 values
+  float* plane = s.planes ? s.planes + ((size_t)(split * s.tiles + ct) * p.tiles_k + kt) * (256 * CT) + (size_t)wave * (4 * FC * 1024) + lane * 4
+                          : nullptr;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < FC; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+      auto read = [&](int st, int ks, v8b (&fa)[4], v8b (&fb)[TERMS][FC]) {
+        const int8_t* base = smem + (st & 1) * STAGE;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fa[i] = *reinterpret_cast<const v8b*>(base + offa + ks * 8192 + i * 1024);
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+          for (int j = 0; j < FC; ++j) {
+            if constexpr (!DUAL) {
+              fb[t][j] = *reinterpret_cast<const v8b*>(base + offb + t * 16384 + j * 4096 + ks * 1024);
+            } else {
+              // tokens 16 ks ...: block ks / 2, its tokens 16 (ks % 2) ...
+              const int at = t * 16384 + (ks >> 1) * (CT / 16 * 1024) + j * 2048 + (ks & 1) * 256;
+              typedef __attribute__((address_space(3))) v4s lds_v4s;
+              const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(base + offb + at));
+              const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(base + flip + at));
+              union { v4s h[2]; v8b v; } f{{x, y}};
+              fb[t][j] = f.v;
+            }
+          }
+      };
+      auto mfma = [&](const v8b (&fa)[4], const v8b (&fb)[TERMS][FC]) {
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < FC; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[t][j], acc[i][j], 0, 0, 0);
+      };
+  v8b fa0[4], fa1[4], fb0[TERMS][FC], fb1[TERMS][FC];
+  issue(0);
+  if (n > 1) {
+    issue(1);
+    wait_loads<8>();
+  } else {
+    wait_loads<0>();
+  }
+  barrier_nofence();
+  read(0, 0, fa0, fb0);
+  for (int st = 0; st + 1 < n; ++st) {
+    read(st, 1, fa1, fb1);
+    mfma(fa0, fb0);
+    interleave<READS, 8>();
+    read(st, 2, fa0, fb0);
+    mfma(fa1, fb1);
+    interleave<READS, 8>();
+    read(st, 3, fa1, fb1);
+    mfma(fa0, fb0);
+    interleave<READS, 8>();
+    wait_loads<0>();
+    barrier_nofence();
+    if (st + 2 < n) issue(st + 2);
+    read(st + 1, 0, fa0, fb0);
+    mfma(fa1, fb1);
+    interleave<READS, 8>();
+  }
+  read(n - 1, 1, fa1, fb1);
+  mfma(fa0, fb0);
+  interleave<READS, 8>();
+  read(n - 1, 2, fa0, fb0);
+  mfma(fa1, fb1);
+  interleave<READS, 8>();
+  read(n - 1, 3, fa1, fb1);
+  mfma(fa0, fb0);
+  interleave<READS, 8>();
+  mfma(fa1, fb1);
+
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < FC; ++j) {
+      const int col = ct * CT + (wc * FC + j) * 32 + (lane & 31);
+      const float scale = !plane && col < p.rows ? p.scale[col] : 1.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v4f v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        if (plane) {
+          v4f* to = reinterpret_cast<v4f*>(plane + ((i * FC + j) * 4 + q) * 256);
+          if (s.add) v += *to;
+          *to = v;
+        } else {
+          const int k = kt * 256 + wk * 128 + i * 32 + 8 * q + 4 * (lane >> 5);
+          if (col < p.rows && k < p.cols) store_grad(p.out, p.ld, p.dtype, col, k, p.cols - k, v, scale);
+        }
+      }
+    }
+}
+
+template <int TERMS>
+__global__ void __launch_bounds__(512, 2) head_grads_kernel(const GradArgs p) {
+  __shared__ __attribute__((aligned(1024))) int8_t smem[131072];
+  const int u = (int)p.first + xcd_order(blockIdx.x, gridDim.x);
+  if (u < p.units_b) grads_unit<TERMS, true>(p, p.b, u, smem);
+  else grads_unit<TERMS, false>(p, p.a, u - p.units_b, smem);
+}
+
+struct FinishArgs {
+  const float* planes;
+  int splits, tiles, tiles_k;
+  int CT;
+  void* out;
+  int64_t ld;
+  int dtype, rows, cols;
+  const float* scale;
+};
+// The planes' sum, in their order, by its row's scale.
+__global__ void __launch_bounds__(256) head_finish_kernel(const FinishArgs p) {
+  const size_t size = (size_t)256 * p.CT, all = (size_t)p.tiles * p.tiles_k * size;
+  const int FC = p.CT / 128;
+  for (size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; at < all; at += (size_t)gridDim.x * 1024) {
+    const int tile = (int)(at / size), in = (int)(at % size) / 4;
+    const int kt = tile % p.tiles_k, ct = tile / p.tiles_k;
+    const int lane = in & 63, q = (in >> 6) & 3, j = (in >> 8) % FC, i = (in >> 8) / FC % 4, wave = (in >> 8) / (FC * 4);
+    const int col = ct * p.CT + ((wave & 3) * FC + j) * 32 + (lane & 31);
+    const int k = kt * 256 + (wave >> 2) * 128 + i * 32 + 8 * q + 4 * (lane >> 5);
+    if (col >= p.rows || k >= p.cols) continue;
+    v4f v = *reinterpret_cast<const v4f*>(p.planes + at);
+    for (int s = 1; s < p.splits; ++s) v += *reinterpret_cast<const v4f*>(p.planes + s * all + at);
+    store_grad(p.out, p.ld, p.dtype, col, k, p.cols - k, v, p.scale[col]);
+  }
+}
+
+// The gradient of no tokens.
+__global__ void __launch_bounds__(256) head_zero_kernel(void* out, int64_t ld, int dtype, int64_t rows, int cols) {
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int k = threadIdx.x * 4; k < cols; k += 1024) store_grad(out, ld, dtype, r, k, cols - k, v4f{0, 0, 0, 0}, 1.0f);
+}
+
+constexpr int64_t kMostGroups = int64_t(1) << 22;   // workgroups of a launch
+
+int up(int64_t a, int b) { return (int)((a + b - 1) / b); }
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+LogitArgs logit_args(const HeadArgs& a) {
+  return LogitArgs{a.A, a.B, a.s_row, a.s_col, a.lda, a.ldb, (int)a.M, (int)a.N, (int)a.K};
+}
+
+// Forward tiles: 256 x 256; up to 64 tokens, where reading the codes is the
+// work, 128 vocabulary rows by 32 tokens.
+struct FwdPlan {
+  int bv, bt;
+};
+FwdPlan fwd_plan(int64_t M) { return M <= 64 ? FwdPlan{128, 32} : FwdPlan{256, 256}; }
+
+// Tokens of a launch, which bounds its workspace and grid (vocabulary rows are
+// at most 2^22, so tiles at most 2^22).
+constexpr int64_t kFwdRows = 65536;
+
+// A piece's columns, and into how many ranges the products' contractions are
+// split: a piece's T has at most kPieceValues values (and one column tile at
+// least); the splits are those with the least estimated time.
+constexpr int64_t kPieceValues = int64_t(1) << 27;
+struct BwdPlan {
+  int terms, ct;
+  int64_t Mp, C;
+  int pieces, tiles_k, sa, sb;
+  size_t code_a, code_b, t, plane_a, plane_b;   // bytes
+  size_t bytes() const { return code_a + code_b + t + plane_a + plane_b; }
+};
+BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, int dtype) {
+  BwdPlan b;
+  b.terms = dtype == DT_BF16 ? 1 : 2;
+  b.ct = 256 / b.terms;
+  b.Mp = (M + 255) / 256 * 256;
+  const int64_t Np = (N + 255) / 256 * 256;
+  int64_t most = kPieceValues / b.Mp / 256 * 256;
+  if (most < 256) most = 256;
+  b.pieces = (int)((Np + most - 1) / most);
+  b.C = ((Np + b.pieces - 1) / b.pieces + 255) / 256 * 256;
+  b.pieces = (int)((Np + b.C - 1) / b.C);
+  b.tiles_k = up(K, 256);
+  const int64_t ta = b.Mp / b.ct * b.tiles_k, tb = b.C / b.ct * b.tiles_k;
+  const int64_t da = b.C / 64, db = b.Mp / 64;
+  double best = 1e300;
+  b.sa = b.sb = 1;
+  for (int sa = 1; sa <= 64 && sa <= da; sa *= 2)
+    for (int sb = 1; sb <= 64 && sb <= db; sb *= 2) {
+      const double ua = 4.0 + (double)((da + sa - 1) / sa), ub = 4.0 + (double)((db + sb - 1) / sb);   // in stages
+      const double all = ((double)(ta * sa) * ua + (double)(tb * sb) * ub) / 256;
+      const double longest = ua > ub ? ua : ub, least = ua < ub ? ua : ub;
+      // planes are written and read at about 4 TB/s; a stage takes about 1 us
+      const double planes = (double)(b.Mp * b.tiles_k) * 256 * 4 * 2 * sa + (sb > 1 ? (double)(b.C * b.tiles_k) * 256 * 4 * 2 * sb : 0);
+      const double t = (all + 0.5 * least > longest ? all + 0.5 * least : longest) + planes / 4e6;
+      if (t < best) {
+        best = t;
+        b.sa = sa;
+        b.sb = sb;
+      }
+    }
+  b.code_a = (size_t)b.Mp * b.tiles_k * 512;
+  b.code_b = (size_t)b.C * b.tiles_k * 512;
+  b.t = (size_t)b.Mp * b.C * 2 * b.terms;
+  b.plane_a = (size_t)b.Mp * b.tiles_k * 1024 * b.sa;
+  b.plane_b = b.sb > 1 ? (size_t)b.C * b.tiles_k * 1024 * b.sb : 0;
+  return b;
+}
+
+hipError_t pack(const int8_t* Q, int64_t ld, int64_t rows, int64_t cols, int64_t row0, int64_t n, int KB, void* out,
+                hipStream_t stream) {
+  PackArgs a{Q, ld, (int)rows, (int)cols, (int)row0, (int)(n / 16), KB, static_cast<v4i*>(out)};
+  const int64_t groups = (n / 16 * KB + 15) / 16;
+  hipLaunchKernelGGL(head_pack_kernel, dim3((unsigned)(groups < kMostGroups ? groups : kMostGroups)), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t head_fwd_bytes(int64_t M, int64_t N) {
+  return align256((size_t)up(N, fwd_plan(M).bv) * (size_t)(M < kFwdRows ? M : kFwdRows) * sizeof(v2f));
+}
+
+hipError_t launch_head_fwd(const HeadArgs& whole, const int64_t* targets, float* logprob, float* lse, void* ws, hipStream_t stream) {
+  const FwdPlan pl = fwd_plan(whole.M);
+  for (int64_t row = 0; row < whole.M; row += kFwdRows) {
+    HeadArgs a = whole;
+    a.M = whole.M - row < kFwdRows ? whole.M - row : kFwdRows;
+    a.A += row * a.lda;
+    a.s_row += row;
+    FwdArgs f{logit_args(a), up(a.N, pl.bv), up(a.M, pl.bt), static_cast<v2f*>(ws)};
+    const dim3 grid((unsigned)f.tiles_v * (unsigned)f.tiles_t);
+    if (pl.bt == 32) hipLaunchKernelGGL((head_fwd_kernel<128, 32, 4, 1, 2>), grid, dim3(256), 0, stream, f);
+    else hipLaunchKernelGGL((head_fwd_kernel<256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, f);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    JoinArgs j{f.l, targets ? targets + row : nullptr, f.parts, f.tiles_v, logprob ? logprob + row : nullptr, lse ? lse + row : nullptr};
+    if (a.M >= 1024) hipLaunchKernelGGL(head_join_kernel<16>, dim3((unsigned)up(a.M, 16)), dim3(256), 0, stream, j);
+    else hipLaunchKernelGGL(head_join_kernel<1>, dim3((unsigned)a.M), dim3(256), 0, stream, j);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+size_t head_bwd_bytes(int64_t M, int64_t N, int64_t K, int dtype) { return bwd_plan(M, N, K, dtype).bytes(); }
+
+hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, hipStream_t stream) {
+  if (a.M == 0) {
+    hipLaunchKernelGGL(head_zero_kernel, dim3((unsigned)(a.N < 65536 ? a.N : 65536)), dim3(256), 0, stream, g.dB, g.lddb, g.dtype,
+                       a.N, (int)a.K);
+    return hipGetLastError();
+  }
+  const BwdPlan b = bwd_plan(a.M, a.N, a.K, g.dtype);
+  char* at = static_cast<char*>(ws);
+  v4i* code_a = reinterpret_cast<v4i*>(at);
+  v4i* code_b = reinterpret_cast<v4i*>(at += b.code_a);
+  v4i* T = reinterpret_cast<v4i*>(at += b.code_b);
+  float* plane_a = reinterpret_cast<float*>(at += b.t);
+  float* plane_b = reinterpret_cast<float*>(at += b.plane_a);
+  const int KB = b.tiles_k * 8;
+  const size_t plane = (size_t)b.Mp * b.C / 8;
+  hipError_t e = pack(a.A, a.lda, a.M, a.K, 0, b.Mp, KB, code_a, stream);
+  if (e != hipSuccess) return e;
+  for (int piece = 0; piece < b.pieces; ++piece) {
+    const int64_t v0 = piece * b.C;
+    if ((e = pack(a.B, a.ldb, a.N, a.K, v0, b.C, KB, code_b, stream)) != hipSuccess) return e;
+    WeightArgs w{logit_args(a), g.targets, g.lse, g.g_logprob, g.g_lse, (int)v0, (int)(b.C / 256), (int)(b.Mp / 256), (int)(b.C / 16), T, plane};
+    const dim3 grid((unsigned)w.tiles_v * (unsigned)w.tiles_t);
+    if (b.terms == 1) hipLaunchKernelGGL(head_weights_kernel<1>, grid, dim3(512), 0, stream, w);
+    else hipLaunchKernelGGL(head_weights_kernel<2>, grid, dim3(512), 0, stream, w);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+
+    GradArgs p{};
+    p.T = T;
+    p.plane = plane;
+    p.C16 = (int)(b.C / 16);
+    p.KB = KB;
+    p.tiles_k = b.tiles_k;
+    const int64_t rows = a.N - v0 < b.C ? a.N - v0 : b.C;
+    auto side = [](const v4i* codes, int64_t tiles, int64_t depth, int splits, float* planes, int add) {
+      const int stages = (int)(depth / 64), per = up(stages, splits);
+      return GradArgs::Side{codes, (int)tiles, up(stages, per), stages, per, planes, add};
+    };
+    p.a = side(code_b, b.Mp / b.ct, b.C, b.sa, plane_a, piece > 0);
+    p.b = side(code_a, up(rows, b.ct), b.Mp, b.sb, b.sb > 1 ? plane_b : nullptr, 0);
+    p.units_b = g.dB ? p.tiles_k * p.b.tiles * p.b.splits : 0;
+    const int64_t esize = g.dtype == DT_F32 ? 4 : 2;
+    p.out = g.dB ? static_cast<char*>(g.dB) + v0 * g.lddb * esize : nullptr;
+    p.ld = g.lddb;
+    p.dtype = g.dtype;
+    p.rows = (int)rows;
+    p.cols = (int)a.K;
+    p.scale = a.s_col + v0;
+    const int64_t units = p.units_b + (g.dA ? (int64_t)p.tiles_k * p.a.tiles * p.a.splits : 0);
+    for (p.first = 0; p.first < units; p.first += kMostGroups) {
+      const unsigned n = (unsigned)(units - p.first < kMostGroups ? units - p.first : kMostGroups);
+      if (b.terms == 1) hipLaunchKernelGGL(head_grads_kernel<1>, dim3(n), dim3(512), 0, stream, p);
+      else hipLaunchKernelGGL(head_grads_kernel<2>, dim3(n), dim3(512), 0, stream, p);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    auto finish = [&](const GradArgs::Side& s, void* out, int64_t ld, int64_t n, const float* scale) {
+      FinishArgs f{s.planes, s.splits, s.tiles, b.tiles_k, b.ct, out, ld, g.dtype, (int)n, (int)a.K, scale};
+      const int64_t groups = (int64_t)s.tiles * b.tiles_k * b.ct / 4;
+      hipLaunchKernelGGL(head_finish_kernel, dim3((unsigned)(groups < kMostGroups ? groups : kMostGroups)), dim3(256), 0, stream, f);
+      return hipGetLastError();
+    };
+    if (g.dB && p.b.planes && (e = finish(p.b, p.out, g.lddb, rows, p.scale)) != hipSuccess) return e;
+    if (g.dA && piece + 1 == b.pieces && (e = finish(p.a, g.dA, g.ldda, a.M, a.s_row)) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace i8g

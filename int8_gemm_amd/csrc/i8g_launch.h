@@ -241,6 +241,56 @@ struct LpBwdArgs {
 };
 hipError_t launch_token_logprobs_bwd(const LpBwdArgs& a, int dtype, hipStream_t stream);
 
+// The LM head without its logits (head.hip).
+struct HeadArgs {
+  const int8_t *A, *B;         // M x K tokens, N x K vocabulary rows (codes)
+  const float *s_row, *s_col;
+  int64_t lda, ldb, M, N, K;
+};
+size_t head_fwd_bytes(int64_t M, int64_t N);
+hipError_t launch_head_fwd(const HeadArgs& a, const int64_t* targets, float* logprob, float* lse, void* ws,
+                           hipStream_t stream);
+struct HeadGradArgs {
+  const int64_t* targets;
+  const float *lse, *g_logprob, *g_lse;   // either gradient may be null
+  void *dA, *dB;                          // either may be null
+  int64_t ldda, lddb;
+  int dtype;
+};
+size_t head_bwd_bytes(int64_t M, int64_t N, int64_t K, int dtype);
+hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, hipStream_t stream);
+
+// Embedding (embedding.hip).
+struct EmbedArgs {
+  const void* W;               // table of the output's type, or codes
+  int64_t vocab, cols, ldw;
+  const float* scale;          // of the codes' rows
+  const int64_t* tokens;
+  int64_t rows;
+  float alpha;
+  const void* P;               // positions, or null
+  int64_t n_pos, ldp;
+  const int64_t* positions;
+  void* Y;
+  int64_t ldy;
+  int chunks;                  // of a row, and the launch's first of all rows': set by the launch
+  int64_t first;
+};
+hipError_t launch_embedding(EmbedArgs a, int dtype, bool codes, hipStream_t stream);
+struct EmbedBwdArgs {
+  const void* dY;
+  int64_t rows, cols, lddy;
+  const int64_t* tokens;
+  int64_t vocab;
+  float alpha;
+  const float* add;            // may be null, or dW
+  int64_t ldadd;
+  float* dW;
+  int64_t lddw;
+};
+size_t embedding_bwd_bytes(int64_t rows, int64_t cols);
+hipError_t launch_embedding_bwd(const EmbedBwdArgs& a, int dtype, void* ws, hipStream_t stream);
+
 // Workspace layout shared by every call: a 256-byte header (word 0 is the
 // share ticket, zero between calls), then 8-byte hash shares, then (GEMM
 // split-K only) int32 partial sums.

@@ -40,6 +40,14 @@ struct Api {
   decltype(&::token_logprobs) token_logprobs;
   decltype(&::token_logprobs_workspace_bytes) token_logprobs_workspace_bytes;
   decltype(&::token_logprobs_bwd) token_logprobs_bwd;
+  decltype(&::gemm_i8_logprobs) gemm_i8_logprobs;
+  decltype(&::gemm_i8_logprobs_workspace_bytes) gemm_i8_logprobs_workspace_bytes;
+  decltype(&::gemm_i8_logprobs_bwd) gemm_i8_logprobs_bwd;
+  decltype(&::gemm_i8_logprobs_bwd_workspace_bytes) gemm_i8_logprobs_bwd_workspace_bytes;
+  decltype(&::embedding) embedding;
+  decltype(&::embedding_i8) embedding_i8;
+  decltype(&::embedding_bwd) embedding_bwd;
+  decltype(&::embedding_bwd_workspace_bytes) embedding_bwd_workspace_bytes;
 } api;
 PyObject* stream_of = nullptr;   // device index -> stream handle
 PyObject* raise_status = nullptr;
@@ -330,14 +338,16 @@ PyObject* checkpoint_quantize_cols_(Args a) {   // Q, scale, group
   return tuple(qt.t, s);
 }
 
-const int64_t* targets(PyObject* o, int64_t rows, const at::Tensor& like) {
-  const at::Tensor& t = tensor_of(o, "targets", "a 1-D int64 tensor");
+// A contiguous int64 vector of `rows` numbers.
+const int64_t* numbers(PyObject* o, const char* name, const char* what, int64_t rows, const at::Tensor& like) {
+  const at::Tensor& t = tensor_of(o, name, "a 1-D int64 tensor");
   if (t.scalar_type() != at::kLong || t.dim() != 1 || t.numel() != rows)
-    refuse("targets must be a 1-D int64 tensor of %lld token numbers", (long long)rows);
-  on_device(t, "targets", &like);
-  if (!t.is_contiguous()) refuse("targets must be contiguous");
+    refuse("%s must be a 1-D int64 tensor of %lld %s numbers", name, (long long)rows, what);
+  on_device(t, name, &like);
+  if (!t.is_contiguous()) refuse("%s must be contiguous", name);
   return static_cast<const int64_t*>(t.data_ptr());
 }
+const int64_t* targets(PyObject* o, int64_t rows, const at::Tensor& like) { return numbers(o, "targets", "token", rows, like); }
 
 PyObject* token_logprobs_(Args a) {   // logits, targets, topk
   const Matrix x = values(a[0], "logits");
@@ -387,6 +397,147 @@ PyObject* token_logprobs_bwd_(Args a) {   // logits, targets, lse, entropy, g_lo
   return wrap(dx);
 }
 
+// The operands of the LM head's product.
+struct Head {
+  Matrix a, b;
+  const float *s_row, *s_col;
+  int64_t lda, ldb;
+  const int8_t* A() const { return static_cast<const int8_t*>(a.data()); }
+  const int8_t* B() const { return static_cast<const int8_t*>(b.data()); }
+};
+Matrix int8_matrix(PyObject* o, const char* name, const at::Tensor* like) {
+  const at::Tensor& t = tensor_of(o, name, "a 2-D int8 tensor");
+  if (t.dim() != 2 || t.scalar_type() != at::kChar) refuse("%s must be a 2-D int8 tensor", name);
+  return layout(t, name, like);
+}
+// A single row of codes has no leading dimension of its own: what the product reads of it is.
+int64_t code_ld(const Matrix& m) { return m.rows > 1 ? m.ld : (m.cols + 15) / 16 * 16; }
+Head head(Args a) {   // QA, s_row, QBt, s_col
+  Head h{int8_matrix(a[0], "QA", nullptr), {}, nullptr, nullptr, 0, 0};
+  h.b = int8_matrix(a[2], "QBt", h.a.t);
+  if (h.a.cols != h.b.cols) refuse("K mismatch: QA has %lld, QBt has %lld", (long long)h.a.cols, (long long)h.b.cols);
+  if (h.b.rows == 0 && h.a.rows > 0) refuse("QBt has no rows");
+  h.s_row = vector(a[1], h.a.rows, "s_row", *h.a.t);
+  h.s_col = vector(a[3], h.b.rows, "s_col", *h.a.t);
+  h.lda = code_ld(h.a);
+  h.ldb = code_ld(h.b);
+  return h;
+}
+
+PyObject* gemm_i8_logprobs_(Args a) {   // QA, s_row, QBt, s_col, targets
+  const Head h = head(a);
+  const at::Tensor& like = *h.a.t;
+  const int64_t* t = targets(a[4], h.a.rows, like);
+  const at::Tensor lp = floats(h.a.rows, like), lse = floats(h.a.rows, like);
+  const size_t bytes = api.gemm_i8_logprobs_workspace_bytes(h.a.rows, h.b.rows, h.a.cols);
+  const at::Tensor ws = scratch(bytes, like);
+  enqueue(api.gemm_i8_logprobs, like, h.A(), h.lda, h.s_row, h.B(), h.ldb, h.s_col, h.a.rows, h.b.rows, h.a.cols, t, f32(lp),
+          f32(lse), ws.data_ptr(), bytes);
+  return tuple(lp, lse);
+}
+
+PyObject* gemm_i8_logprobs_bwd_(Args a) {   // QA, s_row, QBt, s_col, targets, lse, g_logprob, g_lse, dtype code
+  const Head h = head(a);
+  const at::Tensor& like = *h.a.t;
+  if (a[6] == Py_None && a[7] == Py_None) refuse("g_logprob or g_lse is needed");
+  if (a[6] != Py_None && a[4] == Py_None) refuse("targets are needed with g_logprob");
+  const int64_t* t = a[4] == Py_None ? nullptr : targets(a[4], h.a.rows, like);
+  const float* lse = vector(a[5], h.a.rows, "lse", like);
+  const float *g = vector(a[6], h.a.rows, "g_logprob", like, true), *gl = vector(a[7], h.a.rows, "g_lse", like, true);
+  const int64_t dtype = integer(a[8]);
+  const at::ScalarType type = dtype == I8G_F32 ? at::kFloat : dtype == I8G_BF16 ? at::kBFloat16 : at::kHalf;
+  const at::Tensor da = fresh({h.a.rows, h.a.cols}, type, like), db = fresh({h.b.rows, h.b.cols}, type, like);
+  const size_t bytes = api.gemm_i8_logprobs_bwd_workspace_bytes(h.a.rows, h.b.rows, h.a.cols, (uint32_t)dtype);
+  const at::Tensor ws = scratch(bytes, like);
+  enqueue(api.gemm_i8_logprobs_bwd, like, h.A(), h.lda, h.s_row, h.B(), h.ldb, h.s_col, h.a.rows, h.b.rows, h.a.cols, t, lse, g,
+          gl, da.data_ptr(), ld_of(h.a.cols), db.data_ptr(), ld_of(h.a.cols), (uint32_t)dtype, ws.data_ptr(), bytes);
+  return tuple(da, db);
+}
+
+int64_t token_count(PyObject* o) {
+  const at::Tensor& t = tensor_of(o, "tokens", "a 1-D int64 tensor");
+  if (t.dim() != 1) refuse("tokens must be a 1-D int64 tensor");
+  return t.numel();
+}
+
+// pos_table and positions, of a type and as many columns as the output.
+struct Positions {
+  Matrix p{nullptr, 0, 0, 0};
+  const int64_t* at = nullptr;
+  Positions(PyObject* table, PyObject* numbers_of, int64_t rows, int64_t cols, at::ScalarType type, const at::Tensor& like) {
+    if ((table == Py_None) != (numbers_of == Py_None)) refuse("pos_table and positions go together");
+    if (table == Py_None) return;
+    p = values(table, "pos_table");
+    on_device(*p.t, "pos_table", &like);
+    if (p.t->scalar_type() != type || p.cols != cols)
+      refuse("pos_table must have %lld columns of %s", (long long)cols, at::toString(type));
+    at = numbers(numbers_of, "positions", "position", rows, like);
+  }
+  const void* data() const { return p.t ? p.data() : nullptr; }
+};
+
+PyObject* embedding_(Args a) {   // table, tokens, alpha, pos_table, positions
+  const Matrix w = values(a[0], "table");
+  const int64_t rows = token_count(a[1]);
+  const int64_t* t = numbers(a[1], "tokens", "token", rows, *w.t);
+  const float alpha = (float)real(a[2]);
+  const at::ScalarType type = w.t->scalar_type();
+  const Positions p(a[3], a[4], rows, w.cols, type, *w.t);
+  const at::Tensor y = fresh({rows, w.cols}, type, *w.t);
+  enqueue(api.embedding, *w.t, w.data(), dtype_code(type), w.rows, w.cols, w.ld, t, rows, alpha, p.data(), p.p.rows, p.p.ld, p.at,
+          y.data_ptr(), ld_of(w.cols));
+  return wrap(y);
+}
+
+PyObject* embedding_i8_(Args a) {   // Q, scale, tokens, alpha, pos_table, positions, dtype code
+  const Matrix q = int8_matrix(a[0], "Q", nullptr);
+  const float* s = vector(a[1], q.rows, "scale", *q.t);
+  const int64_t rows = token_count(a[2]);
+  const int64_t* t = numbers(a[2], "tokens", "token", rows, *q.t);
+  const float alpha = (float)real(a[3]);
+  const int64_t dtype = integer(a[6]);
+  const at::ScalarType type = dtype == I8G_F32 ? at::kFloat : dtype == I8G_BF16 ? at::kBFloat16 : at::kHalf;
+  const Positions p(a[4], a[5], rows, q.cols, type, *q.t);
+  const at::Tensor y = fresh({rows, q.cols}, type, *q.t);
+  enqueue(api.embedding_i8, *q.t, static_cast<const int8_t*>(q.data()), q.ld, s, q.rows, q.cols, t, rows, alpha, p.data(),
+          p.p.rows, p.p.ld, p.at, y.data_ptr(), (uint32_t)dtype, ld_of(q.cols));
+  return wrap(y);
+}
+
+Matrix f32_matrix(PyObject* o, const char* name, int64_t rows, int64_t cols, const at::Tensor& like) {
+  const at::Tensor& t = tensor_of(o, name, "a 2-D float32 tensor");
+  if (t.dim() != 2 || t.scalar_type() != at::kFloat || t.size(0) != rows || t.size(1) != cols)
+    refuse("%s must be a float32 tensor of shape (%lld, %lld)", name, (long long)rows, (long long)cols);
+  return layout(t, name, &like);
+}
+
+PyObject* embedding_bwd_(Args a) {   // dY, tokens, vocab, alpha, add, out
+  const Matrix dy = values(a[0], "dY");
+  const int64_t* t = numbers(a[1], "tokens", "token", dy.rows, *dy.t);
+  const int64_t vocab = integer(a[2]);
+  if (vocab < 0 || vocab > INT32_MAX) refuse("vocab must be between 0 and 2^31 - 1, got %lld", (long long)vocab);
+  const float alpha = (float)real(a[3]);
+  Matrix add{nullptr, 0, 0, 0}, out{nullptr, 0, 0, 0};
+  if (a[4] != Py_None) add = f32_matrix(a[4], "add", vocab, dy.cols, *dy.t);
+  at::Tensor dw;
+  if (a[5] == Py_None) {
+    dw = fresh({vocab, dy.cols}, at::kFloat, *dy.t);
+    out = Matrix{&dw, vocab, dy.cols, ld_of(dy.cols)};
+  } else {
+    out = f32_matrix(a[5], "out", vocab, dy.cols, *dy.t);
+    dw = *out.t;
+    if (add.t && !i8g::itself_or_apart(bytes_of(out), bytes_of(add))) refuse("out must be `add` itself or not overlap it");
+    if (i8g::share_bytes(bytes_of(out), bytes_of(dy)) || i8g::share_bytes(bytes_of(out), bytes_of(THPVariable_Unpack(a[1]))))
+      refuse("out must not overlap dY or tokens");
+  }
+  const size_t bytes = api.embedding_bwd_workspace_bytes(dy.rows, dy.cols);
+  const at::Tensor ws = scratch(bytes, *dy.t);
+  enqueue(api.embedding_bwd, *dy.t, dy.data(), dtype_code(dy.t->scalar_type()), dy.rows, dy.cols, dy.ld, t, vocab, alpha,
+          add.t ? static_cast<const float*>(add.data()) : nullptr, add.ld, static_cast<float*>(out.data()), out.ld,
+          ws.data_ptr(), bytes);
+  return wrap(dw);
+}
+
 template <PyObject* (*F)(Args), int N>
 PyObject* entry(PyObject*, Args args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -423,7 +574,9 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TAKE(layer_norm); TAKE(layer_norm_quantize_rows); TAKE(layer_norm_bwd); TAKE(layer_norm_bwd_workspace_bytes);
   TAKE(layer_norm_bwd_checkpoint); TAKE(checkpoint_i8); TAKE(checkpoint_restore); TAKE(checkpoint_act_bwd);
   TAKE(checkpoint_quantize_cols); TAKE(checkpoint_quantize_cols_workspace_bytes); TAKE(token_logprobs);
-  TAKE(token_logprobs_workspace_bytes); TAKE(token_logprobs_bwd);
+  TAKE(token_logprobs_workspace_bytes); TAKE(token_logprobs_bwd); TAKE(gemm_i8_logprobs);
+  TAKE(gemm_i8_logprobs_workspace_bytes); TAKE(gemm_i8_logprobs_bwd); TAKE(gemm_i8_logprobs_bwd_workspace_bytes);
+  TAKE(embedding); TAKE(embedding_i8); TAKE(embedding_bwd); TAKE(embedding_bwd_workspace_bytes);
 #undef TAKE
   if (!ok) return nullptr;
   Py_INCREF(a[1]);
@@ -446,6 +599,11 @@ PyMethodDef methods[] = {
     ENTRY(checkpoint_quantize_cols, 3),
     ENTRY(token_logprobs, 3),
     ENTRY(token_logprobs_bwd, 7),
+    ENTRY(gemm_i8_logprobs, 5),
+    ENTRY(gemm_i8_logprobs_bwd, 9),
+    ENTRY(embedding, 5),
+    ENTRY(embedding_i8, 7),
+    ENTRY(embedding_bwd, 6),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "rowops_bind", "Binding of the operators between the GEMMs.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
