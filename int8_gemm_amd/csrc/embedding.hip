@@ -8,7 +8,7 @@
 // in flight.  The gradient sorts the tokens (a stable radix sort of 8192 at a
 // time in LDS, while the other workgroups write the rows that no token names;
 // the sorted runs are merged 8 at a time), then adds rows in the sorted order:
-// a wave takes kPiece places of the order and a chunk of columns, writes the
+// a wave takes a piece of the order and a chunk of columns, writes the
 // rows of tokens whose places it holds all of, and leaves the others' sums in
 // the workspace, which a last launch joins.  No sum depends on which
 // workgroup comes first.
@@ -121,6 +121,7 @@ struct SortArgs {
   int bits;                    // of the keys 0 ... vocab (vocab: no token)
   uint32_t *keys, *order;      // [rows]: sorted within each run of kRun
   int runs;
+  uint32_t* listed;            // zeroed for the sums
 };
 
 __device__ __forceinline__ void fill_rows(const FillArgs& p, int block) {
@@ -133,7 +134,7 @@ __device__ __forceinline__ void fill_rows(const FillArgs& p, int block) {
     for (int c = lane * 4; c < cols; c += 256) {
       float x[4] = {};
       if (from) load_row<float, 4>(from, c, cols, 0.0f, x);
-      store_row<float>(to, c, cols, x);
+      stream_row<float>(to, c, cols, x);
     }
   }
 }
@@ -143,6 +144,7 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const Sort
     fill_rows(fill, (int)blockIdx.x - p.runs);
     return;
   }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.listed = 0;
   __shared__ uint32_t key[2][kRun];
   __shared__ uint16_t at[2][kRun];
   __shared__ uint32_t count[(1 << kDigit) * kSortWaves];   // [digit][wave]
@@ -231,26 +233,35 @@ __global__ void __launch_bounds__(256) embedding_merge_kernel(const MergeArgs p)
   if (i >= p.rows) return;
   const uint32_t k = p.keys[i];
   const int64_t own = i / p.run, group = own / kMerge * kMerge;
-  int64_t place = group * p.run + (i - own * p.run);
-  for (int64_t r = group; r < group + kMerge; ++r) {
-    const int64_t start = r * p.run;
-    if (r == own || start >= p.rows) continue;
-    const uint32_t* a = p.keys + start;
-    int64_t lo = 0, hi = min(p.run, p.rows - start);
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (a[mid] < k || (r < own && a[mid] == k)) lo = mid + 1;
-      else hi = mid;
+  int64_t place = i - (own - group) * p.run;
+  // the searches side by side: each step's loads are independent
+  int64_t before[kMerge];
+#pragma unroll
+  for (int r = 0; r < kMerge; ++r) before[r] = 0;
+  for (int64_t step = p.run; step > 0; step >>= 1) {
+    uint32_t a[kMerge];
+#pragma unroll
+    for (int r = 0; r < kMerge; ++r) a[r] = p.keys[min((group + r) * p.run + before[r] + step, p.rows) - 1];
+#pragma unroll
+    for (int r = 0; r < kMerge; ++r) {
+      const int64_t at = before[r] + step;       // are the run's first `at` before it?
+      const bool there = group + r != own && at <= p.run && (group + r) * p.run + at <= p.rows;
+      if (there && (a[r] < k || (a[r] == k && group + r < own))) before[r] = at;
     }
-    place += lo;
   }
+#pragma unroll
+  for (int r = 0; r < kMerge; ++r) place += before[r];
   p.keys_out[place] = k;
   p.order_out[place] = p.order[i];
 }
 
 // ---- the sums -----------------------------------------------------------------------
-constexpr int kPiece = 16;                     // places of the order that a wave takes
-constexpr int kAhead = 8;                      // rows in flight
+constexpr int kLane = 4;                       // columns of a lane
+// Places whose rows a wave has in flight (fewer where the rows that they are
+// added to are, too).
+template <bool ONTO>
+constexpr int kBatch = ONTO ? 8 : 16;
+constexpr int kPlaces = 16;                    // a piece is a multiple of
 
 struct SumArgs {
   const void* dY;
@@ -260,135 +271,149 @@ struct SumArgs {
   float* dW;
   int64_t lddw;
   int onto;                    // dW holds what the sums are added to
-  double* parts;               // [pieces][2][cols]: sums of the piece's part of a token that began before it, and
+  int64_t piece, pieces;       // places of a piece (a multiple of kBatch), and how many there are
+  double* parts;               // [pieces][2][ldp]: sums of the piece's part of a token that began before it, and
                                // of one that goes on behind it
-  int64_t pieces;
+  int64_t ldp;                 // cols in whole chunks
+  uint32_t *list, *listed;     // the pieces that left a second sum, and how many they are
   int chunks;                  // of 64 vectors
   int64_t first;               // unit
 };
 
-template <int N>
-__device__ __forceinline__ void write_row(const SumArgs& p, uint32_t token, int c, const double (&s)[N]) {
-  float* to = p.dW + (int64_t)token * p.lddw;
-  const int cols = (int)p.cols;
-  float o[N], y[N];
-#pragma unroll
-  for (int e = 0; e < N; ++e) o[e] = 0.0f;
-  if (p.onto) load_row<float, N>(to, c, cols, 0.0f, o);
-#pragma unroll
-  for (int e = 0; e < N; ++e) y[e] = (float)(p.onto ? (double)o[e] + p.alpha * s[e] : p.alpha * s[e]);
-#pragma unroll
-  for (int h = 0; h < N / 4; ++h) {
-    const float q[4] = {y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3]};
-    if (c + 4 * h < cols) store_row<float>(to, c + 4 * h, cols, q);
+template <int B, int E, class F>
+__device__ __forceinline__ void for_each(F&& f) {
+  if constexpr (B < E) {
+    f(std::integral_constant<int, B>{});
+    for_each<B + 1, E>(f);
   }
 }
-template <int N>
-__device__ __forceinline__ void leave_part(const SumArgs& p, int64_t piece, int which, int c, const double (&s)[N]) {
-  double* to = p.parts + (piece * 2 + which) * p.cols;
-#pragma unroll
-  for (int e = 0; e < N; ++e)
-    if (c + e < (int)p.cols) to[c + e] = s[e];
-}
 
-// WHOLE: every lane's vector lies in the row (loads without a condition stay
+// WHOLE: every lane's columns lie in the row (loads without a condition stay
 // where they are written, ahead of their use).
-template <class T, bool WHOLE>
+template <class T, bool WHOLE, bool ONTO>
 __device__ __forceinline__ void sum_piece(const SumArgs& p, int64_t piece, int c) {
-  constexpr int N = kVec<T>;
+  constexpr int N = kLane, B = kBatch<ONTO>;
   const int lane = threadIdx.x & 63;
   const int cols = (int)p.cols;
-  const int64_t begin = piece * kPiece, end = min(begin + kPiece, p.rows);
-  if (uniform(p.keys[begin]) >= (uint32_t)p.vocab) return;         // what is no token sorts last
-  const bool went_on = begin > 0 && uniform(p.keys[begin - 1]) == uniform(p.keys[begin]);
-  const bool goes_on = end < p.rows && uniform(p.keys[end]) == uniform(p.keys[end - 1]);
-  // the places' tokens and rows, one a lane
-  const int n = (int)(end - begin);
-  const uint32_t my_key = lane < n ? p.keys[begin + lane] : 0xFFFFFFFFu;
-  const uint32_t my_row = p.order[begin + min(lane, n - 1)];
+  const int64_t begin = piece * p.piece, end = min(begin + p.piece, p.rows);
+  const uint32_t vocab = (uint32_t)p.vocab;
+  bool head = false;                             // the sum began before the piece
   const T* dy = static_cast<const T*>(p.dY);
-  RawRow<T, N> ahead[kAhead];
-  auto load = [&](int i) {
-    const T* row = dy + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)my_row, i) * p.lddy;
-    if constexpr (WHOLE) __builtin_memcpy(ahead[i % kAhead].t, row + c, sizeof(ahead[0].t));
-    else ahead[i % kAhead].load(row, c, cols);
-  };
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(i);
+  double* parts = p.parts + piece * 2 * p.ldp + c;
   double s[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) s[e] = 0.0;
-  bool head = went_on;
+  for (int64_t at = begin; at < end; at += B) {
+    // lane i: the token and the row of place i - 1 (so the first one's is the
+    // place before the batch, the last one's the place behind it)
+    const int64_t mine = at - 1 + min(lane, B + 1);
+    const uint32_t my_key = mine >= 0 && mine < p.rows ? p.keys[mine] : 0xFFFFFFFFu;
+    const uint32_t my_row = p.order[min(max(mine, begin), end - 1)];
+    const int places = (int)min((int64_t)B, end - at);
+    const int n = __popcll(__builtin_amdgcn_ballot_w64(lane >= 1 && lane <= places && my_key < vocab));   // (no token sorts last)
+    if (at == begin) head = __builtin_amdgcn_readlane((int)my_key, 0) == __builtin_amdgcn_readlane((int)my_key, 1);
+    if (n == 0) return;
+    RawRow<T, N> row[B];
 #pragma unroll
-  for (int i = 0; i < kPiece; ++i) {
-    if (i >= n) break;
-    const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)my_key, i);
-    if (key >= (uint32_t)p.vocab) break;
-#pragma unroll
-    for (int e = 0; e < N; ++e) s[e] += (double)ahead[i % kAhead][e];
-    if (i + kAhead < kPiece) load(i + kAhead);
-    const bool last = i + 1 == n;
-    if (last || (uint32_t)__builtin_amdgcn_readlane((int)my_key, i + 1) != key) {
-      if (WHOLE || c < cols) {
-        if (head) leave_part<N>(p, piece, 0, c, s);
-        else if (last && goes_on) leave_part<N>(p, piece, 1, c, s);
-        else write_row<N>(p, key, c, s);
-      }
-#pragma unroll
-      for (int e = 0; e < N; ++e) s[e] = 0.0;
-      head = false;
+    for (int i = 0; i < B; ++i) {
+      const T* r = dy + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)my_row, i + 1) * p.lddy;
+      if constexpr (WHOLE) __builtin_memcpy(row[i].t, r + c, sizeof(row[i].t));
+      else row[i].load(r, c, cols);
     }
+    // the rows that sums of this batch are added to
+    RawRow<float, N> old[B];
+    if constexpr (ONTO) {
+      for_each<0, B>([&](auto i) {
+        const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)my_key, i + 1);
+        if (i < n && (uint32_t)__builtin_amdgcn_readlane((int)my_key, i + 2) != key) {
+          const float* from = p.dW + (int64_t)key * p.lddw;
+          if constexpr (WHOLE) __builtin_memcpy(old[i].t, from + c, sizeof(old[i].t));
+          else old[i].load(from, c, cols);
+        }
+      });
+    }
+    for_each<0, B>([&](auto i) {
+      if (i < n) {
+        const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)my_key, i + 1);
+        const bool ends = (uint32_t)__builtin_amdgcn_readlane((int)my_key, i + 2) != key;
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[e] += (double)row[i][e];
+        if (ends || at + i + 1 == end) {
+          if (head || !ends) {
+            __builtin_memcpy(parts + (head ? 0 : p.ldp), s, sizeof(s));
+            // (the list's order is no matter: its entries have nothing in common)
+            if (!head && c == 0) p.list[atomicAdd(p.listed, 1u)] = (uint32_t)piece;
+          } else if (WHOLE || c < cols) {
+            float* to = p.dW + (int64_t)key * p.lddw;
+            float y[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) y[e] = (float)(ONTO ? (double)old[i][e] + p.alpha * s[e] : p.alpha * s[e]);
+            if constexpr (WHOLE) __builtin_memcpy(to + c, y, sizeof(y));
+            else store_row<float, N>(to, c, cols, y);
+          }
+#pragma unroll
+          for (int e = 0; e < N; ++e) s[e] = 0.0;
+          head = false;
+        }
+      }
+    });
   }
 }
 
-template <class T>
+template <class T, bool ONTO>
 __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs p) {
-  constexpr int N = kVec<T>;
   const int64_t unit = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + p.first;
   const int64_t piece = p.chunks == 1 ? unit : unit / p.chunks;
   if (piece >= p.pieces) return;
-  const int c0 = (int)(unit - piece * p.chunks) * 64 * N;
-  const int c = c0 + (threadIdx.x & 63) * N;
-  if (c0 + 64 * N <= (int)p.cols) sum_piece<T, true>(p, piece, c);
-  else sum_piece<T, false>(p, piece, c);
+  const int c0 = (int)(unit - piece * p.chunks) * 64 * kLane;
+  const int c = c0 + (threadIdx.x & 63) * kLane;
+  if (c0 + 64 * kLane <= (int)p.cols) sum_piece<T, true, ONTO>(p, piece, c);
+  else sum_piece<T, false, ONTO>(p, piece, c);
 }
 
-// A workgroup for each piece and 64 columns: where a token's places begin in
-// the piece and go on behind it, its parts are added, 4 waves taking every
-// fourth, the waves' sums in their order.
+// Workgroups take a listed piece and 256 columns at a time: the sums of the
+// token that goes on behind the piece, added in their order.
+constexpr int kJoinGroups = 2048;
 __global__ void __launch_bounds__(256) embedding_join_kernel(const SumArgs p) {
-  const int64_t unit = (int64_t)blockIdx.x + p.first;
-  const int64_t piece = unit / p.chunks;
-  const int64_t end = (piece + 1) * kPiece;
-  if (end >= p.rows) return;
-  const uint32_t key = uniform(p.keys[end - 1]);
-  if (uniform(p.keys[end]) != key || key >= (uint32_t)p.vocab) return;
-  const int64_t begin = piece * kPiece;
-  if (uniform(p.keys[begin]) == key && begin > 0 && uniform(p.keys[begin - 1]) == key) return;   // began earlier
-  // the last place of the token
-  int64_t lo = end, hi = p.rows;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (uniform(p.keys[mid]) == key) lo = mid + 1;
-    else hi = mid;
+  const int64_t items = (int64_t)uniform(*p.listed) * p.chunks;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t entry = p.chunks == 1 ? item : item / p.chunks;
+    const int64_t piece = uniform(p.list[entry]);
+    const int64_t c = (item - entry * p.chunks) * 256 + threadIdx.x;
+    const uint32_t key = uniform(p.keys[(piece + 1) * p.piece - 1]);
+    // the last piece that it goes on in: 64 of their first places at a time
+    int64_t last = piece + 1;
+    for (;; last += 64) {
+      const int64_t at = (last + 1 + (threadIdx.x & 63)) * p.piece;
+      const uint64_t on = __builtin_amdgcn_ballot_w64(at < p.rows && p.keys[min(at, p.rows - 1)] == key);
+      if (~on != 0) {
+        last += __builtin_ctzll(~on);
+        break;
+      }
+    }
+    if (c >= p.cols) continue;
+    const double* part = p.parts + c;
+    double s = part[(piece * 2 + 1) * p.ldp];
+    float* to = p.dW + (int64_t)key * p.lddw + c;
+    const float old = p.onto ? *to : 0.0f;
+    int64_t q = piece + 1;
+    for (; q + 31 <= last; q += 32) {
+      double x[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = part[(q + i) * 2 * p.ldp];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s += x[i];
+    }
+    for (; q <= last; q += 4) {
+      double x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = part[min(q + i, last) * 2 * p.ldp];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (q + i <= last) s += x[i];
+    }
+    *to = (float)(p.onto ? (double)old + p.alpha * s : p.alpha * s);
   }
-  const int64_t last = (lo - 1) / kPiece;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = (int)(unit - piece * p.chunks) * 64 + lane;
-  const bool in = c < (int)p.cols;
-  double s = 0.0;
-  if (in) {
-    if (wave == 0) s = p.parts[(piece * 2 + 1) * p.cols + c];
-#pragma unroll 4
-    for (int64_t q = piece + 1 + wave; q <= last; q += 4) s += p.parts[q * 2 * p.cols + c];
-  }
-  __shared__ double sum[4][64];
-  sum[wave][lane] = s;
-  __syncthreads();
-  if (wave != 0 || !in) return;
-  s = (sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]);
-  float* to = p.dW + (int64_t)key * p.lddw + c;
-  *to = (float)(p.onto ? (double)*to + p.alpha * s : p.alpha * s);
 }
 
 // Launches of at most 2^22 workgroups.
@@ -427,22 +452,39 @@ hipError_t launch_embedding(EmbedArgs a, int dtype, bool codes, hipStream_t stre
   });
 }
 
-// The workspace: the sorted keys and rows (twice where runs are merged), then
-// the parts.
-size_t embedding_bwd_bytes(int64_t rows, int64_t cols) {
-  const size_t list = aligned((size_t)rows * 4);
-  return list * (merges(rows) > 0 ? 4 : 2) + aligned((size_t)up64(rows, kPiece) * 2 * (size_t)cols * 8);
+// Places of a piece: as few as leave at most about 4096 waves, 16 to 128.
+int64_t piece_of(int64_t rows, int64_t cols) {
+  const int64_t n = up64(rows, kPlaces) * up64(cols, 64 * kLane) / 4096;
+  return kPlaces * (n < 1 ? 1 : n > 8 ? 8 : n);
 }
+int64_t part_ld(int64_t cols) { return up64(cols, 64 * kLane) * (64 * kLane); }
+
+// The workspace: the sorted keys and rows (twice where runs are merged), the
+// pieces to be joined and their count, and the parts.
+struct BwdLayout {
+  size_t list, joined, bytes;  // of a list of keys or rows; where the pieces' list and the parts begin
+  size_t parts;
+};
+BwdLayout bwd_layout(int64_t rows, int64_t cols) {
+  BwdLayout l;
+  const int64_t pieces = up64(rows, piece_of(rows, cols));
+  l.list = aligned((size_t)rows * 4);
+  l.joined = l.list * (merges(rows) > 0 ? 4 : 2);
+  l.parts = l.joined + aligned((size_t)(pieces + 1) * 4);
+  l.bytes = l.parts + (size_t)pieces * 2 * (size_t)part_ld(cols) * 8;
+  return l;
+}
+size_t embedding_bwd_bytes(int64_t rows, int64_t cols) { return bwd_layout(rows, cols).bytes; }
 
 hipError_t launch_embedding_bwd(const EmbedBwdArgs& a, int dtype, void* ws, hipStream_t stream) {
   char* at = static_cast<char*>(ws);
-  const size_t list = aligned((size_t)a.rows * 4);
-  const int64_t n_merges = merges(a.rows);
+  const BwdLayout lay = bwd_layout(a.rows, a.cols);
+  const size_t list = lay.list;
   uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(at), reinterpret_cast<uint32_t*>(at + 2 * list)};
   uint32_t* order[2] = {reinterpret_cast<uint32_t*>(at + list), reinterpret_cast<uint32_t*>(at + 3 * list)};
-  double* parts = reinterpret_cast<double*>(at + list * (n_merges > 0 ? 4 : 2));
+  uint32_t* listed = reinterpret_cast<uint32_t*>(at + lay.joined);
   const bool in_place = a.add == a.dW;
-  SortArgs s{a.tokens, a.rows, a.vocab, 0, keys[0], order[0], (int)up64(a.rows, kRun)};
+  SortArgs s{a.tokens, a.rows, a.vocab, 0, keys[0], order[0], (int)up64(a.rows, kRun), listed};
   while ((a.vocab >> s.bits) != 0) ++s.bits;              // vocab itself is a key
   if (s.bits == 0) s.bits = 1;
   // 1024 workgroups fill: 4 for each of the 256 CUs
@@ -456,21 +498,23 @@ hipError_t launch_embedding_bwd(const EmbedBwdArgs& a, int dtype, void* ws, hipS
     hipLaunchKernelGGL(embedding_merge_kernel, dim3((unsigned)up64(a.rows, 256)), dim3(256), 0, stream, m);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  const int n = dtype == DT_F32 ? 4 : 8;
+  const int64_t piece = piece_of(a.rows, a.cols);
   SumArgs u{a.dY, a.rows, a.cols, a.lddy, a.vocab, keys[from], order[from], (double)a.alpha, a.dW, a.lddw, a.add != nullptr,
-            parts, up64(a.rows, kPiece), (int)up64(a.cols, 64 * n), 0};
+            piece, up64(a.rows, piece), reinterpret_cast<double*>(at + lay.parts), part_ld(a.cols), listed + 1, listed, (int)up64(a.cols, 64 * kLane), 0};
   e = in_slabs(up64(u.pieces * u.chunks, 4), [&](unsigned grid, int64_t first) {
     u.first = first * 4;
-    if (dtype == DT_F32) hipLaunchKernelGGL(embedding_sum_kernel<float>, dim3(grid), dim3(256), 0, stream, u);
-    else if (dtype == DT_BF16) hipLaunchKernelGGL(embedding_sum_kernel<bf16_t>, dim3(grid), dim3(256), 0, stream, u);
-    else hipLaunchKernelGGL(embedding_sum_kernel<f16_t>, dim3(grid), dim3(256), 0, stream, u);
+    const dim3 g(grid), b(256);
+    if (dtype == DT_F32 && u.onto) hipLaunchKernelGGL((embedding_sum_kernel<float, true>), g, b, 0, stream, u);
+    else if (dtype == DT_BF16 && u.onto) hipLaunchKernelGGL((embedding_sum_kernel<bf16_t, true>), g, b, 0, stream, u);
+    else if (u.onto) hipLaunchKernelGGL((embedding_sum_kernel<f16_t, true>), g, b, 0, stream, u);
+    else if (dtype == DT_F32) hipLaunchKernelGGL((embedding_sum_kernel<float, false>), g, b, 0, stream, u);
+    else if (dtype == DT_BF16) hipLaunchKernelGGL((embedding_sum_kernel<bf16_t, false>), g, b, 0, stream, u);
+    else hipLaunchKernelGGL((embedding_sum_kernel<f16_t, false>), g, b, 0, stream, u);
   });
   if (e != hipSuccess || u.pieces == 1) return e;
-  u.chunks = (int)up64(a.cols, 64);
-  return in_slabs((u.pieces - 1) * u.chunks, [&](unsigned grid, int64_t first) {
-    u.first = first;
-    hipLaunchKernelGGL(embedding_join_kernel, dim3(grid), dim3(256), 0, stream, u);
-  });
+  const int64_t items = (u.pieces - 1) * u.chunks;
+  hipLaunchKernelGGL(embedding_join_kernel, dim3((unsigned)(items < kJoinGroups ? items : kJoinGroups)), dim3(256), 0, stream, u);
+  return hipGetLastError();
 }
 
 }  // namespace i8g

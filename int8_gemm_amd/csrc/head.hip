@@ -9,9 +9,12 @@
 //   dA_ik = sum_j G_ij s_col_j QBt_jk     dBt_jk = sum_i G_ij s_row_i QA_ik
 // Both gradients read one matrix T_ij = s_row_i G_ij s_col_j:
 //   dA_ik = (1 / s_row_i) sum_j T_ij QBt_jk,  dBt_jk = (1 / s_col_j) sum_i T_ij QA_ik,
-// and the codes are exact in bf16, so T is all that is rounded for the matrix
-// cores: to bf16 for bf16 gradients (2^-9 of each value, what the outputs are
-// rounded by too), to a sum of two bf16 (2^-18) for f32 and f16 ones.
+// and the codes are exact in f16, so T is all that is rounded for the matrix
+// cores: to f16 for bf16 gradients (2^-12 of each value, less than the outputs'
+// own rounding), to a sum of two f16 (2^-24) for f32 and f16 ones.  (Two bf16
+// would be 2^-18; f16 takes the same time.)  T is scaled by a power of two that
+// puts max (|g| + |gl|) s_row max s_col at 2^13 to 2^14: a value's error is then
+// at most 2^-40 of that maximum where it is below f16's normal numbers.
 //
 // Forward: a workgroup multiplies a tile of vocabulary rows by a tile of
 // tokens; the vocabulary is the accumulators' row dimension, so that a lane
@@ -38,8 +41,8 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef short v4s __attribute__((ext_vector_type(4)));
-typedef __bf16 v8b __attribute__((ext_vector_type(8)));
-typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.44269502f;
 constexpr float kLowest = -2e38f;      // the least maximum of a row's part: its product with kLog2e is finite
@@ -347,27 +350,35 @@ __global__ void __launch_bounds__(256) head_join_kernel(const JoinArgs p) {
   __shared__ float out[R];
   const int tid = threadIdx.x, r = tid % R, slot = tid / R;
   const int row = blockIdx.x * R + r;
-  float m = -__builtin_inff();
+  // maxima are finite or +inf, never NaN (they ignore it; the sum is NaN then)
+  float m = -3.4e38f;
+  if (row < p.l.M)
+#pragma unroll 4
+    for (int i = slot; i < p.n_parts; i += S) m = fmaxf(m, p.parts[(size_t)i * p.l.M + row].x);
+  top[slot][r] = m;
+  __syncthreads();
+#pragma unroll
+  for (int d = S / 2; d >= 1; d >>= 1) {
+    if (slot < d) top[slot][r] = fmaxf(top[slot][r], top[slot + d][r]);
+    __syncthreads();
+  }
+  m = top[0][r];
   double s = 0.0;
   if (row < p.l.M)
+#pragma unroll 4
     for (int i = slot; i < p.n_parts; i += S) {
       const v2f a = p.parts[(size_t)i * p.l.M + row];
-      // (a NaN maximum does not occur: maxima ignore NaN and their rows have a NaN sum)
-      if (a.x > m) {
-        s *= exp2((double)m - (double)a.x);
-        m = a.x;
-      }
-      s += (double)a.y * exp2((double)a.x - (double)m);
+      s += (double)(a.y * __builtin_amdgcn_exp2f(a.x - m));
     }
-  top[slot][r] = m;
   sum[slot][r] = s;
   __syncthreads();
-  if (tid < R) {
-    for (int i = 1; i < S; ++i) m = fmaxf(m, top[i][r]);
-    s = 0.0;
-    for (int i = 0; i < S; ++i)
-      if (top[i][r] > -__builtin_inff()) s += sum[i][r] * exp2((double)top[i][r] - (double)m);
-    const float lse = (float)(((double)m + log2(s)) / (double)kLog2e);
+#pragma unroll
+  for (int d = S / 2; d >= 1; d >>= 1) {
+    if (slot < d) sum[slot][r] += sum[slot + d][r];
+    __syncthreads();
+  }
+  if (slot == 0) {
+    const float lse = (float)(((double)m + log2(sum[0][r])) / (double)kLog2e);
     out[r] = lse;
     if (row < p.l.M && p.lse) p.lse[row] = lse;
   }
@@ -402,44 +413,89 @@ __global__ void __launch_bounds__(256) head_join_kernel(const JoinArgs p) {
 }
 
 // ---- backward ---------------------------------------------------------------------
-// Codes as bf16 blocks of 16 rows (the contraction) by 32 columns, 1 KiB in the
+// T's power of two, from parts of the two maxima: max |T| is at most 2^14.
+constexpr int kBounds = 64;
+struct Bound {
+  float row, col;              // largest (|g| + |gl|) s_row and s_col of a part
+};
+__device__ __forceinline__ float t_scale(const Bound* bounds) {
+  const Bound b = bounds[threadIdx.x & 63];
+  const float row = __uint_as_float(lanes_max_u32<64>(__float_as_uint(b.row)));
+  const float col = __uint_as_float(lanes_max_u32<64>(__float_as_uint(b.col)));
+  if (!(row > 0.0f && row < __builtin_inff() && col > 0.0f && col < __builtin_inff())) return 1.0f;
+  const int e = 14 - __builtin_amdgcn_frexp_expf(row) - __builtin_amdgcn_frexp_expf(col);   // row < 2^frexp_exp(row)
+  return __builtin_ldexpf(1.0f, e < -120 ? -120 : e > 120 ? 120 : e);
+}
+
+// Before the pieces, in one launch: the parts of the bound, and both operands'
+// codes as f16 blocks of 16 rows (the contraction) by 32 columns, 1 KiB in the
 // order of a fragment: lane l holds column l%32, rows 8 (l/32) ... + 7.  Zero
 // beyond `rows` and `cols`.
 struct PackArgs {
-  const int8_t* Q;
-  int64_t ld;
-  int rows, cols;
-  int row0;                    // first row of the piece
-  int blocks;                  // blocks of 16 rows
+  LogitArgs l;
+  const int64_t* targets;
+  const float *g, *gl;
+  Bound* bounds;
+  int blocks_a, blocks_b;      // blocks of 16 rows
   int KB;                      // blocks of 32 columns
-  v4i* out;                    // [blocks][KB][64]
+  v4i *out_a, *out_b;          // [blocks][KB][64]
 };
-__global__ void __launch_bounds__(256) head_pack_kernel(const PackArgs p) {
-  const int c4 = threadIdx.x & 7, half = (threadIdx.x >> 3) & 1;  // 16 threads a block, 4 columns and 8 rows each
-  for (int64_t block = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); block < (int64_t)p.blocks * p.KB; block += (int64_t)gridDim.x * 16) {
-    const int b16 = (int)(block / p.KB), kb = (int)(block % p.KB);
+__global__ void __launch_bounds__(256) head_prepare_kernel(const PackArgs p) {
+  const int tid = threadIdx.x;
+  if (blockIdx.x < kBounds) {
+    float row = 0.0f, col = 0.0f;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + tid; i < p.l.M; i += kBounds * 256) {
+      float a = p.gl ? fabsf(p.gl[i]) : 0.0f;
+      if (p.g) {
+        const int64_t t = p.targets[i];
+        if (t >= 0 && t < p.l.N) a += fabsf(p.g[i]);
+      }
+      row = fmaxf(row, a * p.l.s_row[i]);
+    }
+    for (int64_t j = (int64_t)blockIdx.x * 256 + tid; j < p.l.N; j += kBounds * 256) col = fmaxf(col, p.l.s_col[j]);
+    __shared__ uint32_t most[2][4];
+    const uint32_t r = lanes_max_u32<64>(__float_as_uint(row)), c = lanes_max_u32<64>(__float_as_uint(col));
+    most[0][tid >> 6] = r;
+    most[1][tid >> 6] = c;
+    __syncthreads();
+    if (tid == 0)
+      p.bounds[blockIdx.x] = Bound{__uint_as_float(max(max(most[0][0], most[0][1]), max(most[0][2], most[0][3]))),
+                                   __uint_as_float(max(max(most[1][0], most[1][1]), max(most[1][2], most[1][3])))};
+    return;
+  }
+  const int c4 = tid & 7, half = (tid >> 3) & 1;           // 16 threads a block, 4 columns and 8 rows each
+  const int64_t blocks = (int64_t)(p.blocks_a + (int64_t)p.blocks_b) * p.KB;
+  for (int64_t at = (int64_t)(blockIdx.x - kBounds) * 16 + (tid >> 4); at < blocks; at += (int64_t)(gridDim.x - kBounds) * 16) {
+    const bool a = at < (int64_t)p.blocks_a * p.KB;
+    const int64_t block = a ? at : at - (int64_t)p.blocks_a * p.KB;
+    const int8_t* Q = a ? p.l.A : p.l.B;
+    const int64_t ld = a ? p.l.lda : p.l.ldb;
+    const int rows = a ? p.l.M : p.l.N;
+    const int64_t b16 = block / p.KB;
+    const int kb = (int)(block - b16 * p.KB);
     const int k = kb * 32 + c4 * 4;
     uint32_t w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int64_t r = (int64_t)p.row0 + b16 * 16 + half * 8 + e;
+      const int64_t r = b16 * 16 + half * 8 + e;
       w[e] = 0;
-      if (r < p.rows && k < p.cols) {
-        w[e] = *reinterpret_cast<const uint32_t*>(p.Q + r * p.ld + k);
-        if (p.cols - k < 4) w[e] &= (1u << (8 * (p.cols - k))) - 1;
+      if (r < rows && k < p.l.K) {
+        w[e] = *reinterpret_cast<const uint32_t*>(Q + r * ld + k);
+        if (p.l.K - k < 4) w[e] &= (1u << (8 * (p.l.K - k))) - 1;
       }
     }
+    v4i* out = (a ? p.out_a : p.out_b) + block * 64 + half * 32 + c4 * 4;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       v4i o;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {      // |q| <= 128 has 8 bits: its binary32's upper half is the bf16
-        const uint32_t lo = __float_as_uint((float)(int8_t)(w[2 * e] >> (8 * c)));
-        const uint32_t hi = __float_as_uint((float)(int8_t)(w[2 * e + 1] >> (8 * c)));
-        o[e] = (int)(lo >> 16 | (hi & 0xFFFF0000u));
+      for (int e = 0; e < 4; ++e) {
+        const v2f v = {(float)(int8_t)(w[2 * e] >> (8 * c)), (float)(int8_t)(w[2 * e + 1] >> (8 * c))};
+        o[e] = __builtin_bit_cast(int, __builtin_convertvector(v, v2h));
       }
-      p.out[block * 64 + half * 32 + c4 * 4 + c] = o;
-    }  }
+      out[c] = o;
+    }
+  }
 }
 
 struct WeightArgs {            // T of a piece
@@ -449,28 +505,31 @@ struct WeightArgs {            // T of a piece
   int v0;                      // the piece's first vocabulary row
   int tiles_v, tiles_t;        // of the piece
   int C16;                     // blocks of 16 vocabulary rows in a row of blocks
+  const Bound* bounds;
   v4i* T;                      // [tokens / 32][C16][64]
-  size_t plane;                // from the first to the second bf16 of a value (v4i), TERMS 2
+  size_t plane;                // from the first to the second f16 of a value (v4i), TERMS 2
 };
 
-template <int TERMS>
-__global__ void __launch_bounds__(512, 2) head_weights_kernel(const WeightArgs p) {
-  using Tile = LogitTile<256, 256, 2, 4>;
+template <int TERMS, int BV, int BT, int WV, int WT, int PER_CU>
+__global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weights_kernel(const WeightArgs p) {
+  using Tile = LogitTile<BV, BT, WV, WT>;
   constexpr int FV = Tile::FV, FT = Tile::FT;
   __shared__ __attribute__((aligned(1024))) int8_t smem[Tile::LDS];
-  __shared__ __attribute__((aligned(16))) float sc[256];
+  __shared__ __attribute__((aligned(16))) float sc[BV];
   int tv, tt;
   tile_of(xcd_order(blockIdx.x, gridDim.x), p.tiles_v, p.tiles_t, tv, tt);
-  const int v0 = p.v0 + tv * 256, t0 = tt * 256;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wv = wave >> 2, wt = wave & 3;
-  if (tid < 256) sc[tid] = p.l.s_col[min(v0 + tid, p.l.N - 1)];
+  const int v0 = p.v0 + tv * BV, t0 = tt * BT;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wv = wave / WT, wt = wave % WT;
+  const float scale = t_scale(p.bounds);
+  for (int i = tid; i < BV; i += Tile::NT) sc[i] = p.l.s_col[min(v0 + i, p.l.N - 1)];
   float sr[FT], lse2[FT], share[FT], given[FT];
-  int target[FT];              // in this tile, or -1
+  int target[FT];              // in this tile, or far outside
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
     const int t = t0 + (wt * FT + j) * 32 + (lane & 31);
-    sr[j] = share[j] = given[j] = lse2[j] = 0.0f;
-    target[j] = -1;
+    sr[j] = share[j] = given[j] = 0.0f;
+    lse2[j] = 3e38f;           // p = 0
+    target[j] = -1024;
     if (t < p.l.M) {
       sr[j] = p.l.s_row[t];
       const float lse = p.lse[t];
@@ -484,10 +543,11 @@ __global__ void __launch_bounds__(512, 2) head_weights_kernel(const WeightArgs p
       // a row whose log-sum-exp is off by a factor e or more in p has no gradient
       if (!(fabsf(lse) >= 16777216.0f)) {
         lse2[j] = lse * kLog2e;
-        const float rest = __builtin_fmaf(lse, kLog2e, -lse2[j]);       // exp2(-lse2 - rest) is the row's factor
-        share[j] = ((p.gl ? p.gl[t] : 0.0f) - g) * __builtin_amdgcn_exp2f(-rest) * sr[j];
-        given[j] = g * sr[j];
-        if (at >= v0 && at < v0 + 256) target[j] = (int)(at - v0);
+        const float rest = __builtin_fmaf(lse, kLog2e, -lse2[j]);       // exp2(-rest) is the row's factor
+        const float f = sr[j] * scale;
+        share[j] = ((p.gl ? p.gl[t] : 0.0f) - g) * __builtin_amdgcn_exp2f(-rest) * f;
+        given[j] = g * f;
+        if (at >= v0 && at < v0 + BV) target[j] = (int)(at - v0);
       }
     }
   }
@@ -495,38 +555,46 @@ __global__ void __launch_bounds__(512, 2) head_weights_kernel(const WeightArgs p
   Tile::multiply(p.l, smem, v0, t0, acc);
   if (p.l.K == 0) __syncthreads();
   const int half = lane >> 5;
-  const bool ragged = v0 + 256 > p.l.N;
+  const bool ragged = v0 + BV > p.l.N;
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
-    v4i* row = p.T + ((size_t)(tt * 8 + wt * FT + j) * p.C16 + (size_t)tv * 16) * 64 + lane;
+    v4i* row = p.T + ((size_t)(tt * (BT / 32) + wt * FT + j) * p.C16 + (size_t)tv * (BV / 16)) * 64 + lane;
 #pragma unroll
     for (int i = 0; i < FV; ++i) {
-      uint32_t hi[8], lo[8];
-      const int r0 = (wv * FV + i) * 32;
-      const bool here = __builtin_amdgcn_ballot_w64(target[j] >= r0 && target[j] < r0 + 32) != 0;
+      const int r0 = (wv * FV + i) * 32 + 4 * half;
+      float y[16];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int r = r0 + 8 * q + 4 * half;
-        const v4f s4 = *reinterpret_cast<const v4f*>(sc + r);
-        float y[4];
+        const v4f s4 = *reinterpret_cast<const v4f*>(sc + r0 + 8 * q);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float x = epilogue1(acc[i][j][4 * q + e], sr[j], s4[e]);
-          float v = share[j] * __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2e, -lse2[j]));
-          if (here && target[j] == r + e) v += given[j];
-          v *= s4[e];
-          if (share[j] == 0.0f && !(here && target[j] == r + e)) v = 0.0f;
-          if (ragged && v0 + r + e >= p.l.N) v = 0.0f;
-          y[e] = v;
+          y[4 * q + e] = share[j] * __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2e, -lse2[j]));
         }
+      }
+      const int in = target[j] - r0;                       // 0 ... 27 for a row of this lane's
+      if (__builtin_amdgcn_ballot_w64((unsigned)in < 28u) != 0) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (in == 8 * (e / 4) + e % 4) y[e] += given[j];
+      }
+      if (ragged) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (v0 + r0 + 8 * (e / 4) + e % 4 >= p.l.N) y[e] = 0.0f;
+      }
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const v4f s4 = *reinterpret_cast<const v4f*>(sc + r0 + 8 * q);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const v2b b = __builtin_convertvector(v2f{y[2 * e], y[2 * e + 1]}, v2b);
-          const uint32_t u = __builtin_bit_cast(uint32_t, b);
-          hi[2 * q + e] = u;
+          const v2f v = {y[4 * q + 2 * e] * s4[2 * e], y[4 * q + 2 * e + 1] * s4[2 * e + 1]};
+          const v2h h = __builtin_convertvector(v, v2h);
+          hi[2 * q + e] = __builtin_bit_cast(uint32_t, h);
           if (TERMS == 2) {
-            const v2f left = {y[2 * e] - __uint_as_float(u << 16), y[2 * e + 1] - __uint_as_float(u & 0xFFFF0000u)};
-            lo[2 * q + e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(left, v2b));
+            const v2f back = __builtin_convertvector(h, v2f);
+            lo[2 * q + e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{v.x - back.x, v.y - back.y}, v2h));
           }
         }
       }
@@ -552,6 +620,7 @@ __global__ void __launch_bounds__(512, 2) head_weights_kernel(const WeightArgs p
 // contraction in stages of 64.
 struct GradArgs {
   const v4i* T;
+  const Bound* bounds;
   size_t plane;                // TERMS 2
   int C16;
   int KB, tiles_k;
@@ -563,8 +632,8 @@ struct GradArgs {
     float* planes;             // [splits][tiles][tiles_k][256 * CT] in register order, or null: write `out`
     int add;                   // add to the planes
   } a, b;                      // dA: contraction over the piece's vocabulary; dBt: over the tokens
-  int units_b;
-  int64_t first;               // unit of the launch
+  int units_a, units_b;
+  int first;                   // place of the launch in every XCD's list
   // dBt written here (without planes)
   void* out;
   int64_t ld;
@@ -661,37 +730,37 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-      auto read = [&](int st, int ks, v8b (&fa)[4], v8b (&fb)[TERMS][FC]) {
+      auto read = [&](int st, int ks, v8h (&fa)[4], v8h (&fb)[TERMS][FC]) {
         const int8_t* base = smem + (st & 1) * STAGE;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) fa[i] = *reinterpret_cast<const v8b*>(base + offa + ks * 8192 + i * 1024);
+        for (int i = 0; i < 4; ++i) fa[i] = *reinterpret_cast<const v8h*>(base + offa + ks * 8192 + i * 1024);
 #pragma unroll
         for (int t = 0; t < TERMS; ++t)
 #pragma unroll
           for (int j = 0; j < FC; ++j) {
             if constexpr (!DUAL) {
-              fb[t][j] = *reinterpret_cast<const v8b*>(base + offb + t * 16384 + j * 4096 + ks * 1024);
+              fb[t][j] = *reinterpret_cast<const v8h*>(base + offb + t * 16384 + j * 4096 + ks * 1024);
             } else {
               // tokens 16 ks ...: block ks / 2, its tokens 16 (ks % 2) ...
               const int at = t * 16384 + (ks >> 1) * (CT / 16 * 1024) + j * 2048 + (ks & 1) * 256;
               typedef __attribute__((address_space(3))) v4s lds_v4s;
               const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(base + offb + at));
               const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(base + flip + at));
-              union { v4s h[2]; v8b v; } f{{x, y}};
+              union { v4s h[2]; v8h v; } f{{x, y}};
               fb[t][j] = f.v;
             }
           }
       };
-      auto mfma = [&](const v8b (&fa)[4], const v8b (&fb)[TERMS][FC]) {
+      auto mfma = [&](const v8h (&fa)[4], const v8h (&fb)[TERMS][FC]) {
 #pragma unroll
         for (int t = 0; t < TERMS; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < FC; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[t][j], acc[i][j], 0, 0, 0);
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[t][j], acc[i][j], 0, 0, 0);
       };
-  v8b fa0[4], fa1[4], fb0[TERMS][FC], fb1[TERMS][FC];
+  v8h fa0[4], fa1[4], fb0[TERMS][FC], fb1[TERMS][FC];
   issue(0);
   if (n > 1) {
     issue(1);
@@ -729,12 +798,13 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
   interleave<READS, 8>();
   mfma(fa1, fb1);
 
+  const float factor = plane ? 1.0f : t_scale(p.bounds);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < FC; ++j) {
       const int col = ct * CT + (wc * FC + j) * 32 + (lane & 31);
-      const float scale = !plane && col < p.rows ? p.scale[col] : 1.0f;
+      const float scale = !plane && col < p.rows ? p.scale[col] * factor : 1.0f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         v4f v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
@@ -750,16 +820,27 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
     }
 }
 
+// Each XCD (workgroups are dealt to the 8 in turn) takes an eighth of either
+// side's units, neighbours in their order: they share T or codes in its L2.
+// The longer ones go first.
 template <int TERMS>
 __global__ void __launch_bounds__(512, 2) head_grads_kernel(const GradArgs p) {
   __shared__ __attribute__((aligned(1024))) int8_t smem[131072];
-  const int u = (int)p.first + xcd_order(blockIdx.x, gridDim.x);
-  if (u < p.units_b) grads_unit<TERMS, true>(p, p.b, u, smem);
-  else grads_unit<TERMS, false>(p, p.a, u - p.units_b, smem);
+  const int xcd = blockIdx.x & 7, at = p.first + (blockIdx.x >> 3);
+  const int a0 = (int)((int64_t)p.units_a * xcd / 8), na = (int)((int64_t)p.units_a * (xcd + 1) / 8) - a0;
+  const int b0 = (int)((int64_t)p.units_b * xcd / 8), nb = (int)((int64_t)p.units_b * (xcd + 1) / 8) - b0;
+  const bool a_first = p.a.per >= p.b.per;
+  const int n1 = a_first ? na : nb;
+  if (at >= na + nb) return;
+  const bool second = at >= n1;
+  const int in = second ? at - n1 : at;
+  if (a_first != second) grads_unit<TERMS, false>(p, p.a, a0 + in, smem);
+  else grads_unit<TERMS, true>(p, p.b, b0 + in, smem);
 }
 
 struct FinishArgs {
   const float* planes;
+  const Bound* bounds;
   int splits, tiles, tiles_k;
   int CT;
   void* out;
@@ -771,6 +852,7 @@ struct FinishArgs {
 __global__ void __launch_bounds__(256) head_finish_kernel(const FinishArgs p) {
   const size_t size = (size_t)256 * p.CT, all = (size_t)p.tiles * p.tiles_k * size;
   const int FC = p.CT / 128;
+  const float factor = t_scale(p.bounds);
   for (size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; at < all; at += (size_t)gridDim.x * 1024) {
     const int tile = (int)(at / size), in = (int)(at % size) / 4;
     const int kt = tile % p.tiles_k, ct = tile / p.tiles_k;
@@ -780,7 +862,7 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const FinishArgs p) {
     if (col >= p.rows || k >= p.cols) continue;
     v4f v = *reinterpret_cast<const v4f*>(p.planes + at);
     for (int s = 1; s < p.splits; ++s) v += *reinterpret_cast<const v4f*>(p.planes + s * all + at);
-    store_grad(p.out, p.ld, p.dtype, col, k, p.cols - k, v, p.scale[col]);
+    store_grad(p.out, p.ld, p.dtype, col, k, p.cols - k, v, p.scale[col] * factor);
   }
 }
 
@@ -819,7 +901,7 @@ struct BwdPlan {
   int64_t Mp, C;
   int pieces, tiles_k, sa, sb;
   size_t code_a, code_b, t, plane_a, plane_b;   // bytes
-  size_t bytes() const { return code_a + code_b + t + plane_a + plane_b; }
+  size_t bytes() const { return kBounds * sizeof(Bound) + code_a + code_b + t + plane_a + plane_b; }
 };
 BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, int dtype) {
   BwdPlan b;
@@ -852,19 +934,11 @@ BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, int dtype) {
       }
     }
   b.code_a = (size_t)b.Mp * b.tiles_k * 512;
-  b.code_b = (size_t)b.C * b.tiles_k * 512;
+  b.code_b = (size_t)b.C * b.pieces * b.tiles_k * 512;
   b.t = (size_t)b.Mp * b.C * 2 * b.terms;
   b.plane_a = (size_t)b.Mp * b.tiles_k * 1024 * b.sa;
   b.plane_b = b.sb > 1 ? (size_t)b.C * b.tiles_k * 1024 * b.sb : 0;
   return b;
-}
-
-hipError_t pack(const int8_t* Q, int64_t ld, int64_t rows, int64_t cols, int64_t row0, int64_t n, int KB, void* out,
-                hipStream_t stream) {
-  PackArgs a{Q, ld, (int)rows, (int)cols, (int)row0, (int)(n / 16), KB, static_cast<v4i*>(out)};
-  const int64_t groups = (n / 16 * KB + 15) / 16;
-  hipLaunchKernelGGL(head_pack_kernel, dim3((unsigned)(groups < kMostGroups ? groups : kMostGroups)), dim3(256), 0, stream, a);
-  return hipGetLastError();
 }
 
 }  // namespace
@@ -904,37 +978,51 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
   }
   const BwdPlan b = bwd_plan(a.M, a.N, a.K, g.dtype);
   char* at = static_cast<char*>(ws);
-  v4i* code_a = reinterpret_cast<v4i*>(at);
+  Bound* bounds = reinterpret_cast<Bound*>(at);
+  v4i* code_a = reinterpret_cast<v4i*>(at += kBounds * sizeof(Bound));
   v4i* code_b = reinterpret_cast<v4i*>(at += b.code_a);
   v4i* T = reinterpret_cast<v4i*>(at += b.code_b);
   float* plane_a = reinterpret_cast<float*>(at += b.t);
   float* plane_b = reinterpret_cast<float*>(at += b.plane_a);
   const int KB = b.tiles_k * 8;
   const size_t plane = (size_t)b.Mp * b.C / 8;
-  hipError_t e = pack(a.A, a.lda, a.M, a.K, 0, b.Mp, KB, code_a, stream);
+  const LogitArgs l = logit_args(a);
+  PackArgs k{l, g.targets, g.g_logprob, g.g_lse, bounds, (int)(b.Mp / 16), (int)(b.C * b.pieces / 16), KB, code_a, code_b};
+  const int64_t groups = ((int64_t)(k.blocks_a + (int64_t)k.blocks_b) * KB + 15) / 16;
+  hipLaunchKernelGGL(head_prepare_kernel, dim3(kBounds + (unsigned)(groups < kMostGroups ? groups : kMostGroups)), dim3(256), 0, stream, k);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  auto finish = [&](const GradArgs::Side& s, void* out, int64_t ld, int64_t n, const float* scale) {
+    FinishArgs f{s.planes, bounds, s.splits, s.tiles, b.tiles_k, b.ct, out, ld, g.dtype, (int)n, (int)a.K, scale};
+    const int64_t n_groups = (int64_t)s.tiles * b.tiles_k * b.ct / 4;
+    hipLaunchKernelGGL(head_finish_kernel, dim3((unsigned)(n_groups < kMostGroups ? n_groups : kMostGroups)), dim3(256), 0, stream, f);
+    return hipGetLastError();
+  };
   for (int piece = 0; piece < b.pieces; ++piece) {
-    const int64_t v0 = piece * b.C;
-    if ((e = pack(a.B, a.ldb, a.N, a.K, v0, b.C, KB, code_b, stream)) != hipSuccess) return e;
-    WeightArgs w{logit_args(a), g.targets, g.lse, g.g_logprob, g.g_lse, (int)v0, (int)(b.C / 256), (int)(b.Mp / 256), (int)(b.C / 16), T, plane};
+    const int64_t v0 = piece * b.C, rows = a.N - v0 < b.C ? a.N - v0 : b.C;
+    WeightArgs w{l, g.targets, g.lse, g.g_logprob, g.g_lse, (int)v0, 0, 0, (int)(b.C / 16), bounds, T, plane};
+    constexpr int BV = 256, BT = 256;
+    w.tiles_v = (int)(b.C / BV);
+    w.tiles_t = (int)(b.Mp / BT);
     const dim3 grid((unsigned)w.tiles_v * (unsigned)w.tiles_t);
-    if (b.terms == 1) hipLaunchKernelGGL(head_weights_kernel<1>, grid, dim3(512), 0, stream, w);
-    else hipLaunchKernelGGL(head_weights_kernel<2>, grid, dim3(512), 0, stream, w);
+    if (b.terms == 1) hipLaunchKernelGGL((head_weights_kernel<1, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
+    else hipLaunchKernelGGL((head_weights_kernel<2, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
     if ((e = hipGetLastError()) != hipSuccess) return e;
 
     GradArgs p{};
     p.T = T;
+    p.bounds = bounds;
     p.plane = plane;
     p.C16 = (int)(b.C / 16);
     p.KB = KB;
     p.tiles_k = b.tiles_k;
-    const int64_t rows = a.N - v0 < b.C ? a.N - v0 : b.C;
     auto side = [](const v4i* codes, int64_t tiles, int64_t depth, int splits, float* planes, int add) {
       const int stages = (int)(depth / 64), per = up(stages, splits);
       return GradArgs::Side{codes, (int)tiles, up(stages, per), stages, per, planes, add};
     };
-    p.a = side(code_b, b.Mp / b.ct, b.C, b.sa, plane_a, piece > 0);
+    p.a = side(code_b + (size_t)piece * (b.C / 16) * KB * 64, b.Mp / b.ct, b.C, b.sa, plane_a, piece > 0);
     p.b = side(code_a, up(rows, b.ct), b.Mp, b.sb, b.sb > 1 ? plane_b : nullptr, 0);
+    p.units_a = g.dA ? p.tiles_k * p.a.tiles * p.a.splits : 0;
     p.units_b = g.dB ? p.tiles_k * p.b.tiles * p.b.splits : 0;
     const int64_t esize = g.dtype == DT_F32 ? 4 : 2;
     p.out = g.dB ? static_cast<char*>(g.dB) + v0 * g.lddb * esize : nullptr;
@@ -943,19 +1031,13 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
     p.rows = (int)rows;
     p.cols = (int)a.K;
     p.scale = a.s_col + v0;
-    const int64_t units = p.units_b + (g.dA ? (int64_t)p.tiles_k * p.a.tiles * p.a.splits : 0);
-    for (p.first = 0; p.first < units; p.first += kMostGroups) {
-      const unsigned n = (unsigned)(units - p.first < kMostGroups ? units - p.first : kMostGroups);
+    const int most = up(p.units_a, 8) + up(p.units_b, 8);    // of an XCD
+    for (p.first = 0; p.first < most; p.first += kMostGroups / 8) {
+      const unsigned n = 8u * (unsigned)(most - p.first < kMostGroups / 8 ? most - p.first : kMostGroups / 8);
       if (b.terms == 1) hipLaunchKernelGGL(head_grads_kernel<1>, dim3(n), dim3(512), 0, stream, p);
       else hipLaunchKernelGGL(head_grads_kernel<2>, dim3(n), dim3(512), 0, stream, p);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    auto finish = [&](const GradArgs::Side& s, void* out, int64_t ld, int64_t n, const float* scale) {
-      FinishArgs f{s.planes, s.splits, s.tiles, b.tiles_k, b.ct, out, ld, g.dtype, (int)n, (int)a.K, scale};
-      const int64_t groups = (int64_t)s.tiles * b.tiles_k * b.ct / 4;
-      hipLaunchKernelGGL(head_finish_kernel, dim3((unsigned)(groups < kMostGroups ? groups : kMostGroups)), dim3(256), 0, stream, f);
-      return hipGetLastError();
-    };
     if (g.dB && p.b.planes && (e = finish(p.b, p.out, g.lddb, rows, p.scale)) != hipSuccess) return e;
     if (g.dA && piece + 1 == b.pieces && (e = finish(p.a, g.dA, g.ldda, a.M, a.s_row)) != hipSuccess) return e;
   }
