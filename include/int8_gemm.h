@@ -543,9 +543,8 @@ int token_logprobs_bwd(const void* logits, uint32_t dtype, int64_t rows, int64_t
  *            256-byte aligned, any contents.
  * Sums are held in binary32 over at most 64 values a lane against their
  * maximum, and in binary64 beyond a tile of 256 (128) columns; exponentials
- * are the hardware's (1 ulp).  A row whose largest logit is 2^127 / log2(e) or
- * more, or that holds a NaN, is NaN; one whose logits are all below -2e38 has
- * lse and logprob -inf.
+ * are the hardware's (1 ulp).  A logit of -inf has probability 0, a row of
+ * -inf only has lse and logprob -inf, a row with a NaN or +inf is NaN.
  * Errors: I8G_EINVAL (null pointer, negative size, M above I8G_HEAD_ROWS_MAX,
  * N above I8G_VOCAB_MAX, N == 0 with M > 0, misaligned vector), I8G_EKRANGE,
  * I8G_EALIGN, I8G_EWORKSPACE, I8G_EHIP.
@@ -568,13 +567,16 @@ int gemm_i8_logprobs(const int8_t* QA, int64_t lda, const float* s_row, const in
  *   dA, dBt  either may be NULL.  With M == 0 dBt is 0.
  *   workspace  device scratch of gemm_i8_logprobs_bwd_workspace_bytes(M, N, K,
  *            dtype), 256-byte aligned, any contents (not needed with M == 0).
- * The products run on the matrix cores in bf16 with binary32 sums, over pieces
- * of the vocabulary whose G has at most 2^27 values (or 256 columns): codes are
- * exact, s_row[i] G[i,j] s_col[j] is rounded to bf16 for bf16 gradients and to
- * a sum of two bf16 (2^-18) for f32 and f16.  Scales have to be positive, as
- * the quantize passes write them.  As in token_logprobs_bwd, a row with
- * |lse| >= 2^24 gets 0 (and adds nothing to dBt).  A NaN in a row's lse,
- * gradients or scale makes its row of dA and all of dBt NaN.
+ * The products run on the matrix cores in f16 with binary32 sums, over pieces
+ * of the vocabulary whose G has at most 3 * 2^26 values (or 256 columns).
+ * Codes are exact; T = s_row[i] G[i,j] s_col[j] is rounded to f16 for bf16
+ * gradients (2^-11 of the value) and to a sum of two f16 (2^-22) for f32 and
+ * f16 ones, scaled by a power of two of max (|g_logprob| + |g_lse|) s_row
+ * max s_col, so that a value is off by at most 2^-37 of that maximum besides.
+ * Scales have to be positive, as the quantize passes write them.  As in
+ * token_logprobs_bwd, a row with |lse| >= 2^24 gets 0 (and adds nothing to
+ * dBt).  A NaN in a row's lse, gradients or scale makes its row of dA and all
+ * of dBt NaN.
  * Errors: as gemm_i8_logprobs; I8G_EINVAL for an unknown dtype, a leading
  * dimension below K, a misaligned output.
  */

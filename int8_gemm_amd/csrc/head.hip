@@ -10,11 +10,11 @@
 // Both gradients read one matrix T_ij = s_row_i G_ij s_col_j:
 //   dA_ik = (1 / s_row_i) sum_j T_ij QBt_jk,  dBt_jk = (1 / s_col_j) sum_i T_ij QA_ik,
 // and the codes are exact in f16, so T is all that is rounded for the matrix
-// cores: to f16 for bf16 gradients (2^-12 of each value, less than the outputs'
-// own rounding), to a sum of two f16 (2^-24) for f32 and f16 ones.  (Two bf16
-// would be 2^-18; f16 takes the same time.)  T is scaled by a power of two that
-// puts max (|g| + |gl|) s_row max s_col at 2^13 to 2^14: a value's error is then
-// at most 2^-40 of that maximum where it is below f16's normal numbers.
+// cores: to f16 for bf16 gradients (2^-11 of each value, where the outputs' own
+// rounding is 2^-8), to a sum of two f16 (2^-22) for f32 and f16 ones.  (Two bf16
+// would be 2^-16 in the same time.)  T is scaled by a power of two that puts
+// max (|g| + |gl|) s_row max s_col between 2^12 and 2^14, so that the least
+// spacing of f16 is at most 2^-36 of that maximum.
 //
 // Forward: a workgroup multiplies a tile of vocabulary rows by a tile of
 // tokens; the vocabulary is the accumulators' row dimension, so that a lane
@@ -31,6 +31,7 @@
 #include "i8g_row.h"
 
 #include <type_traits>
+#include <utility>
 
 namespace i8g {
 namespace {
@@ -45,7 +46,7 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.44269502f;
-constexpr float kLowest = -2e38f;      // the least maximum of a row's part: its product with kLog2e is finite
+constexpr float kLowest = -3.40282347e38f;   // the running maximum's start: finite, so that x - m is no NaN for a finite x or -inf
 
 template <int N>
 __device__ __forceinline__ void wait_loads() {   // all but the last N vector loads, and every LDS access
@@ -258,7 +259,7 @@ struct LogitTile {
 struct FwdArgs {
   LogitArgs l;
   int tiles_v, tiles_t;
-  v2f* parts;                  // [tiles_v][M]: the maximum times kLog2e, and the sum against it
+  v2f* parts;                  // [tiles_v][M]: the maximum, and the sum of exp(x - maximum)
 };
 
 // Tiles of tokens that share a vocabulary tile in an L2 before the next one.
@@ -309,14 +310,28 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_fwd_k
         }
       }
     m = fmaxf(m, other_half(m));
+    // exp(x - m) as 2^(x c - m2), c = log2 e and m2 = RN(m c): one fused step,
+    // and one factor for m2's rounding; where that rounding may be more than a
+    // factor of two, the difference by itself (in these lanes only: a row's
+    // bits do not depend on another's)
     const float m2 = m * kLog2e;
+    const bool far = !(fabsf(m2) < 16777216.0f);
     float s = 0.0f;
+    if (__builtin_amdgcn_ballot_w64(far) == 0) {
 #pragma unroll
-    for (int i = 0; i < FV; ++i)
+      for (int i = 0; i < FV; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i][e], kLog2e, -m2));
+        for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i][e], kLog2e, -m2));
+    } else {
+#pragma unroll
+      for (int i = 0; i < FV; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          s += __builtin_amdgcn_exp2f(far ? (x[i][e] - m) * kLog2e : __builtin_fmaf(x[i][e], kLog2e, -m2));
+    }
+    if (!far) s *= __builtin_amdgcn_exp2f(-__builtin_fmaf(m, kLog2e, -m2));
     s += other_half(s);
-    if (half == 0) part[wv][(wt * FT + j) * 32 + lane] = v2f{m2, s};
+    if (half == 0) part[wv][(wt * FT + j) * 32 + lane] = v2f{m, s};
   }
   __syncthreads();
   if (tid < BT && t0 + tid < p.l.M) {
@@ -324,9 +339,9 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_fwd_k
 #pragma unroll
     for (int w = 1; w < WV; ++w) {
       const v2f b = part[w][tid];
-      const float m2 = fmaxf(a.x, b.x);
-      a.y = a.y * __builtin_amdgcn_exp2f(a.x - m2) + b.y * __builtin_amdgcn_exp2f(b.x - m2);
-      a.x = m2;
+      const float m = fmaxf(a.x, b.x);
+      a.y = a.y * __builtin_amdgcn_exp2f((a.x - m) * kLog2e) + b.y * __builtin_amdgcn_exp2f((b.x - m) * kLog2e);
+      a.x = m;
     }
     p.parts[(size_t)tv * p.l.M + t0 + tid] = a;
   }
@@ -351,7 +366,7 @@ __global__ void __launch_bounds__(256) head_join_kernel(const JoinArgs p) {
   const int tid = threadIdx.x, r = tid % R, slot = tid / R;
   const int row = blockIdx.x * R + r;
   // maxima are finite or +inf, never NaN (they ignore it; the sum is NaN then)
-  float m = -3.4e38f;
+  float m = kLowest;
   if (row < p.l.M)
 #pragma unroll 4
     for (int i = slot; i < p.n_parts; i += S) m = fmaxf(m, p.parts[(size_t)i * p.l.M + row].x);
@@ -368,7 +383,7 @@ __global__ void __launch_bounds__(256) head_join_kernel(const JoinArgs p) {
 #pragma unroll 4
     for (int i = slot; i < p.n_parts; i += S) {
       const v2f a = p.parts[(size_t)i * p.l.M + row];
-      s += (double)(a.y * __builtin_amdgcn_exp2f(a.x - m));
+      s += (double)(a.y * __builtin_amdgcn_exp2f((a.x - m) * kLog2e));
     }
   sum[slot][r] = s;
   __syncthreads();
@@ -378,7 +393,7 @@ __global__ void __launch_bounds__(256) head_join_kernel(const JoinArgs p) {
     __syncthreads();
   }
   if (slot == 0) {
-    const float lse = (float)(((double)m + log2(sum[0][r])) / (double)kLog2e);
+    const float lse = (float)((double)m + log(sum[0][r]));
     out[r] = lse;
     if (row < p.l.M && p.lse) p.lse[row] = lse;
   }
@@ -506,7 +521,7 @@ struct WeightArgs {            // T of a piece
   int tiles_v, tiles_t;        // of the piece
   int C16;                     // blocks of 16 vocabulary rows in a row of blocks
   const Bound* bounds;
-  v4i* T;                      // [tokens / 32][C16][64]
+  v4i* T;                      // [tokens / (32 TB)][C16][TB][64], TB = 8 / TERMS: the blocks that a stage of dA reads are in a row
   size_t plane;                // from the first to the second f16 of a value (v4i), TERMS 2
 };
 
@@ -558,7 +573,9 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
   const bool ragged = v0 + BV > p.l.N;
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
-    v4i* row = p.T + ((size_t)(tt * (BT / 32) + wt * FT + j) * p.C16 + (size_t)tv * (BV / 16)) * 64 + lane;
+    constexpr int TB = 8 / TERMS;
+    const int tb = tt * (BT / 32) + wt * FT + j;
+    v4i* row = p.T + (((size_t)(tb / TB) * p.C16 + (size_t)tv * (BV / 16)) * TB + tb % TB) * 64 + lane;
 #pragma unroll
     for (int i = 0; i < FV; ++i) {
       const int r0 = (wv * FV + i) * 32 + 4 * half;
@@ -602,7 +619,7 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
       // holds 8 in a row
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        v4i* to = row + (size_t)((wv * FV + i) * 2 + s) * 64;
+        v4i* to = row + (size_t)((wv * FV + i) * 2 + s) * (TB * 64);
 #pragma unroll
         for (int term = 0; term < TERMS; ++term) {
           const uint32_t* w = term ? lo : hi;
@@ -617,7 +634,7 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
 
 // Both products of a piece.  A unit is a tile of 256 columns k (rows of the
 // accumulators) by CT tokens (dA) or vocabulary rows (dBt), over a range of the
-// contraction in stages of 64.
+// contraction in stages of 32.
 struct GradArgs {
   const v4i* T;
   const Bound* bounds;
@@ -664,59 +681,61 @@ __device__ __forceinline__ void store_grad(void* out, int64_t ld, int dtype, int
   else store4(static_cast<f16_t*>(out) + row * ld + k, n, v);
 }
 
-// DUAL: dBt, for which T is read transposed.
+// DUAL: dBt, for which T is read transposed.  LDS holds five stages of 32 of the
+// contraction: up to four are on their way while one is multiplied (two stages of 64
+// leave a load half the time to land: 8192 x 50304 x 768 bf16 1759 us in place of 1669).
+constexpr int kGradStage = 32768, kGradSlots = 5;
 template <int TERMS, bool DUAL>
 __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Side& s, int u, int8_t* smem) {
-  constexpr int FC = 2 / TERMS, CT = 256 / TERMS, STAGE = 65536;
+  constexpr int FC = 2 / TERMS, CT = 256 / TERMS, TB = CT / 32;   // TB: 32-token blocks of a tile of T
   constexpr int READS = DUAL ? 8 : 6;                      // LDS reads of a k-step
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wk = wave >> 2, wc = wave & 3;
   const int kt = u % p.tiles_k, ct = (u / p.tiles_k) % s.tiles, split = u / (p.tiles_k * s.tiles);
   const int first = split * s.per, n = min(s.per, s.stages - first);
 
-  // sources of this wave's 4 + 4 loads of a stage: the same in every lane but
+  // sources of this wave's 2 + 2 loads of a stage: the same in every lane but
   // for the lane's 16 bytes of a block
-  const char* ga = reinterpret_cast<const char*>(s.codes + ((size_t)(first * 4) * p.KB + kt * 8 + wave) * 64);
-  const char* gb = reinterpret_cast<const char*>(p.T);
   const size_t row_a = (size_t)p.KB * 1024, row_b = (size_t)p.C16 * 1024, plane_b = p.plane * 16;
+  const char* ga = reinterpret_cast<const char*>(s.codes) + (size_t)(first * 2) * row_a + (size_t)(kt * 8 + wave) * 1024;
+  const char* gb = reinterpret_cast<const char*>(p.T);
   const int lane_a = lane * 16;
   int lane_b = lane_a;
-  size_t step_b = 4096, q_b;   // from stage to stage, and from a wave's load to its next of the same term
+  // T's loads: TERMS 1, 16 blocks of a stage in two; TERMS 2, 8 blocks of each term
   if constexpr (!DUAL) {
-    // [32 tokens][16 of the contraction]: q takes two rows of blocks each
-    gb += (size_t)(ct * (CT / 32) + (wave >> 2)) * row_b + (size_t)(first * 4 + (wave & 3)) * 1024;
-    q_b = 2 * row_b;
+    // blocks [16 of the contraction 2][32 tokens TB] are in a row
+    gb += (size_t)ct * TB * row_b + (size_t)(first * 2) * (TB * 1024) + wave * 1024;
   } else {
-    // [32 tokens of the contraction][16 vocabulary rows]; the 16-byte pieces of a block (half h, token t) are
-    // placed at (h, t ^ (4h + 8 (block % 2))), so that a transposing read of 32 lanes covers all banks
+    // 16 vocabulary rows each, of one block of 32 tokens; the 16-byte pieces of a block (half h, token t) are placed at
+    // (h, t ^ (4h + 8 (vocabulary block % 2))), so that a transposing read of 32 lanes covers all banks
     lane_b = ((lane & 32) | ((lane & 31) ^ (4 * (lane >> 5) + 8 * (wave & 1)))) * 16;
-    gb += (size_t)(first * 2) * row_b + (size_t)(ct * (CT / 16) + wave) * 1024;
-    q_b = TERMS == 2 ? row_b : 8192;                     // TERMS 1: two loads a row of blocks
-    step_b = 2 * row_b;
+    gb += ((size_t)ct * (CT / 16) + wave) * (TB * 1024);
   }
   auto issue = [&](int st) {
-    int8_t* base = smem + (st & 1) * STAGE + wave * 1024;
-    const char* a = ga + (size_t)st * 4 * row_a;
-    const char* b = gb + (size_t)st * step_b;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) lds_load16(a + q * row_a, lane_a, base + q * 8192);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      size_t at;
-      if (TERMS == 2) at = (q >> 1) * plane_b + (q & 1) * q_b;
-      else at = DUAL ? (q >> 1) * row_b + (q & 1) * q_b : q * q_b;
-      lds_load16(b + at, lane_b, base + 32768 + q * 8192);
+    int8_t* base = smem + (st % kGradSlots) * kGradStage + wave * 1024;
+    const char* a = ga + (size_t)st * 2 * row_a;
+    const char* b = gb;
+    if constexpr (!DUAL) {
+      b += (size_t)st * (2 * TB * 1024);
+    } else {
+      const int tb = first + st;
+      b += (size_t)(tb / TB) * (TB * row_b) + (size_t)(tb % TB) * 1024;
     }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) lds_load16(a + q * row_a, lane_a, base + q * 8192);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      lds_load16(b + q * (TERMS == 2 ? plane_b : (size_t)(DUAL ? 8 * TB * 1024 : 8192)), lane_b, base + 16384 + q * 8192);
   };
-  // LDS: codes [k-step 4][32 columns 8]; T [term][32 tokens][k-step 4], or [term][32 tokens 2][16 vocabulary rows]
+  // LDS: codes [k-step 2][32 columns 8]; T [term][k-step 2][32 tokens TB], or [term][16 vocabulary rows CT / 16]
   const int offa = wk * 4096 + lane * 16;
   int offb, flip = 0;
   if constexpr (!DUAL) {
-    offb = 32768 + wc * FC * 4096 + lane * 16;
+    offb = 16384 + wc * FC * 1024 + lane * 16;
   } else {
     const int g = lane >> 4, r = (lane & 15) >> 2, c = lane & 3, h = c >> 1;
     const int t = ((8 * (g >> 1)) ^ (8 * (g & 1))) + 4 * h + r;
-    offb = 32768 + (wc * FC * 2 + (g & 1)) * 1024 + h * 512 + t * 16 + (c & 1) * 8;
+    offb = 16384 + (wc * FC * 2 + (g & 1)) * 1024 + h * 512 + t * 16 + (c & 1) * 8;
     flip = offb ^ 64;                                       // the fragment's other 4 tokens
   }
   v16f acc[4][FC];
@@ -730,92 +749,116 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-      auto read = [&](int st, int ks, v8h (&fa)[4], v8h (&fb)[TERMS][FC]) {
-        const int8_t* base = smem + (st & 1) * STAGE;
+  auto read = [&](const int8_t* base, auto ks_t, v8h (&fa)[4], v8h (&fb)[TERMS][FC]) {
+    constexpr int ks = decltype(ks_t)::value;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) fa[i] = *reinterpret_cast<const v8h*>(base + offa + ks * 8192 + i * 1024);
+    for (int i = 0; i < 4; ++i) fa[i] = *reinterpret_cast<const v8h*>(base + offa + ks * 8192 + i * 1024);
 #pragma unroll
-        for (int t = 0; t < TERMS; ++t)
+    for (int t = 0; t < TERMS; ++t)
 #pragma unroll
-          for (int j = 0; j < FC; ++j) {
-            if constexpr (!DUAL) {
-              fb[t][j] = *reinterpret_cast<const v8h*>(base + offb + t * 16384 + j * 4096 + ks * 1024);
-            } else {
-              // tokens 16 ks ...: block ks / 2, its tokens 16 (ks % 2) ...
-              const int at = t * 16384 + (ks >> 1) * (CT / 16 * 1024) + j * 2048 + (ks & 1) * 256;
-              typedef __attribute__((address_space(3))) v4s lds_v4s;
-              const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(base + offb + at));
-              const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(base + flip + at));
-              union { v4s h[2]; v8h v; } f{{x, y}};
-              fb[t][j] = f.v;
-            }
-          }
-      };
-      auto mfma = [&](const v8h (&fa)[4], const v8h (&fb)[TERMS][FC]) {
+      for (int j = 0; j < FC; ++j) {
+        if constexpr (!DUAL) {
+          fb[t][j] = *reinterpret_cast<const v8h*>(base + offb + t * 8192 + ks * (TB * 1024) + j * 1024);
+        } else {
+          // tokens 16 ks ... of the block
+          const int at = t * 8192 + j * 2048 + ks * 256;
+          typedef __attribute__((address_space(3))) v4s lds_v4s;
+          const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(base + offb + at));
+          const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(base + flip + at));
+          union { v4s h[2]; v8h v; } f{{x, y}};
+          fb[t][j] = f.v;
+        }
+      }
+  };
+  auto mfma = [&](const v8h (&fa)[4], const v8h (&fb)[TERMS][FC]) {
 #pragma unroll
-        for (int t = 0; t < TERMS; ++t)
+    for (int t = 0; t < TERMS; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < FC; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[t][j], acc[i][j], 0, 0, 0);
-      };
+        for (int j = 0; j < FC; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[t][j], acc[i][j], 0, 0, 0);
+  };
+  const std::integral_constant<int, 0> k0;
+  const std::integral_constant<int, 1> k1;
   v8h fa0[4], fa1[4], fb0[TERMS][FC], fb1[TERMS][FC];
-  issue(0);
-  if (n > 1) {
-    issue(1);
-    wait_loads<8>();
-  } else {
-    wait_loads<0>();
-  }
+  // n is 8 at least: contractions are whole blocks of 256
+  constexpr int LOADS = 4;
+#pragma unroll
+  for (int st = 0; st < kGradSlots; ++st) issue(st);
+  wait_loads<LOADS * (kGradSlots - 1)>();
   barrier_nofence();
-  read(0, 0, fa0, fb0);
-  for (int st = 0; st + 1 < n; ++st) {
-    read(st, 1, fa1, fb1);
+  read(smem, k0, fa0, fb0);
+  int slot = 0;
+  // one stage; the next one's first fragments are read behind the barrier that
+  // frees this one's slot, and multiplied after it
+  auto stage = [&](int st, auto left_t) {                  // left: stages in flight behind the next one
+    constexpr int left = decltype(left_t)::value;
+    const int8_t* base = smem + slot * kGradStage;
+    slot = slot + 1 == kGradSlots ? 0 : slot + 1;
+    read(base, k1, fa1, fb1);
     mfma(fa0, fb0);
     interleave<READS, 8>();
-    read(st, 2, fa0, fb0);
-    mfma(fa1, fb1);
-    interleave<READS, 8>();
-    read(st, 3, fa1, fb1);
-    mfma(fa0, fb0);
-    interleave<READS, 8>();
-    wait_loads<0>();
+    // the next stage has landed, and this one's last fragments are in registers
+    wait_loads<LOADS * left>();
     barrier_nofence();
-    if (st + 2 < n) issue(st + 2);
-    read(st + 1, 0, fa0, fb0);
+    if constexpr (left == kGradSlots - 2) {
+      if (st + kGradSlots < n) issue(st + kGradSlots);
+    }
+    read(smem + slot * kGradStage, k0, fa0, fb0);
     mfma(fa1, fb1);
     interleave<READS, 8>();
-  }
-  read(n - 1, 1, fa1, fb1);
-  mfma(fa0, fb0);
-  interleave<READS, 8>();
-  read(n - 1, 2, fa0, fb0);
-  mfma(fa1, fb1);
-  interleave<READS, 8>();
-  read(n - 1, 3, fa1, fb1);
+  };
+  int st = 0;
+  for (; st + kGradSlots - 1 < n; ++st) stage(st, std::integral_constant<int, kGradSlots - 2>{});
+  stage(st, std::integral_constant<int, 2>{});
+  stage(st + 1, std::integral_constant<int, 1>{});
+  stage(st + 2, std::integral_constant<int, 0>{});
+  read(smem + slot * kGradStage, k1, fa1, fb1);
   mfma(fa0, fb0);
   interleave<READS, 8>();
   mfma(fa1, fb1);
 
-  const float factor = plane ? 1.0f : t_scale(p.bounds);
+  if (plane) {
+    // (what is added to is read before the stores of two rows of blocks: a load
+    // behind a store would wait for it)
+#pragma unroll
+    for (int i0 = 0; i0 < 4; i0 += 2) {
+      v4f old[2][FC][4];
+      if (s.add) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < FC; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) old[i][j][q] = *reinterpret_cast<const v4f*>(plane + (((i0 + i) * FC + j) * 4 + q) * 256);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < FC; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const v16f& a = acc[i0 + i][j];
+            v4f v = {a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+            if (s.add) v += old[i][j][q];
+            *reinterpret_cast<v4f*>(plane + (((i0 + i) * FC + j) * 4 + q) * 256) = v;
+          }
+    }
+    return;
+  }
+  const float factor = t_scale(p.bounds);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < FC; ++j) {
       const int col = ct * CT + (wc * FC + j) * 32 + (lane & 31);
-      const float scale = !plane && col < p.rows ? p.scale[col] * factor : 1.0f;
+      const float scale = col < p.rows ? p.scale[col] * factor : 1.0f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        v4f v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        if (plane) {
-          v4f* to = reinterpret_cast<v4f*>(plane + ((i * FC + j) * 4 + q) * 256);
-          if (s.add) v += *to;
-          *to = v;
-        } else {
-          const int k = kt * 256 + wk * 128 + i * 32 + 8 * q + 4 * (lane >> 5);
-          if (col < p.rows && k < p.cols) store_grad(p.out, p.ld, p.dtype, col, k, p.cols - k, v, scale);
-        }
+        const v4f v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        const int k = kt * 256 + wk * 128 + i * 32 + 8 * q + 4 * (lane >> 5);
+        if (col < p.rows && k < p.cols) store_grad(p.out, p.ld, p.dtype, col, k, p.cols - k, v, scale);
       }
     }
 }
@@ -825,7 +868,7 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
 // The longer ones go first.
 template <int TERMS>
 __global__ void __launch_bounds__(512, 2) head_grads_kernel(const GradArgs p) {
-  __shared__ __attribute__((aligned(1024))) int8_t smem[131072];
+  __shared__ __attribute__((aligned(1024))) int8_t smem[kGradSlots * kGradStage];
   const int xcd = blockIdx.x & 7, at = p.first + (blockIdx.x >> 3);
   const int a0 = (int)((int64_t)p.units_a * xcd / 8), na = (int)((int64_t)p.units_a * (xcd + 1) / 8) - a0;
   const int b0 = (int)((int64_t)p.units_b * xcd / 8), nb = (int)((int64_t)p.units_b * (xcd + 1) / 8) - b0;
@@ -892,10 +935,10 @@ FwdPlan fwd_plan(int64_t M) { return M <= 64 ? FwdPlan{128, 32} : FwdPlan{256, 2
 // at most 2^22, so tiles at most 2^22).
 constexpr int64_t kFwdRows = 65536;
 
-// A piece's columns, and into how many ranges the products' contractions are
-// split: a piece's T has at most kPieceValues values (and one column tile at
-// least); the splits are those with the least estimated time.
-constexpr int64_t kPieceValues = int64_t(1) << 27;
+// Pieces of the vocabulary and, in each, the ranges that the products'
+// contractions are split into: a piece's T has at most kPieceValues values (or
+// 256 columns); among the allowed the least estimated time is taken.
+constexpr int64_t kPieceValues = int64_t(3) << 26;
 struct BwdPlan {
   int terms, ct;
   int64_t Mp, C;
@@ -903,36 +946,72 @@ struct BwdPlan {
   size_t code_a, code_b, t, plane_a, plane_b;   // bytes
   size_t bytes() const { return kBounds * sizeof(Bound) + code_a + code_b + t + plane_a + plane_b; }
 };
+// When units of two lengths are done on the 32 CUs of an XCD, which takes an
+// eighth of them: the longer ones first, then each CU the next one as it
+// becomes free.
+double makespan(int64_t n1, double t1, int64_t n2, double t2) {
+  if (t1 < t2) {
+    std::swap(n1, n2);
+    std::swap(t1, t2);
+  }
+  n1 = (n1 + 7) / 8;
+  n2 = (n2 + 7) / 8;
+  const int64_t late = n1 % 32, soon = 32 - late;          // CUs that end the longer ones at `low` and at `high`
+  const double low = (double)(n1 / 32) * t1, high = low + t1;
+  if (n2 == 0) return late ? high : low;
+  const int64_t lag = (int64_t)(t1 / t2);                  // whole short units between the two
+  double end = 1e300;
+  // the earliest end of a short unit by which all of them fit
+  for (int64_t k = n2 / 32 > 1 ? n2 / 32 - 1 : 1; end == 1e300; ++k)      // ends of CUs that started at `low`
+    if (soon * k + late * (k > lag ? (int64_t)(((double)k * t2 - t1) / t2) : 0) >= n2) end = low + (double)k * t2;
+  if (late == 0) return end;
+  for (int64_t k = 0;; ++k) {                              // and at `high`
+    const double t = high + (double)k * t2;
+    if (t >= end) break;
+    if (soon * (int64_t)((t - low) / t2) + late * k >= n2) end = t;
+  }
+  return end > high ? end : high;
+}
 BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, int dtype) {
   BwdPlan b;
   b.terms = dtype == DT_BF16 ? 1 : 2;
   b.ct = 256 / b.terms;
   b.Mp = (M + 255) / 256 * 256;
-  const int64_t Np = (N + 255) / 256 * 256;
-  int64_t most = kPieceValues / b.Mp / 256 * 256;
-  if (most < 256) most = 256;
-  b.pieces = (int)((Np + most - 1) / most);
-  b.C = ((Np + b.pieces - 1) / b.pieces + 255) / 256 * 256;
-  b.pieces = (int)((Np + b.C - 1) / b.C);
   b.tiles_k = up(K, 256);
-  const int64_t ta = b.Mp / b.ct * b.tiles_k, tb = b.C / b.ct * b.tiles_k;
-  const int64_t da = b.C / 64, db = b.Mp / 64;
+  const int64_t blocks = (N + 255) / 256;                  // of 256 columns
+  int64_t most = kPieceValues / b.Mp / 256;
+  if (most < 1) most = 1;
+  const int64_t least = (blocks + most - 1) / most;
+  const int64_t mt = b.Mp / 256, ta = b.Mp / b.ct * b.tiles_k, db = mt;
+  // microseconds, fitted to 25 plans at 8192 x 50304 x 768 (bf16) and 2048 x
+  // 50257 x 768 (f32), whose times it orders as they are to a few per cent: 64
+  // of the contraction of a unit, a unit's start and end, a tile of T, two
+  // launches; planes at 4 TB/s
+  constexpr double kStep = 1.65, kUnit = 6.0, kLaunches = 8.0;
+  const double tile = 6.0 + 1.6 * (double)((K + 127) / 128);
   double best = 1e300;
-  b.sa = b.sb = 1;
-  for (int sa = 1; sa <= 64 && sa <= da; sa *= 2)
-    for (int sb = 1; sb <= 64 && sb <= db; sb *= 2) {
-      const double ua = 4.0 + (double)((da + sa - 1) / sa), ub = 4.0 + (double)((db + sb - 1) / sb);   // in stages
-      const double all = ((double)(ta * sa) * ua + (double)(tb * sb) * ub) / 256;
-      const double longest = ua > ub ? ua : ub, least = ua < ub ? ua : ub;
-      // planes are written and read at about 4 TB/s; a stage takes about 1 us
-      const double planes = (double)(b.Mp * b.tiles_k) * 256 * 4 * 2 * sa + (sb > 1 ? (double)(b.C * b.tiles_k) * 256 * 4 * 2 * sb : 0);
-      const double t = (all + 0.5 * least > longest ? all + 0.5 * least : longest) + planes / 4e6;
-      if (t < best) {
-        best = t;
-        b.sa = sa;
-        b.sb = sb;
+  b.sa = b.sb = b.pieces = 1;
+  b.C = 256;
+  for (int64_t pieces = least; pieces <= least + 3 && pieces <= blocks; ++pieces) {
+    const int64_t c = (blocks + pieces - 1) / pieces, n = (blocks + c - 1) / c, last = blocks - (n - 1) * c;
+    const double weights = (double)((c * mt + 255) / 256) * tile;
+    for (int64_t sa = 1; sa <= 64 && sa <= c; sa += sa < 4 ? 1 : sa)
+      for (int64_t sb = 1; sb <= 64 && sb <= db; sb += sb < 4 ? 1 : sb) {
+        const int64_t pa = (c + sa - 1) / sa, pb = (db + sb - 1) / sb;
+        const double ua = kUnit + kStep * 4 * (double)pa, ub = kUnit + kStep * 4 * (double)pb;
+        const int64_t na = ta * ((c + pa - 1) / pa), nb = 256 / b.ct * b.tiles_k * ((db + pb - 1) / pb);   // nb: for 256 columns
+        const double planes = (double)(b.Mp * b.tiles_k) * 1024 * sa * 2 * n + (sb > 1 ? (double)(blocks * 256 * b.tiles_k) * 1024 * sb * 2 : 0.0);
+        const double t = n * (weights + kLaunches + (sb > 1 ? 4.0 : 0.0)) + (n - 1) * makespan(na, ua, nb * c, ub) +
+                         makespan(na, ua, nb * last, ub) + planes / 4e6;
+        if (t < best) {
+          best = t;
+          b.sa = (int)sa;
+          b.sb = (int)sb;
+          b.pieces = (int)n;
+          b.C = c * 256;
+        }
       }
-    }
+  }
   b.code_a = (size_t)b.Mp * b.tiles_k * 512;
   b.code_b = (size_t)b.C * b.pieces * b.tiles_k * 512;
   b.t = (size_t)b.Mp * b.C * 2 * b.terms;
@@ -985,6 +1064,7 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
   float* plane_a = reinterpret_cast<float*>(at += b.t);
   float* plane_b = reinterpret_cast<float*>(at += b.plane_a);
   const int KB = b.tiles_k * 8;
+  const int C16 = (int)(b.C / 16);
   const size_t plane = (size_t)b.Mp * b.C / 8;
   const LogitArgs l = logit_args(a);
   PackArgs k{l, g.targets, g.g_logprob, g.g_lse, bounds, (int)(b.Mp / 16), (int)(b.C * b.pieces / 16), KB, code_a, code_b};
@@ -1000,7 +1080,7 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
   };
   for (int piece = 0; piece < b.pieces; ++piece) {
     const int64_t v0 = piece * b.C, rows = a.N - v0 < b.C ? a.N - v0 : b.C;
-    WeightArgs w{l, g.targets, g.lse, g.g_logprob, g.g_lse, (int)v0, 0, 0, (int)(b.C / 16), bounds, T, plane};
+    WeightArgs w{l, g.targets, g.lse, g.g_logprob, g.g_lse, (int)v0, 0, 0, C16, bounds, T, plane};
     constexpr int BV = 256, BT = 256;
     w.tiles_v = (int)(b.C / BV);
     w.tiles_t = (int)(b.Mp / BT);
@@ -1013,11 +1093,12 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
     p.T = T;
     p.bounds = bounds;
     p.plane = plane;
-    p.C16 = (int)(b.C / 16);
+    p.C16 = C16;
     p.KB = KB;
     p.tiles_k = b.tiles_k;
     auto side = [](const v4i* codes, int64_t tiles, int64_t depth, int splits, float* planes, int add) {
-      const int stages = (int)(depth / 64), per = up(stages, splits);
+      // (whole blocks of 256: a range has 8 stages at least)
+      const int stages = (int)(depth / 32), per = up(stages / 8, splits) * 8;
       return GradArgs::Side{codes, (int)tiles, up(stages, per), stages, per, planes, add};
     };
     p.a = side(code_b + (size_t)piece * (b.C / 16) * KB * 64, b.Mp / b.ct, b.C, b.sa, plane_a, piece > 0);
