@@ -521,7 +521,9 @@ struct WeightArgs {            // T of a piece
   int tiles_v, tiles_t;        // of the piece
   int C16;                     // blocks of 16 vocabulary rows in a row of blocks
   const Bound* bounds;
-  v4i* T;                      // [tokens / (32 TB)][C16][TB][64], TB = 8 / TERMS: the blocks that a stage of dA reads are in a row
+  int64_t first;               // tile of the launch
+  int tb_log;                  // TB = 2^tb_log blocks of 32 tokens in a tile of dA's product
+  v4i* T;                      // [tokens / (32 TB)][C16][TB][64]: the blocks that a stage of dA reads are in a row
   size_t plane;                // from the first to the second f16 of a value (v4i), TERMS 2
 };
 
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
   __shared__ __attribute__((aligned(1024))) int8_t smem[Tile::LDS];
   __shared__ __attribute__((aligned(16))) float sc[BV];
   int tv, tt;
-  tile_of(xcd_order(blockIdx.x, gridDim.x), p.tiles_v, p.tiles_t, tv, tt);
+  tile_of((int)p.first + xcd_order(blockIdx.x, gridDim.x), p.tiles_v, p.tiles_t, tv, tt);
   const int v0 = p.v0 + tv * BV, t0 = tt * BT;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wv = wave / WT, wt = wave % WT;
   const float scale = t_scale(p.bounds);
@@ -573,9 +575,8 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
   const bool ragged = v0 + BV > p.l.N;
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
-    constexpr int TB = 8 / TERMS;
     const int tb = tt * (BT / 32) + wt * FT + j;
-    v4i* row = p.T + (((size_t)(tb / TB) * p.C16 + (size_t)tv * (BV / 16)) * TB + tb % TB) * 64 + lane;
+    v4i* row = p.T + ((((size_t)(tb >> p.tb_log) * p.C16 + (size_t)tv * (BV / 16)) << p.tb_log) + (tb & ((1 << p.tb_log) - 1))) * 64 + lane;
 #pragma unroll
     for (int i = 0; i < FV; ++i) {
       const int r0 = (wv * FV + i) * 32 + 4 * half;
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
       // holds 8 in a row
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        v4i* to = row + (size_t)((wv * FV + i) * 2 + s) * (TB * 64);
+        v4i* to = row + ((size_t)((wv * FV + i) * 2 + s) << (p.tb_log + 6));
 #pragma unroll
         for (int term = 0; term < TERMS; ++term) {
           const uint32_t* w = term ? lo : hi;
@@ -658,6 +659,18 @@ struct GradArgs {
   const float* scale;          // of its rows
 };
 
+// How a tile is shared by the 8 waves.  FEW: at most 64 tokens, whose tile of
+// dA is 64 wide, each wave 32 columns k of it.
+template <int TERMS, bool DUAL, bool FEW>
+struct GradTile {
+  static constexpr bool NARROW = FEW && !DUAL;
+  static constexpr int WK = NARROW ? 8 : 2, WC = 8 / WK;   // waves along k and along CT
+  static constexpr int FC = NARROW ? 2 : 2 / TERMS;        // 32-blocks of a wave along CT
+  static constexpr int CT = 32 * FC * WC;
+  static constexpr int FA = 8 / WK;                        // and along k: its i-th is block i WK + wk of the tile
+  static constexpr int TB = FEW ? 2 : 8 / TERMS;           // 32-token blocks of a tile of T
+};
+
 template <class T>
 __device__ __forceinline__ void store4(T* to, int n, const float (&v)[4]) {
   T t[4];
@@ -682,37 +695,48 @@ __device__ __forceinline__ void store_grad(void* out, int64_t ld, int dtype, int
 }
 
 // DUAL: dBt, for which T is read transposed.  LDS holds five stages of 32 of the
-// contraction: up to four are on their way while one is multiplied (two stages of 64
-// leave a load half the time to land: 8192 x 50304 x 768 bf16 1759 us in place of 1669).
+// contraction: up to four are on their way while one is multiplied (two stages of
+// 64 leave a load half the time to land: 8192 x 50304 x 768 bf16 1759 us in place
+// of 1669).  FA: 32-blocks along k that a wave multiplies, fewer than the tile's
+// where K ends in it.
 constexpr int kGradStage = 32768, kGradSlots = 5;
-template <int TERMS, bool DUAL>
+template <int TERMS, bool DUAL, bool FEW, int FA>
 __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Side& s, int u, int8_t* smem) {
-  constexpr int FC = 2 / TERMS, CT = 256 / TERMS, TB = CT / 32;   // TB: 32-token blocks of a tile of T
-  constexpr int READS = DUAL ? 8 : 6;                      // LDS reads of a k-step
+  using Tile = GradTile<TERMS, DUAL, FEW>;
+  constexpr bool NARROW = Tile::NARROW;
+  constexpr int WK = Tile::WK, WC = Tile::WC, FC = Tile::FC, CT = Tile::CT, TB = Tile::TB;
+  constexpr int READS = FA + TERMS * FC * (DUAL ? 2 : 1), MFMAS = TERMS * FA * FC;   // of a k-step
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wk = wave >> 2, wc = wave & 3;
+  const int wk = wave / WC, wc = wave % WC;
   const int kt = u % p.tiles_k, ct = (u / p.tiles_k) % s.tiles, split = u / (p.tiles_k * s.tiles);
   const int first = split * s.per, n = min(s.per, s.stages - first);
 
-  // sources of this wave's 2 + 2 loads of a stage: the same in every lane but
-  // for the lane's 16 bytes of a block
+  // sources of this wave's loads of a stage, two of codes and two of T (one in a
+  // narrow tile): the same in every lane but for the lane's 16 bytes of a block
+  constexpr int T_LOADS = NARROW ? 1 : 2, LOADS = 2 + T_LOADS;
   const size_t row_a = (size_t)p.KB * 1024, row_b = (size_t)p.C16 * 1024, plane_b = p.plane * 16;
   const char* ga = reinterpret_cast<const char*>(s.codes) + (size_t)(first * 2) * row_a + (size_t)(kt * 8 + wave) * 1024;
   const char* gb = reinterpret_cast<const char*>(p.T);
   const int lane_a = lane * 16;
-  int lane_b = lane_a;
-  // T's loads: TERMS 1, 16 blocks of a stage in two; TERMS 2, 8 blocks of each term
-  if constexpr (!DUAL) {
-    // blocks [16 of the contraction 2][32 tokens TB] are in a row
+  int lane_b = lane_a, wave_b = wave;                      // wave_b: block of T's stage in LDS
+  size_t next_b = 8192;                                    // from the first to the second load of T
+  if constexpr (NARROW) {
+    // blocks [term][16 of the contraction 2][32 tokens 2]: 4 a term, twice where there is one term
+    gb += (size_t)(first * 2) * (TB * 1024) + (size_t)(wave & 3) * 1024 + (TERMS == 2 ? (wave >> 2) * plane_b : 0);
+    wave_b = TERMS == 2 ? wave : wave & 3;
+  } else if constexpr (!DUAL) {
+    // blocks [16 of the contraction 2][32 tokens TB], in a row; of each term 8
     gb += (size_t)ct * TB * row_b + (size_t)(first * 2) * (TB * 1024) + wave * 1024;
+    if (TERMS == 2) next_b = plane_b;
   } else {
     // 16 vocabulary rows each, of one block of 32 tokens; the 16-byte pieces of a block (half h, token t) are placed at
     // (h, t ^ (4h + 8 (vocabulary block % 2))), so that a transposing read of 32 lanes covers all banks
     lane_b = ((lane & 32) | ((lane & 31) ^ (4 * (lane >> 5) + 8 * (wave & 1)))) * 16;
     gb += ((size_t)ct * (CT / 16) + wave) * (TB * 1024);
+    next_b = TERMS == 2 ? plane_b : (size_t)(8 * TB * 1024);
   }
   auto issue = [&](int st) {
-    int8_t* base = smem + (st % kGradSlots) * kGradStage + wave * 1024;
+    int8_t* base = smem + (st % kGradSlots) * kGradStage;
     const char* a = ga + (size_t)st * 2 * row_a;
     const char* b = gb;
     if constexpr (!DUAL) {
@@ -722,13 +746,13 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
       b += (size_t)(tb / TB) * (TB * row_b) + (size_t)(tb % TB) * 1024;
     }
 #pragma unroll
-    for (int q = 0; q < 2; ++q) lds_load16(a + q * row_a, lane_a, base + q * 8192);
+    for (int q = 0; q < 2; ++q) lds_load16(a + q * row_a, lane_a, base + wave * 1024 + q * 8192);
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-      lds_load16(b + q * (TERMS == 2 ? plane_b : (size_t)(DUAL ? 8 * TB * 1024 : 8192)), lane_b, base + 16384 + q * 8192);
+    for (int q = 0; q < T_LOADS; ++q) lds_load16(b + q * next_b, lane_b, base + 16384 + wave_b * 1024 + q * 8192);
   };
   // LDS: codes [k-step 2][32 columns 8]; T [term][k-step 2][32 tokens TB], or [term][16 vocabulary rows CT / 16]
-  const int offa = wk * 4096 + lane * 16;
+  constexpr int TERM = DUAL ? CT / 16 * 1024 : 2 * TB * 1024;
+  const int offa = wk * 1024 + lane * 16;
   int offb, flip = 0;
   if constexpr (!DUAL) {
     offb = 16384 + wc * FC * 1024 + lane * 16;
@@ -738,30 +762,30 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
     offb = 16384 + (wc * FC * 2 + (g & 1)) * 1024 + h * 512 + t * 16 + (c & 1) * 8;
     flip = offb ^ 64;                                       // the fragment's other 4 tokens
   }
-  v16f acc[4][FC];
+  v16f acc[FA][FC];
   // register order of a plane: [wave][i][j][q][lane] of 4 values
-  float* plane = s.planes ? s.planes + ((size_t)(split * s.tiles + ct) * p.tiles_k + kt) * (256 * CT) + (size_t)wave * (4 * FC * 1024) + lane * 4
+  float* plane = s.planes ? s.planes + ((size_t)(split * s.tiles + ct) * p.tiles_k + kt) * (256 * CT) + (size_t)wave * (Tile::FA * FC * 1024) + lane * 4
                           : nullptr;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < FA; ++i)
 #pragma unroll
     for (int j = 0; j < FC; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  auto read = [&](const int8_t* base, auto ks_t, v8h (&fa)[4], v8h (&fb)[TERMS][FC]) {
+  auto read = [&](const int8_t* base, auto ks_t, v8h (&fa)[FA], v8h (&fb)[TERMS][FC]) {
     constexpr int ks = decltype(ks_t)::value;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) fa[i] = *reinterpret_cast<const v8h*>(base + offa + ks * 8192 + i * 1024);
+    for (int i = 0; i < FA; ++i) fa[i] = *reinterpret_cast<const v8h*>(base + offa + ks * 8192 + i * (WK * 1024));
 #pragma unroll
     for (int t = 0; t < TERMS; ++t)
 #pragma unroll
       for (int j = 0; j < FC; ++j) {
         if constexpr (!DUAL) {
-          fb[t][j] = *reinterpret_cast<const v8h*>(base + offb + t * 8192 + ks * (TB * 1024) + j * 1024);
+          fb[t][j] = *reinterpret_cast<const v8h*>(base + offb + t * TERM + ks * (TB * 1024) + j * 1024);
         } else {
           // tokens 16 ks ... of the block
-          const int at = t * 8192 + j * 2048 + ks * 256;
+          const int at = t * TERM + j * 2048 + ks * 256;
           typedef __attribute__((address_space(3))) v4s lds_v4s;
           const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(base + offb + at));
           const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(base + flip + at));
@@ -770,71 +794,85 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
         }
       }
   };
-  auto mfma = [&](const v8h (&fa)[4], const v8h (&fb)[TERMS][FC]) {
+  auto mfma = [&](const v8h (&fa)[FA], const v8h (&fb)[TERMS][FC]) {
 #pragma unroll
     for (int t = 0; t < TERMS; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < FA; ++i)
 #pragma unroll
         for (int j = 0; j < FC; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[t][j], acc[i][j], 0, 0, 0);
   };
   const std::integral_constant<int, 0> k0;
   const std::integral_constant<int, 1> k1;
-  v8h fa0[4], fa1[4], fb0[TERMS][FC], fb1[TERMS][FC];
-  // n is 8 at least: contractions are whole blocks of 256
-  constexpr int LOADS = 4;
-#pragma unroll
-  for (int st = 0; st < kGradSlots; ++st) issue(st);
-  wait_loads<LOADS * (kGradSlots - 1)>();
-  barrier_nofence();
-  read(smem, k0, fa0, fb0);
-  int slot = 0;
-  // one stage; the next one's first fragments are read behind the barrier that
-  // frees this one's slot, and multiplied after it
-  auto stage = [&](int st, auto left_t) {                  // left: stages in flight behind the next one
-    constexpr int left = decltype(left_t)::value;
-    const int8_t* base = smem + slot * kGradStage;
-    slot = slot + 1 == kGradSlots ? 0 : slot + 1;
-    read(base, k1, fa1, fb1);
-    mfma(fa0, fb0);
-    interleave<READS, 8>();
-    // the next stage has landed, and this one's last fragments are in registers
-    wait_loads<LOADS * left>();
+  v8h fa0[FA], fa1[FA], fb0[TERMS][FC], fb1[TERMS][FC];
+  if constexpr (FEW && DUAL) {
+    // 64 tokens are two stages
+    issue(0);
+    if (n > 1) issue(1);
+    wait_loads<0>();
     barrier_nofence();
-    if constexpr (left == kGradSlots - 2) {
-      if (st + kGradSlots < n) issue(st + kGradSlots);
+    for (int st = 0; st < n; ++st) {
+      read(smem + st * kGradStage, k0, fa0, fb0);
+      read(smem + st * kGradStage, k1, fa1, fb1);
+      mfma(fa0, fb0);
+      mfma(fa1, fb1);
     }
-    read(smem + slot * kGradStage, k0, fa0, fb0);
+  } else {
+    // n is 8 at least: contractions are whole blocks of 256
+#pragma unroll
+    for (int st = 0; st < kGradSlots; ++st) issue(st);
+    wait_loads<LOADS * (kGradSlots - 1)>();
+    barrier_nofence();
+    read(smem, k0, fa0, fb0);
+    int slot = 0;
+    // one stage; the next one's first fragments are read behind the barrier that
+    // frees this one's slot, and multiplied after it
+    auto stage = [&](int st, auto left_t) {                // left: stages in flight behind the next one
+      constexpr int left = decltype(left_t)::value;
+      const int8_t* base = smem + slot * kGradStage;
+      slot = slot + 1 == kGradSlots ? 0 : slot + 1;
+      read(base, k1, fa1, fb1);
+      mfma(fa0, fb0);
+      interleave<READS, MFMAS>();
+      // the next stage has landed, and this one's last fragments are in registers
+      wait_loads<LOADS * left>();
+      barrier_nofence();
+      if constexpr (left == kGradSlots - 2) {
+        if (st + kGradSlots < n) issue(st + kGradSlots);
+      }
+      read(smem + slot * kGradStage, k0, fa0, fb0);
+      mfma(fa1, fb1);
+      interleave<READS, MFMAS>();
+    };
+    int st = 0;
+    for (; st + kGradSlots - 1 < n; ++st) stage(st, std::integral_constant<int, kGradSlots - 2>{});
+    stage(st, std::integral_constant<int, 2>{});
+    stage(st + 1, std::integral_constant<int, 1>{});
+    stage(st + 2, std::integral_constant<int, 0>{});
+    read(smem + slot * kGradStage, k1, fa1, fb1);
+    mfma(fa0, fb0);
+    interleave<READS, MFMAS>();
     mfma(fa1, fb1);
-    interleave<READS, 8>();
-  };
-  int st = 0;
-  for (; st + kGradSlots - 1 < n; ++st) stage(st, std::integral_constant<int, kGradSlots - 2>{});
-  stage(st, std::integral_constant<int, 2>{});
-  stage(st + 1, std::integral_constant<int, 1>{});
-  stage(st + 2, std::integral_constant<int, 0>{});
-  read(smem + slot * kGradStage, k1, fa1, fb1);
-  mfma(fa0, fb0);
-  interleave<READS, 8>();
-  mfma(fa1, fb1);
+  }
 
   if (plane) {
     // (what is added to is read before the stores of two rows of blocks: a load
     // behind a store would wait for it)
+    constexpr int STEP = FA < 2 ? 1 : 2;
 #pragma unroll
-    for (int i0 = 0; i0 < 4; i0 += 2) {
-      v4f old[2][FC][4];
+    for (int i0 = 0; i0 < FA; i0 += STEP) {
+      v4f old[STEP][FC][4];
       if (s.add) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < STEP; ++i)
 #pragma unroll
           for (int j = 0; j < FC; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) old[i][j][q] = *reinterpret_cast<const v4f*>(plane + (((i0 + i) * FC + j) * 4 + q) * 256);
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < STEP; ++i)
 #pragma unroll
         for (int j = 0; j < FC; ++j)
 #pragma unroll
@@ -849,7 +887,7 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
   }
   const float factor = t_scale(p.bounds);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < FA; ++i)
 #pragma unroll
     for (int j = 0; j < FC; ++j) {
       const int col = ct * CT + (wc * FC + j) * 32 + (lane & 31);
@@ -857,7 +895,7 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const v4f v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        const int k = kt * 256 + wk * 128 + i * 32 + 8 * q + 4 * (lane >> 5);
+        const int k = kt * 256 + (i * WK + wk) * 32 + 8 * q + 4 * (lane >> 5);
         if (col < p.rows && k < p.cols) store_grad(p.out, p.ld, p.dtype, col, k, p.cols - k, v, scale);
       }
     }
@@ -866,7 +904,8 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
 // Each XCD (workgroups are dealt to the 8 in turn) takes an eighth of either
 // side's units, neighbours in their order: they share T or codes in its L2.
 // The longer ones go first.
-template <int TERMS>
+// LAST: 32-blocks along k that a wave multiplies in the last tile of k.
+template <int TERMS, bool FEW, int LAST>
 __global__ void __launch_bounds__(512, 2) head_grads_kernel(const GradArgs p) {
   __shared__ __attribute__((aligned(1024))) int8_t smem[kGradSlots * kGradStage];
   const int xcd = blockIdx.x & 7, at = p.first + (blockIdx.x >> 3);
@@ -877,15 +916,23 @@ __global__ void __launch_bounds__(512, 2) head_grads_kernel(const GradArgs p) {
   if (at >= na + nb) return;
   const bool second = at >= n1;
   const int in = second ? at - n1 : at;
-  if (a_first != second) grads_unit<TERMS, false>(p, p.a, a0 + in, smem);
-  else grads_unit<TERMS, true>(p, p.b, b0 + in, smem);
+  if (a_first != second) {
+    const int u = a0 + in;
+    if constexpr (FEW) grads_unit<TERMS, false, true, 1>(p, p.a, u, smem);
+    else if (LAST == 4 || u % p.tiles_k + 1 < p.tiles_k) grads_unit<TERMS, false, false, 4>(p, p.a, u, smem);
+    else grads_unit<TERMS, false, false, LAST>(p, p.a, u, smem);
+  } else {
+    const int u = b0 + in;
+    if (LAST == 4 || u % p.tiles_k + 1 < p.tiles_k) grads_unit<TERMS, true, FEW, 4>(p, p.b, u, smem);
+    else grads_unit<TERMS, true, FEW, LAST>(p, p.b, u, smem);
+  }
 }
 
 struct FinishArgs {
   const float* planes;
   const Bound* bounds;
   int splits, tiles, tiles_k;
-  int CT;
+  int CT, WK;                  // of the tile
   void* out;
   int64_t ld;
   int dtype, rows, cols;
@@ -894,14 +941,14 @@ struct FinishArgs {
 // The planes' sum, in their order, by its row's scale.
 __global__ void __launch_bounds__(256) head_finish_kernel(const FinishArgs p) {
   const size_t size = (size_t)256 * p.CT, all = (size_t)p.tiles * p.tiles_k * size;
-  const int FC = p.CT / 128;
+  const int WC = 8 / p.WK, FC = p.CT / 32 / WC, FA = 8 / p.WK;
   const float factor = t_scale(p.bounds);
   for (size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; at < all; at += (size_t)gridDim.x * 1024) {
     const int tile = (int)(at / size), in = (int)(at % size) / 4;
     const int kt = tile % p.tiles_k, ct = tile / p.tiles_k;
-    const int lane = in & 63, q = (in >> 6) & 3, j = (in >> 8) % FC, i = (in >> 8) / FC % 4, wave = (in >> 8) / (FC * 4);
-    const int col = ct * p.CT + ((wave & 3) * FC + j) * 32 + (lane & 31);
-    const int k = kt * 256 + (wave >> 2) * 128 + i * 32 + 8 * q + 4 * (lane >> 5);
+    const int lane = in & 63, q = (in >> 6) & 3, j = (in >> 8) % FC, i = (in >> 8) / FC % FA, wave = (in >> 8) / (FC * FA);
+    const int col = ct * p.CT + (wave % WC * FC + j) * 32 + (lane & 31);
+    const int k = kt * 256 + (i * p.WK + wave / WC) * 32 + 8 * q + 4 * (lane >> 5);
     if (col >= p.rows || k >= p.cols) continue;
     v4f v = *reinterpret_cast<const v4f*>(p.planes + at);
     for (int s = 1; s < p.splits; ++s) v += *reinterpret_cast<const v4f*>(p.planes + s * all + at);
@@ -924,12 +971,25 @@ LogitArgs logit_args(const HeadArgs& a) {
   return LogitArgs{a.A, a.B, a.s_row, a.s_col, a.lda, a.ldb, (int)a.M, (int)a.N, (int)a.K};
 }
 
-// Forward tiles: 256 x 256; up to 64 tokens, where reading the codes is the
-// work, 128 vocabulary rows by 32 tokens.
-struct FwdPlan {
+// Tiles of logits: 256 vocabulary rows by 256 tokens, or, with three workgroups a
+// CU, 128 by 64 or 128 by 32, which leave more of the chip busy where there are
+// few, and fewer tokens unused.  The times (us) of a round of 256 or 768 of them
+// are fitted to 13 shapes: 8192 x 16384 x 768 takes 145, 178 and 242 us, 1180 x
+// 13260 x 246 29.3, 22.7 and 26.9, one token x 50257 x 768 21.3, 13.9 and 13.0.
+struct LogitPlan {
   int bv, bt;
+  double time;
 };
-FwdPlan fwd_plan(int64_t M) { return M <= 64 ? FwdPlan{128, 32} : FwdPlan{256, 256}; }
+LogitPlan logit_plan(int64_t M, int64_t N, int64_t K) {
+  const double k = (double)((K + 127) / 128);
+  const auto tiles = [&](int bv, int bt) { return (double)((N + bv - 1) / bv) * (double)((M + bt - 1) / bt); };
+  const auto rounds = [](double n) { return n < 0.6 ? 0.6 : n; };
+  const LogitPlan wide{256, 256, (double)(int64_t)((tiles(256, 256) + 255) / 256) * (6.0 + 1.7 * k)};
+  const LogitPlan mid{128, 64, rounds(tiles(128, 64) / 768) * (2.4 + 1.0 * k)};
+  const LogitPlan thin{128, 32, rounds(tiles(128, 32) / 768) * (1.7 + 0.7 * k)};
+  const LogitPlan& small = thin.time < mid.time ? thin : mid;
+  return small.time < wide.time ? small : wide;
+}
 
 // Tokens of a launch, which bounds its workspace and grid (vocabulary rows are
 // at most 2^22, so tiles at most 2^22).
@@ -940,7 +1000,9 @@ constexpr int64_t kFwdRows = 65536;
 // 256 columns); among the allowed the least estimated time is taken.
 constexpr int64_t kPieceValues = int64_t(3) << 26;
 struct BwdPlan {
-  int terms, ct;
+  int terms;
+  bool few;                    // at most 64 tokens
+  int ca, cb, tb_log;          // CT of dA's and dBt's tiles, and TB, as GradTile has them
   int64_t Mp, C;
   int pieces, tiles_k, sa, sb;
   size_t code_a, code_b, t, plane_a, plane_b;   // bytes
@@ -975,31 +1037,32 @@ double makespan(int64_t n1, double t1, int64_t n2, double t2) {
 BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, int dtype) {
   BwdPlan b;
   b.terms = dtype == DT_BF16 ? 1 : 2;
-  b.ct = 256 / b.terms;
-  b.Mp = (M + 255) / 256 * 256;
+  b.few = M <= 64;
+  b.cb = 256 / b.terms;
+  b.ca = b.few ? 64 : b.cb;
+  b.tb_log = b.few ? 1 : 4 - b.terms;
+  b.Mp = b.few ? 64 : (M + 255) / 256 * 256;
   b.tiles_k = up(K, 256);
   const int64_t blocks = (N + 255) / 256;                  // of 256 columns
   int64_t most = kPieceValues / b.Mp / 256;
   if (most < 1) most = 1;
   const int64_t least = (blocks + most - 1) / most;
-  const int64_t mt = b.Mp / 256, ta = b.Mp / b.ct * b.tiles_k, db = mt;
+  const int64_t ta = b.Mp / b.ca * b.tiles_k, db = up(b.Mp, 256);
   // microseconds, fitted to 25 plans at 8192 x 50304 x 768 (bf16) and 2048 x
   // 50257 x 768 (f32), whose times it orders as they are to a few per cent: 64
-  // of the contraction of a unit, a unit's start and end, a tile of T, two
-  // launches; planes at 4 TB/s
+  // of the contraction of a unit, a unit's start and end, two launches; planes at 4 TB/s
   constexpr double kStep = 1.65, kUnit = 6.0, kLaunches = 8.0;
-  const double tile = 6.0 + 1.6 * (double)((K + 127) / 128);
   double best = 1e300;
   b.sa = b.sb = b.pieces = 1;
   b.C = 256;
   for (int64_t pieces = least; pieces <= least + 3 && pieces <= blocks; ++pieces) {
     const int64_t c = (blocks + pieces - 1) / pieces, n = (blocks + c - 1) / c, last = blocks - (n - 1) * c;
-    const double weights = (double)((c * mt + 255) / 256) * tile;
+    const double weights = logit_plan(b.Mp, c * 256, K).time;
     for (int64_t sa = 1; sa <= 64 && sa <= c; sa += sa < 4 ? 1 : sa)
       for (int64_t sb = 1; sb <= 64 && sb <= db; sb += sb < 4 ? 1 : sb) {
         const int64_t pa = (c + sa - 1) / sa, pb = (db + sb - 1) / sb;
         const double ua = kUnit + kStep * 4 * (double)pa, ub = kUnit + kStep * 4 * (double)pb;
-        const int64_t na = ta * ((c + pa - 1) / pa), nb = 256 / b.ct * b.tiles_k * ((db + pb - 1) / pb);   // nb: for 256 columns
+        const int64_t na = ta * ((c + pa - 1) / pa), nb = 256 / b.cb * b.tiles_k * ((db + pb - 1) / pb);   // nb: for 256 columns
         const double planes = (double)(b.Mp * b.tiles_k) * 1024 * sa * 2 * n + (sb > 1 ? (double)(blocks * 256 * b.tiles_k) * 1024 * sb * 2 : 0.0);
         const double t = n * (weights + kLaunches + (sb > 1 ? 4.0 : 0.0)) + (n - 1) * makespan(na, ua, nb * c, ub) +
                          makespan(na, ua, nb * last, ub) + planes / 4e6;
@@ -1022,12 +1085,27 @@ BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, int dtype) {
 
 }  // namespace
 
+template <int TERMS, bool FEW>
+static void launch_grads_of(int last, unsigned n, hipStream_t stream, const GradArgs& p) {
+  if (last > 2) hipLaunchKernelGGL((head_grads_kernel<TERMS, FEW, 4>), dim3(n), dim3(512), 0, stream, p);
+  else if (last == 2) hipLaunchKernelGGL((head_grads_kernel<TERMS, FEW, 2>), dim3(n), dim3(512), 0, stream, p);
+  else hipLaunchKernelGGL((head_grads_kernel<TERMS, FEW, 1>), dim3(n), dim3(512), 0, stream, p);
+}
+static void launch_grads(const BwdPlan& b, int K, unsigned n, hipStream_t stream, const GradArgs& p) {
+  const int last = (K - (b.tiles_k - 1) * 256 + 63) / 64;  // pairs of 32 columns in the last tile
+  if (b.terms == 1 && b.few) launch_grads_of<1, true>(last, n, stream, p);
+  else if (b.terms == 1) launch_grads_of<1, false>(last, n, stream, p);
+  else if (b.few) launch_grads_of<2, true>(last, n, stream, p);
+  else launch_grads_of<2, false>(last, n, stream, p);
+}
+
 size_t head_fwd_bytes(int64_t M, int64_t N) {
-  return align256((size_t)up(N, fwd_plan(M).bv) * (size_t)(M < kFwdRows ? M : kFwdRows) * sizeof(v2f));
+  // (the narrower tiles leave the most parts)
+  return align256((size_t)up(N, 128) * (size_t)(M < kFwdRows ? M : kFwdRows) * sizeof(v2f));
 }
 
 hipError_t launch_head_fwd(const HeadArgs& whole, const int64_t* targets, float* logprob, float* lse, void* ws, hipStream_t stream) {
-  const FwdPlan pl = fwd_plan(whole.M);
+  const LogitPlan pl = logit_plan(whole.M < kFwdRows ? whole.M : kFwdRows, whole.N, whole.K);
   for (int64_t row = 0; row < whole.M; row += kFwdRows) {
     HeadArgs a = whole;
     a.M = whole.M - row < kFwdRows ? whole.M - row : kFwdRows;
@@ -1035,7 +1113,8 @@ hipError_t launch_head_fwd(const HeadArgs& whole, const int64_t* targets, float*
     a.s_row += row;
     FwdArgs f{logit_args(a), up(a.N, pl.bv), up(a.M, pl.bt), static_cast<v2f*>(ws)};
     const dim3 grid((unsigned)f.tiles_v * (unsigned)f.tiles_t);
-    if (pl.bt == 32) hipLaunchKernelGGL((head_fwd_kernel<128, 32, 4, 1, 2>), grid, dim3(256), 0, stream, f);
+    if (pl.bt == 32) hipLaunchKernelGGL((head_fwd_kernel<128, 32, 4, 1, 3>), grid, dim3(256), 0, stream, f);
+    else if (pl.bt == 64) hipLaunchKernelGGL((head_fwd_kernel<128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, f);
     else hipLaunchKernelGGL((head_fwd_kernel<256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, f);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -1072,22 +1151,29 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
   hipLaunchKernelGGL(head_prepare_kernel, dim3(kBounds + (unsigned)(groups < kMostGroups ? groups : kMostGroups)), dim3(256), 0, stream, k);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  auto finish = [&](const GradArgs::Side& s, void* out, int64_t ld, int64_t n, const float* scale) {
-    FinishArgs f{s.planes, bounds, s.splits, s.tiles, b.tiles_k, b.ct, out, ld, g.dtype, (int)n, (int)a.K, scale};
-    const int64_t n_groups = (int64_t)s.tiles * b.tiles_k * b.ct / 4;
+  auto finish = [&](bool side_a, const GradArgs::Side& s, void* out, int64_t ld, int64_t n, const float* scale) {
+    const int ct = side_a ? b.ca : b.cb;
+    FinishArgs f{s.planes, bounds, s.splits, s.tiles, b.tiles_k, ct, side_a && b.few ? 8 : 2, out, ld, g.dtype, (int)n, (int)a.K, scale};
+    const int64_t n_groups = (int64_t)s.tiles * b.tiles_k * ct / 4;
     hipLaunchKernelGGL(head_finish_kernel, dim3((unsigned)(n_groups < kMostGroups ? n_groups : kMostGroups)), dim3(256), 0, stream, f);
     return hipGetLastError();
   };
   for (int piece = 0; piece < b.pieces; ++piece) {
     const int64_t v0 = piece * b.C, rows = a.N - v0 < b.C ? a.N - v0 : b.C;
-    WeightArgs w{l, g.targets, g.lse, g.g_logprob, g.g_lse, (int)v0, 0, 0, C16, bounds, T, plane};
-    constexpr int BV = 256, BT = 256;
-    w.tiles_v = (int)(b.C / BV);
-    w.tiles_t = (int)(b.Mp / BT);
-    const dim3 grid((unsigned)w.tiles_v * (unsigned)w.tiles_t);
-    if (b.terms == 1) hipLaunchKernelGGL((head_weights_kernel<1, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
-    else hipLaunchKernelGGL((head_weights_kernel<2, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    WeightArgs w{l, g.targets, g.lse, g.g_logprob, g.g_lse, (int)v0, 0, 0, C16, bounds, 0, b.tb_log, T, plane};
+    const LogitPlan pl = logit_plan(b.Mp, b.C, a.K);
+    const bool wide = pl.bt == 256 && !b.few;
+    w.tiles_v = (int)(b.C / (wide ? 256 : 128));
+    w.tiles_t = (int)(b.Mp / (wide ? 256 : 64));
+    for (w.first = 0; w.first < (int64_t)w.tiles_v * w.tiles_t; w.first += kMostGroups) {
+      const int64_t left = (int64_t)w.tiles_v * w.tiles_t - w.first;
+      const dim3 grid((unsigned)(left < kMostGroups ? left : kMostGroups));
+      if (wide && b.terms == 1) hipLaunchKernelGGL((head_weights_kernel<1, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
+      else if (wide) hipLaunchKernelGGL((head_weights_kernel<2, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
+      else if (b.terms == 1) hipLaunchKernelGGL((head_weights_kernel<1, 128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, w);
+      else hipLaunchKernelGGL((head_weights_kernel<2, 128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, w);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
 
     GradArgs p{};
     p.T = T;
@@ -1097,12 +1183,12 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
     p.KB = KB;
     p.tiles_k = b.tiles_k;
     auto side = [](const v4i* codes, int64_t tiles, int64_t depth, int splits, float* planes, int add) {
-      // (whole blocks of 256: a range has 8 stages at least)
-      const int stages = (int)(depth / 32), per = up(stages / 8, splits) * 8;
+      // (whole blocks of 256: a range has 8 stages at least; 64 tokens are 2)
+      const int stages = (int)(depth / 32), per = stages < 8 ? stages : up(stages / 8, splits) * 8;
       return GradArgs::Side{codes, (int)tiles, up(stages, per), stages, per, planes, add};
     };
-    p.a = side(code_b + (size_t)piece * (b.C / 16) * KB * 64, b.Mp / b.ct, b.C, b.sa, plane_a, piece > 0);
-    p.b = side(code_a, up(rows, b.ct), b.Mp, b.sb, b.sb > 1 ? plane_b : nullptr, 0);
+    p.a = side(code_b + (size_t)piece * (b.C / 16) * KB * 64, b.Mp / b.ca, b.C, b.sa, plane_a, piece > 0);
+    p.b = side(code_a, up(rows, b.cb), b.Mp, b.sb, b.sb > 1 ? plane_b : nullptr, 0);
     p.units_a = g.dA ? p.tiles_k * p.a.tiles * p.a.splits : 0;
     p.units_b = g.dB ? p.tiles_k * p.b.tiles * p.b.splits : 0;
     const int64_t esize = g.dtype == DT_F32 ? 4 : 2;
@@ -1115,12 +1201,11 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
     const int most = up(p.units_a, 8) + up(p.units_b, 8);    // of an XCD
     for (p.first = 0; p.first < most; p.first += kMostGroups / 8) {
       const unsigned n = 8u * (unsigned)(most - p.first < kMostGroups / 8 ? most - p.first : kMostGroups / 8);
-      if (b.terms == 1) hipLaunchKernelGGL(head_grads_kernel<1>, dim3(n), dim3(512), 0, stream, p);
-      else hipLaunchKernelGGL(head_grads_kernel<2>, dim3(n), dim3(512), 0, stream, p);
+      launch_grads(b, (int)a.K, n, stream, p);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    if (g.dB && p.b.planes && (e = finish(p.b, p.out, g.lddb, rows, p.scale)) != hipSuccess) return e;
-    if (g.dA && piece + 1 == b.pieces && (e = finish(p.a, g.dA, g.ldda, a.M, a.s_row)) != hipSuccess) return e;
+    if (g.dB && p.b.planes && (e = finish(false, p.b, p.out, g.lddb, rows, p.scale)) != hipSuccess) return e;
+    if (g.dA && piece + 1 == b.pieces && (e = finish(true, p.a, g.dA, g.ldda, a.M, a.s_row)) != hipSuccess) return e;
   }
   return hipSuccess;
 }
