@@ -258,6 +258,7 @@ struct LogitTile {
 // ---- forward --------------------------------------------------------------------
 struct FwdArgs {
   LogitArgs l;
+  int v0;                      // first vocabulary row
   int tiles_v, tiles_t;
   v2f* parts;                  // [tiles_v][M]: the maximum, and the sum of exp(x - maximum)
 };
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_fwd_k
   __shared__ v2f part[WV][BT];
   int tv, tt;
   tile_of(xcd_order(blockIdx.x, gridDim.x), p.tiles_v, p.tiles_t, tv, tt);
-  const int v0 = tv * BV, t0 = tt * BT;
+  const int v0 = p.v0 + tv * BV, t0 = tt * BT;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wv = wave / WT, wt = wave % WT;
   for (int i = tid; i < BV; i += Tile::NT) sc[i] = p.l.s_col[min(v0 + i, p.l.N - 1)];
   float sr[FT];
@@ -517,7 +518,7 @@ struct WeightArgs {            // T of a piece
   LogitArgs l;
   const int64_t* targets;
   const float *lse, *g, *gl;   // g or gl may be null (0)
-  int v0;                      // the piece's first vocabulary row
+  int v0, c0;                  // the first vocabulary row, and its place in the piece
   int tiles_v, tiles_t;        // of the piece
   int C16;                     // blocks of 16 vocabulary rows in a row of blocks
   const Bound* bounds;
@@ -576,7 +577,7 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
     const int tb = tt * (BT / 32) + wt * FT + j;
-    v4i* row = p.T + ((((size_t)(tb >> p.tb_log) * p.C16 + (size_t)tv * (BV / 16)) << p.tb_log) + (tb & ((1 << p.tb_log) - 1))) * 64 + lane;
+    v4i* row = p.T + ((((size_t)(tb >> p.tb_log) * p.C16 + (size_t)(p.c0 / 16 + tv * (BV / 16))) << p.tb_log) + (tb & ((1 << p.tb_log) - 1))) * 64 + lane;
 #pragma unroll
     for (int i = 0; i < FV; ++i) {
       const int r0 = (wv * FV + i) * 32 + 4 * half;
@@ -649,23 +650,23 @@ struct GradArgs {
     int per;                   // stages of a range
     float* planes;             // [splits][tiles][tiles_k][256 * CT] in register order, or null: write `out`
     int add;                   // add to the planes
+    void* out;                 // the gradient's rows of the piece, `rows` of them exist
+    int64_t ld;
+    int rows;
+    const float* scale;        // of its rows
   } a, b;                      // dA: contraction over the piece's vocabulary; dBt: over the tokens
   int units_a, units_b;
   int first;                   // place of the launch in every XCD's list
-  // dBt written here (without planes)
-  void* out;
-  int64_t ld;
-  int dtype, rows, cols;       // rows of the piece that exist
-  const float* scale;          // of its rows
+  int dtype, cols;
 };
 
 // How a tile is shared by the 8 waves.  FEW: at most 64 tokens, whose tile of
-// dA is 64 wide, each wave 32 columns k of it.
+// dA is 64 wide, each wave 32 columns k of it; two workgroups run on a CU.
 template <int TERMS, bool DUAL, bool FEW>
 struct GradTile {
   static constexpr bool NARROW = FEW && !DUAL;
   static constexpr int WK = NARROW ? 8 : 2, WC = 8 / WK;   // waves along k and along CT
-  static constexpr int FC = NARROW ? 2 : 2 / TERMS;        // 32-blocks of a wave along CT
+  static constexpr int FC = NARROW ? 2 : FEW ? 1 : 2 / TERMS;   // 32-blocks of a wave along CT
   static constexpr int CT = 32 * FC * WC;
   static constexpr int FA = 8 / WK;                        // and along k: its i-th is block i WK + wk of the tile
   static constexpr int TB = FEW ? 2 : 8 / TERMS;           // 32-token blocks of a tile of T
@@ -699,11 +700,16 @@ __device__ __forceinline__ void store_grad(void* out, int64_t ld, int dtype, int
 // 64 leave a load half the time to land: 8192 x 50304 x 768 bf16 1759 us in place
 // of 1669).  FA: 32-blocks along k that a wave multiplies, fewer than the tile's
 // where K ends in it.
-constexpr int kGradStage = 32768, kGradSlots = 5;
+// At most 64 tokens: three stages of 24 KiB for dA, and dBt's two.
+constexpr int grad_stage(bool few, bool dual) { return few && !dual ? 24576 : 32768; }
+constexpr int grad_slots(bool few, bool dual) { return !few ? 5 : dual ? 2 : 3; }
+constexpr int grad_lds(bool few) { return grad_stage(few, false) * grad_slots(few, false); }
+static_assert(grad_lds(true) >= grad_stage(true, true) * grad_slots(true, true), "dBt's stages fit");
 template <int TERMS, bool DUAL, bool FEW, int FA>
 __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Side& s, int u, int8_t* smem) {
   using Tile = GradTile<TERMS, DUAL, FEW>;
   constexpr bool NARROW = Tile::NARROW;
+  constexpr int kStage = grad_stage(FEW, DUAL), kSlots = grad_slots(FEW, DUAL);
   constexpr int WK = Tile::WK, WC = Tile::WC, FC = Tile::FC, CT = Tile::CT, TB = Tile::TB;
   constexpr int READS = FA + TERMS * FC * (DUAL ? 2 : 1), MFMAS = TERMS * FA * FC;   // of a k-step
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -711,11 +717,12 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
   const int kt = u % p.tiles_k, ct = (u / p.tiles_k) % s.tiles, split = u / (p.tiles_k * s.tiles);
   const int first = split * s.per, n = min(s.per, s.stages - first);
 
-  // sources of this wave's loads of a stage, two of codes and two of T (one in a
-  // narrow tile): the same in every lane but for the lane's 16 bytes of a block
-  constexpr int T_LOADS = NARROW ? 1 : 2, LOADS = 2 + T_LOADS;
+  // sources of this wave's loads of a stage, two of codes and one or two of T: the
+  // same in every lane but for the lane's 16 bytes of a block (codes behind KB are
+  // not used: the last block in their place)
+  constexpr int T_LOADS = NARROW || (FEW && TERMS == 1) ? 1 : 2, LOADS = 2 + T_LOADS;
   const size_t row_a = (size_t)p.KB * 1024, row_b = (size_t)p.C16 * 1024, plane_b = p.plane * 16;
-  const char* ga = reinterpret_cast<const char*>(s.codes) + (size_t)(first * 2) * row_a + (size_t)(kt * 8 + wave) * 1024;
+  const char* ga = reinterpret_cast<const char*>(s.codes) + (size_t)(first * 2) * row_a + (size_t)min(kt * 8 + wave, p.KB - 1) * 1024;
   const char* gb = reinterpret_cast<const char*>(p.T);
   const int lane_a = lane * 16;
   int lane_b = lane_a, wave_b = wave;                      // wave_b: block of T's stage in LDS
@@ -736,7 +743,7 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
     next_b = TERMS == 2 ? plane_b : (size_t)(8 * TB * 1024);
   }
   auto issue = [&](int st) {
-    int8_t* base = smem + (st % kGradSlots) * kGradStage;
+    int8_t* base = smem + (st % kSlots) * kStage;
     const char* a = ga + (size_t)st * 2 * row_a;
     const char* b = gb;
     if constexpr (!DUAL) {
@@ -813,16 +820,16 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
     wait_loads<0>();
     barrier_nofence();
     for (int st = 0; st < n; ++st) {
-      read(smem + st * kGradStage, k0, fa0, fb0);
-      read(smem + st * kGradStage, k1, fa1, fb1);
+      read(smem + st * kStage, k0, fa0, fb0);
+      read(smem + st * kStage, k1, fa1, fb1);
       mfma(fa0, fb0);
       mfma(fa1, fb1);
     }
   } else {
     // n is 8 at least: contractions are whole blocks of 256
 #pragma unroll
-    for (int st = 0; st < kGradSlots; ++st) issue(st);
-    wait_loads<LOADS * (kGradSlots - 1)>();
+    for (int st = 0; st < kSlots; ++st) issue(st);
+    wait_loads<LOADS * (kSlots - 1)>();
     barrier_nofence();
     read(smem, k0, fa0, fb0);
     int slot = 0;
@@ -830,27 +837,27 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
     // frees this one's slot, and multiplied after it
     auto stage = [&](int st, auto left_t) {                // left: stages in flight behind the next one
       constexpr int left = decltype(left_t)::value;
-      const int8_t* base = smem + slot * kGradStage;
-      slot = slot + 1 == kGradSlots ? 0 : slot + 1;
+      const int8_t* base = smem + slot * kStage;
+      slot = slot + 1 == kSlots ? 0 : slot + 1;
       read(base, k1, fa1, fb1);
       mfma(fa0, fb0);
       interleave<READS, MFMAS>();
       // the next stage has landed, and this one's last fragments are in registers
       wait_loads<LOADS * left>();
       barrier_nofence();
-      if constexpr (left == kGradSlots - 2) {
-        if (st + kGradSlots < n) issue(st + kGradSlots);
+      if constexpr (left == kSlots - 2) {
+        if (st + kSlots < n) issue(st + kSlots);
       }
-      read(smem + slot * kGradStage, k0, fa0, fb0);
+      read(smem + slot * kStage, k0, fa0, fb0);
       mfma(fa1, fb1);
       interleave<READS, MFMAS>();
     };
     int st = 0;
-    for (; st + kGradSlots - 1 < n; ++st) stage(st, std::integral_constant<int, kGradSlots - 2>{});
-    stage(st, std::integral_constant<int, 2>{});
-    stage(st + 1, std::integral_constant<int, 1>{});
-    stage(st + 2, std::integral_constant<int, 0>{});
-    read(smem + slot * kGradStage, k1, fa1, fb1);
+    for (; st + kSlots - 1 < n; ++st) stage(st, std::integral_constant<int, kSlots - 2>{});
+    if constexpr (kSlots > 4) stage(st++, std::integral_constant<int, 2>{});
+    if constexpr (kSlots > 3) stage(st++, std::integral_constant<int, 1>{});
+    stage(st, std::integral_constant<int, 0>{});
+    read(smem + slot * kStage, k1, fa1, fb1);
     mfma(fa0, fb0);
     interleave<READS, MFMAS>();
     mfma(fa1, fb1);
@@ -891,12 +898,12 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
 #pragma unroll
     for (int j = 0; j < FC; ++j) {
       const int col = ct * CT + (wc * FC + j) * 32 + (lane & 31);
-      const float scale = col < p.rows ? p.scale[col] * factor : 1.0f;
+      const float scale = col < s.rows ? s.scale[col] * factor : 1.0f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const v4f v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
         const int k = kt * 256 + (i * WK + wk) * 32 + 8 * q + 4 * (lane >> 5);
-        if (col < p.rows && k < p.cols) store_grad(p.out, p.ld, p.dtype, col, k, p.cols - k, v, scale);
+        if (col < s.rows && k < p.cols) store_grad(s.out, s.ld, p.dtype, col, k, p.cols - k, v, scale);
       }
     }
 }
@@ -906,8 +913,8 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
 // The longer ones go first.
 // LAST: 32-blocks along k that a wave multiplies in the last tile of k.
 template <int TERMS, bool FEW, int LAST>
-__global__ void __launch_bounds__(512, 2) head_grads_kernel(const GradArgs p) {
-  __shared__ __attribute__((aligned(1024))) int8_t smem[kGradSlots * kGradStage];
+__global__ void __launch_bounds__(512, FEW ? 4 : 2) head_grads_kernel(const GradArgs p) {
+  __shared__ __attribute__((aligned(1024))) int8_t smem[grad_lds(FEW)];
   const int xcd = blockIdx.x & 7, at = p.first + (blockIdx.x >> 3);
   const int a0 = (int)((int64_t)p.units_a * xcd / 8), na = (int)((int64_t)p.units_a * (xcd + 1) / 8) - a0;
   const int b0 = (int)((int64_t)p.units_b * xcd / 8), nb = (int)((int64_t)p.units_b * (xcd + 1) / 8) - b0;
@@ -929,30 +936,38 @@ __global__ void __launch_bounds__(512, 2) head_grads_kernel(const GradArgs p) {
 }
 
 struct FinishArgs {
-  const float* planes;
+  struct Side {
+    const float* planes;
+    int splits, tiles;
+    int CT, WK;                // of the tile
+    void* out;
+    int64_t ld;
+    int rows;
+    const float* scale;
+  } side[2];
+  int64_t groups;              // workgroups of side[0]; those behind take side[1]
   const Bound* bounds;
-  int splits, tiles, tiles_k;
-  int CT, WK;                  // of the tile
-  void* out;
-  int64_t ld;
-  int dtype, rows, cols;
-  const float* scale;
+  int tiles_k, dtype, cols;
 };
 // The planes' sum, in their order, by its row's scale.
 __global__ void __launch_bounds__(256) head_finish_kernel(const FinishArgs p) {
-  const size_t size = (size_t)256 * p.CT, all = (size_t)p.tiles * p.tiles_k * size;
-  const int WC = 8 / p.WK, FC = p.CT / 32 / WC, FA = 8 / p.WK;
+  const bool second = blockIdx.x >= p.groups;
+  const FinishArgs::Side& s = p.side[second];
+  const int64_t group = second ? blockIdx.x - p.groups : blockIdx.x, groups = second ? gridDim.x - p.groups : p.groups;
+  const size_t size = (size_t)256 * s.CT, all = (size_t)s.tiles * p.tiles_k * size;
+  const int WC = 8 / s.WK, FC = s.CT / 32 / WC, FA = 8 / s.WK;
   const float factor = t_scale(p.bounds);
-  for (size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; at < all; at += (size_t)gridDim.x * 1024) {
+  for (size_t at = ((size_t)group * 256 + threadIdx.x) * 4; at < all; at += (size_t)groups * 1024) {
     const int tile = (int)(at / size), in = (int)(at % size) / 4;
     const int kt = tile % p.tiles_k, ct = tile / p.tiles_k;
     const int lane = in & 63, q = (in >> 6) & 3, j = (in >> 8) % FC, i = (in >> 8) / FC % FA, wave = (in >> 8) / (FC * FA);
-    const int col = ct * p.CT + (wave % WC * FC + j) * 32 + (lane & 31);
-    const int k = kt * 256 + (i * p.WK + wave / WC) * 32 + 8 * q + 4 * (lane >> 5);
-    if (col >= p.rows || k >= p.cols) continue;
-    v4f v = *reinterpret_cast<const v4f*>(p.planes + at);
-    for (int s = 1; s < p.splits; ++s) v += *reinterpret_cast<const v4f*>(p.planes + s * all + at);
-    store_grad(p.out, p.ld, p.dtype, col, k, p.cols - k, v, p.scale[col] * factor);
+    const int col = ct * s.CT + (wave % WC * FC + j) * 32 + (lane & 31);
+    const int k = kt * 256 + (i * s.WK + wave / WC) * 32 + 8 * q + 4 * (lane >> 5);
+    if (col >= s.rows || k >= p.cols) continue;
+    v4f v = *reinterpret_cast<const v4f*>(s.planes + at);
+#pragma unroll 8
+    for (int n = 1; n < s.splits; ++n) v += *reinterpret_cast<const v4f*>(s.planes + n * all + at);
+    store_grad(s.out, s.ld, p.dtype, col, k, p.cols - k, v, s.scale[col] * factor);
   }
 }
 
@@ -976,19 +991,35 @@ LogitArgs logit_args(const HeadArgs& a) {
 // few, and fewer tokens unused.  The times (us) of a round of 256 or 768 of them
 // are fitted to 13 shapes: 8192 x 16384 x 768 takes 145, 178 and 242 us, 1180 x
 // 13260 x 246 29.3, 22.7 and 26.9, one token x 50257 x 768 21.3, 13.9 and 13.0.
+// Wide tiles may take whole rounds of the vocabulary's first columns and the
+// small ones the rest, in a launch of their own.
 struct LogitPlan {
-  int bv, bt;
+  int64_t wide;                // columns of the wide tiles (whole tiles, or all)
+  int bv, bt;                  // of the others
   double time;
 };
 LogitPlan logit_plan(int64_t M, int64_t N, int64_t K) {
-  const double k = (double)((K + 127) / 128);
-  const auto tiles = [&](int bv, int bt) { return (double)((N + bv - 1) / bv) * (double)((M + bt - 1) / bt); };
-  const auto rounds = [](double n) { return n < 0.6 ? 0.6 : n; };
-  const LogitPlan wide{256, 256, (double)(int64_t)((tiles(256, 256) + 255) / 256) * (6.0 + 1.7 * k)};
-  const LogitPlan mid{128, 64, rounds(tiles(128, 64) / 768) * (2.4 + 1.0 * k)};
-  const LogitPlan thin{128, 32, rounds(tiles(128, 32) / 768) * (1.7 + 0.7 * k)};
-  const LogitPlan& small = thin.time < mid.time ? thin : mid;
-  return small.time < wide.time ? small : wide;
+  const double k = (double)((K + 127) / 128), round = 6.0 + 1.7 * k;
+  const auto small = [&](int64_t n) {
+    const auto of = [&](int bt, double t) {
+      const double tiles = (double)((n + 127) / 128) * (double)((M + bt - 1) / bt) / 768;
+      return (tiles < 0.6 ? 0.6 : tiles) * t;
+    };
+    const double mid = of(64, 2.4 + 1.0 * k), thin = of(32, 1.7 + 0.7 * k);
+    return thin < mid ? LogitPlan{0, 128, 32, thin} : LogitPlan{0, 128, 64, mid};
+  };
+  const int64_t across = (M + 255) / 256, all = (N + 255) / 256, rounds = all * across / 256;
+  const LogitPlan wide{N, 128, 64, (double)((all * across + 255) / 256) * round};
+  LogitPlan best = small(N);
+  if (wide.time < best.time) best = wide;
+  const int64_t cols = rounds * 256 / across;              // tile columns of whole rounds
+  if (cols > 0 && cols < all) {
+    LogitPlan part = small(N - cols * 256);
+    part.time += (double)((cols * across + 255) / 256) * round + 3.0;
+    part.wide = cols * 256;
+    if (part.time < best.time) best = part;
+  }
+  return best;
 }
 
 // Tokens of a launch, which bounds its workspace and grid (vocabulary rows are
@@ -1005,6 +1036,7 @@ struct BwdPlan {
   int ca, cb, tb_log;          // CT of dA's and dBt's tiles, and TB, as GradTile has them
   int64_t Mp, C;
   int pieces, tiles_k, sa, sb;
+  int KB;                      // 32-blocks of K, in pairs
   size_t code_a, code_b, t, plane_a, plane_b;   // bytes
   size_t bytes() const { return kBounds * sizeof(Bound) + code_a + code_b + t + plane_a + plane_b; }
 };
@@ -1038,7 +1070,7 @@ BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, int dtype) {
   BwdPlan b;
   b.terms = dtype == DT_BF16 ? 1 : 2;
   b.few = M <= 64;
-  b.cb = 256 / b.terms;
+  b.cb = b.few ? 128 : 256 / b.terms;
   b.ca = b.few ? 64 : b.cb;
   b.tb_log = b.few ? 1 : 4 - b.terms;
   b.Mp = b.few ? 64 : (M + 255) / 256 * 256;
@@ -1075,10 +1107,11 @@ BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, int dtype) {
         }
       }
   }
-  b.code_a = (size_t)b.Mp * b.tiles_k * 512;
-  b.code_b = (size_t)b.C * b.pieces * b.tiles_k * 512;
+  b.KB = up(K, 64) * 2;
+  b.code_a = (size_t)b.Mp * b.KB * 64;
+  b.code_b = (size_t)b.C * b.pieces * b.KB * 64;
   b.t = (size_t)b.Mp * b.C * 2 * b.terms;
-  b.plane_a = (size_t)b.Mp * b.tiles_k * 1024 * b.sa;
+  b.plane_a = b.sa > 1 || b.pieces > 1 ? (size_t)b.Mp * b.tiles_k * 1024 * b.sa : 0;
   b.plane_b = b.sb > 1 ? (size_t)b.C * b.tiles_k * 1024 * b.sb : 0;
   return b;
 }
@@ -1111,14 +1144,24 @@ hipError_t launch_head_fwd(const HeadArgs& whole, const int64_t* targets, float*
     a.M = whole.M - row < kFwdRows ? whole.M - row : kFwdRows;
     a.A += row * a.lda;
     a.s_row += row;
-    FwdArgs f{logit_args(a), up(a.N, pl.bv), up(a.M, pl.bt), static_cast<v2f*>(ws)};
-    const dim3 grid((unsigned)f.tiles_v * (unsigned)f.tiles_t);
-    if (pl.bt == 32) hipLaunchKernelGGL((head_fwd_kernel<128, 32, 4, 1, 3>), grid, dim3(256), 0, stream, f);
-    else if (pl.bt == 64) hipLaunchKernelGGL((head_fwd_kernel<128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, f);
-    else hipLaunchKernelGGL((head_fwd_kernel<256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, f);
+    FwdArgs f{logit_args(a), 0, up(pl.wide, 256), up(a.M, 256), static_cast<v2f*>(ws)};
+    if (f.tiles_v > 0)
+      hipLaunchKernelGGL((head_fwd_kernel<256, 256, 2, 4, 1>), dim3((unsigned)f.tiles_v * (unsigned)f.tiles_t), dim3(512), 0, stream, f);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    JoinArgs j{f.l, targets ? targets + row : nullptr, f.parts, f.tiles_v, logprob ? logprob + row : nullptr, lse ? lse + row : nullptr};
+    int n_parts = f.tiles_v;
+    if (pl.wide < a.N) {
+      f.v0 = (int)pl.wide;
+      f.parts += (size_t)n_parts * a.M;
+      f.tiles_v = up(a.N - pl.wide, pl.bv);
+      f.tiles_t = up(a.M, pl.bt);
+      n_parts += f.tiles_v;
+      const dim3 grid((unsigned)f.tiles_v * (unsigned)f.tiles_t);
+      if (pl.bt == 32) hipLaunchKernelGGL((head_fwd_kernel<128, 32, 4, 1, 3>), grid, dim3(256), 0, stream, f);
+      else hipLaunchKernelGGL((head_fwd_kernel<128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, f);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    JoinArgs j{f.l, targets ? targets + row : nullptr, static_cast<const v2f*>(ws), n_parts, logprob ? logprob + row : nullptr, lse ? lse + row : nullptr};
     if (a.M >= 1024) hipLaunchKernelGGL(head_join_kernel<16>, dim3((unsigned)up(a.M, 16)), dim3(256), 0, stream, j);
     else hipLaunchKernelGGL(head_join_kernel<1>, dim3((unsigned)a.M), dim3(256), 0, stream, j);
     if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -1142,7 +1185,7 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
   v4i* T = reinterpret_cast<v4i*>(at += b.code_b);
   float* plane_a = reinterpret_cast<float*>(at += b.t);
   float* plane_b = reinterpret_cast<float*>(at += b.plane_a);
-  const int KB = b.tiles_k * 8;
+  const int KB = b.KB;
   const int C16 = (int)(b.C / 16);
   const size_t plane = (size_t)b.Mp * b.C / 8;
   const LogitArgs l = logit_args(a);
@@ -1151,28 +1194,28 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
   hipLaunchKernelGGL(head_prepare_kernel, dim3(kBounds + (unsigned)(groups < kMostGroups ? groups : kMostGroups)), dim3(256), 0, stream, k);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  auto finish = [&](bool side_a, const GradArgs::Side& s, void* out, int64_t ld, int64_t n, const float* scale) {
-    const int ct = side_a ? b.ca : b.cb;
-    FinishArgs f{s.planes, bounds, s.splits, s.tiles, b.tiles_k, ct, side_a && b.few ? 8 : 2, out, ld, g.dtype, (int)n, (int)a.K, scale};
-    const int64_t n_groups = (int64_t)s.tiles * b.tiles_k * ct / 4;
-    hipLaunchKernelGGL(head_finish_kernel, dim3((unsigned)(n_groups < kMostGroups ? n_groups : kMostGroups)), dim3(256), 0, stream, f);
-    return hipGetLastError();
+  const auto finish_side = [&](bool a_side, const GradArgs::Side& s) {
+    return FinishArgs::Side{s.planes, s.splits, s.tiles, a_side ? b.ca : b.cb, a_side && b.few ? 8 : 2, s.out, s.ld, s.rows, s.scale};
   };
   for (int piece = 0; piece < b.pieces; ++piece) {
     const int64_t v0 = piece * b.C, rows = a.N - v0 < b.C ? a.N - v0 : b.C;
-    WeightArgs w{l, g.targets, g.lse, g.g_logprob, g.g_lse, (int)v0, 0, 0, C16, bounds, 0, b.tb_log, T, plane};
+    WeightArgs w{l, g.targets, g.lse, g.g_logprob, g.g_lse, (int)v0, 0, 0, 0, C16, bounds, 0, b.tb_log, T, plane};
     const LogitPlan pl = logit_plan(b.Mp, b.C, a.K);
-    const bool wide = pl.bt == 256 && !b.few;
-    w.tiles_v = (int)(b.C / (wide ? 256 : 128));
-    w.tiles_t = (int)(b.Mp / (wide ? 256 : 64));
-    for (w.first = 0; w.first < (int64_t)w.tiles_v * w.tiles_t; w.first += kMostGroups) {
-      const int64_t left = (int64_t)w.tiles_v * w.tiles_t - w.first;
-      const dim3 grid((unsigned)(left < kMostGroups ? left : kMostGroups));
-      if (wide && b.terms == 1) hipLaunchKernelGGL((head_weights_kernel<1, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
-      else if (wide) hipLaunchKernelGGL((head_weights_kernel<2, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
-      else if (b.terms == 1) hipLaunchKernelGGL((head_weights_kernel<1, 128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, w);
-      else hipLaunchKernelGGL((head_weights_kernel<2, 128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, w);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
+    const int64_t wide_cols = b.few ? 0 : pl.wide;         // (few tokens: T has 64)
+    for (const bool wide : {true, false}) {
+      w.c0 = wide ? 0 : (int)wide_cols;
+      w.v0 = (int)v0 + w.c0;
+      w.tiles_v = (int)(wide ? wide_cols / 256 : (b.C - wide_cols) / 128);
+      w.tiles_t = (int)(b.Mp / (wide ? 256 : 64));
+      for (w.first = 0; w.first < (int64_t)w.tiles_v * w.tiles_t; w.first += kMostGroups) {
+        const int64_t left = (int64_t)w.tiles_v * w.tiles_t - w.first;
+        const dim3 grid((unsigned)(left < kMostGroups ? left : kMostGroups));
+        if (wide && b.terms == 1) hipLaunchKernelGGL((head_weights_kernel<1, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
+        else if (wide) hipLaunchKernelGGL((head_weights_kernel<2, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
+        else if (b.terms == 1) hipLaunchKernelGGL((head_weights_kernel<1, 128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, w);
+        else hipLaunchKernelGGL((head_weights_kernel<2, 128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, w);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+      }
     }
 
     GradArgs p{};
@@ -1182,30 +1225,44 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
     p.C16 = C16;
     p.KB = KB;
     p.tiles_k = b.tiles_k;
-    auto side = [](const v4i* codes, int64_t tiles, int64_t depth, int splits, float* planes, int add) {
+    p.dtype = g.dtype;
+    p.cols = (int)a.K;
+    const auto side = [](const v4i* codes, int64_t tiles, int64_t depth, int splits, float* planes, int add, void* out, int64_t ld,
+                         int64_t n, const float* scale) {
       // (whole blocks of 256: a range has 8 stages at least; 64 tokens are 2)
       const int stages = (int)(depth / 32), per = stages < 8 ? stages : up(stages / 8, splits) * 8;
-      return GradArgs::Side{codes, (int)tiles, up(stages, per), stages, per, planes, add};
+      return GradArgs::Side{codes, (int)tiles, up(stages, per), stages, per, planes, add, out, ld, (int)n, scale};
     };
-    p.a = side(code_b + (size_t)piece * (b.C / 16) * KB * 64, b.Mp / b.ca, b.C, b.sa, plane_a, piece > 0);
-    p.b = side(code_a, up(rows, b.cb), b.Mp, b.sb, b.sb > 1 ? plane_b : nullptr, 0);
+    const int64_t esize = g.dtype == DT_F32 ? 4 : 2;
+    p.a = side(code_b + (size_t)piece * (b.C / 16) * KB * 64, b.Mp / b.ca, b.C, b.sa, b.plane_a > 0 ? plane_a : nullptr, piece > 0, g.dA,
+               g.ldda, a.M, a.s_row);
+    p.b = side(code_a, up(rows, b.cb), b.Mp, b.sb, b.sb > 1 ? plane_b : nullptr, 0,
+               g.dB ? static_cast<char*>(g.dB) + v0 * g.lddb * esize : nullptr, g.lddb, rows, a.s_col + v0);
     p.units_a = g.dA ? p.tiles_k * p.a.tiles * p.a.splits : 0;
     p.units_b = g.dB ? p.tiles_k * p.b.tiles * p.b.splits : 0;
-    const int64_t esize = g.dtype == DT_F32 ? 4 : 2;
-    p.out = g.dB ? static_cast<char*>(g.dB) + v0 * g.lddb * esize : nullptr;
-    p.ld = g.lddb;
-    p.dtype = g.dtype;
-    p.rows = (int)rows;
-    p.cols = (int)a.K;
-    p.scale = a.s_col + v0;
     const int most = up(p.units_a, 8) + up(p.units_b, 8);    // of an XCD
     for (p.first = 0; p.first < most; p.first += kMostGroups / 8) {
       const unsigned n = 8u * (unsigned)(most - p.first < kMostGroups / 8 ? most - p.first : kMostGroups / 8);
       launch_grads(b, (int)a.K, n, stream, p);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    if (g.dB && p.b.planes && (e = finish(false, p.b, p.out, g.lddb, rows, p.scale)) != hipSuccess) return e;
-    if (g.dA && piece + 1 == b.pieces && (e = finish(true, p.a, g.dA, g.ldda, a.M, a.s_row)) != hipSuccess) return e;
+    FinishArgs f{};
+    f.bounds = bounds;
+    f.tiles_k = b.tiles_k;
+    f.dtype = g.dtype;
+    f.cols = (int)a.K;
+    int64_t finish_groups[2] = {0, 0};
+    int n = 0;
+    const auto take = [&](bool a_side, const GradArgs::Side& s) {
+      f.side[n] = finish_side(a_side, s);
+      const int64_t all = (int64_t)s.tiles * b.tiles_k * (a_side ? b.ca : b.cb) / 4;
+      finish_groups[n++] = all < kMostGroups ? all : kMostGroups;
+    };
+    if (g.dA && p.a.planes && piece + 1 == b.pieces) take(true, p.a);
+    if (g.dB && p.b.planes) take(false, p.b);
+    f.groups = finish_groups[0];
+    if (n > 0) hipLaunchKernelGGL(head_finish_kernel, dim3((unsigned)(finish_groups[0] + finish_groups[1])), dim3(256), 0, stream, f);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;
 }
