@@ -113,6 +113,8 @@ struct FillArgs {              // the rows of dW before the sums: zeros, or thos
   int64_t lddw, vocab, cols;
   const float* add;            // null: zeros
   int64_t ldadd;
+  int lanes_log;
+  int64_t first, end;          // rows of the launch
   int blocks;                  // workgroups that fill; 0 where dW is `add`
 };
 struct SortArgs {
@@ -124,24 +126,34 @@ struct SortArgs {
   uint32_t* listed;            // zeroed for the sums
 };
 
-__device__ __forceinline__ void fill_rows(const FillArgs& p, int block) {
-  // whole rows a wave; 4 vectors of 4 values a lane in flight
-  const int lane = threadIdx.x & 63, wave = block * kSortWaves + (threadIdx.x >> 6), waves = p.blocks * kSortWaves;
+// Rows v0 ... of a wave, as many as 64 lanes hold at 4 columns each (all lanes one
+// row of 256 columns or more): lane l has row v0 + (l >> lanes_log).
+int lanes_log(int64_t cols) {
+  int n = 0;
+  while (n < 6 && (int64_t(4) << n) < cols) ++n;
+  return n;
+}
+__device__ __forceinline__ void fill_row(const FillArgs& p, int64_t v) {
+  const int in = threadIdx.x & ((1 << p.lanes_log) - 1), step = 4 << p.lanes_log;
   const int cols = (int)p.cols;
-  for (int64_t v = wave; v < p.vocab; v += waves) {
-    float* to = p.dW + v * p.lddw;
-    const float* from = p.add ? p.add + v * p.ldadd : nullptr;
-    for (int c = lane * 4; c < cols; c += 256) {
-      float x[4] = {};
-      if (from) load_row<float, 4>(from, c, cols, 0.0f, x);
-      stream_row<float>(to, c, cols, x);
-    }
+  float* to = p.dW + v * p.lddw;
+  const float* from = p.add ? p.add + v * p.ldadd : nullptr;
+  for (int c = in * 4; c < cols; c += step) {
+    float x[4] = {};
+    if (from) load_row<float, 4>(from, c, cols, 0.0f, x);
+    stream_row<float>(to, c, cols, x);
   }
+}
+template <int WAVES>
+__device__ __forceinline__ void fill_rows(const FillArgs& p, int block) {
+  const int rows = 64 >> p.lanes_log, lane_row = (threadIdx.x & 63) >> p.lanes_log;
+  const int64_t wave = block * WAVES + (threadIdx.x >> 6), waves = p.blocks * WAVES;
+  for (int64_t v = p.first + wave * rows + lane_row; v < p.end; v += waves * rows) fill_row(p, v);
 }
 
 __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const SortArgs p, const FillArgs fill) {
   if ((int)blockIdx.x >= p.runs) {
-    fill_rows(fill, (int)blockIdx.x - p.runs);
+    fill_rows<kSortWaves>(fill, (int)blockIdx.x - p.runs);
     return;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.listed = 0;
@@ -227,8 +239,13 @@ struct MergeArgs {
   const uint32_t *keys, *order;
   uint32_t *keys_out, *order_out;
   int64_t rows, run;
+  int64_t groups;              // workgroups that merge; those behind fill
 };
-__global__ void __launch_bounds__(256) embedding_merge_kernel(const MergeArgs p) {
+__global__ void __launch_bounds__(256) embedding_merge_kernel(const MergeArgs p, const FillArgs fill) {
+  if (blockIdx.x >= p.groups) {
+    fill_rows<4>(fill, (int)(blockIdx.x - p.groups));
+    return;
+  }
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= p.rows) return;
   const uint32_t k = p.keys[i];
@@ -253,6 +270,109 @@ __global__ void __launch_bounds__(256) embedding_merge_kernel(const MergeArgs p)
   for (int r = 0; r < kMerge; ++r) place += before[r];
   p.keys_out[place] = k;
   p.order_out[place] = p.order[i];
+}
+
+// ---- at most 1024 rows: one launch ---------------------------------------------------
+// Every wave holds all tokens, WORDS a lane.  A workgroup a row and 256 columns:
+// if no earlier row has its token, it adds all that have, each wave those of every
+// fourth 64 rows, the waves' sums in their order.  The workgroups behind fill the
+// rows of the table that no token names.  (88 x 159 onto 720 rows 7.4 us, 701 x 76
+// onto 31438 15.2, 782 x 715 onto 115 18.4, where sorting, adding and joining in
+// three launches take 16.5, 19.5 and 18.6.)
+constexpr int kFewWords = 16, kFew = kFewWords * 64;
+struct FewArgs {
+  const void* dY;
+  int64_t rows, cols, lddy;
+  const int64_t* tokens;
+  double alpha;
+  int chunks;                  // of 256 columns
+  int64_t sums;                // workgroups that add
+  FillArgs fill;
+};
+template <class T, int WORDS>
+__global__ void __launch_bounds__(256) embedding_few_kernel(const FewArgs p) {
+  constexpr int N = 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cols = (int)p.cols;
+  int t[WORDS];                                  // (at most 2^31 - 1; -1: no token)
+#pragma unroll
+  for (int w = 0; w < WORDS; ++w) {
+    const int64_t x = p.tokens[min(w * 64 + lane, (int)p.rows - 1)];
+    t[w] = w * 64 + lane < (int)p.rows && x >= 0 && x < p.fill.vocab ? (int)x : -1;
+  }
+  if (blockIdx.x >= p.sums) {
+    const FillArgs& f = p.fill;
+    const int rows = 64 >> f.lanes_log, lane_row = lane >> f.lanes_log;
+    const int64_t waves = (int64_t)(gridDim.x - p.sums) * 4;
+    for (int64_t v0 = ((int64_t)(blockIdx.x - p.sums) * 4 + wave) * rows; v0 < f.vocab; v0 += waves * rows) {
+      uint64_t named = 0;                        // of the wave's rows
+      for (int r = 0; r < rows; ++r) {
+        bool here = false;
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) here = here || t[w] == (int)(v0 + r);
+        if (__builtin_amdgcn_ballot_w64(here) != 0) named |= 1ull << r;
+      }
+      if (v0 + lane_row < f.vocab && ((named >> lane_row) & 1) == 0) fill_row(f, v0 + lane_row);
+    }
+    return;
+  }
+  const int row = (int)(p.chunks == 1 ? blockIdx.x : blockIdx.x / p.chunks);
+  const int c = (int)(blockIdx.x - (int64_t)row * p.chunks) * 64 * N + lane * N;
+  const int64_t token = uniform64(p.tokens[row]);
+  if (token < 0 || token >= p.fill.vocab) return;
+  bool earlier = false;
+  uint64_t has[WORDS];
+#pragma unroll
+  for (int w = 0; w < WORDS; ++w) {
+    has[w] = __builtin_amdgcn_ballot_w64(t[w] == (int)token);
+    if (w < (row >> 6)) earlier = earlier || has[w] != 0;
+    if (w == (row >> 6)) earlier = earlier || (has[w] & ((1ull << (row & 63)) - 1)) != 0;
+  }
+  if (earlier) return;
+  double s[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) s[e] = 0.0;
+#pragma unroll
+  for (int w = 0; w < WORDS; w += 4) {
+    uint64_t mine = wave == 0 ? has[w] : wave == 1 ? has[w + 1] : wave == 2 ? has[w + 2] : has[w + 3];
+    const T* dy = static_cast<const T*>(p.dY) + (int64_t)((w + wave) * 64) * p.lddy;
+    while (mine != 0) {
+      RawRow<T, N> x[8];
+      uint64_t left = mine;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = __builtin_ctzll(left != 0 ? left : mine);
+        left &= left - 1;
+        x[i].load(dy + at * p.lddy, c, cols);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (mine != 0) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) s[e] += (double)x[i][e];
+          mine &= mine - 1;
+        }
+    }
+  }
+  __shared__ double sum[4][64][N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) sum[wave][lane][e] = s[e];
+  __syncthreads();
+  if (wave != 0 || c >= cols) return;
+  float y[N], old[N];
+  if (p.fill.add) load_row<float, N>(p.fill.add + token * p.fill.ldadd, c, cols, 0.0f, old);
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const double all = p.alpha * (((sum[0][lane][e] + sum[1][lane][e]) + sum[2][lane][e]) + sum[3][lane][e]);
+    y[e] = (float)(p.fill.add ? (double)old[e] + all : all);
+  }
+  store_row<float, N>(p.fill.dW + token * p.fill.lddw, c, cols, y);
+}
+template <int WORDS>
+void launch_few(int dtype, dim3 grid, hipStream_t stream, const FewArgs& a) {
+  if (dtype == DT_F32) hipLaunchKernelGGL((embedding_few_kernel<float, WORDS>), grid, dim3(256), 0, stream, a);
+  else if (dtype == DT_BF16) hipLaunchKernelGGL((embedding_few_kernel<bf16_t, WORDS>), grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((embedding_few_kernel<f16_t, WORDS>), grid, dim3(256), 0, stream, a);
 }
 
 // ---- the sums -----------------------------------------------------------------------
@@ -477,25 +597,47 @@ BwdLayout bwd_layout(int64_t rows, int64_t cols) {
 size_t embedding_bwd_bytes(int64_t rows, int64_t cols) { return bwd_layout(rows, cols).bytes; }
 
 hipError_t launch_embedding_bwd(const EmbedBwdArgs& a, int dtype, void* ws, hipStream_t stream) {
+  const bool in_place = a.add == a.dW;
+  const int lanes = lanes_log(a.cols);
+  const auto fill = [&](int64_t first, int64_t end, int waves) {
+    const int64_t blocks = in_place ? 0 : up64(end - first, (int64_t)waves * (64 >> lanes));
+    const int64_t most = 16384 / waves;                    // 4 workgroups of 16 waves for each of the 256 CUs
+    return FillArgs{a.dW, a.lddw, a.vocab, a.cols, a.add, a.ldadd, lanes, first, end, (int)(blocks < most ? blocks : most)};
+  };
+  const int64_t chunks = up64(a.cols, 256);
+  if (a.rows > 0 && a.rows <= kFew && a.rows * chunks <= (1 << 22)) {
+    FewArgs w{a.dY, a.rows, a.cols, a.lddy, a.tokens, (double)a.alpha, (int)chunks, a.rows * chunks, fill(0, a.vocab, 4)};
+    const dim3 grid((unsigned)(w.sums + w.fill.blocks));
+    if (a.rows <= 256) launch_few<4>(dtype, grid, stream, w);
+    else launch_few<kFewWords>(dtype, grid, stream, w);
+    return hipGetLastError();
+  }
   char* at = static_cast<char*>(ws);
   const BwdLayout lay = bwd_layout(a.rows, a.cols);
   const size_t list = lay.list;
   uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(at), reinterpret_cast<uint32_t*>(at + 2 * list)};
   uint32_t* order[2] = {reinterpret_cast<uint32_t*>(at + list), reinterpret_cast<uint32_t*>(at + 3 * list)};
   uint32_t* listed = reinterpret_cast<uint32_t*>(at + lay.joined);
-  const bool in_place = a.add == a.dW;
   SortArgs s{a.tokens, a.rows, a.vocab, 0, keys[0], order[0], (int)up64(a.rows, kRun), listed};
   while ((a.vocab >> s.bits) != 0) ++s.bits;              // vocab itself is a key
   if (s.bits == 0) s.bits = 1;
-  // 1024 workgroups fill: 4 for each of the 256 CUs
-  FillArgs f{a.dW, a.lddw, a.vocab, a.cols, a.add, a.ldadd, in_place ? 0 : (int)(up64(a.vocab, kSortWaves) < 1024 ? up64(a.vocab, kSortWaves) : 1024)};
+  // The rows are filled beside the sorting and the merging, which leave most of
+  // the chip free: a merge takes as long as about a fifth of a fill of 150 MB.
+  int n_merges = (int)merges(a.rows);
+  if (n_merges > 2) n_merges = 2;
+  const int64_t later = in_place ? 0 : a.vocab / 5 * n_merges;
+  FillArgs f = fill(0, a.vocab - later, kSortWaves);
   if (s.runs + f.blocks > 0) hipLaunchKernelGGL(embedding_sort_kernel, dim3((unsigned)(s.runs + f.blocks)), dim3(kSortThreads), 0, stream, s, f);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.rows == 0) return e;
   int from = 0;
+  int64_t filled = a.vocab - later;
   for (int64_t run = kRun; run < a.rows; run *= kMerge, from ^= 1) {
-    MergeArgs m{keys[from], order[from], keys[from ^ 1], order[from ^ 1], a.rows, run};
-    hipLaunchKernelGGL(embedding_merge_kernel, dim3((unsigned)up64(a.rows, 256)), dim3(256), 0, stream, m);
+    MergeArgs m{keys[from], order[from], keys[from ^ 1], order[from ^ 1], a.rows, run, up64(a.rows, 256)};
+    const int64_t to = run * kMerge >= a.rows ? a.vocab : filled + a.vocab / 5 < a.vocab ? filled + a.vocab / 5 : a.vocab;
+    f = fill(filled, to, 4);
+    filled = to;
+    hipLaunchKernelGGL(embedding_merge_kernel, dim3((unsigned)(m.groups + f.blocks)), dim3(256), 0, stream, m, f);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   const int64_t piece = piece_of(a.rows, a.cols);
