@@ -503,7 +503,7 @@ static int bad_head(const int8_t* QA, int64_t lda, const float* s_row, const int
 
 size_t gemm_i8_logprobs_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || M > I8G_HEAD_ROWS_MAX || N <= 0 || N > I8G_VOCAB_MAX || K < 0) return 256;
-  return head_fwd_bytes(M, N);
+  return head_fwd_bytes(M, N, K);
 }
 
 int gemm_i8_logprobs(const int8_t* QA, int64_t lda, const float* s_row, const int8_t* QBt, int64_t ldb, const float* s_col,
@@ -512,7 +512,7 @@ int gemm_i8_logprobs(const int8_t* QA, int64_t lda, const float* s_row, const in
   if (const int bad = bad_head(QA, lda, s_row, QBt, ldb, s_col, M, N, K)) return bad;
   if (bad_i64(targets) || bad_f32(logprob) || bad_f32(lse) || (M > 0 && logprob && !targets)) return I8G_EINVAL;
   if (M == 0 || (!logprob && !lse)) return I8G_OK;
-  if (!workspace || (uintptr_t)workspace % 256 != 0 || workspace_bytes < head_fwd_bytes(M, N)) return I8G_EWORKSPACE;
+  if (!workspace || (uintptr_t)workspace % 256 != 0 || workspace_bytes < head_fwd_bytes(M, N, K)) return I8G_EWORKSPACE;
   return hip_status(launch_head_fwd(HeadArgs{QA, QBt, s_row, s_col, lda, ldb, M, N, K}, targets, logprob, lse, workspace,
                                     as_stream(stream)));
 }

@@ -83,6 +83,12 @@ __device__ __forceinline__ void lds_load16(const char* base, int offset, const i
                : "s"(lds_address(lds)), "v"(offset), "s"(base)
                : "memory");
 }
+__device__ __forceinline__ void lds_load4(const void* g, const void* lds) {     // 4 bytes a lane to lds + 4 * lane
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(lds_address(static_cast<const int8_t*>(lds))), "v"(g)
+               : "memory");
+}
 // Asks for the READS fragment reads of the next k-step between this one's
 // MFMAs, one by one.
 template <int READS, int MFMAS>
@@ -94,11 +100,6 @@ __device__ __forceinline__ void interleave() {
   }
   if constexpr (READS < MFMAS) __builtin_amdgcn_sched_group_barrier(0x008, MFMAS - READS, 0);
   __builtin_amdgcn_sched_barrier(0);
-}
-// Undoes the dealing of workgroups to the 8 XCDs: consecutive results share an L2.
-__device__ __forceinline__ int xcd_order(int wg, int total) {
-  const int xcd = wg & 7, per = total >> 3, rem = total & 7;
-  return xcd * per + (xcd < rem ? xcd : rem) + (wg >> 3);
 }
 __device__ __forceinline__ float other_half(float x) {   // the value of lane ^ 32
   const Pair32 p = lane_pair<32>(__float_as_uint(x));
@@ -124,12 +125,51 @@ struct LogitTile {
   static constexpr int INS = (BV + BT) / (8 * NW), INS_V = BV / (8 * NW);
   static_assert(INS * 8 * NW == BV + BT && INS_V * 8 * NW == BV && NW % 2 == 0, "whole loads");
   static constexpr int LDS = 2 * STAGE;
+  static constexpr int TOKENS = BT < 64 ? 64 : BT;         // values of a token in LDS: whole waves' loads
 
-  static __device__ __forceinline__ void multiply(const LogitArgs& p, int8_t* smem, int v0, int t0,
+  // Where a lane's loads of a tile begin: rows (q * NW + wave) * 8 + lane / 8; NW
+  // is even, so (row / 2) % 8 does not depend on q.
+  struct Source {
+    const int8_t* at[INS];
+  };
+  static __device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+  static __device__ __forceinline__ void issue(const LogitArgs& p, int8_t* smem, const Source& src, int kt) {
+    const int lane = threadIdx.x & 63, wave = wave_of();
+    const int chunk = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
+    int8_t* base = smem + (kt & 1) * STAGE + wave * 1024;
+    const int at = min(kt * 128 + chunk * 16, ((p.K + 15) & ~15) - 16);   // (what lies beyond K is cleared below)
+#pragma unroll
+    for (int q = 0; q < INS; ++q) lds_load16(src.at[q] + at, base + q * NW * 1024);
+  }
+  // n values of 4 bytes from `first` on into LDS, the last of `all` again behind them.
+  template <int n>
+  static __device__ __forceinline__ void load_values(const void* from, int64_t first, int64_t all, void* lds) {
+    const int lane = threadIdx.x & 63;
+    for (int i = wave_of(); i < n / 64; i += NW) {
+      const int64_t at = first + i * 64 + lane;
+      lds_load4(static_cast<const float*>(from) + (at < all ? at : all - 1), static_cast<float*>(lds) + i * 64);
+    }
+  }
+  // The first two stages of a tile, into LDS that no wave reads any more.
+  static __device__ __forceinline__ void start(const LogitArgs& p, int8_t* smem, int v0, int t0, Source& src) {
+    const int lane = threadIdx.x & 63, wave = wave_of();
+#pragma unroll
+    for (int q = 0; q < INS; ++q) {
+      const int r = (q * NW + wave) * 8 + (lane >> 3);
+      if (q < INS_V) src.at[q] = p.B + (int64_t)min(v0 + r, p.N - 1) * p.ldb;
+      else src.at[q] = p.A + (int64_t)min(t0 + r - BV, p.M - 1) * p.lda;
+    }
+    if (p.K > 0) issue(p, smem, src, 0);
+    if (p.K > 128) issue(p, smem, src, 1);
+  }
+
+  // What this wave asked for up to start() is waited for here, but not the BEHIND vector stores
+  // that this wave has issued after it where `behind` says so.
+  template <int BEHIND>
+  static __device__ __forceinline__ void multiply(const LogitArgs& p, int8_t* smem, const Source& src, bool behind,
                                                   v16i (&acc)[FV][FT]) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_of();
     const int wv = wave / WT, wt = wave % WT;
-    const int k16 = (p.K + 15) & ~15;
     const int n = (p.K + 127) / 128;
 #pragma unroll
     for (int i = 0; i < FV; ++i)
@@ -137,28 +177,11 @@ struct LogitTile {
       for (int j = 0; j < FT; ++j)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
-    if (n == 0) return;
-
-    // rows (q * NW + wave) * 8 + lane / 8; NW is even, so (row / 2) % 8 does not depend on q
-    const int chunk = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
-    const int8_t* src[INS];
-#pragma unroll
-    for (int q = 0; q < INS; ++q) {
-      const int r = (q * NW + wave) * 8 + (lane >> 3);
-      if (q < INS_V) {
-        const int v = min(v0 + r, p.N - 1);
-        src[q] = p.B + (int64_t)v * p.ldb;
-      } else {
-        const int t = min(t0 + r - BV, p.M - 1);
-        src[q] = p.A + (int64_t)t * p.lda;
-      }
+    if (n == 0) {
+      wait_loads<0>();
+      barrier_nofence();
+      return;
     }
-    auto issue = [&](int kt) {
-      int8_t* base = smem + (kt & 1) * STAGE + wave * 1024;
-      const int at = min(kt * 128 + chunk * 16, k16 - 16);   // (what lies beyond K is cleared below)
-#pragma unroll
-      for (int q = 0; q < INS; ++q) lds_load16(src[q] + at, base + q * NW * 1024);
-    };
     // The last stage's bytes beyond K: cleared in the tokens' rows, which makes
     // those products 0 whatever the other operand's bytes are.
     auto clear_tail = [&](int kt) {
@@ -210,13 +233,9 @@ struct LogitTile {
           acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fv[i], ft[j], acc[i][j], 0, 0, 0);
     };
     v4i fv0[FV], ft0[FT], fv1[FV], ft1[FT];
-    issue(0);
-    if (n > 1) {
-      issue(1);
-      wait_loads<INS>();
-    } else {
-      wait_loads<0>();
-    }
+    if (n == 1) wait_loads<0>();
+    else if (BEHIND > 0 && behind) wait_loads<INS + BEHIND>();
+    else wait_loads<INS>();
     barrier_nofence();
     if (n == 1) clear_tail(0);
     read(0, 0, fv0, ft0);
@@ -236,7 +255,7 @@ struct LogitTile {
       // registers: its buffer is free
       wait_loads<0>();
       barrier_nofence();
-      if (kt + 2 < n) issue(kt + 2);
+      if (kt + 2 < n) issue(p, smem, src, kt + 2);
       else clear_tail(kt + 1);
       read(kt + 1, 0, fv0, ft0);
       mfma(fv1, ft1);
@@ -263,6 +282,21 @@ struct FwdArgs {
   v2f* parts;                  // [tiles_v][M]: the maximum, and the sum of exp(x - maximum)
 };
 
+// The tiles of a workgroup: an XCD (workgroups are dealt to the 8 in turn) takes
+// an eighth of the tiles, neighbours in their order, its workgroups every so
+// many.  Where a workgroup has several, the next one's first loads are on their
+// way while this one's logits are worked on (8192 x 50304 x 768: 377 us, and 385
+// with a workgroup a tile; with T in place of the sums 440 and 465).
+struct Walk {
+  int at, end, step;
+  __device__ Walk(int first, int total, int tiles) {       // tiles first ... first + total - 1 of `tiles`
+    const int xcd = blockIdx.x & 7;
+    const int n = min(total, tiles - first);
+    at = first + (int)((int64_t)n * xcd / 8) + (int)(blockIdx.x >> 3);
+    end = first + (int)((int64_t)n * (xcd + 1) / 8);
+    step = (int)(gridDim.x >> 3);
+  }
+};
 // Tiles of tokens that share a vocabulary tile in an L2 before the next one.
 constexpr int kGroupT = 8;
 __device__ __forceinline__ void tile_of(int w, int tiles_v, int tiles_t, int& tv, int& tt) {
@@ -277,74 +311,91 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_fwd_k
   using Tile = LogitTile<BV, BT, WV, WT>;
   constexpr int FV = Tile::FV, FT = Tile::FT;
   __shared__ __attribute__((aligned(1024))) int8_t smem[Tile::LDS];
-  __shared__ __attribute__((aligned(16))) float sc[BV];
+  __shared__ __attribute__((aligned(16))) float sc[2][BV], rows[2][Tile::TOKENS];
   __shared__ v2f part[WV][BT];
-  int tv, tt;
-  tile_of(xcd_order(blockIdx.x, gridDim.x), p.tiles_v, p.tiles_t, tv, tt);
-  const int v0 = p.v0 + tv * BV, t0 = tt * BT;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wv = wave / WT, wt = wave % WT;
-  for (int i = tid; i < BV; i += Tile::NT) sc[i] = p.l.s_col[min(v0 + i, p.l.N - 1)];
-  float sr[FT];
+  Walk walk(0, p.tiles_v * p.tiles_t, p.tiles_v * p.tiles_t);
+  if (walk.at >= walk.end) return;
+  int tv, tt;
+  tile_of(walk.at, p.tiles_v, p.tiles_t, tv, tt);
+  typename Tile::Source src;
+  const auto start = [&](int turn) {
+    Tile::template load_values<BV>(p.l.s_col, p.v0 + tv * BV, p.l.N, sc[turn]);
+    Tile::template load_values<Tile::TOKENS>(p.l.s_row, tt * BT, p.l.M, rows[turn]);
+    Tile::start(p.l, smem, p.v0 + tv * BV, tt * BT, src);
+  };
+  start(0);
+  for (int turn = 0;; turn ^= 1) {
+    const int v0 = p.v0 + tv * BV, t0 = tt * BT, tile_v = tv;
+    v16i acc[FV][FT];
+    Tile::template multiply<0>(p.l, smem, src, false, acc);
+    walk.at += walk.step;
+    const bool more = walk.at < walk.end;
+    if (more) {
+      barrier_nofence();                                   // every wave has read this tile's last fragments
+      tile_of(walk.at, p.tiles_v, p.tiles_t, tv, tt);
+      start(turn ^ 1);
+    }
+    const float* scale = sc[turn];
+    const int half = lane >> 5;
+    const bool ragged = v0 + BV > p.l.N;
 #pragma unroll
-  for (int j = 0; j < FT; ++j) sr[j] = p.l.s_row[min(t0 + (wt * FT + j) * 32 + (lane & 31), p.l.M - 1)];
-  v16i acc[FV][FT];
-  Tile::multiply(p.l, smem, v0, t0, acc);
-  if (p.l.K == 0) __syncthreads();
-  const int half = lane >> 5;
-  const bool ragged = v0 + BV > p.l.N;
+    for (int j = 0; j < FT; ++j) {
+      const float sr = rows[turn][(wt * FT + j) * 32 + (lane & 31)];
+      float x[FV][16];
+      float m = kLowest;
 #pragma unroll
-  for (int j = 0; j < FT; ++j) {
-    float x[FV][16];
-    float m = kLowest;
+      for (int i = 0; i < FV; ++i)
 #pragma unroll
-    for (int i = 0; i < FV; ++i)
+        for (int q = 0; q < 4; ++q) {
+          const int r = (wv * FV + i) * 32 + 8 * q + 4 * half;
+          const v4f s4 = *reinterpret_cast<const v4f*>(scale + r);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int r = (wv * FV + i) * 32 + 8 * q + 4 * half;
-        const v4f s4 = *reinterpret_cast<const v4f*>(sc + r);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float y = epilogue1(acc[i][j][4 * q + e], sr[j], s4[e]);
-          if (ragged && v0 + r + e >= p.l.N) y = -__builtin_inff();
-          x[i][4 * q + e] = y;
-          m = fmaxf(m, y);
+          for (int e = 0; e < 4; ++e) {
+            float y = epilogue1(acc[i][j][4 * q + e], sr, s4[e]);
+            if (ragged && v0 + r + e >= p.l.N) y = -__builtin_inff();
+            x[i][4 * q + e] = y;
+            m = fmaxf(m, y);
+          }
         }
+      m = fmaxf(m, other_half(m));
+      // exp(x - m) as 2^(x c - m2), c = log2 e and m2 = RN(m c): one fused step,
+      // and one factor for m2's rounding; where that rounding may be more than a
+      // factor of two, the difference by itself (in these lanes only: a row's
+      // bits do not depend on another's)
+      const float m2 = m * kLog2e;
+      const bool far = !(fabsf(m2) < 16777216.0f);
+      float s = 0.0f;
+      if (__builtin_amdgcn_ballot_w64(far) == 0) {
+#pragma unroll
+        for (int i = 0; i < FV; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i][e], kLog2e, -m2));
+      } else {
+#pragma unroll
+        for (int i = 0; i < FV; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            s += __builtin_amdgcn_exp2f(far ? (x[i][e] - m) * kLog2e : __builtin_fmaf(x[i][e], kLog2e, -m2));
       }
-    m = fmaxf(m, other_half(m));
-    // exp(x - m) as 2^(x c - m2), c = log2 e and m2 = RN(m c): one fused step,
-    // and one factor for m2's rounding; where that rounding may be more than a
-    // factor of two, the difference by itself (in these lanes only: a row's
-    // bits do not depend on another's)
-    const float m2 = m * kLog2e;
-    const bool far = !(fabsf(m2) < 16777216.0f);
-    float s = 0.0f;
-    if (__builtin_amdgcn_ballot_w64(far) == 0) {
-#pragma unroll
-      for (int i = 0; i < FV; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i][e], kLog2e, -m2));
-    } else {
-#pragma unroll
-      for (int i = 0; i < FV; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          s += __builtin_amdgcn_exp2f(far ? (x[i][e] - m) * kLog2e : __builtin_fmaf(x[i][e], kLog2e, -m2));
+      if (!far) s *= __builtin_amdgcn_exp2f(-__builtin_fmaf(m, kLog2e, -m2));
+      s += other_half(s);
+      if (half == 0) part[wv][(wt * FT + j) * 32 + lane] = v2f{m, s};
     }
-    if (!far) s *= __builtin_amdgcn_exp2f(-__builtin_fmaf(m, kLog2e, -m2));
-    s += other_half(s);
-    if (half == 0) part[wv][(wt * FT + j) * 32 + lane] = v2f{m, s};
-  }
-  __syncthreads();
-  if (tid < BT && t0 + tid < p.l.M) {
-    v2f a = part[0][tid];
+    __builtin_amdgcn_s_waitcnt(0xC07F);                      // lgkmcnt(0)
+    barrier_nofence();
+    if (tid < BT && t0 + tid < p.l.M) {
+      v2f a = part[0][tid];
 #pragma unroll
-    for (int w = 1; w < WV; ++w) {
-      const v2f b = part[w][tid];
-      const float m = fmaxf(a.x, b.x);
-      a.y = a.y * __builtin_amdgcn_exp2f((a.x - m) * kLog2e) + b.y * __builtin_amdgcn_exp2f((b.x - m) * kLog2e);
-      a.x = m;
+      for (int w = 1; w < WV; ++w) {
+        const v2f b = part[w][tid];
+        const float m = fmaxf(a.x, b.x);
+        a.y = a.y * __builtin_amdgcn_exp2f((a.x - m) * kLog2e) + b.y * __builtin_amdgcn_exp2f((b.x - m) * kLog2e);
+        a.x = m;
+      }
+      p.parts[(size_t)tile_v * p.l.M + t0 + tid] = a;
     }
-    p.parts[(size_t)tv * p.l.M + t0 + tid] = a;
+    if (!more) return;
   }
 }
 
@@ -394,7 +445,10 @@ __global__ void __launch_bounds__(256) head_join_kernel(const JoinArgs p) {
     __syncthreads();
   }
   if (slot == 0) {
-    const float lse = (float)((double)m + log(sum[0][r]));
+    // the largest logit's share is 1: roundings below it would put a logprob above 0
+    // (a sum of 0: every logit is -inf)
+    const double all = sum[0][r];
+    const float lse = (float)((double)m + log(all > 0.0 && all < 1.0 ? 1.0 : all));
     out[r] = lse;
     if (row < p.l.M && p.lse) p.lse[row] = lse;
   }
@@ -522,7 +576,8 @@ struct WeightArgs {            // T of a piece
   int tiles_v, tiles_t;        // of the piece
   int C16;                     // blocks of 16 vocabulary rows in a row of blocks
   const Bound* bounds;
-  int64_t first;               // tile of the launch
+  int64_t first;               // tiles of the launch
+  int count;
   int tb_log;                  // TB = 2^tb_log blocks of 32 tokens in a tile of dA's product
   v4i* T;                      // [tokens / (32 TB)][C16][TB][64]: the blocks that a stage of dA reads are in a row
   size_t plane;                // from the first to the second f16 of a value (v4i), TERMS 2
@@ -533,104 +588,129 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
   using Tile = LogitTile<BV, BT, WV, WT>;
   constexpr int FV = Tile::FV, FT = Tile::FT;
   __shared__ __attribute__((aligned(1024))) int8_t smem[Tile::LDS];
-  __shared__ __attribute__((aligned(16))) float sc[BV];
-  int tv, tt;
-  tile_of((int)p.first + xcd_order(blockIdx.x, gridDim.x), p.tiles_v, p.tiles_t, tv, tt);
-  const int v0 = p.v0 + tv * BV, t0 = tt * BT;
+  constexpr int TOKENS = Tile::TOKENS;
+  __shared__ __attribute__((aligned(16))) float sc[2][BV];
+  __shared__ float rows[2][4][TOKENS];                     // s_row, the log-sum-exp, g, gl
+  __shared__ int64_t targets[2][TOKENS];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wv = wave / WT, wt = wave % WT;
-  const float scale = t_scale(p.bounds);
-  for (int i = tid; i < BV; i += Tile::NT) sc[i] = p.l.s_col[min(v0 + i, p.l.N - 1)];
-  float sr[FT], lse2[FT], share[FT], given[FT];
-  int target[FT];              // in this tile, or far outside
-#pragma unroll
-  for (int j = 0; j < FT; ++j) {
-    const int t = t0 + (wt * FT + j) * 32 + (lane & 31);
-    sr[j] = share[j] = given[j] = 0.0f;
-    lse2[j] = 3e38f;           // p = 0
-    target[j] = -1024;
-    if (t < p.l.M) {
-      sr[j] = p.l.s_row[t];
-      const float lse = p.lse[t];
-      int64_t at = -1;
-      float g = 0.0f;
-      if (p.g) {
-        at = p.targets[t];
-        if (at < 0 || at >= p.l.N) at = -1;
-        else g = p.g[t];
-      }
-      // a row whose log-sum-exp is off by a factor e or more in p has no gradient
-      if (!(fabsf(lse) >= 16777216.0f)) {
-        lse2[j] = lse * kLog2e;
-        const float rest = __builtin_fmaf(lse, kLog2e, -lse2[j]);       // exp2(-rest) is the row's factor
-        const float f = sr[j] * scale;
-        share[j] = ((p.gl ? p.gl[t] : 0.0f) - g) * __builtin_amdgcn_exp2f(-rest) * f;
-        given[j] = g * f;
-        if (at >= v0 && at < v0 + BV) target[j] = (int)(at - v0);
-      }
+  Walk walk((int)p.first, p.count, p.tiles_v * p.tiles_t);
+  if (walk.at >= walk.end) return;
+  int tv, tt;
+  tile_of(walk.at, p.tiles_v, p.tiles_t, tv, tt);
+  typename Tile::Source src;
+  const auto start = [&](int turn) {
+    const int t0 = tt * BT;
+    Tile::template load_values<BV>(p.l.s_col, p.v0 + tv * BV, p.l.N, sc[turn]);
+    Tile::template load_values<TOKENS>(p.l.s_row, t0, p.l.M, rows[turn][0]);
+    Tile::template load_values<TOKENS>(p.lse, t0, p.l.M, rows[turn][1]);
+    if (p.g) {
+      Tile::template load_values<TOKENS>(p.g, t0, p.l.M, rows[turn][2]);
+      Tile::template load_values<2 * TOKENS>(p.targets, 2 * (int64_t)t0, 2 * (int64_t)p.l.M, targets[turn]);
     }
-  }
-  v16i acc[FV][FT];
-  Tile::multiply(p.l, smem, v0, t0, acc);
-  if (p.l.K == 0) __syncthreads();
-  const int half = lane >> 5;
-  const bool ragged = v0 + BV > p.l.N;
+    if (p.gl) Tile::template load_values<TOKENS>(p.gl, t0, p.l.M, rows[turn][3]);
+    Tile::start(p.l, smem, p.v0 + tv * BV, t0, src);
+  };
+  const float scale = t_scale(p.bounds);
+  start(0);
+  bool before = false;
+  for (int turn = 0;; turn ^= 1) {
+    const int v0 = p.v0 + tv * BV, t0 = tt * BT, tile_v = tv, tile_t = tt;
+    v16i acc[FV][FT];
+    // (a tile before this one left its T behind this one's first loads)
+    Tile::template multiply<FT * FV * 2 * TERMS>(p.l, smem, src, before, acc);
+    before = true;
+    walk.at += walk.step;
+    const bool more = walk.at < walk.end;
+    if (more) {
+      barrier_nofence();                                     // every wave has read this tile's last fragments
+      tile_of(walk.at, p.tiles_v, p.tiles_t, tv, tt);
+      start(turn ^ 1);
+    }
+    const float* col = sc[turn];
+    const int half = lane >> 5;
+    const bool ragged = v0 + BV > p.l.N;
 #pragma unroll
-  for (int j = 0; j < FT; ++j) {
-    const int tb = tt * (BT / 32) + wt * FT + j;
-    v4i* row = p.T + ((((size_t)(tb >> p.tb_log) * p.C16 + (size_t)(p.c0 / 16 + tv * (BV / 16))) << p.tb_log) + (tb & ((1 << p.tb_log) - 1))) * 64 + lane;
-#pragma unroll
-    for (int i = 0; i < FV; ++i) {
-      const int r0 = (wv * FV + i) * 32 + 4 * half;
-      float y[16];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const v4f s4 = *reinterpret_cast<const v4f*>(sc + r0 + 8 * q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = epilogue1(acc[i][j][4 * q + e], sr[j], s4[e]);
-          y[4 * q + e] = share[j] * __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2e, -lse2[j]));
+    for (int j = 0; j < FT; ++j) {
+      const int r = (wt * FT + j) * 32 + (lane & 31);
+      float sr = 0.0f, share = 0.0f, given = 0.0f, lse2 = 3e38f;          // p = 0
+      int target = -1024;                                    // in this tile, or far outside
+      if (t0 + r < p.l.M) {
+        sr = rows[turn][0][r];
+        const float lse = rows[turn][1][r];
+        int64_t at = -1;
+        float g = 0.0f;
+        if (p.g) {
+          at = targets[turn][r];
+          if (at < 0 || at >= p.l.N) at = -1;
+          else g = rows[turn][2][r];
+        }
+        // a row whose log-sum-exp is off by a factor e or more in p has no gradient
+        if (!(fabsf(lse) >= 16777216.0f)) {
+          lse2 = lse * kLog2e;
+          const float rest = __builtin_fmaf(lse, kLog2e, -lse2);         // exp2(-rest) is the row's factor
+          const float f = sr * scale;
+          share = ((p.gl ? rows[turn][3][r] : 0.0f) - g) * __builtin_amdgcn_exp2f(-rest) * f;
+          given = g * f;
+          if (at >= v0 && at < v0 + BV) target = (int)(at - v0);
         }
       }
-      const int in = target[j] - r0;                       // 0 ... 27 for a row of this lane's
-      if (__builtin_amdgcn_ballot_w64((unsigned)in < 28u) != 0) {
+      const int tb = tile_t * (BT / 32) + wt * FT + j;
+      v4i* row = p.T + ((((size_t)(tb >> p.tb_log) * p.C16 + (size_t)(p.c0 / 16 + tile_v * (BV / 16))) << p.tb_log) + (tb & ((1 << p.tb_log) - 1))) * 64 + lane;
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (in == 8 * (e / 4) + e % 4) y[e] += given[j];
-      }
-      if (ragged) {
+      for (int i = 0; i < FV; ++i) {
+        const int r0 = (wv * FV + i) * 32 + 4 * half;
+        float y[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (v0 + r0 + 8 * (e / 4) + e % 4 >= p.l.N) y[e] = 0.0f;
-      }
-      uint32_t hi[8], lo[8];
+        for (int q = 0; q < 4; ++q) {
+          const v4f s4 = *reinterpret_cast<const v4f*>(col + r0 + 8 * q);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const v4f s4 = *reinterpret_cast<const v4f*>(sc + r0 + 8 * q);
+          for (int e = 0; e < 4; ++e) {
+            const float x = epilogue1(acc[i][j][4 * q + e], sr, s4[e]);
+            y[4 * q + e] = share * __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2e, -lse2));
+          }
+        }
+        const int in = target - r0;                       // 0 ... 27 for a row of this lane's
+        if (__builtin_amdgcn_ballot_w64((unsigned)in < 28u) != 0) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const v2f v = {y[4 * q + 2 * e] * s4[2 * e], y[4 * q + 2 * e + 1] * s4[2 * e + 1]};
-          const v2h h = __builtin_convertvector(v, v2h);
-          hi[2 * q + e] = __builtin_bit_cast(uint32_t, h);
-          if (TERMS == 2) {
-            const v2f back = __builtin_convertvector(h, v2f);
-            lo[2 * q + e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{v.x - back.x, v.y - back.y}, v2h));
+          for (int e = 0; e < 16; ++e)
+            if (in == 8 * (e / 4) + e % 4) y[e] += given;
+        }
+        if (ragged) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (v0 + r0 + 8 * (e / 4) + e % 4 >= p.l.N) y[e] = 0.0f;
+        }
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const v4f s4 = *reinterpret_cast<const v4f*>(col + r0 + 8 * q);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const v2f v = {y[4 * q + 2 * e] * s4[2 * e], y[4 * q + 2 * e + 1] * s4[2 * e + 1]};
+            const v2h h = __builtin_convertvector(v, v2h);
+            hi[2 * q + e] = __builtin_bit_cast(uint32_t, h);
+            if (TERMS == 2) {
+              const v2f back = __builtin_convertvector(h, v2f);
+              lo[2 * q + e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{v.x - back.x, v.y - back.y}, v2h));
+            }
+          }
+        }
+        // lanes l and l ^ 32 hold rows 8q + 0..3 and 8q + 4..7: a fragment's lane
+        // holds 8 in a row
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          v4i* to = row + ((size_t)((wv * FV + i) * 2 + s) << (p.tb_log + 6));
+#pragma unroll
+          for (int term = 0; term < TERMS; ++term) {
+            const uint32_t* w = term ? lo : hi;
+            const auto a = __builtin_amdgcn_permlane32_swap(w[4 * s], w[4 * s + 2], false, false);
+            const auto b = __builtin_amdgcn_permlane32_swap(w[4 * s + 1], w[4 * s + 3], false, false);
+            to[term ? p.plane : 0] = v4i{(int)a[0], (int)b[0], (int)a[1], (int)b[1]};
           }
         }
       }
-      // lanes l and l ^ 32 hold rows 8q + 0..3 and 8q + 4..7: a fragment's lane
-      // holds 8 in a row
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        v4i* to = row + ((size_t)((wv * FV + i) * 2 + s) << (p.tb_log + 6));
-#pragma unroll
-        for (int term = 0; term < TERMS; ++term) {
-          const uint32_t* w = term ? lo : hi;
-          const auto a = __builtin_amdgcn_permlane32_swap(w[4 * s], w[4 * s + 2], false, false);
-          const auto b = __builtin_amdgcn_permlane32_swap(w[4 * s + 1], w[4 * s + 3], false, false);
-          to[term ? p.plane : 0] = v4i{(int)a[0], (int)b[0], (int)a[1], (int)b[1]};
-        }
-      }
     }
+    if (!more) return;
   }
 }
 
@@ -1022,6 +1102,13 @@ LogitPlan logit_plan(int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
+// Workgroups of a launch over tiles: at most one a CU for the wide ones, each of
+// which walks over several.
+dim3 tile_grid(int64_t tiles, bool wide) {
+  const int64_t n = (tiles + 7) / 8 * 8;
+  return dim3((unsigned)(wide && n > 256 ? 256 : n));
+}
+
 // Tokens of a launch, which bounds its workspace and grid (vocabulary rows are
 // at most 2^22, so tiles at most 2^22).
 constexpr int64_t kFwdRows = 65536;
@@ -1132,9 +1219,10 @@ static void launch_grads(const BwdPlan& b, int K, unsigned n, hipStream_t stream
   else launch_grads_of<2, false>(last, n, stream, p);
 }
 
-size_t head_fwd_bytes(int64_t M, int64_t N) {
-  // (the narrower tiles leave the most parts)
-  return align256((size_t)up(N, 128) * (size_t)(M < kFwdRows ? M : kFwdRows) * sizeof(v2f));
+size_t head_fwd_bytes(int64_t M, int64_t N, int64_t K) {
+  const int64_t rows = M < kFwdRows ? M : kFwdRows;
+  const LogitPlan pl = logit_plan(rows, N, K);
+  return align256((size_t)(up(pl.wide, 256) + up(N - pl.wide, 128)) * (size_t)rows * sizeof(v2f));
 }
 
 hipError_t launch_head_fwd(const HeadArgs& whole, const int64_t* targets, float* logprob, float* lse, void* ws, hipStream_t stream) {
@@ -1146,7 +1234,7 @@ hipError_t launch_head_fwd(const HeadArgs& whole, const int64_t* targets, float*
     a.s_row += row;
     FwdArgs f{logit_args(a), 0, up(pl.wide, 256), up(a.M, 256), static_cast<v2f*>(ws)};
     if (f.tiles_v > 0)
-      hipLaunchKernelGGL((head_fwd_kernel<256, 256, 2, 4, 1>), dim3((unsigned)f.tiles_v * (unsigned)f.tiles_t), dim3(512), 0, stream, f);
+      hipLaunchKernelGGL((head_fwd_kernel<256, 256, 2, 4, 1>), tile_grid((int64_t)f.tiles_v * f.tiles_t, true), dim3(512), 0, stream, f);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     int n_parts = f.tiles_v;
@@ -1156,7 +1244,7 @@ hipError_t launch_head_fwd(const HeadArgs& whole, const int64_t* targets, float*
       f.tiles_v = up(a.N - pl.wide, pl.bv);
       f.tiles_t = up(a.M, pl.bt);
       n_parts += f.tiles_v;
-      const dim3 grid((unsigned)f.tiles_v * (unsigned)f.tiles_t);
+      const dim3 grid = tile_grid((int64_t)f.tiles_v * f.tiles_t, false);
       if (pl.bt == 32) hipLaunchKernelGGL((head_fwd_kernel<128, 32, 4, 1, 3>), grid, dim3(256), 0, stream, f);
       else hipLaunchKernelGGL((head_fwd_kernel<128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, f);
       if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -1199,7 +1287,7 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
   };
   for (int piece = 0; piece < b.pieces; ++piece) {
     const int64_t v0 = piece * b.C, rows = a.N - v0 < b.C ? a.N - v0 : b.C;
-    WeightArgs w{l, g.targets, g.lse, g.g_logprob, g.g_lse, (int)v0, 0, 0, 0, C16, bounds, 0, b.tb_log, T, plane};
+    WeightArgs w{l, g.targets, g.lse, g.g_logprob, g.g_lse, (int)v0, 0, 0, 0, C16, bounds, 0, 0, b.tb_log, T, plane};
     const LogitPlan pl = logit_plan(b.Mp, b.C, a.K);
     const int64_t wide_cols = b.few ? 0 : pl.wide;         // (few tokens: T has 64)
     for (const bool wide : {true, false}) {
@@ -1209,7 +1297,8 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
       w.tiles_t = (int)(b.Mp / (wide ? 256 : 64));
       for (w.first = 0; w.first < (int64_t)w.tiles_v * w.tiles_t; w.first += kMostGroups) {
         const int64_t left = (int64_t)w.tiles_v * w.tiles_t - w.first;
-        const dim3 grid((unsigned)(left < kMostGroups ? left : kMostGroups));
+        w.count = (int)(left < kMostGroups ? left : kMostGroups);
+        const dim3 grid = tile_grid(w.count, wide);
         if (wide && b.terms == 1) hipLaunchKernelGGL((head_weights_kernel<1, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
         else if (wide) hipLaunchKernelGGL((head_weights_kernel<2, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
         else if (b.terms == 1) hipLaunchKernelGGL((head_weights_kernel<1, 128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, w);

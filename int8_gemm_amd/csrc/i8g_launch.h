@@ -247,7 +247,7 @@ struct HeadArgs {
   const float *s_row, *s_col;
   int64_t lda, ldb, M, N, K;
 };
-size_t head_fwd_bytes(int64_t M, int64_t N);
+size_t head_fwd_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_head_fwd(const HeadArgs& a, const int64_t* targets, float* logprob, float* lse, void* ws,
                            hipStream_t stream);
 struct HeadGradArgs {

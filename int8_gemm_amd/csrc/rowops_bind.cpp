@@ -410,8 +410,13 @@ Matrix int8_matrix(PyObject* o, const char* name, const at::Tensor* like) {
   if (t.dim() != 2 || t.scalar_type() != at::kChar) refuse("%s must be a 2-D int8 tensor", name);
   return layout(t, name, like);
 }
-// A single row of codes has no leading dimension of its own: what the product reads of it is.
-int64_t code_ld(const Matrix& m) { return m.rows > 1 ? m.ld : (m.cols + 15) / 16 * 16; }
+// The stride of a single row of codes says how much of it may be read, a multiple
+// of 16 bytes; whole 16s need no more than the row itself.
+int64_t code_ld(const Matrix& m) {
+  if (m.rows > 1) return m.ld;
+  const int64_t k16 = (m.cols + 15) / 16 * 16;
+  return m.rows == 0 || m.cols == k16 ? k16 : m.t->stride(0);
+}
 Head head(Args a) {   // QA, s_row, QBt, s_col
   Head h{int8_matrix(a[0], "QA", nullptr), {}, nullptr, nullptr, 0, 0};
   h.b = int8_matrix(a[2], "QBt", h.a.t);

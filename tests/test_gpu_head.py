@@ -338,3 +338,40 @@ def test_arguments():
     with pytest.raises(g.I8GError) as e:                   # rows of 10 codes are not whole 16 bytes
         g.gemm_i8_logprobs(torch.zeros((4, 10), dtype=torch.int8, device="cuda"), s, torch.zeros((4, 10), dtype=torch.int8, device="cuda"), s, t)
     assert e.value.status == 3
+
+
+def test_a_single_row():
+    """One row is read in whole 16 bytes, which its stride has to allow or its length to make."""
+    rng = np.random.default_rng(41)
+    for k in (16, 45):
+        qa, sa, qb, sb, t = case(rng, 1, 1, k)
+        A, B = R.padded(qa), R.padded(qb)
+        SA, SB, T = dev(sa, sb, t)
+        lp, lse = g.gemm_i8_logprobs(A, SA, B, SB, T)
+        assert lp.item() == 0.0                            # the only row of the vocabulary
+        short = A.contiguous().reshape(-1)[:k].clone().reshape(1, k)
+        if k == 16:
+            assert torch.equal(g.gemm_i8_logprobs(short, SA, B, SB, T)[1], lse)
+            continue
+        for args in ((short, SA, B, SB, T), (A, SA, short, SB, T)):
+            with pytest.raises(g.I8GError) as e:
+                g.gemm_i8_logprobs(*args)
+            assert e.value.status == 3
+            with pytest.raises(g.I8GError) as e:
+                g.gemm_i8_logprobs_bwd(*args, lse, lse)
+            assert e.value.status == 3
+
+
+@pytest.mark.parametrize("k,dtype", [(24, "f16"), (200, "f32"), (300, "bf16")])
+def test_workgroups_of_several_tiles(k, dtype):
+    """More tiles than workgroups: each but the first is asked for while the one before it is finished."""
+    m, n = 4100, 12000
+    say("several tiles", m, n, k, dtype)
+    rng = np.random.default_rng(k)
+    qa, sa, qb, sb, t = case(rng, m, n, k)
+    lse = check_forward(qa, sa, qb, sb, t)
+    again = forward(qa, sa, qb, sb, t)[1]
+    same_bits(lse, again, "twice")
+    size = 64.0 / m if dtype == "f16" else 1.0 / m
+    check_grads(qa, sa, qb, sb, t, host(lse).astype(np.float32), (-size * rng.uniform(0.5, 1.5, m)).astype(np.float32),
+                (size * 0.1 * rng.standard_normal(m)).astype(np.float32), dtype)
