@@ -272,20 +272,25 @@ __global__ void __launch_bounds__(256) embedding_merge_kernel(const MergeArgs p,
   p.order_out[place] = p.order[i];
 }
 
-// ---- at most 1024 rows: one launch ---------------------------------------------------
-// Every wave holds all tokens, WORDS a lane.  A workgroup a row and 256 columns:
-// if no earlier row has its token, it adds all that have, each wave those of every
-// fourth 64 rows, the waves' sums in their order.  The workgroups behind fill the
-// rows of the table that no token names.  (88 x 159 onto 720 rows 7.4 us, 701 x 76
-// onto 31438 15.2, 782 x 715 onto 115 18.4, where sorting, adding and joining in
-// three launches take 16.5, 19.5 and 18.6.)
-constexpr int kFewWords = 16, kFew = kFewWords * 64;
+// ---- few rows: one launch ------------------------------------------------------------
+// Every wave holds all tokens, WORDS a lane.  The workgroups of a row take 256
+// columns at a time: if no earlier row has its token, they add all that have, each
+// wave those of every fourth 64 rows, the waves' sums in their order.  The
+// workgroups behind fill the rows of the table that no token names.  Against the
+// three launches of sorting, adding and joining (us): 64 x 768 onto 100 rows 4.1
+// and 11.0, 256 x 5000 onto 300 10.4 and 17.7, 700 x 76 onto 31438 14.4 and 17.7,
+// 1024 x 768 onto 1024 13.5 and 15.8; but 512 x 4096 onto 1024 19.7 and 15.0,
+// 918 x 2252 onto 1365 24 and 19, as every workgroup looks through all tokens.
+constexpr int kFewWords = 16, kFew = kFewWords * 64, kFewGroups = 2048;
+bool few_rows(int64_t rows, int64_t cols) {
+  return rows <= 256 || (rows <= kFew && rows * ((cols + 255) / 256) <= 3 * kFew);
+}
 struct FewArgs {
   const void* dY;
   int64_t rows, cols, lddy;
   const int64_t* tokens;
   double alpha;
-  int chunks;                  // of 256 columns
+  int chunks;                  // workgroups of a row
   int64_t sums;                // workgroups that add
   FillArgs fill;
 };
@@ -317,7 +322,7 @@ __global__ void __launch_bounds__(256) embedding_few_kernel(const FewArgs p) {
     return;
   }
   const int row = (int)(p.chunks == 1 ? blockIdx.x : blockIdx.x / p.chunks);
-  const int c = (int)(blockIdx.x - (int64_t)row * p.chunks) * 64 * N + lane * N;
+  const int chunk = (int)(blockIdx.x - (int64_t)row * p.chunks);
   const int64_t token = uniform64(p.tokens[row]);
   if (token < 0 || token >= p.fill.vocab) return;
   bool earlier = false;
@@ -329,44 +334,49 @@ __global__ void __launch_bounds__(256) embedding_few_kernel(const FewArgs p) {
     if (w == (row >> 6)) earlier = earlier || (has[w] & ((1ull << (row & 63)) - 1)) != 0;
   }
   if (earlier) return;
-  double s[N];
-#pragma unroll
-  for (int e = 0; e < N; ++e) s[e] = 0.0;
-#pragma unroll
-  for (int w = 0; w < WORDS; w += 4) {
-    uint64_t mine = wave == 0 ? has[w] : wave == 1 ? has[w + 1] : wave == 2 ? has[w + 2] : has[w + 3];
-    const T* dy = static_cast<const T*>(p.dY) + (int64_t)((w + wave) * 64) * p.lddy;
-    while (mine != 0) {
-      RawRow<T, N> x[8];
-      uint64_t left = mine;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int at = __builtin_ctzll(left != 0 ? left : mine);
-        left &= left - 1;
-        x[i].load(dy + at * p.lddy, c, cols);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (mine != 0) {
-#pragma unroll
-          for (int e = 0; e < N; ++e) s[e] += (double)x[i][e];
-          mine &= mine - 1;
-        }
-    }
-  }
   __shared__ double sum[4][64][N];
+  for (int64_t first = (int64_t)chunk * 64 * N; first < cols; first += (int64_t)p.chunks * 64 * N) {
+    const int c = (int)first + lane * N;
+    double s[N];
 #pragma unroll
-  for (int e = 0; e < N; ++e) sum[wave][lane][e] = s[e];
-  __syncthreads();
-  if (wave != 0 || c >= cols) return;
-  float y[N], old[N];
-  if (p.fill.add) load_row<float, N>(p.fill.add + token * p.fill.ldadd, c, cols, 0.0f, old);
+    for (int e = 0; e < N; ++e) s[e] = 0.0;
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const double all = p.alpha * (((sum[0][lane][e] + sum[1][lane][e]) + sum[2][lane][e]) + sum[3][lane][e]);
-    y[e] = (float)(p.fill.add ? (double)old[e] + all : all);
+    for (int w = 0; w < WORDS; w += 4) {
+      uint64_t mine = wave == 0 ? has[w] : wave == 1 ? has[w + 1] : wave == 2 ? has[w + 2] : has[w + 3];
+      const T* dy = static_cast<const T*>(p.dY) + (int64_t)((w + wave) * 64) * p.lddy;
+      while (mine != 0) {
+        RawRow<T, N> x[8];
+        uint64_t left = mine;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int at = __builtin_ctzll(left != 0 ? left : mine);
+          left &= left - 1;
+          x[i].load(dy + at * p.lddy, c, cols);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (mine != 0) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) s[e] += (double)x[i][e];
+            mine &= mine - 1;
+          }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum[wave][lane][e] = s[e];
+    __syncthreads();
+    if (wave == 0 && c < cols) {
+      float y[N], old[N];
+      if (p.fill.add) load_row<float, N>(p.fill.add + token * p.fill.ldadd, c, cols, 0.0f, old);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const double all = p.alpha * (((sum[0][lane][e] + sum[1][lane][e]) + sum[2][lane][e]) + sum[3][lane][e]);
+        y[e] = (float)(p.fill.add ? (double)old[e] + all : all);
+      }
+      store_row<float, N>(p.fill.dW + token * p.fill.lddw, c, cols, y);
+    }
+    __syncthreads();
   }
-  store_row<float, N>(p.fill.dW + token * p.fill.lddw, c, cols, y);
 }
 template <int WORDS>
 void launch_few(int dtype, dim3 grid, hipStream_t stream, const FewArgs& a) {
@@ -604,8 +614,8 @@ hipError_t launch_embedding_bwd(const EmbedBwdArgs& a, int dtype, void* ws, hipS
     const int64_t most = 16384 / waves;                    // 4 workgroups of 16 waves for each of the 256 CUs
     return FillArgs{a.dW, a.lddw, a.vocab, a.cols, a.add, a.ldadd, lanes, first, end, (int)(blocks < most ? blocks : most)};
   };
-  const int64_t chunks = up64(a.cols, 256);
-  if (a.rows > 0 && a.rows <= kFew && a.rows * chunks <= (1 << 22)) {
+  if (a.rows > 0 && few_rows(a.rows, a.cols)) {
+    const int64_t all = up64(a.cols, 256), most = up64(kFewGroups, a.rows), chunks = all < most ? all : most;
     FewArgs w{a.dY, a.rows, a.cols, a.lddy, a.tokens, (double)a.alpha, (int)chunks, a.rows * chunks, fill(0, a.vocab, 4)};
     const dim3 grid((unsigned)(w.sums + w.fill.blocks));
     if (a.rows <= 256) launch_few<4>(dtype, grid, stream, w);

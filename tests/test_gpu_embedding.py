@@ -183,3 +183,12 @@ def test_arguments():
         with pytest.raises(ValueError, match=match):
             g.embedding_bwd(*args)
     assert g.embedding(w, t[:0]).shape == (0, 8) and g.embedding_bwd(dy[:0], t[:0], 5).abs().sum() == 0
+
+
+# workgroups that take several parts of a row's columns, and the sorting of fewer rows than a wave sorts
+@pytest.mark.parametrize("rows,vocab,cols", [(255, 40, 2600), (600, 400, 1100), (1000, 30, 1100), (257, 300, 3333)])
+def test_gradient_of_few_long_rows(rows, vocab, cols):
+    say("long rows", rows, vocab, cols)
+    rng = np.random.default_rng(rows)
+    for i, dtype in enumerate(DTYPES):
+        check_grad(rng, rows, vocab, cols, dtype, tokens_of(rng, rows, vocab), add=i != 1, pad=i, in_place=i == 2)
