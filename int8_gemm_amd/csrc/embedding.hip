@@ -5,13 +5,14 @@
 //   dW_v = alpha sum_{t_i = v} dY_i          binary64 sums in the order of i
 //
 // The lookup is one pass: a wave takes up to 256 vectors of a row, four loads
-// in flight.  The gradient sorts the tokens (a stable radix sort of 8192 at a
-// time in LDS, while the other workgroups write the rows that no token names;
-// the sorted runs are merged 8 at a time), then adds rows in the sorted order:
-// a wave takes a piece of the order and a chunk of columns, writes the
-// rows of tokens whose places it holds all of, and leaves the others' sums in
-// the workspace, which a last launch joins.  No sum depends on which
-// workgroup comes first.
+// in flight.  The gradient of few rows is one launch that looks through all
+// tokens.  That of more sorts them, while other workgroups write the rows that
+// no token names (up to kRankRows each key's place is counted by the whole
+// chip; beyond, a stable radix sort of kRun at a time in LDS, the sorted runs
+// merged kMerge at a time), then adds rows in the sorted order: a wave takes a
+// piece of the order and a chunk of columns, writes the rows of tokens whose
+// places it holds all of, and leaves the others' sums in the workspace, which
+// a last launch joins.  No sum depends on which workgroup comes first.
 #include "../../include/int8_gemm.h"
 #include "i8g_launch.h"
 #include "i8g_row.h"
@@ -117,13 +118,21 @@ struct FillArgs {              // the rows of dW before the sums: zeros, or thos
   int64_t first, end;          // rows of the launch
   int blocks;                  // workgroups that fill; 0 where dW is `add`
 };
+// The pieces that left a second sum (see the sums) are listed by a counter each
+// kLists-th piece has: 4 kB of them, a cache line each.  (On one address the
+// additions take some 10 ns each, one after the other: 32000 x 76 took 22 us.)
+constexpr int kLists = 64, kListStep = 16;
+__device__ __forceinline__ void clear_lists(uint32_t* listed) {
+  if (threadIdx.x < kLists) listed[threadIdx.x * kListStep] = 0;
+}
+
 struct SortArgs {
   const int64_t* tokens;
   int64_t rows, vocab;
   int bits;                    // of the keys 0 ... vocab (vocab: no token)
   uint32_t *keys, *order;      // [rows]: sorted within each run of kRun
   int runs;
-  uint32_t* listed;            // zeroed for the sums
+  uint32_t* listed;            // the lists' counters, zeroed for the sums
 };
 
 // Rows v0 ... of a wave, as many as 64 lanes hold at 4 columns each (all lanes one
@@ -156,7 +165,7 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const Sort
     fill_rows<kSortWaves>(fill, (int)blockIdx.x - p.runs);
     return;
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.listed = 0;
+  if (blockIdx.x == 0) clear_lists(p.listed);
   __shared__ uint32_t key[2][kRun];
   __shared__ uint16_t at[2][kRun];
   __shared__ uint32_t count[(1 << kDigit) * kSortWaves];   // [digit][wave]
@@ -164,10 +173,17 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const Sort
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t first = (int64_t)blockIdx.x * kRun;
   const int n = (int)min((int64_t)kRun, p.rows - first);
-  for (int i = tid; i < n; i += kSortThreads) {
-    const int64_t t = p.tokens[first + i];
-    key[0][i] = t >= 0 && t < p.vocab ? (uint32_t)t : (uint32_t)p.vocab;
-    at[0][i] = (uint16_t)i;
+  constexpr int kOwn = kRun / kSortThreads;
+  int64_t t[kOwn];
+#pragma unroll
+  for (int q = 0; q < kOwn; ++q) t[q] = p.tokens[first + min(tid + q * kSortThreads, n - 1)];
+#pragma unroll
+  for (int q = 0; q < kOwn; ++q) {
+    const int i = tid + q * kSortThreads;
+    if (i < n) {
+      key[0][i] = t[q] >= 0 && t[q] < p.vocab ? (uint32_t)t[q] : (uint32_t)p.vocab;
+      at[0][i] = (uint16_t)i;
+    }
   }
   const int passes = (p.bits + kDigit - 1) / kDigit, width = (p.bits + passes - 1) / passes, bins = 1 << width;
   // a wave's keys: kRun / kSortWaves in a row, or what an even share of fewer is
@@ -232,6 +248,67 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const Sort
   }
 }
 
+// Few enough rows are sorted by the whole chip: a workgroup has all keys in LDS
+// and finds the places of kRank of them, as the keys that come before each: a
+// thread counts for one row over an even share of them.  (With the table hardly
+// larger than the tokens, 3363 rows take 8 us and 8192 14, and 12 and 21 where a
+// workgroup sorts up to kRun of them; 11270 24 and 33, with the merge; 16384 34
+// and 33.)
+constexpr int kRank = 32, kRankThreads = 512, kRankRows = 12288;
+constexpr int kRankShares = kRankThreads / kRank;
+static_assert(kRank == 32, "the loops below");
+__global__ void __launch_bounds__(kRankThreads) embedding_rank_kernel(const SortArgs p, const FillArgs fill) {
+  if ((int)blockIdx.x >= p.runs) {
+    fill_rows<kRankThreads / 64>(fill, (int)blockIdx.x - p.runs);
+    return;
+  }
+  if (blockIdx.x == 0) clear_lists(p.listed);
+  extern __shared__ __attribute__((aligned(16))) uint32_t keys[];          // whole kRanks, those behind the rows 2^32 - 1
+  __shared__ uint32_t count[kRankThreads / 64][kRank];
+  const int tid = threadIdx.x, rows = (int)p.rows, all = (rows + kRank - 1) / kRank * kRank;
+  for (int i0 = tid; i0 < all; i0 += 8 * kRankThreads) {
+    int64_t t[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) t[q] = p.tokens[min(i0 + q * kRankThreads, rows - 1)];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int i = i0 + q * kRankThreads;
+      if (i < all) keys[i] = i >= rows ? 0xFFFFFFFFu : t[q] >= 0 && t[q] < p.vocab ? (uint32_t)t[q] : (uint32_t)p.vocab;
+    }
+  }
+  __syncthreads();
+  const int first = (int)blockIdx.x * kRank, own = first + tid % kRank, share = tid / kRank;
+  const int per = (all / kRank + kRankShares - 1) / kRankShares * kRank;   // keys of a share
+  const int begin = min(share * per, all), end = min(begin + per, all);
+  const uint32_t mine = keys[own];
+  uint32_t n = 0;
+  const auto below = [&](int from, int to, uint32_t limit) {
+    for (int i = from; i < to; i += 32) {                  // (all are whole kRanks)
+      uint4 k[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) k[q] = *reinterpret_cast<const uint4*>(keys + i + 4 * q);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) n += (k[q].x < limit) + (k[q].y < limit) + (k[q].z < limit) + (k[q].w < limit);
+    }
+  };
+  below(begin, min(end, first), mine + 1);                 // equal ones of earlier rows come before it
+  below(max(begin, first + kRank), end, mine);
+#pragma unroll
+  for (int i = share * (kRank / kRankShares); i < (share + 1) * (kRank / kRankShares); ++i) {
+    const uint32_t k = keys[first + i];
+    n += k < mine || (k == mine && first + i < own);
+  }
+  n += __shfl_xor(n, 32, 64);
+  if ((tid & 63) < kRank) count[tid >> 6][tid & 63] = n;
+  __syncthreads();
+  if (tid >= kRank || own >= rows) return;
+  uint32_t place = 0;
+#pragma unroll
+  for (int w = 0; w < kRankThreads / 64; ++w) place += count[w][tid];
+  p.keys[place] = mine;
+  p.order[place] = (uint32_t)own;
+}
+
 // kMerge sorted runs of `run` places each to one: an element's place is its own
 // plus, for each other run of its group, the elements there that come before
 // it (equal ones of earlier runs do).
@@ -294,6 +371,52 @@ struct FewArgs {
   int64_t sums;                // workgroups that add
   FillArgs fill;
 };
+// WHOLE: as for the sums below.
+template <class T, int WORDS, bool WHOLE>
+__device__ __forceinline__ void few_sums(const FewArgs& p, const uint64_t (&has)[WORDS], double (&sum)[4][64][4], int64_t token,
+                                         int c, int wave) {
+  constexpr int N = 4;
+  const int lane = threadIdx.x & 63, cols = (int)p.cols;
+  double s[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) s[e] = 0.0;
+#pragma unroll
+  for (int w = 0; w < WORDS; w += 4) {
+    uint64_t mine = wave == 0 ? has[w] : wave == 1 ? has[w + 1] : wave == 2 ? has[w + 2] : has[w + 3];
+    const T* dy = static_cast<const T*>(p.dY) + (int64_t)((w + wave) * 64) * p.lddy;
+    while (mine != 0) {
+      RawRow<T, N> x[8];
+      uint64_t left = mine;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = __builtin_ctzll(left != 0 ? left : mine);
+        left &= left - 1;
+        if constexpr (WHOLE) __builtin_memcpy(x[i].t, dy + at * p.lddy + c, sizeof(x[i].t));
+        else x[i].load(dy + at * p.lddy, c, cols);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (mine != 0) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) s[e] += (double)x[i][e];
+          mine &= mine - 1;
+        }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) sum[wave][lane][e] = s[e];
+  __syncthreads();
+  if (wave != 0 || (!WHOLE && c >= cols)) return;
+  float y[N], old[N];
+  if (p.fill.add) load_row<float, N>(p.fill.add + token * p.fill.ldadd, c, cols, 0.0f, old);
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const double all = p.alpha * (((sum[0][lane][e] + sum[1][lane][e]) + sum[2][lane][e]) + sum[3][lane][e]);
+    y[e] = (float)(p.fill.add ? (double)old[e] + all : all);
+  }
+  store_row<float, N>(p.fill.dW + token * p.fill.lddw, c, cols, y);
+}
+
 template <class T, int WORDS>
 __global__ void __launch_bounds__(256) embedding_few_kernel(const FewArgs p) {
   constexpr int N = 4;
@@ -337,44 +460,8 @@ __global__ void __launch_bounds__(256) embedding_few_kernel(const FewArgs p) {
   __shared__ double sum[4][64][N];
   for (int64_t first = (int64_t)chunk * 64 * N; first < cols; first += (int64_t)p.chunks * 64 * N) {
     const int c = (int)first + lane * N;
-    double s[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) s[e] = 0.0;
-#pragma unroll
-    for (int w = 0; w < WORDS; w += 4) {
-      uint64_t mine = wave == 0 ? has[w] : wave == 1 ? has[w + 1] : wave == 2 ? has[w + 2] : has[w + 3];
-      const T* dy = static_cast<const T*>(p.dY) + (int64_t)((w + wave) * 64) * p.lddy;
-      while (mine != 0) {
-        RawRow<T, N> x[8];
-        uint64_t left = mine;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int at = __builtin_ctzll(left != 0 ? left : mine);
-          left &= left - 1;
-          x[i].load(dy + at * p.lddy, c, cols);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (mine != 0) {
-#pragma unroll
-            for (int e = 0; e < N; ++e) s[e] += (double)x[i][e];
-            mine &= mine - 1;
-          }
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < N; ++e) sum[wave][lane][e] = s[e];
-    __syncthreads();
-    if (wave == 0 && c < cols) {
-      float y[N], old[N];
-      if (p.fill.add) load_row<float, N>(p.fill.add + token * p.fill.ldadd, c, cols, 0.0f, old);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const double all = p.alpha * (((sum[0][lane][e] + sum[1][lane][e]) + sum[2][lane][e]) + sum[3][lane][e]);
-        y[e] = (float)(p.fill.add ? (double)old[e] + all : all);
-      }
-      store_row<float, N>(p.fill.dW + token * p.fill.lddw, c, cols, y);
-    }
+    if (cols - (int)first >= N) few_sums<T, WORDS, true>(p, has, sum, token, min(c, cols - N), wave);
+    else few_sums<T, WORDS, false>(p, has, sum, token, c, wave);
     __syncthreads();
   }
 }
@@ -405,7 +492,8 @@ struct SumArgs {
   double* parts;               // [pieces][2][ldp]: sums of the piece's part of a token that began before it, and
                                // of one that goes on behind it
   int64_t ldp;                 // cols in whole chunks
-  uint32_t *list, *listed;     // the pieces that left a second sum, and how many they are
+  uint32_t *list, *listed;     // the pieces that left a second sum: kLists lists, and how many are in each
+  int64_t list_ld;
   int chunks;                  // of 64 vectors
   int64_t first;               // unit
 };
@@ -418,10 +506,12 @@ __device__ __forceinline__ void for_each(F&& f) {
   }
 }
 
-// WHOLE: every lane's columns lie in the row (loads without a condition stay
-// where they are written, ahead of their use).
+// WHOLE: every lane's columns lie in the row, where the last lanes' begin before
+// theirs so that they do: these have what others have too, to the bit.  (Loads
+// without a condition stay where they are written, ahead of their use: 2135 x 207
+// takes 5.6 us, and 9.3 with conditions.)
 template <class T, bool WHOLE, bool ONTO>
-__device__ __forceinline__ void sum_piece(const SumArgs& p, int64_t piece, int c) {
+__device__ __forceinline__ void sum_piece(const SumArgs& p, int64_t piece, int c, bool first) {
   constexpr int N = kLane, B = kBatch<ONTO>;
   const int lane = threadIdx.x & 63;
   const int cols = (int)p.cols;
@@ -471,8 +561,11 @@ __device__ __forceinline__ void sum_piece(const SumArgs& p, int64_t piece, int c
         if (ends || at + i + 1 == end) {
           if (head || !ends) {
             __builtin_memcpy(parts + (head ? 0 : p.ldp), s, sizeof(s));
-            // (the list's order is no matter: its entries have nothing in common)
-            if (!head && c == 0) p.list[atomicAdd(p.listed, 1u)] = (uint32_t)piece;
+            // (a list's order is no matter: its entries have nothing in common)
+            if (!head && lane == 0 && first) {
+              const int l = (int)(piece % kLists);
+              p.list[l * p.list_ld + atomicAdd(p.listed + l * kListStep, 1u)] = (uint32_t)piece;
+            }
           } else if (WHOLE || c < cols) {
             float* to = p.dW + (int64_t)key * p.lddw;
             float y[N];
@@ -497,18 +590,21 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs p) {
   if (piece >= p.pieces) return;
   const int c0 = (int)(unit - piece * p.chunks) * 64 * kLane;
   const int c = c0 + (threadIdx.x & 63) * kLane;
-  if (c0 + 64 * kLane <= (int)p.cols) sum_piece<T, true, ONTO>(p, piece, c);
-  else sum_piece<T, false, ONTO>(p, piece, c);
+  // (not into another wave's columns, which it may have added to already)
+  if ((int)p.cols - c0 >= kLane) sum_piece<T, true, ONTO>(p, piece, min(c, (int)p.cols - kLane), c0 == 0);
+  else sum_piece<T, false, ONTO>(p, piece, c, c0 == 0);
 }
 
 // Workgroups take a listed piece and 256 columns at a time: the sums of the
 // token that goes on behind the piece, added in their order.
-constexpr int kJoinGroups = 2048;
+constexpr int kJoinGroups = 2048;              // whole kLists
+
 __global__ void __launch_bounds__(256) embedding_join_kernel(const SumArgs p) {
-  const int64_t items = (int64_t)uniform(*p.listed) * p.chunks;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+  const int l = (int)(blockIdx.x % kLists);
+  const int64_t items = (int64_t)uniform(p.listed[l * kListStep]) * p.chunks;
+  for (int64_t item = blockIdx.x / kLists; item < items; item += gridDim.x / kLists) {
     const int64_t entry = p.chunks == 1 ? item : item / p.chunks;
-    const int64_t piece = uniform(p.list[entry]);
+    const int64_t piece = uniform(p.list[l * p.list_ld + entry]);
     const int64_t c = (item - entry * p.chunks) * 256 + threadIdx.x;
     const uint32_t key = uniform(p.keys[(piece + 1) * p.piece - 1]);
     // the last piece that it goes on in: 64 of their first places at a time
@@ -594,13 +690,15 @@ int64_t part_ld(int64_t cols) { return up64(cols, 64 * kLane) * (64 * kLane); }
 struct BwdLayout {
   size_t list, joined, bytes;  // of a list of keys or rows; where the pieces' list and the parts begin
   size_t parts;
+  int64_t list_ld;
 };
 BwdLayout bwd_layout(int64_t rows, int64_t cols) {
   BwdLayout l;
   const int64_t pieces = up64(rows, piece_of(rows, cols));
   l.list = aligned((size_t)rows * 4);
   l.joined = l.list * (merges(rows) > 0 ? 4 : 2);
-  l.parts = l.joined + aligned((size_t)(pieces + 1) * 4);
+  l.list_ld = up64(pieces, kLists);
+  l.parts = l.joined + aligned((size_t)(kListStep + l.list_ld) * kLists * 4);
   l.bytes = l.parts + (size_t)pieces * 2 * (size_t)part_ld(cols) * 8;
   return l;
 }
@@ -631,28 +729,36 @@ hipError_t launch_embedding_bwd(const EmbedBwdArgs& a, int dtype, void* ws, hipS
   SortArgs s{a.tokens, a.rows, a.vocab, 0, keys[0], order[0], (int)up64(a.rows, kRun), listed};
   while ((a.vocab >> s.bits) != 0) ++s.bits;              // vocab itself is a key
   if (s.bits == 0) s.bits = 1;
-  // The rows are filled beside the sorting and the merging, which leave most of
-  // the chip free: a merge takes as long as about a fifth of a fill of 150 MB.
-  int n_merges = (int)merges(a.rows);
-  if (n_merges > 2) n_merges = 2;
-  const int64_t later = in_place ? 0 : a.vocab / 5 * n_merges;
-  FillArgs f = fill(0, a.vocab - later, kSortWaves);
-  if (s.runs + f.blocks > 0) hipLaunchKernelGGL(embedding_sort_kernel, dim3((unsigned)(s.runs + f.blocks)), dim3(kSortThreads), 0, stream, s, f);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.rows == 0) return e;
+  hipError_t e;
   int from = 0;
-  int64_t filled = a.vocab - later;
-  for (int64_t run = kRun; run < a.rows; run *= kMerge, from ^= 1) {
-    MergeArgs m{keys[from], order[from], keys[from ^ 1], order[from ^ 1], a.rows, run, up64(a.rows, 256)};
-    const int64_t to = run * kMerge >= a.rows ? a.vocab : filled + a.vocab / 5 < a.vocab ? filled + a.vocab / 5 : a.vocab;
-    f = fill(filled, to, 4);
-    filled = to;
-    hipLaunchKernelGGL(embedding_merge_kernel, dim3((unsigned)(m.groups + f.blocks)), dim3(256), 0, stream, m, f);
+  if (a.rows > 0 && a.rows <= kRankRows) {
+    s.runs = (int)up64(a.rows, kRank);
+    const FillArgs f = fill(0, a.vocab, kRankThreads / 64);
+    hipLaunchKernelGGL(embedding_rank_kernel, dim3((unsigned)(s.runs + f.blocks)), dim3(kRankThreads), (size_t)s.runs * kRank * 4, stream, s, f);
     if ((e = hipGetLastError()) != hipSuccess) return e;
+  } else {
+    // The rows are filled beside the sorting and the merging, which leave most of
+    // the chip free: a merge takes as long as about a fifth of a fill of 150 MB.
+    int n_merges = (int)merges(a.rows);
+    if (n_merges > 2) n_merges = 2;
+    const int64_t later = in_place ? 0 : a.vocab / 5 * n_merges;
+    FillArgs f = fill(0, a.vocab - later, kSortWaves);
+    if (s.runs + f.blocks > 0) hipLaunchKernelGGL(embedding_sort_kernel, dim3((unsigned)(s.runs + f.blocks)), dim3(kSortThreads), 0, stream, s, f);
+    e = hipGetLastError();
+    if (e != hipSuccess || a.rows == 0) return e;
+    int64_t filled = a.vocab - later;
+    for (int64_t run = kRun; run < a.rows; run *= kMerge, from ^= 1) {
+      MergeArgs m{keys[from], order[from], keys[from ^ 1], order[from ^ 1], a.rows, run, up64(a.rows, 256)};
+      const int64_t to = run * kMerge >= a.rows ? a.vocab : filled + a.vocab / 5 < a.vocab ? filled + a.vocab / 5 : a.vocab;
+      f = fill(filled, to, 4);
+      filled = to;
+      hipLaunchKernelGGL(embedding_merge_kernel, dim3((unsigned)(m.groups + f.blocks)), dim3(256), 0, stream, m, f);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
   }
   const int64_t piece = piece_of(a.rows, a.cols);
   SumArgs u{a.dY, a.rows, a.cols, a.lddy, a.vocab, keys[from], order[from], (double)a.alpha, a.dW, a.lddw, a.add != nullptr,
-            piece, up64(a.rows, piece), reinterpret_cast<double*>(at + lay.parts), part_ld(a.cols), listed + 1, listed, (int)up64(a.cols, 64 * kLane), 0};
+            piece, up64(a.rows, piece), reinterpret_cast<double*>(at + lay.parts), part_ld(a.cols), listed + kLists * kListStep, listed, lay.list_ld, (int)up64(a.cols, 64 * kLane), 0};
   e = in_slabs(up64(u.pieces * u.chunks, 4), [&](unsigned grid, int64_t first) {
     u.first = first * 4;
     const dim3 g(grid), b(256);
@@ -664,7 +770,7 @@ hipError_t launch_embedding_bwd(const EmbedBwdArgs& a, int dtype, void* ws, hipS
     else hipLaunchKernelGGL((embedding_sum_kernel<f16_t, false>), g, b, 0, stream, u);
   });
   if (e != hipSuccess || u.pieces == 1) return e;
-  const int64_t items = (u.pieces - 1) * u.chunks;
+  const int64_t items = up64(u.pieces - 1, kLists) * kLists * u.chunks;
   hipLaunchKernelGGL(embedding_join_kernel, dim3((unsigned)(items < kJoinGroups ? items : kJoinGroups)), dim3(256), 0, stream, u);
   return hipGetLastError();
 }

@@ -192,3 +192,15 @@ def test_gradient_of_few_long_rows(rows, vocab, cols):
     rng = np.random.default_rng(rows)
     for i, dtype in enumerate(DTYPES):
         check_grad(rng, rows, vocab, cols, dtype, tokens_of(rng, rows, vocab), add=i != 1, pad=i, in_place=i == 2)
+
+
+# what counts places and what sorts; rows of less than a vector, and of a vector's part behind whole chunks
+@pytest.mark.parametrize("rows,vocab,cols", [(12288, 5000, 3), (12289, 5000, 6), (16385, 9, 1), (2000, 1500, 2), (2000, 30, 258), (1300, 700, 513)])
+def test_gradient_at_borders(rows, vocab, cols):
+    say("borders", rows, vocab, cols)
+    rng = np.random.default_rng(rows * 3 + cols)
+    for i, dtype in enumerate(DTYPES):
+        t = tokens_of(rng, rows, vocab)
+        a = check_grad(np.random.default_rng(8), rows, vocab, cols, dtype, t, add=i != 1, pad=i, in_place=i == 2)
+        b = check_grad(np.random.default_rng(8), rows, vocab, cols, dtype, t, add=i != 1, pad=i, in_place=i == 2)
+        same_bits(a, b, "twice")
