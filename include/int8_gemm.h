@@ -571,8 +571,10 @@ int gemm_i8_logprobs(const int8_t* QA, int64_t lda, const float* s_row, const in
  * of the vocabulary whose G has at most 3 * 2^26 values (or 256 columns).
  * Codes are exact; T = s_row[i] G[i,j] s_col[j] is rounded to f16 for bf16
  * gradients (2^-11 of the value) and to a sum of two f16 (2^-22) for f32 and
- * f16 ones, scaled by a power of two of max (|g_logprob| + |g_lse|) s_row
- * max s_col, so that a value is off by at most 2^-37 of that maximum besides.
+ * f16 ones, scaled by powers of two of its row and column, so that a value is
+ * off by at most 2^-37 of (|g_logprob[i]| + |g_lse[i]|) s_row[i] s_col[j]
+ * besides (a row or column more than 2^24 below the largest one: as if it were
+ * 2^24 below).
  * Scales have to be positive, as the quantize passes write them.  As in
  * token_logprobs_bwd, a row with |lse| >= 2^24 gets 0 (and adds nothing to
  * dBt).  A NaN in a row's lse, gradients or scale makes its row of dA and all

@@ -12,9 +12,8 @@
 // and the codes are exact in f16, so T is all that is rounded for the matrix
 // cores: to f16 for bf16 gradients (2^-11 of each value, where the outputs' own
 // rounding is 2^-8), to a sum of two f16 (2^-22) for f32 and f16 ones.  (Two bf16
-// would be 2^-16 in the same time.)  T is scaled by a power of two that puts
-// max (|g| + |gl|) s_row max s_col between 2^12 and 2^14, so that the least
-// spacing of f16 is at most 2^-36 of that maximum.
+// would be 2^-16 in the same time.)  Powers of two of each row and column keep it
+// from f16's ends (see the backward part).
 //
 // Forward: a workgroup multiplies a tile of vocabulary rows by a tile of
 // tokens; the vocabulary is the accumulators' row dimension, so that a lane
@@ -483,59 +482,103 @@ __global__ void __launch_bounds__(256) head_join_kernel(const JoinArgs p) {
 }
 
 // ---- backward ---------------------------------------------------------------------
-// T's power of two, from parts of the two maxima: max |T| is at most 2^14.
-constexpr int kBounds = 64;
+// Powers of two.  With r = |g_i| + |gl_i|, a row's (|g| + |gl|) s_row is below
+// 2^(exponent r + exponent s_row), E of the rows at most, and s_col below its
+// power, F at most.  T_ij is multiplied by 2^(15 - E + a_i - F + b_j), where a_i
+// and b_j are how far the row and the column are below E and F, and the codes of
+// row i (j) by 2^-a_i (2^-b_j), which is exact up to 2^-24: a_i and b_j are 24 at
+// most.  So the least spacing of f16 is 2^-36 of a value's own (|g| + |gl|) s_row
+// s_col, not of the largest: rows of small numbers (of zeros, whose scale is the
+// least one) have gradients as exact as others.  |T| is at most 2^15, times what
+// the rounding of a log-sum-exp below 2^24 makes of p, 1.65 at most.
+constexpr int kBounds = 64, kMostShift = 24;
 struct Bound {
-  float row, col;              // largest (|g| + |gl|) s_row and s_col of a part
+  uint32_t row, col;           // E + 1024 and F + 1024 of a part, 0: none
 };
-__device__ __forceinline__ float t_scale(const Bound* bounds) {
-  const Bound b = bounds[threadIdx.x & 63];
-  const float row = __uint_as_float(lanes_max_u32<64>(__float_as_uint(b.row)));
-  const float col = __uint_as_float(lanes_max_u32<64>(__float_as_uint(b.col)));
-  if (!(row > 0.0f && row < __builtin_inff() && col > 0.0f && col < __builtin_inff())) return 1.0f;
-  const int e = 14 - __builtin_amdgcn_frexp_expf(row) - __builtin_amdgcn_frexp_expf(col);   // row < 2^frexp_exp(row)
-  return __builtin_ldexpf(1.0f, e < -120 ? -120 : e > 120 ? 120 : e);
+struct Scale {                 // acc / m 2^x is the gradient
+  float m;
+  int x;
+};
+struct RowArgs {
+  const int64_t* targets;
+  const float *g, *gl, *s_row, *s_col;
+  int M, N;
+};
+struct TokenRow {
+  float g, gl, s;              // g 0 for a row without a token
+  int eg, es;
+  __device__ TokenRow(const RowArgs& p, int64_t i) : g(0.0f), gl(p.gl ? p.gl[i] : 0.0f), s(p.s_row[i]) {
+    if (p.g) {
+      const int64_t t = p.targets[i];
+      const float at_t = p.g[i];
+      g = t >= 0 && t < p.N ? at_t : 0.0f;
+    }
+    eg = __builtin_amdgcn_frexp_expf(fabsf(g) + fabsf(gl));
+    es = __builtin_amdgcn_frexp_expf(s);
+  }
+  __device__ uint32_t bound() const {            // (of a finite row that has a gradient)
+    const float r = fabsf(g) + fabsf(gl);
+    return r > 0.0f && r < __builtin_inff() && s > 0.0f && s < __builtin_inff() ? (uint32_t)(eg + es + 1024) : 0u;
+  }
+};
+__device__ __forceinline__ uint32_t col_bound(float s) {
+  return s > 0.0f && s < __builtin_inff() ? (uint32_t)(__builtin_amdgcn_frexp_expf(s) + 1024) : 0u;
+}
+// Of a workgroup's part of the rows; the same in all its threads.
+__device__ Bound bound_of(const RowArgs& p, int part, int parts) {
+  __shared__ uint32_t most[2][4];
+  const int tid = threadIdx.x;
+  uint32_t row = 0, col = 0;
+  const int64_t first = (int64_t)part * 256 + tid, step = parts * 256;
+  for (int64_t i = first; i < p.M; i += 4 * step)          // (the last row's again behind it)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) row = max(row, TokenRow(p, min(i + q * step, (int64_t)p.M - 1)).bound());
+  for (int64_t j = first; j < p.N; j += 4 * step)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) col = max(col, col_bound(p.s_col[min(j + q * step, (int64_t)p.N - 1)]));
+  row = lanes_max_u32<64>(row);
+  col = lanes_max_u32<64>(col);
+  most[0][tid >> 6] = row;
+  most[1][tid >> 6] = col;
+  __syncthreads();
+  return Bound{max(max(most[0][0], most[0][1]), max(most[0][2], most[0][3])),
+               max(max(most[1][0], most[1][1]), max(most[1][2], most[1][3]))};
+}
+__global__ void __launch_bounds__(256) head_bounds_kernel(const RowArgs p, Bound* bounds) {
+  const Bound b = bound_of(p, blockIdx.x, kBounds);
+  if (threadIdx.x == 0) bounds[blockIdx.x] = b;
 }
 
-// Before the pieces, in one launch: the parts of the bound, and both operands'
-// codes as f16 blocks of 16 rows (the contraction) by 32 columns, 1 KiB in the
-// order of a fragment: lane l holds column l%32, rows 8 (l/32) ... + 7.  Zero
-// beyond `rows` and `cols`.
+// Before the pieces: both operands' codes as f16 blocks of 16 rows (the
+// contraction) by 32 columns, 1 KiB in the order of a fragment: lane l holds
+// column l%32, rows 8 (l/32) ... + 7.  Zero beyond the rows and `cols`.  And what
+// the products need of each row.
+constexpr int kOwnBounds = 2048;               // rows of both sides that every workgroup looks through itself: no launch before
 struct PackArgs {
   LogitArgs l;
-  const int64_t* targets;
-  const float *g, *gl;
-  Bound* bounds;
+  RowArgs rows;
+  const Bound* bounds;         // null: each workgroup's own
   int blocks_a, blocks_b;      // blocks of 16 rows
   int KB;                      // blocks of 32 columns
   v4i *out_a, *out_b;          // [blocks][KB][64]
+  float *share, *given;        // of a token, in T: (gl - g) s_row and g s_row times their power of two
+  float* col;                  // of a vocabulary row, in T: s_col times its power of two
+  Scale *scale_a, *scale_b;
 };
 __global__ void __launch_bounds__(256) head_prepare_kernel(const PackArgs p) {
   const int tid = threadIdx.x;
-  if (blockIdx.x < kBounds) {
-    float row = 0.0f, col = 0.0f;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + tid; i < p.l.M; i += kBounds * 256) {
-      float a = p.gl ? fabsf(p.gl[i]) : 0.0f;
-      if (p.g) {
-        const int64_t t = p.targets[i];
-        if (t >= 0 && t < p.l.N) a += fabsf(p.g[i]);
-      }
-      row = fmaxf(row, a * p.l.s_row[i]);
-    }
-    for (int64_t j = (int64_t)blockIdx.x * 256 + tid; j < p.l.N; j += kBounds * 256) col = fmaxf(col, p.l.s_col[j]);
-    __shared__ uint32_t most[2][4];
-    const uint32_t r = lanes_max_u32<64>(__float_as_uint(row)), c = lanes_max_u32<64>(__float_as_uint(col));
-    most[0][tid >> 6] = r;
-    most[1][tid >> 6] = c;
-    __syncthreads();
-    if (tid == 0)
-      p.bounds[blockIdx.x] = Bound{__uint_as_float(max(max(most[0][0], most[0][1]), max(most[0][2], most[0][3]))),
-                                   __uint_as_float(max(max(most[1][0], most[1][1]), max(most[1][2], most[1][3])))};
-    return;
+  Bound most;
+  if (p.bounds) {
+    most = p.bounds[tid & 63];
+    most.row = lanes_max_u32<64>(most.row);
+    most.col = lanes_max_u32<64>(most.col);
+  } else {
+    most = bound_of(p.rows, 0, 1);
   }
+  const int E = most.row ? (int)most.row - 1024 : 0, F = most.col ? (int)most.col - 1024 : 0;
   const int c4 = tid & 7, half = (tid >> 3) & 1;           // 16 threads a block, 4 columns and 8 rows each
   const int64_t blocks = (int64_t)(p.blocks_a + (int64_t)p.blocks_b) * p.KB;
-  for (int64_t at = (int64_t)(blockIdx.x - kBounds) * 16 + (tid >> 4); at < blocks; at += (int64_t)(gridDim.x - kBounds) * 16) {
+  for (int64_t at = (int64_t)blockIdx.x * 16 + (tid >> 4); at < blocks; at += (int64_t)gridDim.x * 16) {
     const bool a = at < (int64_t)p.blocks_a * p.KB;
     const int64_t block = a ? at : at - (int64_t)p.blocks_a * p.KB;
     const int8_t* Q = a ? p.l.A : p.l.B;
@@ -544,6 +587,29 @@ __global__ void __launch_bounds__(256) head_prepare_kernel(const PackArgs p) {
     const int64_t b16 = block / p.KB;
     const int kb = (int)(block - b16 * p.KB);
     const int k = kb * 32 + c4 * 4;
+    // the 8 threads of a half have a row each
+    const int64_t own = b16 * 16 + half * 8 + c4;
+    int shift = 0;
+    if (a && own < rows) {
+      const TokenRow r(p.rows, own);
+      const int below = E - r.eg - r.es;
+      shift = min(max(below, 0), kMostShift);
+      if (kb == 0) {
+        const float f = __builtin_ldexpf(r.s, 15 - r.es + min(shift - below, 0));
+        p.share[own] = __builtin_ldexpf(r.gl - r.g, -r.eg) * f;
+        p.given[own] = __builtin_ldexpf(r.g, -r.eg) * f;
+        p.scale_a[own] = Scale{__builtin_amdgcn_frexp_mantf(r.s), E + F - 15 - shift - r.es};
+      }
+    } else if (own < rows) {
+      const float c = p.l.s_col[own];
+      const int e = __builtin_amdgcn_frexp_expf(c);
+      shift = min(max(F - e, 0), kMostShift);
+      if (kb == 0) {
+        p.col[own] = __builtin_ldexpf(c, shift - F);
+        p.scale_b[own] = Scale{__builtin_amdgcn_frexp_mantf(c), E + F - 15 - shift - e};
+      }
+    }
+    const float factor = __builtin_ldexpf(1.0f, -shift);
     uint32_t w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -554,13 +620,16 @@ __global__ void __launch_bounds__(256) head_prepare_kernel(const PackArgs p) {
         if (p.l.K - k < 4) w[e] &= (1u << (8 * (p.l.K - k))) - 1;
       }
     }
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = __shfl(factor, (tid & 56) + e, 64);
     v4i* out = (a ? p.out_a : p.out_b) + block * 64 + half * 32 + c4 * 4;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       v4i o;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const v2f v = {(float)(int8_t)(w[2 * e] >> (8 * c)), (float)(int8_t)(w[2 * e + 1] >> (8 * c))};
+        const v2f v = {(float)(int8_t)(w[2 * e] >> (8 * c)) * f[2 * e], (float)(int8_t)(w[2 * e + 1] >> (8 * c)) * f[2 * e + 1]};
         o[e] = __builtin_bit_cast(int, __builtin_convertvector(v, v2h));
       }
       out[c] = o;
@@ -570,12 +639,11 @@ __global__ void __launch_bounds__(256) head_prepare_kernel(const PackArgs p) {
 
 struct WeightArgs {            // T of a piece
   LogitArgs l;
-  const int64_t* targets;
-  const float *lse, *g, *gl;   // g or gl may be null (0)
+  const int64_t* targets;      // null: no row has a token
+  const float *lse, *share, *given, *col;
   int v0, c0;                  // the first vocabulary row, and its place in the piece
   int tiles_v, tiles_t;        // of the piece
   int C16;                     // blocks of 16 vocabulary rows in a row of blocks
-  const Bound* bounds;
   int64_t first;               // tiles of the launch
   int count;
   int tb_log;                  // TB = 2^tb_log blocks of 32 tokens in a tile of dA's product
@@ -589,8 +657,8 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
   constexpr int FV = Tile::FV, FT = Tile::FT;
   __shared__ __attribute__((aligned(1024))) int8_t smem[Tile::LDS];
   constexpr int TOKENS = Tile::TOKENS;
-  __shared__ __attribute__((aligned(16))) float sc[2][BV];
-  __shared__ float rows[2][4][TOKENS];                     // s_row, the log-sum-exp, g, gl
+  __shared__ __attribute__((aligned(16))) float sc[2][BV], factor[2][BV];
+  __shared__ float rows[2][4][TOKENS];                     // s_row, the log-sum-exp, share, given
   __shared__ int64_t targets[2][TOKENS];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wv = wave / WT, wt = wave % WT;
   Walk walk((int)p.first, p.count, p.tiles_v * p.tiles_t);
@@ -601,16 +669,16 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
   const auto start = [&](int turn) {
     const int t0 = tt * BT;
     Tile::template load_values<BV>(p.l.s_col, p.v0 + tv * BV, p.l.N, sc[turn]);
+    Tile::template load_values<BV>(p.col, p.v0 + tv * BV, p.l.N, factor[turn]);
     Tile::template load_values<TOKENS>(p.l.s_row, t0, p.l.M, rows[turn][0]);
     Tile::template load_values<TOKENS>(p.lse, t0, p.l.M, rows[turn][1]);
-    if (p.g) {
-      Tile::template load_values<TOKENS>(p.g, t0, p.l.M, rows[turn][2]);
+    Tile::template load_values<TOKENS>(p.share, t0, p.l.M, rows[turn][2]);
+    if (p.targets) {
+      Tile::template load_values<TOKENS>(p.given, t0, p.l.M, rows[turn][3]);
       Tile::template load_values<2 * TOKENS>(p.targets, 2 * (int64_t)t0, 2 * (int64_t)p.l.M, targets[turn]);
     }
-    if (p.gl) Tile::template load_values<TOKENS>(p.gl, t0, p.l.M, rows[turn][3]);
     Tile::start(p.l, smem, p.v0 + tv * BV, t0, src);
   };
-  const float scale = t_scale(p.bounds);
   start(0);
   bool before = false;
   for (int turn = 0;; turn ^= 1) {
@@ -637,21 +705,16 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
       if (t0 + r < p.l.M) {
         sr = rows[turn][0][r];
         const float lse = rows[turn][1][r];
-        int64_t at = -1;
-        float g = 0.0f;
-        if (p.g) {
-          at = targets[turn][r];
-          if (at < 0 || at >= p.l.N) at = -1;
-          else g = rows[turn][2][r];
-        }
         // a row whose log-sum-exp is off by a factor e or more in p has no gradient
         if (!(fabsf(lse) >= 16777216.0f)) {
           lse2 = lse * kLog2e;
           const float rest = __builtin_fmaf(lse, kLog2e, -lse2);         // exp2(-rest) is the row's factor
-          const float f = sr * scale;
-          share = ((p.gl ? rows[turn][3][r] : 0.0f) - g) * __builtin_amdgcn_exp2f(-rest) * f;
-          given = g * f;
-          if (at >= v0 && at < v0 + BV) target = (int)(at - v0);
+          share = rows[turn][2][r] * __builtin_amdgcn_exp2f(-rest);
+          if (p.targets) {
+            const int64_t at = targets[turn][r];
+            given = rows[turn][3][r];
+            if (at >= v0 && at < v0 + BV && at < p.l.N) target = (int)(at - v0);
+          }
         }
       }
       const int tb = tile_t * (BT / 32) + wt * FT + j;
@@ -683,7 +746,7 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const v4f s4 = *reinterpret_cast<const v4f*>(col + r0 + 8 * q);
+          const v4f s4 = *reinterpret_cast<const v4f*>(factor[turn] + r0 + 8 * q);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const v2f v = {y[4 * q + 2 * e] * s4[2 * e], y[4 * q + 2 * e + 1] * s4[2 * e + 1]};
@@ -719,7 +782,6 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
 // contraction in stages of 32.
 struct GradArgs {
   const v4i* T;
-  const Bound* bounds;
   size_t plane;                // TERMS 2
   int C16;
   int KB, tiles_k;
@@ -733,7 +795,7 @@ struct GradArgs {
     void* out;                 // the gradient's rows of the piece, `rows` of them exist
     int64_t ld;
     int rows;
-    const float* scale;        // of its rows
+    const Scale* scale;        // of its rows
   } a, b;                      // dA: contraction over the piece's vocabulary; dBt: over the tokens
   int units_a, units_b;
   int first;                   // place of the launch in every XCD's list
@@ -766,10 +828,10 @@ __device__ __forceinline__ void store4(T* to, int n, const float (&v)[4]) {
   }
 }
 // Values k ... k + 3 of a gradient's row, n of them.
-__device__ __forceinline__ void store_grad(void* out, int64_t ld, int dtype, int64_t row, int k, int n, v4f acc, float scale) {
+__device__ __forceinline__ void store_grad(void* out, int64_t ld, int dtype, int64_t row, int k, int n, v4f acc, Scale scale) {
   float v[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = acc[e] / scale;
+  for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(acc[e] / scale.m, scale.x);
   if (dtype == DT_F32) store4(static_cast<float*>(out) + row * ld + k, n, v);
   else if (dtype == DT_BF16) store4(static_cast<bf16_t*>(out) + row * ld + k, n, v);
   else store4(static_cast<f16_t*>(out) + row * ld + k, n, v);
@@ -972,13 +1034,12 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
     }
     return;
   }
-  const float factor = t_scale(p.bounds);
 #pragma unroll
   for (int i = 0; i < FA; ++i)
 #pragma unroll
     for (int j = 0; j < FC; ++j) {
       const int col = ct * CT + (wc * FC + j) * 32 + (lane & 31);
-      const float scale = col < s.rows ? s.scale[col] * factor : 1.0f;
+      const Scale scale = col < s.rows ? s.scale[col] : Scale{1.0f, 0};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const v4f v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
@@ -1023,10 +1084,9 @@ struct FinishArgs {
     void* out;
     int64_t ld;
     int rows;
-    const float* scale;
+    const Scale* scale;
   } side[2];
   int64_t groups;              // workgroups of side[0]; those behind take side[1]
-  const Bound* bounds;
   int tiles_k, dtype, cols;
 };
 // The planes' sum, in their order, by its row's scale.
@@ -1036,7 +1096,6 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const FinishArgs p) {
   const int64_t group = second ? blockIdx.x - p.groups : blockIdx.x, groups = second ? gridDim.x - p.groups : p.groups;
   const size_t size = (size_t)256 * s.CT, all = (size_t)s.tiles * p.tiles_k * size;
   const int WC = 8 / s.WK, FC = s.CT / 32 / WC, FA = 8 / s.WK;
-  const float factor = t_scale(p.bounds);
   for (size_t at = ((size_t)group * 256 + threadIdx.x) * 4; at < all; at += (size_t)groups * 1024) {
     const int tile = (int)(at / size), in = (int)(at % size) / 4;
     const int kt = tile % p.tiles_k, ct = tile / p.tiles_k;
@@ -1047,14 +1106,14 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const FinishArgs p) {
     v4f v = *reinterpret_cast<const v4f*>(s.planes + at);
 #pragma unroll 8
     for (int n = 1; n < s.splits; ++n) v += *reinterpret_cast<const v4f*>(s.planes + n * all + at);
-    store_grad(s.out, s.ld, p.dtype, col, k, p.cols - k, v, s.scale[col] * factor);
+    store_grad(s.out, s.ld, p.dtype, col, k, p.cols - k, v, s.scale[col]);
   }
 }
 
 // The gradient of no tokens.
 __global__ void __launch_bounds__(256) head_zero_kernel(void* out, int64_t ld, int dtype, int64_t rows, int cols) {
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int k = threadIdx.x * 4; k < cols; k += 1024) store_grad(out, ld, dtype, r, k, cols - k, v4f{0, 0, 0, 0}, 1.0f);
+    for (int k = threadIdx.x * 4; k < cols; k += 1024) store_grad(out, ld, dtype, r, k, cols - k, v4f{0, 0, 0, 0}, Scale{1.0f, 0});
 }
 
 constexpr int64_t kMostGroups = int64_t(1) << 22;   // workgroups of a launch
@@ -1125,7 +1184,8 @@ struct BwdPlan {
   int pieces, tiles_k, sa, sb;
   int KB;                      // 32-blocks of K, in pairs
   size_t code_a, code_b, t, plane_a, plane_b;   // bytes
-  size_t bytes() const { return kBounds * sizeof(Bound) + code_a + code_b + t + plane_a + plane_b; }
+  size_t rows, cols;           // what is kept of tokens and of vocabulary rows, in whole 256s
+  size_t bytes() const { return kBounds * sizeof(Bound) + rows * 16 + cols * 12 + code_a + code_b + t + plane_a + plane_b; }
 };
 // When units of two lengths are done on the 32 CUs of an XCD, which takes an
 // eighth of them: the longer ones first, then each CU the next one as it
@@ -1194,6 +1254,8 @@ BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, int dtype) {
         }
       }
   }
+  b.rows = align256((size_t)M);
+  b.cols = align256((size_t)N);
   b.KB = up(K, 64) * 2;
   b.code_a = (size_t)b.Mp * b.KB * 64;
   b.code_b = (size_t)b.C * b.pieces * b.KB * 64;
@@ -1268,7 +1330,11 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
   const BwdPlan b = bwd_plan(a.M, a.N, a.K, g.dtype);
   char* at = static_cast<char*>(ws);
   Bound* bounds = reinterpret_cast<Bound*>(at);
-  v4i* code_a = reinterpret_cast<v4i*>(at += kBounds * sizeof(Bound));
+  Scale* scale_a = reinterpret_cast<Scale*>(at += kBounds * sizeof(Bound));
+  Scale* scale_b = scale_a + b.rows;
+  float* share = reinterpret_cast<float*>(scale_b + b.cols);
+  float *given = share + b.rows, *col = given + b.rows;
+  v4i* code_a = reinterpret_cast<v4i*>(at += b.rows * 16 + b.cols * 12);
   v4i* code_b = reinterpret_cast<v4i*>(at += b.code_a);
   v4i* T = reinterpret_cast<v4i*>(at += b.code_b);
   float* plane_a = reinterpret_cast<float*>(at += b.t);
@@ -1277,17 +1343,23 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
   const int C16 = (int)(b.C / 16);
   const size_t plane = (size_t)b.Mp * b.C / 8;
   const LogitArgs l = logit_args(a);
-  PackArgs k{l, g.targets, g.g_logprob, g.g_lse, bounds, (int)(b.Mp / 16), (int)(b.C * b.pieces / 16), KB, code_a, code_b};
-  const int64_t groups = ((int64_t)(k.blocks_a + (int64_t)k.blocks_b) * KB + 15) / 16;
-  hipLaunchKernelGGL(head_prepare_kernel, dim3(kBounds + (unsigned)(groups < kMostGroups ? groups : kMostGroups)), dim3(256), 0, stream, k);
+  const int64_t* targets = g.g_logprob ? g.targets : nullptr;
+  const RowArgs rows{targets, g.g_logprob, g.g_lse, a.s_row, a.s_col, (int)a.M, (int)a.N};
+  const bool own = a.M + a.N <= kOwnBounds;
+  if (!own) hipLaunchKernelGGL(head_bounds_kernel, dim3(kBounds), dim3(256), 0, stream, rows, bounds);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  PackArgs k{l,      rows,   own ? nullptr : bounds, (int)(b.Mp / 16), (int)(b.C * b.pieces / 16), KB, code_a, code_b, share, given, col,
+             scale_a, scale_b};
+  const int64_t groups = ((int64_t)(k.blocks_a + (int64_t)k.blocks_b) * KB + 15) / 16;
+  hipLaunchKernelGGL(head_prepare_kernel, dim3((unsigned)(groups < kMostGroups ? groups : kMostGroups)), dim3(256), 0, stream, k);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
   const auto finish_side = [&](bool a_side, const GradArgs::Side& s) {
     return FinishArgs::Side{s.planes, s.splits, s.tiles, a_side ? b.ca : b.cb, a_side && b.few ? 8 : 2, s.out, s.ld, s.rows, s.scale};
   };
   for (int piece = 0; piece < b.pieces; ++piece) {
-    const int64_t v0 = piece * b.C, rows = a.N - v0 < b.C ? a.N - v0 : b.C;
-    WeightArgs w{l, g.targets, g.lse, g.g_logprob, g.g_lse, (int)v0, 0, 0, 0, C16, bounds, 0, 0, b.tb_log, T, plane};
+    const int64_t v0 = piece * b.C, n_rows = a.N - v0 < b.C ? a.N - v0 : b.C;
+    WeightArgs w{l, targets, g.lse, share, given, col, (int)v0, 0, 0, 0, C16, 0, 0, b.tb_log, T, plane};
     const LogitPlan pl = logit_plan(b.Mp, b.C, a.K);
     const int64_t wide_cols = b.few ? 0 : pl.wide;         // (few tokens: T has 64)
     for (const bool wide : {true, false}) {
@@ -1309,7 +1381,6 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
 
     GradArgs p{};
     p.T = T;
-    p.bounds = bounds;
     p.plane = plane;
     p.C16 = C16;
     p.KB = KB;
@@ -1317,16 +1388,16 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
     p.dtype = g.dtype;
     p.cols = (int)a.K;
     const auto side = [](const v4i* codes, int64_t tiles, int64_t depth, int splits, float* planes, int add, void* out, int64_t ld,
-                         int64_t n, const float* scale) {
+                         int64_t n, const Scale* scale) {
       // (whole blocks of 256: a range has 8 stages at least; 64 tokens are 2)
       const int stages = (int)(depth / 32), per = stages < 8 ? stages : up(stages / 8, splits) * 8;
       return GradArgs::Side{codes, (int)tiles, up(stages, per), stages, per, planes, add, out, ld, (int)n, scale};
     };
     const int64_t esize = g.dtype == DT_F32 ? 4 : 2;
     p.a = side(code_b + (size_t)piece * (b.C / 16) * KB * 64, b.Mp / b.ca, b.C, b.sa, b.plane_a > 0 ? plane_a : nullptr, piece > 0, g.dA,
-               g.ldda, a.M, a.s_row);
-    p.b = side(code_a, up(rows, b.cb), b.Mp, b.sb, b.sb > 1 ? plane_b : nullptr, 0,
-               g.dB ? static_cast<char*>(g.dB) + v0 * g.lddb * esize : nullptr, g.lddb, rows, a.s_col + v0);
+               g.ldda, a.M, scale_a);
+    p.b = side(code_a, up(n_rows, b.cb), b.Mp, b.sb, b.sb > 1 ? plane_b : nullptr, 0,
+               g.dB ? static_cast<char*>(g.dB) + v0 * g.lddb * esize : nullptr, g.lddb, n_rows, scale_b + v0);
     p.units_a = g.dA ? p.tiles_k * p.a.tiles * p.a.splits : 0;
     p.units_b = g.dB ? p.tiles_k * p.b.tiles * p.b.splits : 0;
     const int most = up(p.units_a, 8) + up(p.units_b, 8);    // of an XCD
@@ -1336,7 +1407,6 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     FinishArgs f{};
-    f.bounds = bounds;
     f.tiles_k = b.tiles_k;
     f.dtype = g.dtype;
     f.cols = (int)a.K;

@@ -63,14 +63,15 @@ def lse_bound(x):
     return U32 * (80 + far + 0.23 * (np.abs(lse) + size) + np.abs(lse)) * 1.01
 
 
-def head_grads(qa, sa, qb, sb, t, lse, g, gl, terms):
+def head_grads(qa, sa, qb, sb, t, lse, g, gl, terms, own=False):
     """(dA, dBt) in 64 bits for the given binary32 lse, and how far the computed
     ones may be before their outputs' rounding.
 
     A value of T: p's argument to half a step (|t| ln 2 units of U32, |t| the
     distance from lse in powers of two), the exponential and the row's factor
     2 + 2, products and the given token's sum 8; its rounding to one f16 2^-11 or
-    to two 2^-22, and 2^-37 of the largest (|g| + |gl|) s_row s_col.  Sums: one
+    to two 2^-22, and 2^-37 of the largest (|g| + |gl|) s_row s_col (with own: of
+    the value's own, where all are within 2^24 of the largest).  Sums: one
     binary32 rounding for each 16 products and term, planes and scaling 8.
     """
     x = logits(qa, sa, qb, sb)
@@ -91,7 +92,8 @@ def head_grads(qa, sa, qb, sb, t, lse, g, gl, terms):
     size = size + np.abs(one)
     a, b = sa[:, None].astype(np.float64) * qa, sb[:, None].astype(np.float64) * qb
     away = np.where(p > 0, np.abs(x - lse[:, None]), 0.0)
-    largest = ((np.abs(gi) + np.abs(li)) * sa).max(initial=0.0) * sb.max(initial=0.0)
+    bound_a = (np.abs(gi) + np.abs(li)) * sa
+    largest = bound_a[:, None] * sb[None, :] if own else bound_a.max(initial=0.0) * sb.max(initial=0.0)
     rounding = 2.0 ** -11 if terms == 1 else 2.0 ** -22
     # in values of G s_row s_col
     offT = size * sa[:, None] * sb[None, :] * (U32 * (away + 12) + rounding) + 2.0 ** -37 * largest

@@ -12,7 +12,7 @@ from int8_gemm_amd import build as B
 from test_isa_guard import FORBIDDEN, compile_asm, have_hipcc, scan
 
 SOURCES = ["head.hip", "embedding.hip"]
-KERNELS = ["head_fwd_kernel", "head_join_kernel", "head_prepare_kernel", "head_weights_kernel", "head_grads_kernel",
+KERNELS = ["head_fwd_kernel", "head_join_kernel", "head_bounds_kernel", "head_prepare_kernel", "head_weights_kernel", "head_grads_kernel",
            "head_finish_kernel", "head_zero_kernel", "embedding_kernel", "embedding_sort_kernel", "embedding_merge_kernel",
            "embedding_sum_kernel", "embedding_join_kernel", "embedding_few_kernel", "embedding_rank_kernel"]
 

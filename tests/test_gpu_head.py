@@ -375,3 +375,33 @@ def test_workgroups_of_several_tiles(k, dtype):
     size = 64.0 / m if dtype == "f16" else 1.0 / m
     check_grads(qa, sa, qb, sb, t, host(lse).astype(np.float32), (-size * rng.uniform(0.5, 1.5, m)).astype(np.float32),
                 (size * 0.1 * rng.standard_normal(m)).astype(np.float32), dtype)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("m,n,k", [(200, 600, 70), (700, 3000, 130)])
+def test_gradients_of_rows_of_very_different_size(m, n, k, dtype):
+    """A row's gradient is as exact as if all scales and gradients were its own: zero rows have the least scale
+    (1e-8), others 2^18 times less than the largest, and some tokens next to no gradient.
+
+    Against the formula with T's error relative to each value's own (|g| + |gl|) s_row s_col: 2^-37 of it, where the
+    scales and gradients lie within 2^24 of the largest."""
+    say("sizes", m, n, k, dtype)
+    rng = np.random.default_rng(m)
+    qa, sa, qb, sb, t = case(rng, m, n, k)
+    sa, sb = sa.copy(), sb.copy()
+    sb[::7] *= np.float32(2.0 ** -18)
+    qb[3::11], sb[3::11] = 0, np.float32(1e-8)
+    qa[5::13], sa[5::13] = 0, np.float32(1e-8)
+    lse = R.logsumexp(R.logits(qa, sa, qb, sb)).astype(np.float32)
+    size = 64.0 / m if dtype == "f16" else 1.0 / m
+    gg = (-size * rng.uniform(0.5, 1.5, m)).astype(np.float32)
+    gg[::5] *= np.float32(2.0 ** -8)
+    gl = (size * 0.1 * rng.standard_normal(m)).astype(np.float32) * (gg / gg.min())
+    A, B = R.padded(qa), R.padded(qb)
+    SA, SB, T, L, G, GL = dev(sa, sb, t, lse, gg, gl.astype(np.float32))
+    dA, dB = g.gemm_i8_logprobs_bwd(A, SA, B, SB, T, L, G, GL, DTYPES[dtype])
+    wa, wb, oa, ob = R.head_grads(qa, sa, qb, sb, t, lse, gg, gl.astype(np.float32), TERMS[dtype], own=True)
+    h, least = half_step(DTYPES[dtype]), tiny(DTYPES[dtype])
+    within(host(dA), wa, oa + (np.abs(wa) + oa) * h * 1.001 + least, "dA")
+    within(host(dB), wb, ob + (np.abs(wb) + ob) * h * 1.001 + least, "dBt")
+    assert (host(dB)[3::11] != 0).any(axis=1).all()
