@@ -528,6 +528,7 @@ int token_logprobs_bwd(const void* logits, uint32_t dtype, int64_t rows, int64_t
  * for gemm_i8_blockscaled.
  * ------------------------------------------------------------------------ */
 #define I8G_HEAD_ROWS_MAX 1073741824   /* 2^30 */
+#define I8G_EMBEDDING_COLS_MAX 1073741824   /* 2^30 */
 
 /*
  * gemm_i8_logprobs -- token_logprobs of the output of gemm_i8_blockscaled,
@@ -599,7 +600,8 @@ int gemm_i8_logprobs_bwd(const int8_t* QA, int64_t lda, const float* s_row, cons
  *            nothing.
  *   Y, ldy   rows x cols of dtype; it overlaps no input.
  * Errors: I8G_EINVAL (null pointer, unknown dtype, negative or too large size,
- * leading dimension < cols, misaligned pointer), I8G_EHIP.
+ * cols above I8G_EMBEDDING_COLS_MAX, leading dimension < cols, misaligned
+ * pointer), I8G_EHIP.
  */
 int embedding(const void* W, uint32_t dtype, int64_t vocab, int64_t cols, int64_t ldw, const int64_t* tokens,
               int64_t rows, float alpha, const void* P, int64_t n_pos, int64_t ldp, const int64_t* positions,

@@ -544,7 +544,7 @@ static int embed(const void* W, int64_t w_bytes, const float* scale, uint32_t dt
                  const int64_t* tokens, int64_t rows, float alpha, const void* P, int64_t n_pos, int64_t ldp,
                  const int64_t* positions, void* Y, int64_t ldy, void* stream) {
   const int64_t bytes = dtype_bytes(dtype);
-  if (bytes == 0 || bad_sizes(rows, cols) || bad_sizes(vocab, n_pos)) return I8G_EINVAL;
+  if (bytes == 0 || bad_sizes(rows, cols) || bad_sizes(vocab, n_pos) || cols > I8G_EMBEDDING_COLS_MAX) return I8G_EINVAL;
   if (bad_matrix(W, vocab, cols, ldw, w_bytes ? w_bytes : bytes) || bad_matrix(Y, rows, cols, ldy, bytes)) return I8G_EINVAL;
   if (bad_i64(tokens) || bad_i64(positions) || bad_f32(scale) || (rows > 0 && !tokens)) return I8G_EINVAL;
   if (P && (bad_matrix(P, n_pos, cols, ldp, bytes) || (rows > 0 && !positions))) return I8G_EINVAL;
@@ -567,7 +567,7 @@ int embedding_i8(const int8_t* Q, int64_t ldq, const float* scale, int64_t vocab
 }
 
 size_t embedding_bwd_workspace_bytes(int64_t rows, int64_t cols) {
-  if (rows <= 0 || cols <= 0 || bad_sizes(rows, cols)) return 256;
+  if (rows <= 0 || cols <= 0 || bad_sizes(rows, cols) || cols > I8G_EMBEDDING_COLS_MAX) return 256;
   return embedding_bwd_bytes(rows, cols);
 }
 
@@ -575,7 +575,7 @@ int embedding_bwd(const void* dY, uint32_t dtype, int64_t rows, int64_t cols, in
                   int64_t vocab, float alpha, const float* add, int64_t ldadd, float* dW, int64_t lddw, void* workspace,
                   size_t workspace_bytes, void* stream) {
   const int64_t bytes = dtype_bytes(dtype);
-  if (bytes == 0 || bad_sizes(rows, cols) || bad_sizes(vocab, 0)) return I8G_EINVAL;
+  if (bytes == 0 || bad_sizes(rows, cols) || bad_sizes(vocab, 0) || cols > I8G_EMBEDDING_COLS_MAX) return I8G_EINVAL;
   if (bad_matrix(dY, rows, cols, lddy, bytes) || bad_matrix(dW, vocab, cols, lddw, 4)) return I8G_EINVAL;
   if (bad_i64(tokens) || (rows > 0 && !tokens)) return I8G_EINVAL;
   if (add && (bad_matrix(add, vocab, cols, ldadd, 4) || bad_in_place(dW, lddw, add, ldadd, vocab, cols, 4))) return I8G_EINVAL;

@@ -132,3 +132,12 @@ def test_python_arguments():
         g.embedding_bwd(x, t, 5)
     with pytest.raises(ValueError, match="float32, bfloat16 or float16"):
         g.embedding_bwd(q, t, 5)
+
+
+def test_embedding_columns(lib):
+    """Rows of up to 2^30 columns: a lane's columns are counted in 32 bits."""
+    most = 1 << 30
+    assert lib.embedding(A, 0, 10, most + 1, most + 1, A, 4, 1.0, None, 0, 0, None, A, most + 1, None) == EINVAL
+    assert lib.embedding_i8(A, most + 1, A, 10, most + 1, A, 4, 1.0, None, 0, 0, None, A, 0, most + 1, None) == EINVAL
+    assert lib.embedding_bwd(A, 0, 4, most + 1, most + 1, A, 10, 1.0, None, 0, P(1 << 50), most + 1, WS, 1 << 60, None) == EINVAL
+    assert lib.embedding_bwd_workspace_bytes(4, most + 1) == 256 < lib.embedding_bwd_workspace_bytes(4, most)
