@@ -405,3 +405,28 @@ def test_gradients_of_rows_of_very_different_size(m, n, k, dtype):
     within(host(dA), wa, oa + (np.abs(wa) + oa) * h * 1.001 + least, "dA")
     within(host(dB), wb, ob + (np.abs(wb) + ob) * h * 1.001 + least, "dBt")
     assert (host(dB)[3::11] != 0).any(axis=1).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 1 << 22, 16), (5, 300, 133144), (70, 257, 70000)])
+def test_largest_sizes(m, n, k):
+    """The largest vocabulary, in more pieces than one, and the longest rows of codes."""
+    say("largest", m, n, k)
+    rng = np.random.default_rng(n + k)
+    qa, qb = (rng.integers(-127, 128, (r, k), dtype=np.int8) for r in (m, n))
+    sa, sb = (rng.uniform(0.5, 1.0, r).astype(np.float32) * np.float32(0.01 / k ** 0.25) for r in (m, n))
+    t = rng.integers(0, n, m)
+    lse = check_forward(qa, sa, qb, sb, t)
+    check_grads(qa, sa, qb, sb, t, host(lse).astype(np.float32), np.full(m, -0.25, np.float32), None, "f32")
+
+
+def test_no_codes():
+    """Rows of no codes: every logit is 0."""
+    for m, n in ((5, 300), (600, 70000)):
+        q = torch.empty((m, 0), dtype=torch.int8, device="cuda")
+        w = torch.empty((n, 0), dtype=torch.int8, device="cuda")
+        t = torch.arange(m, device="cuda") % n
+        lp, lse = g.gemm_i8_logprobs(q, torch.ones(m, device="cuda"), w, torch.ones(n, device="cuda"), t)
+        within(host(lse), np.full(m, np.log(n)), np.full(m, R.U32 * 16), "lse")
+        within(host(lp), np.full(m, -np.log(n)), np.full(m, R.U32 * 16), "logprob")
+        dA, dB = g.gemm_i8_logprobs_bwd(q, torch.ones(m, device="cuda"), w, torch.ones(n, device="cuda"), t, lse, lp)
+        assert dA.shape == (m, 0) and dB.shape == (n, 0)
