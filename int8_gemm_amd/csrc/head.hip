@@ -503,9 +503,10 @@ constexpr int kBounds = 64, kMostShift = 24;
 struct Bound {
   uint32_t row, col;           // E + 1024 and F + 1024 of a part, 0: none
 };
-struct Scale {                 // acc / m 2^x is the gradient
+struct Scale {                 // acc m 2^x is the gradient: m = RN(1 / mantissa) of the row's scale
   float m;
   int x;
+  __device__ float of(float acc) const { return __builtin_ldexpf(acc * m, x); }
 };
 struct RowArgs {
   const int64_t* targets;
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(256) head_prepare_kernel(const PackArgs p) {
         const float f = __builtin_ldexpf(r.s, 15 - r.es + min(shift - below, 0));
         p.share[own] = __builtin_ldexpf(r.gl - r.g, -r.eg) * f;
         p.given[own] = __builtin_ldexpf(r.g, -r.eg) * f;
-        p.scale_a[own] = Scale{__builtin_amdgcn_frexp_mantf(r.s), E + F - 15 - shift - r.es};
+        p.scale_a[own] = Scale{1.0f / __builtin_amdgcn_frexp_mantf(r.s), E + F - 15 - shift - r.es};
       }
     } else if (own < rows) {
       const float c = p.l.s_col[own];
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(256) head_prepare_kernel(const PackArgs p) {
       shift = min(max(F - e, 0), kMostShift);
       if (kb == 0) {
         p.col[own] = __builtin_ldexpf(c, shift - F);
-        p.scale_b[own] = Scale{__builtin_amdgcn_frexp_mantf(c), E + F - 15 - shift - e};
+        p.scale_b[own] = Scale{1.0f / __builtin_amdgcn_frexp_mantf(c), E + F - 15 - shift - e};
       }
     }
     const float factor = __builtin_ldexpf(1.0f, -shift);
@@ -844,7 +845,7 @@ __device__ __forceinline__ void store4(T* to, int n, const float (&v)[4]) {
 __device__ __forceinline__ void store_grad(void* out, int64_t ld, int dtype, int64_t row, int k, int n, v4f acc, Scale scale) {
   float v[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(acc[e] / scale.m, scale.x);
+  for (int e = 0; e < 4; ++e) v[e] = scale.of(acc[e]);
   if (dtype == DT_F32) store4(static_cast<float*>(out) + row * ld + k, n, v);
   else if (dtype == DT_BF16) store4(static_cast<bf16_t*>(out) + row * ld + k, n, v);
   else store4(static_cast<f16_t*>(out) + row * ld + k, n, v);
@@ -1047,19 +1048,55 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
     }
     return;
   }
+  const auto write = [&](auto type) {
+    using T = decltype(type);
+    constexpr int ROW = 256 * sizeof(T) + 16;              // (the 16 spread a column's values over the banks)
+    constexpr int COLS = grad_lds(FEW) / ROW >= CT ? CT : CT / 2, N = 16 / sizeof(T), LANES = 256 / N;
+    static_assert(COLS * ROW <= grad_lds(FEW) && COLS % (32 * FC) == 0, "whole waves' columns at a time");
 #pragma unroll
-  for (int i = 0; i < FA; ++i)
+    for (int c0 = 0; c0 < CT; c0 += COLS) {
+      __syncthreads();
+      if (wc * FC * 32 >= c0 && wc * FC * 32 < c0 + COLS) {
 #pragma unroll
-    for (int j = 0; j < FC; ++j) {
-      const int col = ct * CT + (wc * FC + j) * 32 + (lane & 31);
-      const Scale scale = col < s.rows ? s.scale[col] : Scale{1.0f, 0};
+        for (int j = 0; j < FC; ++j) {
+          const int in = (wc * FC + j) * 32 + (lane & 31), col = ct * CT + in;
+          const Scale scale = col < s.rows ? s.scale[col] : Scale{0.0f, 0};
+          int8_t* to = smem + (in - c0) * ROW + 4 * (lane >> 5) * sizeof(T);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const v4f v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        const int k = kt * 256 + (i * WK + wk) * 32 + 8 * q + 4 * (lane >> 5);
-        if (col < s.rows && k < p.cols) store_grad(s.out, s.ld, p.dtype, col, k, p.cols - k, v, scale);
+          for (int i = 0; i < FA; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              T v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] = from_f32<T>(scale.of(acc[i][j][4 * q + e]));
+              __builtin_memcpy(__builtin_assume_aligned(to + ((i * WK + wk) * 32 + 8 * q) * sizeof(T), 4 * sizeof(T)), v, sizeof(v));
+            }
+        }
+      }
+      __syncthreads();
+      const int k = kt * 256 + lane % LANES * N, n = p.cols - k;
+      for (int r = wave * (64 / LANES) + lane / LANES; r < COLS; r += 8 * (64 / LANES)) {
+        const int col = ct * CT + c0 + r;
+        if (col >= s.rows || n <= 0) continue;
+        const v4i x = *reinterpret_cast<const v4i*>(smem + r * ROW + lane % LANES * 16);
+        T* to = static_cast<T*>(s.out) + col * s.ld + k;
+        if (n >= N) {
+          __builtin_memcpy(to, &x, 16);
+        } else {
+          T v[N];
+          __builtin_memcpy(v, &x, 16);
+#pragma unroll
+          for (int e = 0; e < N - 1; ++e)
+            if (e < n) to[e] = v[e];
+        }
       }
     }
+  };
+  // A tile's rows through LDS: a store has 512 bytes of a row or more (23 x 12669 x
+  // 1716 bf16 63 us, and 95 where a lane stores its 8 bytes of 32 rows).
+  if (TERMS == 1) write(bf16_t{});
+  else if (p.dtype == DT_F32) write(float{});
+  else write(f16_t{});
 }
 
 // Each XCD (workgroups are dealt to the 8 in turn) takes an eighth of either
