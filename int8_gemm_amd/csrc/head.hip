@@ -574,7 +574,7 @@ struct PackArgs {
   float* col;                  // of a vocabulary row, in T: s_col times its power of two
   Scale *scale_a, *scale_b;
 };
-// 8192 x 50304 x 768: 45 MB read, 90 MB written in 33 us, and 45 where a thread
+// 8192 x 50304 x 768: 45 MB read, 90 MB written in 26 us, and 45 where a thread
 // stores its 64 bytes itself: they go through LDS, within the wave, so that a
 // store has a block's whole KiB.
 __global__ void __launch_bounds__(256) head_prepare_kernel(const PackArgs p) {
@@ -674,7 +674,7 @@ struct WeightArgs {            // T of a piece
 };
 
 // The forward tiles again, with T in place of the sums: 8192 x 50304 x 768 in three
-// pieces 450 us, 0.82 GB of T (1.65 GB in two f16) written beside the next tile's
+// pieces 490 us, 0.82 GB of T (1.65 GB in two f16) written beside the next tile's
 // loads.
 template <int TERMS, int BV, int BT, int WV, int WT, int PER_CU>
 __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weights_kernel(const WeightArgs p) {
@@ -1112,11 +1112,11 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
 
 // Each XCD (workgroups are dealt to the 8 in turn) takes an eighth of either
 // side's units, neighbours in their order: they share T or codes in its L2.
-// The longer ones go first.  8192 x 50304 x 768 bf16: 1.27 PFLOP in 1280 us, 1.0
+// The longer ones go first.  8192 x 50304 x 768 bf16: 1.27 PFLOP in 1100 us, 1.15
 // PFLOPS (library products of these shapes reach 0.82 and 1.05); without the loads
-// 1.27 PFLOPS, so what is left is the matrix cores' own pace.  (Dealt without regard
+// 1.27 PFLOPS, so most of what is left is the matrix cores' own pace.  (Dealt without regard
 // to the XCDs, dA's units came to lie on one: 2048 x 50257 x 768 f32 1783 us in
-// all, 791 as they are.)
+// all, 791 as they are dealt here.)
 // LAST: 32-blocks along k that a wave multiplies in the last tile of k.
 template <int TERMS, bool FEW, int LAST>
 __global__ void __launch_bounds__(512, FEW ? 4 : 2) head_grads_kernel(const GradArgs p) {
