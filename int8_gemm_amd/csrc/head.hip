@@ -113,30 +113,32 @@ struct LogitArgs {
   int M, N, K;
 };
 
-// BV vocabulary rows by BT tokens, WV x WT waves; stages of 128 bytes of K, two
-// in LDS, filled by direct loads (16-byte chunk c of row r at c ^ (r/2)%8, which
-// spreads a fragment's 32 rows over the banks).
-template <int BV, int BT, int WV, int WT>
+// BV vocabulary rows by BT tokens, WV x WT waves; stages of SB bytes of K, S of
+// them in LDS, filled by direct loads (16-byte chunk c of row r at c ^ (r/2)%8, or c
+// ^ (r/4)%4 of 64 bytes, which spreads a fragment's 32 rows over the banks).
+template <int BV, int BT, int WV, int WT, int SB = 128, int S = 2>
 struct LogitTile {
   static constexpr int NW = WV * WT, NT = NW * 64;
   static constexpr int FV = BV / WV / 32, FT = BT / WT / 32;
-  static constexpr int STAGE = (BV + BT) * 128;
-  static constexpr int INS = (BV + BT) / (8 * NW), INS_V = BV / (8 * NW);
-  static_assert(INS * 8 * NW == BV + BT && INS_V * 8 * NW == BV && NW % 2 == 0, "whole loads");
-  static constexpr int LDS = 2 * STAGE;
+  static constexpr int CH = SB / 16, KS = SB / 32, ROWS = 64 / CH;   // chunks and k-steps of a stage, rows of a load
+  static constexpr int STAGE = (BV + BT) * SB;
+  static constexpr int INS = (BV + BT) / (ROWS * NW), INS_V = BV / (ROWS * NW);
+  static_assert(INS * ROWS * NW == BV + BT && INS_V * ROWS * NW == BV && NW % 2 == 0 && (SB == 128 || SB == 64), "whole loads");
+  static constexpr int LDS = S * STAGE;
+  static __device__ __forceinline__ int turn_of(int row) { return SB == 128 ? (row >> 1) & 7 : (row >> 2) & 3; }
   static constexpr int TOKENS = BT < 64 ? 64 : BT;         // values of a token in LDS: whole waves' loads
 
-  // Where a lane's loads of a tile begin: rows (q * NW + wave) * 8 + lane / 8; NW
-  // is even, so (row / 2) % 8 does not depend on q.
+  // Where a lane's loads of a tile begin: rows (q * NW + wave) * ROWS + lane / CH;
+  // NW is even, so a row's turn does not depend on q.
   struct Source {
     const int8_t* at[INS];
   };
   static __device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
   static __device__ __forceinline__ void issue(const LogitArgs& p, int8_t* smem, const Source& src, int kt) {
     const int lane = threadIdx.x & 63, wave = wave_of();
-    const int chunk = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
-    int8_t* base = smem + (kt & 1) * STAGE + wave * 1024;
-    const int at = min(kt * 128 + chunk * 16, ((p.K + 15) & ~15) - 16);   // (what lies beyond K is cleared below)
+    const int chunk = (lane & (CH - 1)) ^ turn_of(wave * ROWS + lane / CH);
+    int8_t* base = smem + kt % S * STAGE + wave * 1024;
+    const int at = min(kt * SB + chunk * 16, ((p.K + 15) & ~15) - 16);   // (what lies beyond K is cleared below)
 #pragma unroll
     for (int q = 0; q < INS; ++q) lds_load16(src.at[q] + at, base + q * NW * 1024);
   }
@@ -149,17 +151,18 @@ struct LogitTile {
       lds_load4(static_cast<const float*>(from) + (at < all ? at : all - 1), static_cast<float*>(lds) + i * 64);
     }
   }
-  // The first two stages of a tile, into LDS that no wave reads any more.
+  // The first S stages of a tile, into LDS that no wave reads any more.
   static __device__ __forceinline__ void start(const LogitArgs& p, int8_t* smem, int v0, int t0, Source& src) {
     const int lane = threadIdx.x & 63, wave = wave_of();
 #pragma unroll
     for (int q = 0; q < INS; ++q) {
-      const int r = (q * NW + wave) * 8 + (lane >> 3);
+      const int r = (q * NW + wave) * ROWS + lane / CH;
       if (q < INS_V) src.at[q] = p.B + (int64_t)min(v0 + r, p.N - 1) * p.ldb;
       else src.at[q] = p.A + (int64_t)min(t0 + r - BV, p.M - 1) * p.lda;
     }
-    if (p.K > 0) issue(p, smem, src, 0);
-    if (p.K > 128) issue(p, smem, src, 1);
+#pragma unroll
+    for (int st = 0; st < S; ++st)
+      if (p.K > st * SB) issue(p, smem, src, st);
   }
 
   // What this wave asked for up to start() is waited for here, but not the BEHIND vector stores
@@ -169,7 +172,7 @@ struct LogitTile {
                                                   v16i (&acc)[FV][FT]) {
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_of();
     const int wv = wave / WT, wt = wave % WT;
-    const int n = (p.K + 127) / 128;
+    const int n = (p.K + SB - 1) / SB;
 #pragma unroll
     for (int i = 0; i < FV; ++i)
 #pragma unroll
@@ -184,13 +187,13 @@ struct LogitTile {
     // The last stage's bytes beyond K: cleared in the tokens' rows, which makes
     // those products 0 whatever the other operand's bytes are.
     auto clear_tail = [&](int kt) {
-      const int left = p.K - kt * 128;
-      if (left >= 128) return;
-      int8_t* base = smem + (kt & 1) * STAGE + BV * 128;
-      for (int c = tid; c < BT * 8; c += NT) {
-        const int r = c >> 3, first = (c & 7) * 16;
+      const int left = p.K - kt * SB;
+      if (left >= SB) return;
+      int8_t* base = smem + kt % S * STAGE + BV * SB;
+      for (int c = tid; c < BT * CH; c += NT) {
+        const int r = c / CH, first = c % CH * 16;
         if (first + 16 <= left) continue;
-        uint32_t* w = reinterpret_cast<uint32_t*>(base + r * 128 + ((c & 7) ^ ((r >> 1) & 7)) * 16);
+        uint32_t* w = reinterpret_cast<uint32_t*>(base + r * SB + (c % CH ^ turn_of(r)) * 16);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int keep = left - first - 4 * i;             // bytes of this word that are kept
@@ -202,23 +205,23 @@ struct LogitTile {
       barrier_nofence();
     };
 
-    int offv[4][FV], offt[4][FT];
+    int offv[KS][FV], offt[KS][FT];
     const int half = lane >> 5;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < KS; ++s) {
 #pragma unroll
       for (int i = 0; i < FV; ++i) {
         const int r = (wv * FV + i) * 32 + (lane & 31);
-        offv[s][i] = r * 128 + ((2 * s + half) ^ ((r >> 1) & 7)) * 16;
+        offv[s][i] = r * SB + ((2 * s + half) ^ turn_of(r)) * 16;
       }
 #pragma unroll
       for (int j = 0; j < FT; ++j) {
         const int r = BV + (wt * FT + j) * 32 + (lane & 31);
-        offt[s][j] = r * 128 + ((2 * s + half) ^ ((r >> 1) & 7)) * 16;
+        offt[s][j] = r * SB + ((2 * s + half) ^ turn_of(r)) * 16;
       }
     }
     auto read = [&](int kt, int s, v4i (&fv)[FV], v4i (&ft)[FT]) {
-      const int8_t* base = smem + (kt & 1) * STAGE;
+      const int8_t* base = smem + kt % S * STAGE;
 #pragma unroll
       for (int i = 0; i < FV; ++i) fv[i] = *reinterpret_cast<const v4i*>(base + offv[s][i]);
 #pragma unroll
@@ -232,43 +235,42 @@ struct LogitTile {
           acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fv[i], ft[j], acc[i][j], 0, 0, 0);
     };
     v4i fv0[FV], ft0[FT], fv1[FV], ft1[FT];
-    if (n == 1) wait_loads<0>();
-    else if (BEHIND > 0 && behind) wait_loads<INS + BEHIND>();
-    else wait_loads<INS>();
+    if (n < S) wait_loads<0>();
+    else if (BEHIND > 0 && behind) wait_loads<INS * (S - 1) + BEHIND>();
+    else wait_loads<INS * (S - 1)>();
     barrier_nofence();
     if (n == 1) clear_tail(0);
     read(0, 0, fv0, ft0);
+    const auto steps = [&](int kt) {                         // all of a stage but the last
+#pragma unroll
+      for (int s = 0; s + 2 < KS; s += 2) {
+        read(kt, s + 1, fv1, ft1);
+        mfma(fv0, ft0);
+        interleave<FV + FT, FV * FT>();
+        read(kt, s + 2, fv0, ft0);
+        mfma(fv1, ft1);
+        interleave<FV + FT, FV * FT>();
+      }
+      read(kt, KS - 1, fv1, ft1);
+      mfma(fv0, ft0);
+      interleave<FV + FT, FV * FT>();
+    };
     // (the last stage stands apart: a branch around the products would move the
     // accumulators)
     for (int kt = 0; kt + 1 < n; ++kt) {
-      read(kt, 1, fv1, ft1);
-      mfma(fv0, ft0);
-      interleave<FV + FT, FV * FT>();
-      read(kt, 2, fv0, ft0);
-      mfma(fv1, ft1);
-      interleave<FV + FT, FV * FT>();
-      read(kt, 3, fv1, ft1);
-      mfma(fv0, ft0);
-      interleave<FV + FT, FV * FT>();
+      steps(kt);
       // the next stage has landed, and this one's last fragments are in
       // registers: its buffer is free
-      wait_loads<0>();
+      if (S > 2 && kt + S <= n) wait_loads<INS * (S - 2)>();
+      else wait_loads<0>();
       barrier_nofence();
-      if (kt + 2 < n) issue(p, smem, src, kt + 2);
-      else clear_tail(kt + 1);
+      if (kt + S < n) issue(p, smem, src, kt + S);
+      if (kt + 2 == n) clear_tail(kt + 1);
       read(kt + 1, 0, fv0, ft0);
       mfma(fv1, ft1);
       interleave<FV + FT, FV * FT>();
     }
-    read(n - 1, 1, fv1, ft1);
-    mfma(fv0, ft0);
-    interleave<FV + FT, FV * FT>();
-    read(n - 1, 2, fv0, ft0);
-    mfma(fv1, ft1);
-    interleave<FV + FT, FV * FT>();
-    read(n - 1, 3, fv1, ft1);
-    mfma(fv0, ft0);
-    interleave<FV + FT, FV * FT>();
+    steps(n - 1);
     mfma(fv1, ft1);
   }
 };
@@ -311,9 +313,9 @@ __device__ __forceinline__ void tile_of(int w, int tiles_v, int tiles_t, int& tv
 // fragments fill the registers, so one tile's logits cannot go beside the next
 // one's products.  (128 x 128 with two workgroups a CU 406 us, four waves of 128 x
 // 128 490.)  One token: 8.5 us for 38.6 MB of codes, 4.5 TB/s.
-template <int BV, int BT, int WV, int WT, int PER_CU>
+template <int BV, int BT, int WV, int WT, int PER_CU, int SB = 128, int S = 2>
 __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_fwd_kernel(const FwdArgs p) {
-  using Tile = LogitTile<BV, BT, WV, WT>;
+  using Tile = LogitTile<BV, BT, WV, WT, SB, S>;
   constexpr int FV = Tile::FV, FT = Tile::FT;
   __shared__ __attribute__((aligned(1024))) int8_t smem[Tile::LDS];
   __shared__ __attribute__((aligned(16))) float sc[2][BV], rows[2][Tile::TOKENS];
@@ -676,9 +678,9 @@ struct WeightArgs {            // T of a piece
 // The forward tiles again, with T in place of the sums: 8192 x 50304 x 768 in three
 // pieces 490 us, 0.82 GB of T (1.65 GB in two f16) written beside the next tile's
 // loads.
-template <int TERMS, int BV, int BT, int WV, int WT, int PER_CU>
+template <int TERMS, int BV, int BT, int WV, int WT, int PER_CU, int SB = 128, int S = 2>
 __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weights_kernel(const WeightArgs p) {
-  using Tile = LogitTile<BV, BT, WV, WT>;
+  using Tile = LogitTile<BV, BT, WV, WT, SB, S>;
   constexpr int FV = Tile::FV, FT = Tile::FT;
   __shared__ __attribute__((aligned(1024))) int8_t smem[Tile::LDS];
   constexpr int TOKENS = Tile::TOKENS;
@@ -1227,6 +1229,11 @@ LogitPlan logit_plan(int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
+// Wide tiles in four stages of 64 bytes of K where they multiply fewer zeros behind
+// K than two of 128 do: 8192 x 8192 x 64 38.6 us and 45.2, 2048 x 50257 x 300 87.7
+// and 92.5, 4096 x 50304 x 1600 362 and 368; but 8192 x 50304 x 768 385 and 363.
+bool short_stages(int64_t K) { return K > 0 && (K - 1) % 128 < 64; }
+
 // Workgroups of a launch over tiles: at most one a CU for the wide ones, each of
 // which walks over several.
 dim3 tile_grid(int64_t tiles, bool wide) {
@@ -1361,8 +1368,11 @@ hipError_t launch_head_fwd(const HeadArgs& whole, const int64_t* targets, float*
     a.A += row * a.lda;
     a.s_row += row;
     FwdArgs f{logit_args(a), 0, up(pl.wide, 256), up(a.M, 256), static_cast<v2f*>(ws)};
-    if (f.tiles_v > 0)
-      hipLaunchKernelGGL((head_fwd_kernel<256, 256, 2, 4, 1>), tile_grid((int64_t)f.tiles_v * f.tiles_t, true), dim3(512), 0, stream, f);
+    if (f.tiles_v > 0) {
+      const dim3 grid = tile_grid((int64_t)f.tiles_v * f.tiles_t, true);
+      if (short_stages(a.K)) hipLaunchKernelGGL((head_fwd_kernel<256, 256, 2, 4, 1, 64, 4>), grid, dim3(512), 0, stream, f);
+      else hipLaunchKernelGGL((head_fwd_kernel<256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, f);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     int n_parts = f.tiles_v;
@@ -1437,7 +1447,10 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
         const int64_t left = (int64_t)w.tiles_v * w.tiles_t - w.first;
         w.count = (int)(left < kMostGroups ? left : kMostGroups);
         const dim3 grid = tile_grid(w.count, wide);
-        if (wide && b.terms == 1) hipLaunchKernelGGL((head_weights_kernel<1, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
+        const bool brief = short_stages(a.K);
+        if (wide && b.terms == 1 && brief) hipLaunchKernelGGL((head_weights_kernel<1, 256, 256, 2, 4, 1, 64, 4>), grid, dim3(512), 0, stream, w);
+        else if (wide && brief) hipLaunchKernelGGL((head_weights_kernel<2, 256, 256, 2, 4, 1, 64, 4>), grid, dim3(512), 0, stream, w);
+        else if (wide && b.terms == 1) hipLaunchKernelGGL((head_weights_kernel<1, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
         else if (wide) hipLaunchKernelGGL((head_weights_kernel<2, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
         else if (b.terms == 1) hipLaunchKernelGGL((head_weights_kernel<1, 128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, w);
         else hipLaunchKernelGGL((head_weights_kernel<2, 128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, w);

@@ -430,3 +430,14 @@ def test_no_codes():
         within(host(lp), np.full(m, -np.log(n)), np.full(m, R.U32 * 16), "logprob")
         dA, dB = g.gemm_i8_logprobs_bwd(q, torch.ones(m, device="cuda"), w, torch.ones(n, device="cuda"), t, lse, lp)
         assert dA.shape == (m, 0) and dB.shape == (n, 0)
+
+
+@pytest.mark.parametrize("k", [64, 128, 129, 192, 193, 256, 257, 320, 449, 577])
+def test_stages_of_several_tiles(k):
+    """Each number of stages of either length, in workgroups of several tiles."""
+    m, n = 1300, 17000
+    say("stages", m, n, k)
+    rng = np.random.default_rng(k)
+    qa, sa, qb, sb, t = case(rng, m, n, k)
+    lse = check_forward(qa, sa, qb, sb, t)
+    same_bits(lse, forward(qa, sa, qb, sb, t)[1], "twice")
