@@ -564,7 +564,10 @@ __global__ void __launch_bounds__(256) head_bounds_kernel(const RowArgs p, Bound
 // contraction) by 32 columns, 1 KiB in the order of a fragment: lane l holds
 // column l%32, rows 8 (l/32) ... + 7.  Zero beyond the rows and `cols`.  And what
 // the products need of each row.
-constexpr int kOwnBounds = 2048;               // rows of both sides that every workgroup looks through itself: no launch before
+// Up to so many rows of both sides every workgroup looks through them itself, and
+// no launch comes before (805 x 1864 x 296 38.6 us and 39.9; 1500 x 6000 x 100 53.9
+// and 52.1).
+constexpr int kOwnBounds = 4096;
 struct PackArgs {
   LogitArgs l;
   RowArgs rows;
