@@ -6,8 +6,8 @@
 //
 // The lookup is one pass: a wave takes up to 256 vectors of a row, four loads
 // in flight.  The gradient of few rows is one launch that looks through all
-// tokens.  That of more sorts them, while other workgroups write the rows that
-// no token names (up to kRankRows each key's place is counted by the whole
+// tokens.  That of more sorts them, while other workgroups fill dW with zeros or
+// with what is added to (up to kRankRows each key's place is counted by the whole
 // chip; beyond, a stable radix sort of kRun at a time in LDS, the sorted runs
 // merged kMerge at a time), then adds rows in the sorted order: a wave takes a
 // piece of the order and a chunk of columns, writes the rows of tokens whose
