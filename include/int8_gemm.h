@@ -568,14 +568,14 @@ int gemm_i8_logprobs(const int8_t* QA, int64_t lda, const float* s_row, const in
  *   dA, dBt  either may be NULL.  With M == 0 dBt is 0.
  *   workspace  device scratch of gemm_i8_logprobs_bwd_workspace_bytes(M, N, K,
  *            dtype), 256-byte aligned, any contents (not needed with M == 0).
- * The products run on the matrix cores in f16 with binary32 sums, over pieces
- * of the vocabulary whose G has at most 3 * 2^26 values (or 256 columns).
- * Codes are exact; T = s_row[i] G[i,j] s_col[j] is rounded to f16 for bf16
- * gradients (2^-11 of the value) and to a sum of two f16 (2^-22) for f32 and
- * f16 ones, scaled by powers of two of its row and column, so that a value is
- * off by at most 2^-37 of (|g_logprob[i]| + |g_lse[i]|) s_row[i] s_col[j]
- * besides (a row or column more than 2^24 below the largest one: as if it were
- * 2^24 below).
+ * The products run on the matrix cores in bf16 with binary32 sums, over pieces
+ * of the vocabulary whose G has at most 2^27 values, 3 * 2^25 for bf16 gradients
+ * (or 256 columns).  Codes are exact; T = s_row[i] G[i,j] s_col[j], a binary32
+ * number, is a sum of three bf16, exactly, for f32 and f16 gradients, and of two
+ * (2^-16 of the value) for bf16 ones.  It is scaled by powers of two of its row
+ * and column, so that it keeps its bits where scales or gradients are small (a
+ * row or column more than 2^100 below the largest one: as if it were 2^100
+ * below), and where p is, down to p = 2^-126, below which p is 0.
  * Scales have to be positive, as the quantize passes write them.  As in
  * token_logprobs_bwd, a row with |lse| >= 2^24 gets 0 (and adds nothing to
  * dBt).  A NaN in a row's lse, gradients or scale makes its row of dA and all

@@ -9,11 +9,14 @@
 //   dA_ik = sum_j G_ij s_col_j QBt_jk     dBt_jk = sum_i G_ij s_row_i QA_ik
 // Both gradients read one matrix T_ij = s_row_i G_ij s_col_j:
 //   dA_ik = (1 / s_row_i) sum_j T_ij QBt_jk,  dBt_jk = (1 / s_col_j) sum_i T_ij QA_ik,
-// and the codes are exact in f16, so T is all that is rounded for the matrix
-// cores: to f16 for bf16 gradients (2^-11 of each value, where the outputs' own
-// rounding is 2^-8), to a sum of two f16 (2^-22) for f32 and f16 ones.  (Two bf16
-// would be 2^-16 in the same time.)  Powers of two of each row and column keep it
-// from f16's ends (see the backward part).
+// and the codes are exact in bf16.  T goes to the matrix cores as a sum of bf16
+// terms: three for f32 and f16 gradients, which hold all 24 bits of a binary32
+// number, and two for bf16 ones (2^-16 of each value, where the outputs' own
+// rounding is 2^-8).  bf16 has binary32's exponents, so a probability of 2^-120 has
+// as many bits as one of 1/2: a rare token's row of dBt is nothing but such values.
+// (f16 terms are half the products, but their least number is a probability of
+// 2^-40.)  Powers of two of each row and column keep the scales from mattering (see
+// the backward part).
 //
 // Forward: a workgroup multiplies a tile of vocabulary rows by a tile of
 // tokens; the vocabulary is the accumulators' row dimension, so that a lane
@@ -41,8 +44,8 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef short v4s __attribute__((ext_vector_type(4)));
-typedef _Float16 v8h __attribute__((ext_vector_type(8)));
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.44269502f;
 constexpr float kLowest = -3.40282347e38f;   // the running maximum's start: finite, so that x - m is no NaN for a finite x or -inf
@@ -494,14 +497,15 @@ __global__ void __launch_bounds__(256) head_join_kernel(const JoinArgs p) {
 // ---- backward ---------------------------------------------------------------------
 // Powers of two.  With r = |g_i| + |gl_i|, a row's (|g| + |gl|) s_row is below
 // 2^(exponent r + exponent s_row), E of the rows at most, and s_col below its
-// power, F at most.  T_ij is multiplied by 2^(15 - E + a_i - F + b_j), where a_i
+// power, F at most.  T_ij is multiplied by 2^(kTop - E + a_i - F + b_j), where a_i
 // and b_j are how far the row and the column are below E and F, and the codes of
-// row i (j) by 2^-a_i (2^-b_j), which is exact up to 2^-24: a_i and b_j are 24 at
-// most.  So the least spacing of f16 is 2^-36 of a value's own (|g| + |gl|) s_row
-// s_col, not of the largest: rows of small numbers (of zeros, whose scale is the
-// least one) have gradients as exact as others.  |T| is at most 2^15, times what
-// the rounding of a log-sum-exp below 2^24 makes of p, 1.65 at most.
-constexpr int kBounds = 64, kMostShift = 24;
+// row i (j) by 2^-a_i (2^-b_j), which is exact: a_i and b_j are kMostShift at most,
+// and bf16 goes down to 2^-126.  So T is of the size of p, whatever the scales and
+// gradients are: rows of small numbers (of zeros, whose scale is the least one)
+// have gradients as exact as others.  |T| is at most 2^kTop, times what the
+// rounding of a log-sum-exp below 2^24 makes of p, 1.65 at most: the least p, 2^-126,
+// leaves T's low terms 2^-79, and 2^30 products with codes stay below 2^102.
+constexpr int kBounds = 64, kMostShift = 100, kTop = 64;
 struct Bound {
   uint32_t row, col;           // E + 1024 and F + 1024 of a part, 0: none
 };
@@ -560,7 +564,7 @@ __global__ void __launch_bounds__(256) head_bounds_kernel(const RowArgs p, Bound
   if (threadIdx.x == 0) bounds[blockIdx.x] = b;
 }
 
-// Before the pieces: both operands' codes as f16 blocks of 16 rows (the
+// Before the pieces: both operands' codes as bf16 blocks of 16 rows (the
 // contraction) by 32 columns, 1 KiB in the order of a fragment: lane l holds
 // column l%32, rows 8 (l/32) ... + 7.  Zero beyond the rows and `cols`.  And what
 // the products need of each row.
@@ -615,10 +619,10 @@ __global__ void __launch_bounds__(256) head_prepare_kernel(const PackArgs p) {
       const int below = E - r.eg - r.es;
       shift = min(max(below, 0), kMostShift);
       if (kb == 0) {
-        const float f = __builtin_ldexpf(r.s, 15 - r.es + min(shift - below, 0));
+        const float f = __builtin_ldexpf(r.s, kTop - r.es + min(shift - below, 0));
         p.share[own] = __builtin_ldexpf(r.gl - r.g, -r.eg) * f;
         p.given[own] = __builtin_ldexpf(r.g, -r.eg) * f;
-        p.scale_a[own] = Scale{1.0f / __builtin_amdgcn_frexp_mantf(r.s), E + F - 15 - shift - r.es};
+        p.scale_a[own] = Scale{1.0f / __builtin_amdgcn_frexp_mantf(r.s), E + F - kTop - shift - r.es};
       }
     } else if (own < rows) {
       const float c = p.l.s_col[own];
@@ -626,7 +630,7 @@ __global__ void __launch_bounds__(256) head_prepare_kernel(const PackArgs p) {
       shift = min(max(F - e, 0), kMostShift);
       if (kb == 0) {
         p.col[own] = __builtin_ldexpf(c, shift - F);
-        p.scale_b[own] = Scale{1.0f / __builtin_amdgcn_frexp_mantf(c), E + F - 15 - shift - e};
+        p.scale_b[own] = Scale{1.0f / __builtin_amdgcn_frexp_mantf(c), E + F - kTop - shift - e};
       }
     }
     const float factor = __builtin_ldexpf(1.0f, -shift);
@@ -650,7 +654,7 @@ __global__ void __launch_bounds__(256) head_prepare_kernel(const PackArgs p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const v2f v = {(float)(int8_t)(w[2 * e] >> (8 * c)) * f[2 * e], (float)(int8_t)(w[2 * e + 1] >> (8 * c)) * f[2 * e + 1]};
-        o[e] = __builtin_bit_cast(int, __builtin_convertvector(v, v2h));
+        o[e] = __builtin_bit_cast(int, __builtin_convertvector(v, v2b));
       }
       to[c ^ (c4 >> 2)] = o;
     }
@@ -675,12 +679,11 @@ struct WeightArgs {            // T of a piece
   int count;
   int tb_log;                  // TB = 2^tb_log blocks of 32 tokens in a tile of dA's product
   v4i* T;                      // [tokens / (32 TB)][C16][TB][64]: the blocks that a stage of dA reads are in a row
-  size_t plane;                // from the first to the second f16 of a value (v4i), TERMS 2
+  size_t plane;                // from a term of a value to the next (v4i)
 };
 
-// The forward tiles again, with T in place of the sums: 8192 x 50304 x 768 in three
-// pieces 490 us, 0.82 GB of T (1.65 GB in two f16) written beside the next tile's
-// loads.
+// The forward tiles again, with T in place of the sums, written beside the next
+// tile's loads: 8192 x 50304 x 768 in two terms 1.65 GB.
 template <int TERMS, int BV, int BT, int WV, int WT, int PER_CU, int SB = 128, int S = 2>
 __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weights_kernel(const WeightArgs p) {
   using Tile = LogitTile<BV, BT, WV, WT, SB, S>;
@@ -773,18 +776,19 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
           for (int e = 0; e < 16; ++e)
             if (v0 + r0 + 8 * (e / 4) + e % 4 >= p.l.N) y[e] = 0.0f;
         }
-        uint32_t hi[8], lo[8];
+        uint32_t w[TERMS][8];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const v4f s4 = *reinterpret_cast<const v4f*>(factor[turn] + r0 + 8 * q);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const v2f v = {y[4 * q + 2 * e] * s4[2 * e], y[4 * q + 2 * e + 1] * s4[2 * e + 1]};
-            const v2h h = __builtin_convertvector(v, v2h);
-            hi[2 * q + e] = __builtin_bit_cast(uint32_t, h);
-            if (TERMS == 2) {
-              const v2f back = __builtin_convertvector(h, v2f);
-              lo[2 * q + e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{v.x - back.x, v.y - back.y}, v2h));
+            v2f v = {y[4 * q + 2 * e] * s4[2 * e], y[4 * q + 2 * e + 1] * s4[2 * e + 1]};
+#pragma unroll
+            for (int term = 0; term < TERMS; ++term) {
+              const v2b b = __builtin_convertvector(v, v2b);
+              w[term][2 * q + e] = __builtin_bit_cast(uint32_t, b);
+              const v2f back = __builtin_convertvector(b, v2f);
+              v = v2f{v.x - back.x, v.y - back.y};         // exact
             }
           }
         }
@@ -795,10 +799,10 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
           v4i* to = row + ((size_t)((wv * FV + i) * 2 + s) << (p.tb_log + 6));
 #pragma unroll
           for (int term = 0; term < TERMS; ++term) {
-            const uint32_t* w = term ? lo : hi;
-            const auto a = __builtin_amdgcn_permlane32_swap(w[4 * s], w[4 * s + 2], false, false);
-            const auto b = __builtin_amdgcn_permlane32_swap(w[4 * s + 1], w[4 * s + 3], false, false);
-            to[term ? p.plane : 0] = v4i{(int)a[0], (int)b[0], (int)a[1], (int)b[1]};
+            const uint32_t* t = w[term];
+            const auto a = __builtin_amdgcn_permlane32_swap(t[4 * s], t[4 * s + 2], false, false);
+            const auto b = __builtin_amdgcn_permlane32_swap(t[4 * s + 1], t[4 * s + 3], false, false);
+            to[term * p.plane] = v4i{(int)a[0], (int)b[0], (int)a[1], (int)b[1]};
           }
         }
       }
@@ -812,7 +816,7 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
 // contraction in stages of 32.
 struct GradArgs {
   const v4i* T;
-  size_t plane;                // TERMS 2
+  size_t plane;                // from a term to the next (v4i)
   int C16;
   int KB, tiles_k;
   struct Side {
@@ -834,14 +838,14 @@ struct GradArgs {
 
 // How a tile is shared by the 8 waves.  FEW: at most 64 tokens, whose tile of
 // dA is 64 wide, each wave 32 columns k of it; two workgroups run on a CU.
-template <int TERMS, bool DUAL, bool FEW>
+template <bool DUAL, bool FEW>
 struct GradTile {
   static constexpr bool NARROW = FEW && !DUAL;
   static constexpr int WK = NARROW ? 8 : 2, WC = 8 / WK;   // waves along k and along CT
-  static constexpr int FC = NARROW ? 2 : FEW ? 1 : 2 / TERMS;   // 32-blocks of a wave along CT
+  static constexpr int FC = NARROW ? 2 : 1;                // 32-blocks of a wave along CT
   static constexpr int CT = 32 * FC * WC;
   static constexpr int FA = 8 / WK;                        // and along k: its i-th is block i WK + wk of the tile
-  static constexpr int TB = FEW ? 2 : 8 / TERMS;           // 32-token blocks of a tile of T
+  static constexpr int TB = FEW ? 2 : 4;                   // 32-token blocks of a tile of T
 };
 
 template <class T>
@@ -867,21 +871,25 @@ __device__ __forceinline__ void store_grad(void* out, int64_t ld, int dtype, int
   else store4(static_cast<f16_t*>(out) + row * ld + k, n, v);
 }
 
-// DUAL: dBt, for which T is read transposed.  LDS holds five stages of 32 of the
-// contraction: up to four are on their way while one is multiplied (two stages of
-// 64 leave a load half the time to land: 8192 x 50304 x 768 bf16 1759 us in place
-// of 1669).  FA: 32-blocks along k that a wave multiplies, fewer than the tile's
-// where K ends in it.
-// At most 64 tokens: three stages of 24 KiB for dA, and dBt's two.
-constexpr int grad_stage(bool few, bool dual) { return few && !dual ? 24576 : 32768; }
-constexpr int grad_slots(bool few, bool dual) { return !few ? 5 : dual ? 2 : 3; }
-constexpr int grad_lds(bool few) { return grad_stage(few, false) * grad_slots(few, false); }
-static_assert(grad_lds(true) >= grad_stage(true, true) * grad_slots(true, true), "dBt's stages fit");
+// DUAL: dBt, for which T is read transposed.  A stage of 32 of the contraction
+// is 16 KiB of codes and 8 of each term of T (4 for the narrow tile).  LDS holds five
+// stages of two terms, and four of three: all but one are on their way while one is
+// multiplied.  At most 64 tokens: three stages of dA of two terms and two of three,
+// and dBt's two, in half of a CU's LDS.  FA: 32-blocks along k that a wave
+// multiplies, fewer than the tile's where K ends in it.
+constexpr int grad_stage(int terms, bool few, bool dual) { return 16384 + terms * (few && !dual ? 4096 : 8192); }
+constexpr int grad_slots(int terms, bool few, bool dual) { return !few ? 7 - terms : dual ? 2 : 5 - terms; }
+constexpr int grad_lds(int terms, bool few) {
+  const int a = grad_stage(terms, few, false) * grad_slots(terms, few, false);
+  const int b = grad_stage(terms, few, true) * grad_slots(terms, few, true);
+  return a > b ? a : b;
+}
+static_assert(grad_lds(2, false) <= 163840 && grad_lds(3, false) <= 163840 && grad_lds(2, true) <= 81920 && grad_lds(3, true) <= 81920, "LDS");
 template <int TERMS, bool DUAL, bool FEW, int FA>
 __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Side& s, int u, int8_t* smem) {
-  using Tile = GradTile<TERMS, DUAL, FEW>;
+  using Tile = GradTile<DUAL, FEW>;
   constexpr bool NARROW = Tile::NARROW;
-  constexpr int kStage = grad_stage(FEW, DUAL), kSlots = grad_slots(FEW, DUAL);
+  constexpr int kStage = grad_stage(TERMS, FEW, DUAL), kSlots = grad_slots(TERMS, FEW, DUAL);
   constexpr int WK = Tile::WK, WC = Tile::WC, FC = Tile::FC, CT = Tile::CT, TB = Tile::TB;
   constexpr int READS = FA + TERMS * FC * (DUAL ? 2 : 1), MFMAS = TERMS * FA * FC;   // of a k-step
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -889,30 +897,27 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
   const int kt = u % p.tiles_k, ct = (u / p.tiles_k) % s.tiles, split = u / (p.tiles_k * s.tiles);
   const int first = split * s.per, n = min(s.per, s.stages - first);
 
-  // sources of this wave's loads of a stage, two of codes and one or two of T: the
+  // sources of this wave's loads of a stage, two of codes and one to three of T: the
   // same in every lane but for the lane's 16 bytes of a block (codes behind KB are
   // not used: the last block in their place)
-  constexpr int T_LOADS = NARROW || (FEW && TERMS == 1) ? 1 : 2, LOADS = 2 + T_LOADS;
+  constexpr int T_LOADS = NARROW ? TERMS - 1 : TERMS, LOADS = 2 + T_LOADS;
   const size_t row_a = (size_t)p.KB * 1024, row_b = (size_t)p.C16 * 1024, plane_b = p.plane * 16;
   const char* ga = reinterpret_cast<const char*>(s.codes) + (size_t)(first * 2) * row_a + (size_t)min(kt * 8 + wave, p.KB - 1) * 1024;
   const char* gb = reinterpret_cast<const char*>(p.T);
   const int lane_a = lane * 16;
-  int lane_b = lane_a, wave_b = wave;                      // wave_b: block of T's stage in LDS
-  size_t next_b = 8192;                                    // from the first to the second load of T
+  int lane_b = lane_a;
   if constexpr (NARROW) {
-    // blocks [term][16 of the contraction 2][32 tokens 2]: 4 a term, twice where there is one term
-    gb += (size_t)(first * 2) * (TB * 1024) + (size_t)(wave & 3) * 1024 + (TERMS == 2 ? (wave >> 2) * plane_b : 0);
-    wave_b = TERMS == 2 ? wave : wave & 3;
+    // blocks [term][16 of the contraction 2][32 tokens 2]: 4 a term, two terms a load of all waves; the third
+    // term's are loaded twice, to the same place
+    gb += (size_t)(first * 2) * (TB * 1024) + (size_t)(wave & 3) * 1024;
   } else if constexpr (!DUAL) {
     // blocks [16 of the contraction 2][32 tokens TB], in a row; of each term 8
     gb += (size_t)ct * TB * row_b + (size_t)(first * 2) * (TB * 1024) + wave * 1024;
-    if (TERMS == 2) next_b = plane_b;
   } else {
     // 16 vocabulary rows each, of one block of 32 tokens; the 16-byte pieces of a block (half h, token t) are placed at
     // (h, t ^ (4h + 8 (vocabulary block % 2))), so that a transposing read of 32 lanes covers all banks
     lane_b = ((lane & 32) | ((lane & 31) ^ (4 * (lane >> 5) + 8 * (wave & 1)))) * 16;
     gb += ((size_t)ct * (CT / 16) + wave) * (TB * 1024);
-    next_b = TERMS == 2 ? plane_b : (size_t)(8 * TB * 1024);
   }
   auto issue = [&](int st) {
     int8_t* base = smem + (st % kSlots) * kStage;
@@ -927,7 +932,11 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
 #pragma unroll
     for (int q = 0; q < 2; ++q) lds_load16(a + q * row_a, lane_a, base + wave * 1024 + q * 8192);
 #pragma unroll
-    for (int q = 0; q < T_LOADS; ++q) lds_load16(b + q * next_b, lane_b, base + 16384 + wave_b * 1024 + q * 8192);
+    for (int q = 0; q < T_LOADS; ++q) {
+      const int term = NARROW ? min(2 * q + (wave >> 2), TERMS - 1) : q;
+      const int to = NARROW ? term * 4 + (wave & 3) : q * 8 + wave;
+      lds_load16(b + term * plane_b, lane_b, base + 16384 + to * 1024);
+    }
   };
   // LDS: codes [k-step 2][32 columns 8]; T [term][k-step 2][32 tokens TB], or [term][16 vocabulary rows CT / 16]
   constexpr int TERM = DUAL ? CT / 16 * 1024 : 2 * TB * 1024;
@@ -952,39 +961,39 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  auto read = [&](const int8_t* base, auto ks_t, v8h (&fa)[FA], v8h (&fb)[TERMS][FC]) {
+  auto read = [&](const int8_t* base, auto ks_t, v8b (&fa)[FA], v8b (&fb)[TERMS][FC]) {
     constexpr int ks = decltype(ks_t)::value;
 #pragma unroll
-    for (int i = 0; i < FA; ++i) fa[i] = *reinterpret_cast<const v8h*>(base + offa + ks * 8192 + i * (WK * 1024));
+    for (int i = 0; i < FA; ++i) fa[i] = *reinterpret_cast<const v8b*>(base + offa + ks * 8192 + i * (WK * 1024));
 #pragma unroll
     for (int t = 0; t < TERMS; ++t)
 #pragma unroll
       for (int j = 0; j < FC; ++j) {
         if constexpr (!DUAL) {
-          fb[t][j] = *reinterpret_cast<const v8h*>(base + offb + t * TERM + ks * (TB * 1024) + j * 1024);
+          fb[t][j] = *reinterpret_cast<const v8b*>(base + offb + t * TERM + ks * (TB * 1024) + j * 1024);
         } else {
           // tokens 16 ks ... of the block
           const int at = t * TERM + j * 2048 + ks * 256;
           typedef __attribute__((address_space(3))) v4s lds_v4s;
           const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(base + offb + at));
           const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(base + flip + at));
-          union { v4s h[2]; v8h v; } f{{x, y}};
+          union { v4s h[2]; v8b v; } f{{x, y}};
           fb[t][j] = f.v;
         }
       }
   };
-  auto mfma = [&](const v8h (&fa)[FA], const v8h (&fb)[TERMS][FC]) {
+  auto mfma = [&](const v8b (&fa)[FA], const v8b (&fb)[TERMS][FC]) {
 #pragma unroll
     for (int t = 0; t < TERMS; ++t)
 #pragma unroll
       for (int i = 0; i < FA; ++i)
 #pragma unroll
         for (int j = 0; j < FC; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[t][j], acc[i][j], 0, 0, 0);
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[t][j], acc[i][j], 0, 0, 0);
   };
   const std::integral_constant<int, 0> k0;
   const std::integral_constant<int, 1> k1;
-  v8h fa0[FA], fa1[FA], fb0[TERMS][FC], fb1[TERMS][FC];
+  v8b fa0[FA], fa1[FA], fb0[TERMS][FC], fb1[TERMS][FC];
   if constexpr (FEW && DUAL) {
     // 64 tokens are two stages
     issue(0);
@@ -1028,7 +1037,7 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
     for (; st + kSlots - 1 < n; ++st) stage(st, std::integral_constant<int, kSlots - 2>{});
     if constexpr (kSlots > 4) stage(st++, std::integral_constant<int, 2>{});
     if constexpr (kSlots > 3) stage(st++, std::integral_constant<int, 1>{});
-    stage(st, std::integral_constant<int, 0>{});
+    if constexpr (kSlots > 2) stage(st, std::integral_constant<int, 0>{});
     read(smem + slot * kStage, k1, fa1, fb1);
     mfma(fa0, fb0);
     interleave<READS, MFMAS>();
@@ -1067,8 +1076,8 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
   const auto write = [&](auto type) {
     using T = decltype(type);
     constexpr int ROW = 256 * sizeof(T) + 16;              // (the 16 spread a column's values over the banks)
-    constexpr int COLS = grad_lds(FEW) / ROW >= CT ? CT : CT / 2, N = 16 / sizeof(T), LANES = 256 / N;
-    static_assert(COLS * ROW <= grad_lds(FEW) && COLS % (32 * FC) == 0, "whole waves' columns at a time");
+    constexpr int COLS = grad_lds(TERMS, FEW) / ROW >= CT ? CT : CT / 2, N = 16 / sizeof(T), LANES = 256 / N;
+    static_assert(COLS * ROW <= grad_lds(TERMS, FEW) && COLS % (32 * FC) == 0, "whole waves' columns at a time");
 #pragma unroll
     for (int c0 = 0; c0 < CT; c0 += COLS) {
       __syncthreads();
@@ -1110,7 +1119,7 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
   };
   // A tile's rows through LDS: a store has 512 bytes of a row or more (23 x 12669 x
   // 1716 bf16 63 us, and 95 where a lane stores its 8 bytes of 32 rows).
-  if (TERMS == 1) write(bf16_t{});
+  if (TERMS == 2) write(bf16_t{});
   else if (p.dtype == DT_F32) write(float{});
   else write(f16_t{});
 }
@@ -1125,7 +1134,7 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
 // LAST: 32-blocks along k that a wave multiplies in the last tile of k.
 template <int TERMS, bool FEW, int LAST>
 __global__ void __launch_bounds__(512, FEW ? 4 : 2) head_grads_kernel(const GradArgs p) {
-  __shared__ __attribute__((aligned(1024))) int8_t smem[grad_lds(FEW)];
+  __shared__ __attribute__((aligned(1024))) int8_t smem[grad_lds(TERMS, FEW)];
   const int xcd = blockIdx.x & 7, at = p.first + (blockIdx.x >> 3);
   const int a0 = (int)((int64_t)p.units_a * xcd / 8), na = (int)((int64_t)p.units_a * (xcd + 1) / 8) - a0;
   const int b0 = (int)((int64_t)p.units_b * xcd / 8), nb = (int)((int64_t)p.units_b * (xcd + 1) / 8) - b0;
@@ -1249,9 +1258,9 @@ dim3 tile_grid(int64_t tiles, bool wide) {
 constexpr int64_t kFwdRows = 65536;
 
 // Pieces of the vocabulary and, in each, the ranges that the products'
-// contractions are split into: a piece's T has at most kPieceValues values (or
-// 256 columns); among the allowed the least estimated time is taken.
-constexpr int64_t kPieceValues = int64_t(3) << 26;
+// contractions are split into: a piece's T has at most piece_bytes (or 256 columns);
+// among the allowed the least estimated time is taken.
+constexpr int64_t piece_bytes(int terms) { return int64_t(3) << (25 + terms); }   // 403 MB, 805 MB
 struct BwdPlan {
   int terms;
   bool few;                    // at most 64 tokens
@@ -1291,22 +1300,24 @@ double makespan(int64_t n1, double t1, int64_t n2, double t2) {
 }
 BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, int dtype) {
   BwdPlan b;
-  b.terms = dtype == DT_BF16 ? 1 : 2;
+  b.terms = dtype == DT_BF16 ? 2 : 3;
   b.few = M <= 64;
-  b.cb = b.few ? 128 : 256 / b.terms;
-  b.ca = b.few ? 64 : b.cb;
-  b.tb_log = b.few ? 1 : 4 - b.terms;
+  b.cb = 128;
+  b.ca = b.few ? 64 : 128;
+  b.tb_log = b.few ? 1 : 2;
   b.Mp = b.few ? 64 : (M + 255) / 256 * 256;
   b.tiles_k = up(K, 256);
   const int64_t blocks = (N + 255) / 256;                  // of 256 columns
-  int64_t most = kPieceValues / b.Mp / 256;
+  int64_t most = piece_bytes(b.terms) / (b.Mp * 512 * b.terms);
   if (most < 1) most = 1;
   const int64_t least = (blocks + most - 1) / most;
   const int64_t ta = b.Mp / b.ca * b.tiles_k, db = up(b.Mp, 256);
   // microseconds, fitted to 25 plans at 8192 x 50304 x 768 (bf16) and 2048 x
-  // 50257 x 768 (f32), whose times it orders as they are to a few per cent: 64
-  // of the contraction of a unit, a unit's start and end, two launches; planes at 4 TB/s
-  constexpr double kStep = 1.65, kUnit = 6.0, kLaunches = 8.0;
+  // 50257 x 768 (f32) with products of as many terms, whose times it orders as they
+  // are to a few per cent: 64 of the contraction of a unit, a term's half of 1.65; a
+  // unit's start and end, two launches; planes at 4 TB/s
+  const double kStep = 0.825 * b.terms;
+  constexpr double kUnit = 6.0, kLaunches = 8.0;
   double best = 1e300;
   b.sa = b.sb = b.pieces = 1;
   b.C = 256;
@@ -1351,10 +1362,10 @@ static void launch_grads_of(int last, unsigned n, hipStream_t stream, const Grad
 }
 static void launch_grads(const BwdPlan& b, int K, unsigned n, hipStream_t stream, const GradArgs& p) {
   const int last = (K - (b.tiles_k - 1) * 256 + 63) / 64;  // pairs of 32 columns in the last tile
-  if (b.terms == 1 && b.few) launch_grads_of<1, true>(last, n, stream, p);
-  else if (b.terms == 1) launch_grads_of<1, false>(last, n, stream, p);
-  else if (b.few) launch_grads_of<2, true>(last, n, stream, p);
-  else launch_grads_of<2, false>(last, n, stream, p);
+  if (b.terms == 2 && b.few) launch_grads_of<2, true>(last, n, stream, p);
+  else if (b.terms == 2) launch_grads_of<2, false>(last, n, stream, p);
+  else if (b.few) launch_grads_of<3, true>(last, n, stream, p);
+  else launch_grads_of<3, false>(last, n, stream, p);
 }
 
 size_t head_fwd_bytes(int64_t M, int64_t N, int64_t K) {
@@ -1451,12 +1462,12 @@ hipError_t launch_head_bwd(const HeadArgs& a, const HeadGradArgs& g, void* ws, h
         w.count = (int)(left < kMostGroups ? left : kMostGroups);
         const dim3 grid = tile_grid(w.count, wide);
         const bool brief = short_stages(a.K);
-        if (wide && b.terms == 1 && brief) hipLaunchKernelGGL((head_weights_kernel<1, 256, 256, 2, 4, 1, 64, 4>), grid, dim3(512), 0, stream, w);
-        else if (wide && brief) hipLaunchKernelGGL((head_weights_kernel<2, 256, 256, 2, 4, 1, 64, 4>), grid, dim3(512), 0, stream, w);
-        else if (wide && b.terms == 1) hipLaunchKernelGGL((head_weights_kernel<1, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
-        else if (wide) hipLaunchKernelGGL((head_weights_kernel<2, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
-        else if (b.terms == 1) hipLaunchKernelGGL((head_weights_kernel<1, 128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, w);
-        else hipLaunchKernelGGL((head_weights_kernel<2, 128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, w);
+        if (wide && b.terms == 2 && brief) hipLaunchKernelGGL((head_weights_kernel<2, 256, 256, 2, 4, 1, 64, 4>), grid, dim3(512), 0, stream, w);
+        else if (wide && brief) hipLaunchKernelGGL((head_weights_kernel<3, 256, 256, 2, 4, 1, 64, 4>), grid, dim3(512), 0, stream, w);
+        else if (wide && b.terms == 2) hipLaunchKernelGGL((head_weights_kernel<2, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
+        else if (wide) hipLaunchKernelGGL((head_weights_kernel<3, 256, 256, 2, 4, 1>), grid, dim3(512), 0, stream, w);
+        else if (b.terms == 2) hipLaunchKernelGGL((head_weights_kernel<2, 128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, w);
+        else hipLaunchKernelGGL((head_weights_kernel<3, 128, 64, 4, 1, 3>), grid, dim3(256), 0, stream, w);
         if ((e = hipGetLastError()) != hipSuccess) return e;
       }
     }
