@@ -733,13 +733,14 @@ __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weigh
 #pragma unroll
     for (int j = 0; j < FT; ++j) {
       const int r = (wt * FT + j) * 32 + (lane & 31);
-      float sr = 0.0f, share = 0.0f, given = 0.0f, lse2 = 3e38f;          // p = 0
+      // (no row, or one without a gradient: logits of 0 against an infinite lse, p = 0)
+      float sr = 0.0f, share = 0.0f, given = 0.0f, lse2 = __builtin_inff();
       int target = -1024;                                    // in this tile, or far outside
       if (t0 + r < p.l.M) {
-        sr = rows[turn][0][r];
         const float lse = rows[turn][1][r];
         // a row whose log-sum-exp is off by a factor e or more in p has no gradient
         if (!(fabsf(lse) >= 16777216.0f)) {
+          sr = rows[turn][0][r];
           lse2 = lse * kLog2e;
           const float rest = __builtin_fmaf(lse, kLog2e, -lse2);         // exp2(-rest) is the row's factor
           share = rows[turn][2][r] * __builtin_amdgcn_exp2f(-rest);

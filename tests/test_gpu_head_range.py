@@ -93,3 +93,43 @@ def test_scales_far_apart(m, n, k, dtype):
     t = rng.integers(0, n, m)
     gg = (-rng.uniform(0.5, 1.5, m) * 2.0 ** -rng.integers(0, 20, m)).astype(np.float32)
     check(qa, sa, qb, sb, t, gg, None, dtype, "scales")
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("m", [40, 300])
+def test_far_logits_have_no_gradient(m, dtype):
+    """Rows of finite logits up to 2.6e38, whose log-sum-exp is finite and above 2^24: their gradient is 0 and they add
+    nothing to dBt, with or without a token."""
+    say("far", m, dtype)
+    rng = np.random.default_rng(m)
+    n, k = 500, 16
+    qa, sa = R.codes(rng, m, k)
+    qb, sb = R.codes(rng, n, k)
+    far = np.arange(m) % 5 == 2
+    qa[far], qb[::4] = 127, 127
+    sa, sb = (sa * np.where(far, 1e16, 2e-20)).astype(np.float32), np.full(n, 0.9e16, np.float32)
+    sa[far] = np.where(np.arange(int(far.sum())) % 2 == 0, 1.1e17, 1e10).astype(np.float32)
+    t = rng.integers(0, n, m)
+    t[7], t[9] = -1, n
+    size = 64.0 / m if dtype == "f16" else 1.0 / m
+    gg = (-size * rng.uniform(0.5, 1.5, m)).astype(np.float32)
+    gl = (0.1 * size * rng.standard_normal(m)).astype(np.float32)
+    x = R.logits(qa, sa, qb, sb)
+    assert np.isfinite(x).all() and x.max() > 2.5e38
+    lse = x.max(1)
+    lse[~far] = R.logsumexp(x[~far])
+    lse = lse.astype(np.float32)
+    assert np.isfinite(lse).all() and (lse[far] >= 2.0 ** 24).all()
+    A, B = R.padded(qa), R.padded(qb)
+    SA, SB, T, L, G, GL = (torch.from_numpy(v).cuda() for v in (sa, sb, t, lse, gg, gl))
+    _, got = g.gemm_i8_logprobs(A, SA, B, SB, T)
+    assert np.array_equal(host(got)[far], lse[far].astype(np.float64))
+    dA, dB = g.gemm_i8_logprobs_bwd(A, SA, B, SB, T, L, G, GL, DTYPES[dtype])
+    assert (host(dA)[far] == 0).all()
+    near = ~far
+    wa, wb, oa, ob = grads(qa[near], sa[near], qb, sb, t[near], lse[near], gg[near], gl[near], dtype)
+    h, least = half_step(DTYPES[dtype]) * 1.001, tiny(DTYPES[dtype])
+    # (dA holds the vocabulary's values, up to 1e18: f16 has no such numbers)
+    if dtype != "f16":
+        within(host(dA)[near], wa, oa + (np.abs(wa) + oa) * h + least, "dA")
+    within(host(dB), wb, ob + (np.abs(wb) + ob) * h + least, "dBt")
