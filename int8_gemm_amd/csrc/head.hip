@@ -14,8 +14,8 @@
 // number, and two for bf16 ones (2^-16 of each value, where the outputs' own
 // rounding is 2^-8).  bf16 has binary32's exponents, so a probability of 2^-120 has
 // as many bits as one of 1/2: a rare token's row of dBt is nothing but such values.
-// (f16 terms are half the products, but their least number is a probability of
-// 2^-40.)  Powers of two of each row and column keep the scales from mattering (see
+// (f16 terms are half the products, or two thirds, but their least number is a
+// probability of 2^-40.)  Powers of two of each row and column keep the scales from mattering (see
 // the backward part).
 //
 // Forward: a workgroup multiplies a tile of vocabulary rows by a tile of
@@ -290,7 +290,7 @@ struct FwdArgs {
 // an eighth of the tiles, neighbours in their order, its workgroups every so
 // many.  Where a workgroup has several, the next one's first loads are on their
 // way while this one's logits are worked on (8192 x 50304 x 768: 377 us, and 385
-// with a workgroup a tile; with T in place of the sums 440 and 465).
+// with a workgroup a tile).
 struct Walk {
   int at, end, step;
   __device__ Walk(int first, int total, int tiles) {       // tiles first ... first + total - 1 of `tiles`
@@ -569,8 +569,8 @@ __global__ void __launch_bounds__(256) head_bounds_kernel(const RowArgs p, Bound
 // column l%32, rows 8 (l/32) ... + 7.  Zero beyond the rows and `cols`.  And what
 // the products need of each row.
 // Up to so many rows of both sides every workgroup looks through them itself, and
-// no launch comes before (805 x 1864 x 296 38.6 us and 39.9; 1500 x 6000 x 100 53.9
-// and 52.1).
+// no launch comes before (805 x 1864 x 296 takes 1.3 us less than with it, 1500 x
+// 6000 x 100 1.8 more).
 constexpr int kOwnBounds = 4096;
 struct PackArgs {
   LogitArgs l;
@@ -683,7 +683,8 @@ struct WeightArgs {            // T of a piece
 };
 
 // The forward tiles again, with T in place of the sums, written beside the next
-// tile's loads: 8192 x 50304 x 768 in two terms 1.65 GB.
+// tile's loads: 8192 x 50304 x 768 in two terms 590 us for five pieces, 1.68 GB
+// written; 2048 x 50257 x 768 in three terms 184 us for the wide tiles, 0.60 GB.
 template <int TERMS, int BV, int BT, int WV, int WT, int PER_CU, int SB = 128, int S = 2>
 __global__ void __launch_bounds__(WV * WT * 64, PER_CU * WV * WT / 4) head_weights_kernel(const WeightArgs p) {
   using Tile = LogitTile<BV, BT, WV, WT, SB, S>;
@@ -1119,7 +1120,8 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
     }
   };
   // A tile's rows through LDS: a store has 512 bytes of a row or more (23 x 12669 x
-  // 1716 bf16 63 us, and 95 where a lane stores its 8 bytes of 32 rows).
+  // 1716 bf16, products of one term, 63 us, and 95 where a lane stores its 8 bytes of
+  // 32 rows).
   if (TERMS == 2) write(bf16_t{});
   else if (p.dtype == DT_F32) write(float{});
   else write(f16_t{});
@@ -1127,11 +1129,12 @@ __device__ __forceinline__ void grads_unit(const GradArgs& p, const GradArgs::Si
 
 // Each XCD (workgroups are dealt to the 8 in turn) takes an eighth of either
 // side's units, neighbours in their order: they share T or codes in its L2.
-// The longer ones go first.  8192 x 50304 x 768 bf16: 1.27 PFLOP in 1100 us, 1.15
-// PFLOPS (library products of these shapes reach 0.82 and 1.05); without the loads
-// 1.27 PFLOPS, so most of what is left is the matrix cores' own pace.  (Dealt without regard
-// to the XCDs, dA's units came to lie on one: 2048 x 50257 x 768 f32 1783 us in
-// all, 791 as they are dealt here.)
+// The longer ones go first.  8192 x 50304 x 768 bf16, two terms: 2.53 TFLOP in
+// five launches of 463 us (medians), 1.09 PFLOPS (library products of these shapes
+// reach 0.82 and 1.05); 2048 x 50257 x 768 f32, three terms: 0.95 TFLOP in 764 us,
+// 1.24 PFLOPS.  The matrix cores are busy 64 and 68% of the time, at 1.8 to 1.9 GHz.
+// (Dealt without regard to the XCDs, dA's units came to lie on one: the latter, with
+// two terms, took 1783 us in all, and 791 as they are dealt here.)
 // LAST: 32-blocks along k that a wave multiplies in the last tile of k.
 template <int TERMS, bool FEW, int LAST>
 __global__ void __launch_bounds__(512, FEW ? 4 : 2) head_grads_kernel(const GradArgs p) {
@@ -1169,8 +1172,8 @@ struct FinishArgs {
   int64_t groups;              // workgroups of side[0]; those behind take side[1]
   int tiles_k, dtype, cols;
 };
-// The planes' sum, in their order, by its row's scale: memory, 8192 x 768 with 8
-// planes 28 us.
+// The planes' sum, in their order, by its row's scale: memory, 8192 x 768 with 4
+// planes 28 us for 114 MB.
 __global__ void __launch_bounds__(256) head_finish_kernel(const FinishArgs p) {
   const bool second = blockIdx.x >= p.groups;
   const FinishArgs::Side& s = p.side[second];
